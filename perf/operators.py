@@ -1,0 +1,428 @@
+"""The paged key-value cache of a speculative decoding round, and the attention that reads it, as cases to measure.
+
+A round scores N new tokens of every sequence (node 0, the last token emitted, and the drafted nodes): their
+keys and values are appended to the cache, the attention scores them over the cache and their own ancestors, the
+verification picks a path, and the commit keeps that path's entries.  Pages are taken, shared, copied and given back
+around it.  Four operators: "attend", "append", "commit" and "pages" (fork, grow with copy on write, give back).
+
+Cache layout, E = 16 / element size, a sequence's slot s lies in page page_table[b, s // page] at t = s % page:
+    k_pages [P, Hkv, D / E, page, E]   the key's element d of slot t at [p, h, d // E, t, d % E]
+    v_pages [P, Hkv, page / E, D, E]   the value's element d of slot t at [p, h, t // E, d, t % E]
+with a layer axis in front where a call works on every layer.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+#: Row codes: a sequence that the pool has no pages left for.
+NO_PAGES = -9
+
+
+def listed():
+    return [
+        # one token of one chat of about a thousand tokens: the smallest step, where latency counts
+        {"name": "attend one token, short", "op": "attend", "dtype": "bf16", "B": 1, "N": 1, "Hkv": 8, "group": 4, "D": 128,
+         "page": 16, "lo": 1009, "hi": 1009, "tree": False, "ragged": False, "window": 0, "sinks": 0},
+        # plain decoding of a full batch with lengths of every kind: the cache's bytes are all there is
+        {"name": "attend one token, batch", "op": "attend", "dtype": "bf16", "B": 64, "N": 1, "Hkv": 8, "group": 4, "D": 128,
+         "page": 64, "lo": 257, "hi": 16001, "tree": False, "ragged": False, "window": 0, "sinks": 0},
+        # 16 draft trees of 32 nodes, the batch that the tree verification is measured on
+        {"name": "attend trees", "op": "attend", "dtype": "bf16", "B": 16, "N": 32, "Hkv": 8, "group": 4, "D": 128,
+         "page": 32, "lo": 2000, "hi": 8111, "tree": True, "ragged": False, "window": 0, "sinks": 0},
+        # eight float32 chains of up to five drafts on small heads, some sequences with fewer new tokens or none
+        {"name": "attend chains f32", "op": "attend", "dtype": "f32", "B": 8, "N": 6, "Hkv": 4, "group": 2, "D": 64,
+         "page": 16, "lo": 1, "hi": 2500, "tree": False, "ragged": True, "window": 0, "sinks": 0},
+        # chains of four drafts on long contexts of which a window and the first four tokens stay visible, wide heads
+        {"name": "attend window and sinks", "op": "attend", "dtype": "bf16", "B": 32, "N": 5, "Hkv": 2, "group": 8, "D": 256,
+         "page": 64, "lo": 3, "hi": 40009, "tree": False, "ragged": True, "window": 4001, "sinks": 4},
+        # one layer's new keys and values of a batch of four-draft chains
+        {"name": "append chains", "op": "append", "dtype": "bf16", "B": 64, "N": 5, "Hkv": 8, "D": 128, "page": 64,
+         "lo": 1, "hi": 2000, "ragged": True},
+        # a prompt's chunk of a few sequences
+        {"name": "append prompts", "op": "append", "dtype": "bf16", "B": 8, "N": 1000, "Hkv": 8, "D": 128, "page": 64,
+         "lo": 0, "hi": 999, "ragged": True},
+        # the accepted paths of 16 trees of 32 nodes, every layer of a model of 32
+        {"name": "commit trees", "op": "commit", "dtype": "bf16", "L": 32, "B": 16, "N": 32, "Hkv": 8, "D": 128, "page": 32,
+         "lo": 1, "hi": 500},
+        # four float32 trees in the two layers of a draft model
+        {"name": "commit trees f32", "op": "commit", "dtype": "f32", "L": 2, "B": 4, "N": 13, "Hkv": 4, "D": 64, "page": 16,
+         "lo": 0, "hi": 300},
+        # a round's pages for a batch of chains: room for the new tokens, and back after the verification
+        {"name": "pages of a round", "op": "pages", "dtype": "bf16", "L": 1, "B": 256, "N": 8, "forks": 0, "Hkv": 1, "D": 64,
+         "page": 16, "lo": 1, "hi": 2000, "spare": 300},
+        # four prompts, each continued three ways: tables shared, the last pages copied in every layer
+        {"name": "pages forked, few", "op": "pages", "dtype": "bf16", "L": 4, "B": 4, "N": 8, "forks": 3, "Hkv": 4, "D": 64,
+         "page": 32, "lo": 40, "hi": 400, "spare": 40},
+        # 16 prompts, each continued seven ways, every layer of a model of 32
+        {"name": "pages forked, many", "op": "pages", "dtype": "bf16", "L": 32, "B": 16, "N": 8, "forks": 7, "Hkv": 8, "D": 128,
+         "page": 64, "lo": 100, "hi": 1000, "spare": 200},
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["attend", "attend", "attend", "append", "commit", "pages"])
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    D, page = rng.choice([64, 128, 256]), rng.choice([16, 32, 64, 128])
+    if op == "attend":
+        N = 1 if rng.random() < 0.3 else _log(rng, 2, 64)
+        Hkv, group = rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 3, 4, 5, 7, 8, 16])
+        hi = _log(rng, 20, 16000)
+        B = _log(rng, 1, max(1, min(64, int(2e9 / (hi * Hkv * D * (4 * group * N / 64 + 8))))))
+        window = _log(rng, 1, 2 * hi) if rng.random() < 0.3 else 0
+        return {"op": op, "dtype": dtype, "B": B, "N": N, "Hkv": Hkv, "group": group, "D": D, "page": page, "lo": rng.randint(0, hi), "hi": hi,
+                "tree": N > 1 and rng.random() < 0.5, "ragged": rng.random() < 0.5, "window": window, "sinks": rng.randint(0, 20) if window else 0}
+    if op == "append":
+        N = _log(rng, 1, 1000)
+        return {"op": op, "dtype": dtype, "B": _log(rng, 1, max(1, min(256, 8000 // N))), "N": N, "Hkv": rng.choice([1, 2, 4, 8]), "D": D, "page": page,
+                "lo": 0, "hi": _log(rng, 10, 1000), "ragged": rng.random() < 0.5}
+    if op == "commit":
+        return {"op": op, "dtype": dtype, "L": _log(rng, 1, 32), "B": _log(rng, 1, 16), "N": _log(rng, 2, 64), "Hkv": rng.choice([1, 2, 4, 8]),
+                "D": rng.choice([64, 128]), "page": page, "lo": 0, "hi": _log(rng, 10, 300)}
+    return {"op": op, "dtype": dtype, "L": _log(rng, 1, 16), "B": _log(rng, 1, 16), "N": _log(rng, 1, 64), "forks": rng.randint(0, 7),
+            "Hkv": rng.choice([1, 2, 4, 8]), "D": rng.choice([64, 128]), "page": page, "lo": rng.randint(0, 10), "hi": _log(rng, 11, 800),
+            "spare": rng.randint(0, 300)}
+
+
+def _lens(case):
+    """The batch's cached lengths: spread evenly over the case's range."""
+    B, lo, hi = case["B"], case["lo"], case["hi"]
+    return [hi - (hi - lo) * i // max(1, B - 1) for i in range(B)]
+
+
+def _news(case):
+    """New tokens of each sequence: N, or where the batch is ragged every count from N down to 0 in turn."""
+    B, N = case["B"], case["N"]
+    return [N - i * (N + 1) // B if case.get("ragged") else N for i in range(B)]
+
+
+def _paths(case, pick):
+    """Accepted nodes of each tree: increasing, about a third of the nodes at most, some trees none."""
+    out = []
+    for _ in range(case["B"]):
+        most = max(1, case["N"] // 3) if case["N"] > 1 else 0
+        out.append(sorted(pick.sample(range(1, case["N"]), pick.randint(0, most))) if most else [])
+    return out
+
+
+def _pages_of(tokens, page):
+    return -(-tokens // page)
+
+
+def _esz(case):
+    return 4 if case["dtype"] == "f32" else 2
+
+
+def work(case):
+    op, esz, D = case["op"], _esz(case), case["D"]
+    lens = _lens(case)
+    if op == "attend":
+        W, S, tok, vis = case["window"], case["sinks"], 0, 0
+        for n, m in zip(lens, _news(case)):
+            if m:
+                first = max(0, n - W + 1) if W else 0
+                tok += n - first + min(S, first) + m
+                vis += (n - first + min(S, first) + 1) * m
+        rows = sum(_news(case)) * case["Hkv"] * case["group"]
+        return {"bytes": 2 * tok * case["Hkv"] * D * esz + 2 * rows * D * esz, "flops": 4 * vis * case["Hkv"] * case["group"] * D}
+    if op == "append":
+        return {"bytes": 4 * sum(_news(case)) * case["Hkv"] * D * esz, "flops": 0}
+    if op == "commit":
+        moved = case["B"] * max(1, case["N"] // 3) / 2  # the mean over the seeds: a path of up to a third of the nodes
+        return {"bytes": 4 * moved * case["L"] * case["Hkv"] * D * esz + 8 * case["B"] * case["N"], "flops": 0}
+    seqs = case["B"] * (1 + case["forks"])
+    copied = sum(n % case["page"] for n in lens) * (1 + case["forks"]) if case["forks"] else 0
+    tables = 4 * seqs * _pages_of(case["N"], case["page"]) + 4 * sum(_pages_of(n, case["page"]) for n in lens) * case["forks"] * 2
+    return {"bytes": 4 * copied * case["L"] * case["Hkv"] * D * esz + tables + 32 * seqs, "flops": 0}
+
+
+def _cache(case, layers, P, gen):
+    dt, page, D, E = TYPES[case["dtype"]], case["page"], case["D"], 16 // _esz(case)
+    k = torch.randn((layers, P, case["Hkv"], D // E, page, E), generator=gen, device="cuda", dtype=dt)
+    v = torch.randn((layers, P, case["Hkv"], page // E, D, E), generator=gen, device="cuda", dtype=dt)
+    return k, v
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    pick = random.Random(seed)
+    op, B, N, page, dt = case["op"], case["B"], case["N"], case["page"], TYPES[case["dtype"]]
+    lens = _lens(case)
+    pick.shuffle(lens)
+    seqs = B * (1 + case["forks"]) if op == "pages" else B
+    width = _pages_of(max(lens) + N, page) + 1
+    held = [_pages_of(n if op == "pages" else n + N, page) for n in lens]
+    P = sum(held) + (case["spare"] if op == "pages" else 3)
+    ids = list(range(P))
+    pick.shuffle(ids)  # a cache that has served for a while: a sequence's pages lie anywhere
+    table, at = [], 0
+    for n in held:
+        table.append(ids[at:at + n] + [-1] * (width - n))
+        at += n
+    table += [[-1] * width for _ in range(seqs - B)]
+    i32 = dict(device="cuda", dtype=torch.int32)
+    s = {"case": case, "page_table": torch.tensor(table, **i32), "cache_len": torch.tensor(lens + [0] * (seqs - B), **i32)}
+    k, v = _cache(case, case.get("L", 1), P, gen)
+    s["k_pages"], s["v_pages"] = (k, v) if op in ("commit", "pages") else (k[0], v[0])
+    if op in ("attend", "append"):
+        news = _news(case)
+        pick.shuffle(news)
+        s["n_new"] = torch.tensor(news, **i32) if case["ragged"] else None
+    if op == "attend":
+        q = torch.randn((B, N, case["Hkv"] * case["group"], case["D"]), generator=gen, device="cuda")
+        s["q"] = (2 * q).to(dt)  # scores of a spread of about 2: some tokens carry most of a row
+        s["parent"] = None
+        if case["tree"]:
+            back = torch.randint(0, 4, (B, N), generator=gen, device="cuda")
+            node = torch.arange(N, device="cuda")
+            s["parent"] = torch.where(node > 0, (node - 1 - back).clamp_min(0), -1).to(torch.int32)
+    elif op == "append":
+        s["k"] = torch.randn((B, N, case["Hkv"], case["D"]), generator=gen, device="cuda").to(dt)
+        s["v"] = torch.randn((B, N, case["Hkv"], case["D"]), generator=gen, device="cuda").to(dt)
+    elif op == "commit":
+        paths = _paths(case, pick)
+        s["accepted_len"] = torch.tensor([len(p) for p in paths], **i32)
+        s["path_nodes"] = torch.tensor([p + [-1] * (N - len(p)) for p in paths], **i32)
+    else:
+        ref = torch.zeros(P, **i32)
+        ref[torch.tensor(ids[:at], device="cuda", dtype=torch.int64)] = 1
+        s["ref_count"] = ref
+        s["free_map"] = _free_map(ref)
+        s["seq_pages"] = torch.tensor(held + [0] * (seqs - B), **i32)
+        n = B * case["forks"]
+        s["src"] = torch.tensor([i // case["forks"] for i in range(n)], **i32) if n else None
+        s["dst"] = torch.tensor([B + i for i in range(n)], **i32) if n else None
+        full = torch.tensor(lens + [lens[i // case["forks"]] for i in range(n)], **i32)
+        s["grown"] = full + N
+        s["after"] = torch.tensor(lens + [0] * n, **i32)
+    return s
+
+
+def _free_map(ref):
+    """A bit for each page that nobody holds, 32 to a word."""
+    P = ref.numel()
+    bits = torch.zeros(_pages_of(P, 32) * 32, dtype=torch.int64, device=ref.device)
+    bits[:P] = ref == 0
+    words = (bits.view(-1, 32) << torch.arange(32, device=ref.device)).sum(1)
+    return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+
+
+def _slots(table, slot, page):
+    """Page and place in it of each slot [B, n] of each sequence."""
+    return table.gather(1, (slot // page).long()).long(), (slot % page).long()
+
+
+def _plain_attend(s):
+    c = s["case"]
+    B, N, Hkv, g, D, page, W = c["B"], c["N"], c["Hkv"], c["group"], c["D"], c["page"], c["window"]
+    dev, q = s["q"].device, s["q"]
+    n = s["cache_len"].long()
+    m = s["n_new"].long() if s["n_new"] is not None else torch.full_like(n, N)
+    pages = s["page_table"][:, :_pages_of(max(c["hi"], c["lo"]) + N, page)].clamp_min(0).long()
+    T = pages.shape[1] * page
+    k = s["k_pages"][pages].permute(0, 2, 1, 4, 3, 5).reshape(B, Hkv, T, D).float()
+    v = s["v_pages"][pages].permute(0, 2, 1, 3, 5, 4).reshape(B, Hkv, T, D).float()
+    node = torch.arange(N, device=dev)
+    if s["parent"] is None:
+        sees = (node[None, :] <= node[:, None]).expand(B, N, N)
+    else:  # sum of the powers of the parent matrix: one where j is i or an ancestor of i
+        up = (s["parent"][:, :, None] == node).float()
+        eye = torch.eye(N, device=dev).expand(B, N, N)
+        sees = torch.linalg.solve_triangular(eye - up, eye.contiguous(), upper=False, unitriangular=True) > 0.5
+    depth = sees.sum(2) - 1
+    pos_q = n[:, None] + depth
+    t = torch.arange(T, device=dev)
+    new = t[None, :] - n[:, None]  # which new node a slot holds
+    at = new.clamp(0, N - 1)
+    pos_k = torch.where(new < 0, t[None, :], n[:, None] + depth.gather(1, at))
+    seen = (new < 0)[:, None, :] | ((new < m[:, None])[:, None, :] & sees.gather(2, at[:, None, :].expand(B, N, T)))
+    if W:
+        seen = seen & ((pos_q[:, :, None] - pos_k[:, None, :] < W) | (pos_k < c["sinks"])[:, None, :])
+    live = (node[None, :] < m[:, None])
+    z = torch.matmul(q.float().view(B, N, Hkv, g, D).permute(0, 2, 1, 3, 4).reshape(B, Hkv, N * g, D), k.transpose(2, 3).contiguous())
+    z = (z / math.sqrt(D)).view(B, Hkv, N, g, T).masked_fill(~seen[:, None, :, None, :], -math.inf)
+    e = torch.exp(z - z.amax(-1, keepdim=True))
+    p = (e / e.sum(-1, keepdim=True)).reshape(B, Hkv, N * g, T)
+    v = v.masked_fill(~(new < m[:, None])[:, None, :, None], 0.0)
+    o = torch.matmul(p, v).view(B, Hkv, N, g, D).permute(0, 2, 1, 3, 4).reshape(B, N, Hkv * g, D)
+    o = o.masked_fill(~live[:, :, None, None], 0.0)
+    return o.to(q.dtype), torch.zeros(B, dtype=torch.int32, device=dev)
+
+
+def _plain_append(s):
+    c = s["case"]
+    B, N, page = c["B"], c["N"], c["page"]
+    E = 16 // _esz(c)
+    slot = s["cache_len"][:, None] + torch.arange(N, device="cuda", dtype=torch.int32)
+    pg, t = _slots(s["page_table"], slot, page)
+    k, v = s["k"].flatten(0, 1), s["v"].flatten(0, 1)
+    pg, t = pg.flatten(), t.flatten()
+    if s["n_new"] is not None:
+        rows = (torch.arange(N, device="cuda") < s["n_new"][:, None]).flatten().nonzero()[:, 0]
+        pg, t, k, v = pg[rows], t[rows], k[rows], v[rows]
+    s["k_pages"][pg, :, :, t] = k.unflatten(2, (-1, E))
+    s["v_pages"][pg, :, t // E, :, t % E] = v
+    return s["k_pages"], s["v_pages"], torch.zeros(B, dtype=torch.int32, device="cuda")
+
+
+def _plain_commit(s):
+    c = s["case"]
+    N, E = c["N"], 16 // _esz(c)
+    j = torch.arange(N, device="cuda", dtype=torch.int32)
+    kept = j < s["accepted_len"][:, None]
+    n = s["cache_len"][:, None]
+    # entries that stay are moved onto themselves: node 0's slot onto itself
+    sp, st = (x.flatten() for x in _slots(s["page_table"], n + torch.where(kept, s["path_nodes"], 0), c["page"]))
+    dp, dt = (x.flatten() for x in _slots(s["page_table"], n + torch.where(kept, j + 1, 0), c["page"]))
+    s["k_pages"][:, dp, :, :, dt] = s["k_pages"][:, sp, :, :, st]
+    s["v_pages"][:, dp, :, dt // E, :, dt % E] = s["v_pages"][:, sp, :, st // E, :, st % E]
+    return s["k_pages"], s["v_pages"], s["cache_len"] + 1 + s["accepted_len"], torch.zeros_like(s["accepted_len"])
+
+
+def _plain_resize(s, keep, want):
+    """The pages of every sequence after it keeps `keep` tokens and has room for `want`: pages behind are given back, then
+    the lowest free ones taken, in the order of the sequences and of their slots."""
+    table, ref, page = s["page_table"], s["ref_count"], s["case"]["page"]
+    S, width = table.shape
+    i = torch.arange(width, device=table.device)
+    held, goal = s["seq_pages"][:, None], ((want + page - 1) // page)[:, None]
+    ids = table.clamp_min(0).long()
+    drop = (i >= goal) & (i < held)
+    ref.index_put_((ids.flatten(),), -drop.flatten().int(), accumulate=True)
+    shared = (i >= (keep // page)[:, None]) & (i < torch.minimum(held, goal)) & (ref[ids] > 1)
+    need = shared | ((i >= held) & (i < goal))
+    order = torch.argsort((ref != 0).int(), stable=True)  # the free pages first, lowest first
+    ends = need.sum(1).cumsum(0)
+    ok = (ends <= (ref == 0).sum()) | ~need.any(1)
+    need = need & ok[:, None]
+    shared = shared & ok[:, None]
+    rank = (need.flatten().cumsum(0) - 1).clamp(0, ref.numel() - 1)
+    fresh = order[rank].view(S, width)
+    copied = shared & (i == (keep // page)[:, None]) & ((keep % page) > 0)[:, None]
+    b = copied.nonzero()
+    if b.numel():
+        old, new = ids[b[:, 0], b[:, 1]], fresh[b[:, 0], b[:, 1]]
+        s["k_pages"][:, new] = s["k_pages"][:, old]
+        s["v_pages"][:, new] = s["v_pages"][:, old]
+    ref.index_put_((ids.flatten(),), -shared.flatten().int(), accumulate=True)
+    ref.index_put_((fresh.flatten(),), need.flatten().int(), accumulate=True)
+    table.copy_(torch.where(need, fresh.int(), torch.where(drop, -1, table)))
+    s["seq_pages"].copy_(torch.where(ok, goal[:, 0], torch.minimum(held, goal)[:, 0]))
+    s["free_map"].copy_(_free_map(ref))
+    return torch.where(ok, 0, NO_PAGES).int()
+
+
+def _plain_pages(s):
+    out = {}
+    if s["src"] is not None:
+        src, dst, page = s["src"].long(), s["dst"].long(), s["case"]["page"]
+        s["page_table"][dst] = s["page_table"][src]
+        s["seq_pages"][dst] = s["seq_pages"][src]
+        s["cache_len"][dst] = s["cache_len"][src]
+        rows = s["page_table"][src]
+        s["ref_count"].index_put_((rows.clamp_min(0).long().flatten(),), (rows >= 0).int().flatten(), accumulate=True)
+        out["fork"] = torch.zeros_like(s["src"])
+    out["grow"] = _plain_resize(s, s["cache_len"], s["grown"])
+    out["grown"] = s["page_table"].clone()
+    out["shrink"] = _plain_resize(s, s["after"], s["after"])
+    return {**out, **{n: s[n] for n in ("page_table", "seq_pages", "ref_count", "free_map", "cache_len", "k_pages", "v_pages")}}
+
+
+def _own_pages(s, sv):
+    pool = sv.PagePool(s["page_table"], s["seq_pages"], s["ref_count"], s["free_map"])
+    out = {}
+    if s["src"] is not None:
+        out["fork"] = sv.spec_cache_fork(pool, s["cache_len"], s["src"], s["dst"])
+    out["grow"] = sv.spec_cache_resize(pool, s["cache_len"], s["grown"], s["k_pages"], s["v_pages"])
+    out["grown"] = s["page_table"].clone()
+    out["shrink"] = sv.spec_cache_resize(pool, s["after"], s["after"], s["k_pages"], s["v_pages"])
+    return {**out, **{n: s[n] for n in ("page_table", "seq_pages", "ref_count", "free_map", "cache_len", "k_pages", "v_pages")}}
+
+
+def run(s):
+    c = s["case"]
+    if not own:
+        return {"attend": _plain_attend, "append": _plain_append, "commit": _plain_commit, "pages": _plain_pages}[c["op"]](s)
+    import rejection_sampling_verify_02_amd as sv
+    if c["op"] == "attend":
+        return sv.spec_paged_attention(s["q"], s["k_pages"], s["v_pages"], s["page_table"], s["cache_len"], parent=s["parent"], n_new=s["n_new"],
+                                       window=c["window"], sinks=c["sinks"])
+    if c["op"] == "append":
+        st = sv.spec_cache_append(s["k"], s["v"], s["k_pages"], s["v_pages"], s["page_table"], s["cache_len"], n_new=s["n_new"])
+        return s["k_pages"], s["v_pages"], st
+    if c["op"] == "commit":
+        n, st = sv.spec_cache_commit(s["k_pages"], s["v_pages"], s["page_table"], s["cache_len"], s["accepted_len"], s["path_nodes"])
+        return s["k_pages"], s["v_pages"], n, st
+    return _own_pages(s, sv)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "attend":
+        return _exact_attend(case, s), None
+    # the other operators move values and count pages: the copies are exact, entry by entry
+    if case["op"] == "append":
+        return _exact_append(case, s)
+    if case["op"] == "commit":
+        return _exact_commit(case, s)
+    return None
+
+
+def _exact_attend(case, s):
+    N, Hkv, g, D, page = case["N"], case["Hkv"], case["group"], case["D"], case["page"]
+    out = torch.zeros((case["B"], N, Hkv * g, D), dtype=torch.float64, device="cuda")
+    lens = s["cache_len"].tolist()
+    news = s["n_new"].tolist() if s["n_new"] is not None else [N] * case["B"]
+    parents = s["parent"].tolist() if s["parent"] is not None else [[i - 1 for i in range(N)]] * case["B"]
+    for b, (n, m) in enumerate(zip(lens, news)):
+        used = s["page_table"][b, :_pages_of(n + m, page)].long()
+        k = s["k_pages"][used].double().transpose(2, 3).flatten(3).transpose(0, 1).flatten(1, 2)  # [Hkv, slots, D]
+        v = s["v_pages"][used].double().transpose(3, 4).flatten(2, 3).transpose(0, 1).flatten(1, 2)
+        depth = [0] * N
+        for i in range(m):
+            line, j = [], i
+            while j >= 0:
+                line.append(j)
+                j = parents[b][j]
+            depth[i] = len(line) - 1
+            p = n + depth[i]
+            first = max(0, p - case["window"] + 1) if case["window"] else 0
+            head = min(case["sinks"], first, n)
+            slots = list(range(head)) + list(range(min(first, n), n))
+            slots += [n + j for j in sorted(line) if n + depth[j] >= first or n + depth[j] < case["sinks"]]
+            at = torch.tensor(slots, device="cuda")
+            w = torch.einsum("hgd,htd->hgt", s["q"][b, i].double().view(Hkv, g, D), k[:, at]) / math.sqrt(D)
+            out[b, i] = torch.einsum("hgt,htd->hgd", torch.softmax(w, -1), v[:, at]).flatten(0, 1)
+    return out
+
+
+def _exact_append(case, s):
+    page, E = case["page"], 16 // _esz(case)
+    kp, vp = s["k_pages"].double(), s["v_pages"].double()
+    lens, table = s["cache_len"].tolist(), s["page_table"].tolist()
+    for b, m in enumerate(s["n_new"].tolist() if s["n_new"] is not None else [case["N"]] * case["B"]):
+        for i in range(m):
+            p, t = table[b][(lens[b] + i) // page], (lens[b] + i) % page
+            kp[p, :, :, t, :] = s["k"][b, i].double().view(case["Hkv"], -1, E)
+            vp[p, :, t // E, :, t % E] = s["v"][b, i].double()
+    return kp, vp, None
+
+
+def _exact_commit(case, s):
+    page, E = case["page"], 16 // _esz(case)
+    kp, vp = s["k_pages"].double(), s["v_pages"].double()
+    lens, table, path = s["cache_len"].tolist(), s["page_table"].tolist(), s["path_nodes"].tolist()
+    for b, a in enumerate(s["accepted_len"].tolist()):
+        for j in range(a):
+            x, y = lens[b] + path[b][j], lens[b] + 1 + j
+            p, t, r, u = table[b][x // page], x % page, table[b][y // page], y % page
+            kp[:, r, :, :, u] = kp[:, p, :, :, t].clone()
+            vp[:, r, :, u // E, :, u % E] = vp[:, p, :, t // E, :, t % E].clone()
+    return kp, vp, None, None
