@@ -288,7 +288,7 @@ def _plain_commit(s):
 
 def _plain_resize(s, keep, want):
     """The pages of every sequence after it keeps `keep` tokens and has room for `want`: pages behind are given back, then
-    the lowest free ones taken, in the order of the sequences and of their slots."""
+    the lowest free ones taken, in the order of the sequences and of their slots, also for pages to write that others hold."""
     table, ref, page = s["page_table"], s["ref_count"], s["case"]["page"]
     S, width = table.shape
     i = torch.arange(width, device=table.device)
@@ -296,7 +296,7 @@ def _plain_resize(s, keep, want):
     ids = table.clamp_min(0).long()
     drop = (i >= goal) & (i < held)
     ref.index_put_((ids.flatten(),), -drop.flatten().int(), accumulate=True)
-    shared = (i >= (keep // page)[:, None]) & (i < torch.minimum(held, goal)) & (ref[ids] > 1)
+    shared = (i >= (keep // page)[:, None]) & (i < torch.minimum(held, goal)) & (ref[ids] > 1) & (want > keep)[:, None]
     need = shared | ((i >= held) & (i < goal))
     order = torch.argsort((ref != 0).int(), stable=True)  # the free pages first, lowest first
     ends = need.sum(1).cumsum(0)
@@ -309,8 +309,11 @@ def _plain_resize(s, keep, want):
     b = copied.nonzero()
     if b.numel():
         old, new = ids[b[:, 0], b[:, 1]], fresh[b[:, 0], b[:, 1]]
-        s["k_pages"][:, new] = s["k_pages"][:, old]
-        s["v_pages"][:, new] = s["v_pages"][:, old]
+        k, v = s["k_pages"], s["v_pages"]
+        stays = torch.arange(page, device=table.device) < (keep % page)[b[:, 0], None]  # the kept slots alone
+        of_v = stays.view(-1, 1, v.shape[3], 1, v.shape[5])
+        k[:, new] = torch.where(stays[:, None, None, :, None], k[:, old], k[:, new])
+        v[:, new] = torch.where(of_v, v[:, old], v[:, new])
     ref.index_put_((ids.flatten(),), -shared.flatten().int(), accumulate=True)
     ref.index_put_((fresh.flatten(),), need.flatten().int(), accumulate=True)
     table.copy_(torch.where(need, fresh.int(), torch.where(drop, -1, table)))
