@@ -34,7 +34,10 @@ EXPORTED = ("spec_verify", "spec_verify_timed", "sv_workspace_bytes", "sv_worksp
             "sv_tree_workspace_zero_bytes", "sv_tree_launch_plan",
             "spec_typical_verify", "spec_typical_verify_timed", "sv_typical_workspace_bytes",
             "sv_typical_workspace_zero_bytes", "sv_typical_launch_plan", "sv_tag_epoch",
-            "sv_read_probe", "spec_verify_noalloc", "sv_timeline_stamps")
+            "sv_read_probe", "spec_verify_noalloc", "sv_timeline_stamps",
+            "spec_paged_attention", "spec_paged_attention_timed", "sv_attention_workspace_bytes",
+            "sv_attention_launch_plan", "spec_cache_append", "spec_cache_commit", "spec_cache_resize",
+            "sv_resize_workspace_bytes", "spec_cache_fork")
 
 
 class SpecVerifyError(RuntimeError):
@@ -112,6 +115,21 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_launch_plan.argtypes = [I32, I32, I32, I32, F32, I32]
     lib.sv_launch_plan.restype = ctypes.c_char_p
+    SI = ctypes.c_int64  # strides
+    attn = [V, SI, SI, V, V, I32, V, V, V, V, *[I32] * 8, F32, I32, I32, V, V, V, SZ, V]
+    for fn, args in ((lib.spec_paged_attention, attn), (lib.spec_paged_attention_timed, attn + [V, I32, V]),
+                     (lib.spec_cache_append, [V, SI, SI, V, SI, SI, I32, *[V] * 5, *[I32] * 7, V, V]),
+                     (lib.spec_cache_commit, [V, V, I32, *[V] * 4, *[I32] * 8, V, V, V]),
+                     (lib.spec_cache_resize, [*[V] * 8, *[I32] * 8, V, V, SZ, V]),
+                     (lib.spec_cache_fork, [*[V] * 6, *[I32] * 4, V, V])):
+        fn.argtypes = args
+        fn.restype = I32
+    lib.sv_attention_workspace_bytes.argtypes = [I32] * 8
+    lib.sv_attention_workspace_bytes.restype = SZ
+    lib.sv_resize_workspace_bytes.argtypes = [I32, I32]
+    lib.sv_resize_workspace_bytes.restype = SZ
+    lib.sv_attention_launch_plan.argtypes = []
+    lib.sv_attention_launch_plan.restype = ctypes.c_char_p
     if path is None:
         _lib = lib
     return lib
@@ -545,3 +563,18 @@ def spec_verify_noalloc(target_logits, draft_logits, draft_tokens, u_accept, u_s
     if st != 0:
         raise SpecVerifyError(st, sv_status_string(st))
     return acc, toks
+
+
+_CACHE_NAMES = ("PagePool", "empty_pages", "spec_paged_attention", "spec_cache_append", "spec_cache_commit",
+                "spec_cache_resize", "spec_cache_fork", "sv_attention_workspace_bytes", "sv_resize_workspace_bytes",
+                "sv_attention_launch_plan", "ROW_BAD_PAGE", "ROW_BAD_LENGTH", "ROW_NO_PAGES", "ROW_BAD_FORK",
+                "CACHE_MAX_NEW", "CACHE_MAX_SEQS")
+
+
+def __getattr__(name: str):
+    # the cache's binding needs torch when it is imported, this module only when it is called
+    if name in _CACHE_NAMES:
+        from . import cache
+        value = globals()[name] = getattr(cache, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,333 @@
+"""The paged key-value cache of a speculative decoding round and the attention that reads it.
+
+Thin binding over ``include/spec_cache.h`` (which has the layout, the semantics and the row
+codes), in the manner of the verification's binding: arguments are checked and marshalled
+here, every step runs in the library's HIP kernels, and nothing proceeds without the library.
+
+    pool = PagePool.empty(num_pages, max_seqs, table_width, device)
+    k_pages, v_pages = empty_pages(L, num_pages, Hkv, D, page_size, torch.bfloat16, device)
+    spec_cache_resize(pool, cache_len, cache_len + N, k_pages, v_pages)
+    for l in range(L):
+        spec_cache_append(k, v, k_pages[l], v_pages[l], pool.page_table, cache_len)
+        out, status = spec_paged_attention(q, k_pages[l], v_pages[l], pool.page_table, cache_len, parent=parent)
+    acc, tokens, path = spec_tree_verify(target_logits, draft_logits, tokens, parent, ...)
+    cache_len, status = spec_cache_commit(k_pages, v_pages, pool.page_table, cache_len, acc, path)
+    spec_cache_resize(pool, cache_len, cache_len, k_pages, v_pages)
+
+Calls are enqueued on the current stream of the tensors' device, or on ``stream`` (a raw
+hipStream_t), and may be captured into a HIP graph.  Work memory is taken for each call from
+torch's allocator on that stream, so calls on different streams never share any; pass
+``workspace`` (a uint8 tensor of at least the documented size) to keep it yourself.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from contextlib import nullcontext
+from typing import NamedTuple
+
+import torch
+
+from . import SV_BF16, SV_F32, SpecVerifyError, load_library, sv_status_string
+
+ROW_BAD_PAGE, ROW_BAD_LENGTH, ROW_NO_PAGES, ROW_BAD_FORK = -7, -8, -9, -10
+CACHE_MAX_NEW, CACHE_MAX_SEQS = 1024, 8192
+
+
+class PagePool(NamedTuple):
+    """The books of a pool of pages: which sequence holds which, and which are free."""
+    page_table: torch.Tensor  # [S, table_width] int32, -1 behind a sequence's pages
+    seq_pages: torch.Tensor   # [S] int32 pages held
+    ref_count: torch.Tensor   # [P] int32 sequences that hold a page
+    free_map: torch.Tensor    # [ceil(P / 32)] int32, a bit for each page that nobody holds
+
+    @classmethod
+    def empty(cls, num_pages: int, max_seqs: int, table_width: int, device) -> "PagePool":
+        i32 = dict(dtype=torch.int32, device=device)
+        free = torch.full(((num_pages + 31) // 32,), -1, **i32)
+        if num_pages % 32:
+            free[-1] = (1 << num_pages % 32) - 1
+        return cls(torch.full((max_seqs, table_width), -1, **i32), torch.zeros(max_seqs, **i32),
+                   torch.zeros(num_pages, **i32), free)
+
+
+def empty_pages(layers: int, num_pages: int, kv_heads: int, head_dim: int, page_size: int, dtype, device):
+    """Zeroed (k_pages, v_pages) of `layers` layers in the cache's layout."""
+    E = 16 // torch.empty((), dtype=dtype).element_size()
+    return (torch.zeros((layers, num_pages, kv_heads, head_dim // E, page_size, E), dtype=dtype, device=device),
+            torch.zeros((layers, num_pages, kv_heads, page_size // E, head_dim, E), dtype=dtype, device=device))
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    if t.dtype is torch.bfloat16:
+        return SV_BF16
+    if t.dtype is torch.float32:
+        return SV_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _ints(t, name: str, shape: tuple, dev, optional: bool = False):
+    """The address of a contiguous int32 tensor of that shape (None where it may be left out)."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} must be an int32 tensor, got None")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _pages(k_pages, v_pages, dims: int, dtype, dev):
+    """(P, Hkv, D, page_size) of a cache of `dims` dimensions (5: a layer, 6: all of them)."""
+    if k_pages.dim() != dims or v_pages.dim() != dims:
+        raise ValueError(f"k_pages and v_pages must have {dims} dimensions")
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
+        raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")
+    if k_pages.device != dev or v_pages.device != dev:
+        raise ValueError(f"k_pages and v_pages must be on {dev}")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("k_pages and v_pages must be contiguous")
+    P, H, U, page, E = k_pages.shape[-5:]
+    if E != 16 // k_pages.element_size() or page % E:
+        raise ValueError(f"k_pages must be [..., P, Hkv, D / {16 // k_pages.element_size()}, page_size, "
+                         f"{16 // k_pages.element_size()}], got {tuple(k_pages.shape)}")
+    if v_pages.shape != k_pages.shape[:-3] + (page // E, U * E, E):
+        raise ValueError(f"v_pages must have shape {tuple(k_pages.shape[:-3]) + (page // E, U * E, E)}, "
+                         f"got {tuple(v_pages.shape)}")
+    return P, H, U * E, page
+
+
+def _rows(t, name: str, B: int, N: int, H: int, D: int, dtype, dev):
+    """Address and strides (sequence, node) of a [B, N, H, D] tensor whose heads lie together."""
+    if t.shape != (B, N, H, D):
+        raise ValueError(f"{name} must have shape {(B, N, H, D)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    sb, sn, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}'s heads must lie together (strides D and 1), got strides {t.stride()}")
+    # a dimension of one entry may carry any stride: it is never stepped
+    return t.data_ptr(), sb if B > 1 else 0, sn if N > 1 else 0
+
+
+def _device(t, name: str):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _on(dev, stream):
+    """The context to allocate and launch in, and the raw stream."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return nullcontext(), torch.cuda.current_stream(dev).cuda_stream
+    if stream is None:
+        return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)), stream
+
+
+def _work(workspace, nbytes: int, dev):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if workspace.dtype is not torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace
+
+
+def _raise(rc: int):
+    if rc != 0:
+        raise SpecVerifyError(rc, sv_status_string(rc))
+
+
+def sv_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, page_size: int, table_width: int,
+                                 dtype: int) -> int:
+    return int(load_library().sv_attention_workspace_bytes(B, N, Hq, Hkv, D, page_size, table_width, dtype))
+
+
+def sv_resize_workspace_bytes(S: int, num_pages: int) -> int:
+    return int(load_library().sv_resize_workspace_bytes(S, num_pages))
+
+
+def sv_attention_launch_plan() -> list[str]:
+    return load_library().sv_attention_launch_plan().decode().split(";")
+
+
+def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=None, n_new=None, scale: float | None = None,
+                         window: int = 0, sinks: int = 0, workspace=None, stream=None, out=None, events=None):
+    """Attention of the new tokens over a paged cache (see include/spec_cache.h).
+
+    q [B, N, Hq, D] bfloat16 or float32 (heads together, any strides between sequences and
+    nodes), one layer's k_pages [P, Hkv, D/E, page, E] and v_pages [P, Hkv, page/E, D, E],
+    page_table [B, W], cache_len [B], n_new [B] (None: N each) and parent [B, N] (None: a
+    chain) int32.  scale defaults to 1 / sqrt(D).  Returns (out [B, N, Hq, D], row_status [B]);
+    ``out`` may supply the two tensors.  ``events`` as for spec_verify: the number of kernels is
+    then returned last.
+    """
+    lib = load_library()
+    dev = _device(q, "q")
+    dt = _code(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, D]")
+    B, N, Hq, D = q.shape
+    P, Hkv, Dk, page = _pages(k_pages, v_pages, 5, q.dtype, dev)
+    if Dk != D:
+        raise ValueError(f"the cache's heads have {Dk} elements, q's {D}")
+    qp, qb, qn = _rows(q, "q", B, N, Hq, D, q.dtype, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, table_width]")
+    W = page_table.shape[1]
+    ints = (_ints(page_table, "page_table", (B, W), dev), _ints(cache_len, "cache_len", (B,), dev),
+            _ints(n_new, "n_new", (B,), dev, True), _ints(parent, "parent", (B, N), dev, True))
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if out is None:
+            o, st = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
+        else:
+            o, st = out
+            if not o.is_contiguous():
+                raise ValueError("out must be contiguous")
+            _rows(o, "out", B, N, Hq, D, q.dtype, dev)
+            _ints(st, "row_status", (B,), dev)
+        ws = _work(workspace, lib.sv_attention_workspace_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
+        args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, *ints, B, N, Hq, Hkv, D, page, P, W,
+                1.0 / math.sqrt(D) if scale is None else scale, window, sinks, o.data_ptr(), st.data_ptr(),
+                ws.data_ptr(), ws.numel(), raw)
+        if events is None:
+            _raise(lib.spec_paged_attention(*args))
+            return o, st
+        n = ctypes.c_int32(0)
+        _raise(lib.spec_paged_attention_timed(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
+        return o, st, n.value
+
+
+def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=None, stream=None, out=None):
+    """Writes the new tokens' keys and values k, v [B, N, Hkv, D] (heads together, any strides
+    between sequences and nodes) into slots cache_len .. cache_len + n_new - 1 of one layer's
+    k_pages and v_pages (see include/spec_cache.h).  Returns row_status [B] int32, which ``out``
+    may supply."""
+    lib = load_library()
+    dev = _device(k, "k")
+    dt = _code(k, "k")
+    if k.dim() != 4:
+        raise ValueError("k must be [B, N, Hkv, D]")
+    B, N, Hkv, D = k.shape
+    P, Hc, Dk, page = _pages(k_pages, v_pages, 5, k.dtype, dev)
+    if (Hc, Dk) != (Hkv, D):
+        raise ValueError(f"the cache has {Hc} heads of {Dk} elements, k {Hkv} of {D}")
+    kp, kb, kn = _rows(k, "k", B, N, Hkv, D, k.dtype, dev)
+    vp, vb, vn = _rows(v, "v", B, N, Hkv, D, k.dtype, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, table_width]")
+    W = page_table.shape[1]
+    ints = (_ints(page_table, "page_table", (B, W), dev), _ints(cache_len, "cache_len", (B,), dev),
+            _ints(n_new, "n_new", (B,), dev, True))
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        st = torch.empty(B, dtype=torch.int32, device=dev) if out is None else out
+        sp = _ints(st, "row_status", (B,), dev)
+        _raise(lib.spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), *ints, B, N, Hkv, D,
+                                     page, P, W, sp, raw))
+    return st
+
+
+def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes=None, *, max_new: int | None = None,
+                      stream=None, out=None):
+    """Keeps node 0 and the accepted nodes of every sequence in all layers of k_pages
+    [L, P, Hkv, D/E, page, E] and v_pages (see include/spec_cache.h): accepted_len [B] and
+    path_nodes [B, N] int32 as spec_tree_verify returns them, or for chains accepted_len alone
+    and ``max_new``, the N = G + 1 new tokens that were verified.  Returns (new_len [B],
+    row_status [B]) int32; ``out`` may supply them (for chains new_len may be cache_len itself)."""
+    lib = load_library()
+    dev = _device(k_pages, "k_pages")
+    dt = _code(k_pages, "k_pages")
+    P, Hkv, D, page = _pages(k_pages, v_pages, 6, k_pages.dtype, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, table_width]")
+    B, W = page_table.shape
+    if path_nodes is not None:
+        N = path_nodes.shape[1] if path_nodes.dim() == 2 else 0
+        if max_new is not None and max_new != N:
+            raise ValueError(f"path_nodes has {N} nodes, max_new is {max_new}")
+    elif max_new is None:
+        raise ValueError("chains need max_new, the new tokens N = G + 1 of the verification")
+    else:
+        N = max_new
+    ints = (_ints(page_table, "page_table", (B, W), dev), _ints(cache_len, "cache_len", (B,), dev),
+            _ints(accepted_len, "accepted_len", (B,), dev), _ints(path_nodes, "path_nodes", (B, N), dev, True))
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if out is None:
+            n, st = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
+        else:
+            n, st = out
+        np_, sp = _ints(n, "new_len", (B,), dev), _ints(st, "row_status", (B,), dev)
+        _raise(lib.spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, *ints, k_pages.shape[0], B, N, Hkv, D, page, P,
+                                     W, np_, sp, raw))
+    return n, st
+
+
+def _books(pool: PagePool, dev):
+    if pool.page_table.dim() != 2:
+        raise ValueError("page_table must be [S, table_width]")
+    S, W = pool.page_table.shape
+    P = pool.ref_count.numel()
+    return S, W, P, (_ints(pool.page_table, "page_table", (S, W), dev), _ints(pool.seq_pages, "seq_pages", (S,), dev),
+                     _ints(pool.ref_count, "ref_count", (P,), dev))
+
+
+def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=None, *, page_size: int | None = None,
+                      workspace=None, stream=None, out=None):
+    """Gives every sequence of the pool the pages for want_len [S] slots and takes back those
+    behind (see include/spec_cache.h); a page that others hold too and that lies at or behind slot
+    keep_len [S] is replaced by the sequence's own, its kept slots copied in all layers of k_pages
+    [L, P, Hkv, D/E, page, E] and v_pages.  Without them nothing is copied and ``page_size`` is
+    needed.  Returns row_status [S] int32, which ``out`` may supply."""
+    lib = load_library()
+    dev = _device(pool.page_table, "page_table")
+    S, W, P, books = _books(pool, dev)
+    free = _ints(pool.free_map, "free_map", ((P + 31) // 32,), dev)
+    if k_pages is not None:
+        dt = _code(k_pages, "k_pages")
+        Pc, Hkv, D, page = _pages(k_pages, v_pages, 6, k_pages.dtype, dev)
+        if Pc != P:
+            raise ValueError(f"the cache has {Pc} pages, the pool {P}")
+        if page_size is not None and page_size != page:
+            raise ValueError(f"the cache's pages have {page} slots, page_size is {page_size}")
+        L, kp, vp = k_pages.shape[0], k_pages.data_ptr(), v_pages.data_ptr()
+    elif page_size is None:
+        raise ValueError("page_size is needed without k_pages and v_pages")
+    else:
+        dt, L, Hkv, D, page, kp, vp = SV_BF16, 0, 1, 16, page_size, None, None
+    keep, want = _ints(keep_len, "keep_len", (S,), dev), _ints(want_len, "want_len", (S,), dev)
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        st = torch.empty(S, dtype=torch.int32, device=dev) if out is None else out
+        sp = _ints(st, "row_status", (S,), dev)
+        ws = _work(workspace, lib.sv_resize_workspace_bytes(S, P), dev)
+        _raise(lib.spec_cache_resize(*books, free, keep, want, kp, vp, dt, L, S, Hkv, D, page, P, W, sp, ws.data_ptr(),
+                                     ws.numel(), raw))
+    return st
+
+
+def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=None):
+    """Makes sequences dst [F] continuations of sequences src [F] (int32) that share their pages
+    (see include/spec_cache.h); cache_len [S] is written at dst.  Returns pair_status [F] int32,
+    which ``out`` may supply."""
+    lib = load_library()
+    dev = _device(pool.page_table, "page_table")
+    S, W, P, books = _books(pool, dev)
+    F = src.numel()
+    n, s, d = _ints(cache_len, "cache_len", (S,), dev), _ints(src, "src", (F,), dev), _ints(dst, "dst", (F,), dev)
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        st = torch.empty(F, dtype=torch.int32, device=dev) if out is None else out
+        sp = _ints(st, "pair_status", (F,), dev)
+        _raise(lib.spec_cache_fork(*books, n, s, d, F, S, P, W, sp, raw))
+    return st

@@ -1,0 +1,637 @@
+// spec_cache.hip -- the paged key-value cache of a speculative decoding round: new entries
+// appended, an accepted path's entries moved together, pages taken, shared, copied and given
+// back (include/spec_cache.h has the layout and the semantics).
+//
+// All of it is data movement; the floor of each call is its bytes, and below some megabytes
+// the launch.  Every kernel checks what it indexes with, so bad tables cost a row code and
+// never an access outside the pool.
+
+#include "sv_common.h"
+
+#include "spec_cache.h"
+
+namespace sv {
+
+// Where slots of one sequence lie.
+struct Pool {
+  int page_shift, P, W;
+  unsigned Hkv, D;
+};
+// Bytes of one page of one layer, and of one head in it.
+template <typename T>
+SVD size_t head_bytes(const Pool &p) { return ((size_t)p.D << p.page_shift) * sizeof(T); }
+
+// ---------------------------------------------------------------- append
+
+struct AppendArgs {
+  const char *k, *v;
+  long long k_sb, k_sn, v_sb, v_sn;  // bytes
+  char *k_pages, *v_pages;
+  const int32_t *page_table, *cache_len, *n_new;
+  int N, chunks;
+  int32_t *row_status;
+  Pool pool;
+};
+
+constexpr int APPEND_SLOTS = 64;  // slots a workgroup writes: whole value units (8 or 4 slots)
+
+// One workgroup writes up to APPEND_SLOTS slots of one head.  Keys: a thread moves 16 bytes
+// (E values of d of one slot), neighbours along d in the source.  Values: a thread gathers
+// the E slots of one d into 16 bytes; neighbours along d, so the loads of a wave cover whole
+// rows of the source and its stores whole lines of the page; only a unit that the new slots
+// share with older ones is written element by element.
+template <typename T>
+__global__ __launch_bounds__(NT) void k_cache_append(const AppendArgs a) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int tid = threadIdx.x;
+  const int chunk = (int)(blockIdx.x % (unsigned)a.chunks);
+  const unsigned bh = blockIdx.x / (unsigned)a.chunks;
+  const int h = (int)(bh % a.pool.Hkv), b = (int)(bh / a.pool.Hkv);
+  const int len = a.cache_len[b], m = a.n_new ? a.n_new[b] : a.N;
+  const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D;
+  const int32_t *table = a.page_table + (size_t)b * a.pool.W;
+
+  int code = 0;
+  if (len < 0 || m < 0 || m > a.N || (long long)len + m > ((long long)a.pool.W << sh)) {
+    code = SV_ROW_BAD_LENGTH;
+  } else if (m > 0) {
+    const int p0 = len >> sh, p1 = (len + m - 1) >> sh;
+    bool bad = false;
+    for (int i = p0 + tid; i <= p1; i += NT) bad |= (unsigned)table[i] >= (unsigned)a.pool.P;
+    if (__syncthreads_or(bad)) code = SV_ROW_BAD_PAGE;
+  }
+  if (chunk == 0 && h == 0 && tid == 0) a.row_status[b] = code;
+  if (code != 0) return;
+  // chunks start at multiples of APPEND_SLOTS, so that a value unit has one writer
+  const int c0 = (len / APPEND_SLOTS + chunk) * APPEND_SLOTS;
+  const int s0 = max(len, c0), s1 = min(len + m, c0 + APPEND_SLOTS);
+  if (s0 >= s1) return;
+
+  const size_t hb = head_bytes<T>(a.pool);
+  const int U = D / E;
+  const char *ks = a.k + (long long)b * a.k_sb + (size_t)h * D * sizeof(T);
+  for (int x = tid; x < (s1 - s0) * U; x += NT) {
+    const int s = s0 + x / U, u = x % U;
+    const u32x4 w = *reinterpret_cast<const u32x4 *>(ks + (long long)(s - len) * a.k_sn + u * 16);
+    const size_t base = ((size_t)table[s >> sh] * a.pool.Hkv + h) * hb;
+    *reinterpret_cast<u32x4 *>(a.k_pages + base + ((size_t)u * page + (s & (page - 1))) * 16) = w;
+  }
+  const char *vs = a.v + (long long)b * a.v_sb + (size_t)h * D * sizeof(T);
+  const int u0 = s0 / E, u1 = (s1 - 1) / E;
+  for (int x = tid; x < (u1 - u0 + 1) * D; x += NT) {
+    const int u = u0 + x / D, d = x % D, f = u * E;
+    T e[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int s = min(max(f + j, s0), s1 - 1);
+      e[j] = *reinterpret_cast<const T *>(vs + (long long)(s - len) * a.v_sn + (size_t)d * sizeof(T));
+    }
+    const size_t base = ((size_t)table[f >> sh] * a.pool.Hkv + h) * hb;
+    T *out = reinterpret_cast<T *>(a.v_pages + base + ((size_t)((f & (page - 1)) / E) * D + d) * 16);
+    if (f >= s0 && f + E <= s1) {
+      u32x4 w;
+      __builtin_memcpy(&w, e, 16);
+      *reinterpret_cast<u32x4 *>(out) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (f + j >= s0 && f + j < s1) out[j] = e[j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- commit
+
+struct CommitArgs {
+  char *k_pages, *v_pages;
+  const int32_t *page_table, *cache_len, *accepted_len, *path;
+  int N;
+  unsigned B, LH;  // layers times heads
+  int32_t *new_len, *row_status;
+  Pool pool;
+};
+
+// One workgroup moves one head's entries of one sequence in one layer, path position by path
+// position.  Sources lie behind their targets (path_nodes[j] >= j + 1, increasing), so a
+// thread that owns its d and goes up the path never overwrites what it has still to read, and
+// no thread needs another's: COMMIT_STEP entries are read before they are written.
+constexpr int COMMIT_STEP = 8;
+
+template <typename T>
+__global__ __launch_bounds__(NT) void k_cache_commit(const CommitArgs a) {
+  constexpr int E = 16 / (int)sizeof(T);
+  __shared__ int s_path[SV_CACHE_MAX_NEW];
+  const int tid = threadIdx.x;
+  const int b = (int)(blockIdx.x % a.B);
+  const unsigned lh = blockIdx.x / a.B;
+  const int len = a.cache_len[b], acc = a.accepted_len[b];
+  const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D;
+  const int32_t *table = a.page_table + (size_t)b * a.pool.W;
+
+  int code = 0, top = 0;  // top: the last node kept
+  if (acc < 0) {
+    code = acc;
+  } else if (len < 0 || acc > a.N - 1) {
+    code = SV_ROW_BAD_LENGTH;
+  } else {
+    top = acc;
+    if (a.path && acc > 0) {
+      bool bad = false;
+      for (int j = tid; j < acc; j += NT) {
+        const int x = a.path[(size_t)b * a.N + j], y = j ? a.path[(size_t)b * a.N + j - 1] : 0;
+        s_path[j] = x;
+        bad |= x <= y || x >= a.N;
+      }
+      if (__syncthreads_or(bad)) code = SV_ROW_BAD_TREE;
+      else top = s_path[acc - 1];
+    }
+    if (code == 0 && (long long)len + top + 1 > ((long long)a.pool.W << sh)) code = SV_ROW_BAD_LENGTH;
+    if (code == 0) {
+      bool bad = false;
+      for (int i = (len >> sh) + tid; i <= (len + top) >> sh; i += NT) bad |= (unsigned)table[i] >= (unsigned)a.pool.P;
+      if (__syncthreads_or(bad)) code = SV_ROW_BAD_PAGE;
+    }
+  }
+  if (lh == 0 && tid == 0) {
+    a.row_status[b] = code;
+    a.new_len[b] = (code == 0) ? len + 1 + acc : len;
+  }
+  if (code != 0 || !a.path || top == acc) return;  // entries that lie together already
+
+  const size_t hb = head_bytes<T>(a.pool);
+  const unsigned l = lh / a.pool.Hkv, h = lh % a.pool.Hkv;
+  const size_t lay = (size_t)l * a.pool.P;
+  auto base = [&](int s) { return ((lay + (size_t)table[s >> sh]) * a.pool.Hkv + h) * hb; };
+  const int U = D / E;
+  // thread x < U owns key unit x, threads behind it own the values of one d each
+  for (int x = tid; x < U + D; x += NT) {
+    for (int j0 = 0; j0 < acc; j0 += COMMIT_STEP) {
+      if (x < U) {
+        u32x4 w[COMMIT_STEP];
+#pragma unroll
+        for (int j = 0; j < COMMIT_STEP; ++j) {
+          const int s = len + s_path[min(j0 + j, acc - 1)];
+          w[j] = *reinterpret_cast<const u32x4 *>(a.k_pages + base(s) + ((size_t)x * page + (s & (page - 1))) * 16);
+        }
+#pragma unroll
+        for (int j = 0; j < COMMIT_STEP; ++j) {
+          const int s = len + 1 + j0 + j;
+          if (j0 + j < acc) *reinterpret_cast<u32x4 *>(a.k_pages + base(s) + ((size_t)x * page + (s & (page - 1))) * 16) = w[j];
+        }
+      } else {
+        const int d = x - U;
+        T w[COMMIT_STEP];
+#pragma unroll
+        for (int j = 0; j < COMMIT_STEP; ++j) {
+          const int s = len + s_path[min(j0 + j, acc - 1)], t = s & (page - 1);
+          w[j] = *reinterpret_cast<const T *>(a.v_pages + base(s) + ((size_t)(t / E) * D + d) * 16 + (size_t)(t % E) * sizeof(T));
+        }
+#pragma unroll
+        for (int j = 0; j < COMMIT_STEP; ++j) {
+          const int s = len + 1 + j0 + j, t = s & (page - 1);
+          if (j0 + j < acc)
+            *reinterpret_cast<T *>(a.v_pages + base(s) + ((size_t)(t / E) * D + d) * 16 + (size_t)(t % E) * sizeof(T)) = w[j];
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- resize
+
+struct ResizeArgs {
+  int32_t *page_table, *seq_pages, *ref_count;
+  unsigned *free_map;
+  const int32_t *keep_len, *want_len;
+  int S, P, W, page_shift;
+  int32_t *row_status;
+  // workspace
+  int32_t *alloc;   // [P] the fresh pages in order, then the pages they replaced (-1: none)
+  int4 *copies;     // [S] page to copy from, page to copy to, slots to copy
+  int32_t *n_copy;
+};
+
+constexpr int RZ_NT = 1024, RZ_NW = RZ_NT / WAVE;
+
+// Exclusive prefix over the workgroup of 1024, and the total.
+SVD unsigned rz_scan(unsigned v, unsigned *s_w, unsigned &total) {
+  const int lane = lane_id(), wid = (int)threadIdx.x / WAVE;
+  const unsigned inc = scan_add_u(v);
+  if (lane == WAVE - 1) s_w[wid] = inc;
+  __syncthreads();
+  unsigned before = 0, tot = 0;
+#pragma unroll
+  for (int k = 0; k < RZ_NW; ++k) {
+    before += (k < wid) ? s_w[k] : 0u;
+    tot += s_w[k];
+  }
+  __syncthreads();
+  total = tot;
+  return before + inc - v;
+}
+SVD int ld_ref(const int32_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+SVD unsigned ld_map(const unsigned *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// One holder less; a page without holders is marked free.
+SVD void give_back(const ResizeArgs &a, int p) {
+  if (atomicSub(&a.ref_count[p], 1) == 1) atomicOr(&a.free_map[p >> 5], 1u << (p & 31));
+}
+
+// The pool's books are a few kilobytes and every sequence's pages depend on those of the
+// sequences before it, so one workgroup does them, a wave a sequence at a time where rows
+// are walked: give back, count needs, pick the lowest free pages, hand them out.  Which
+// pages are picked does not depend on the order in which atomics land: the counts are sums,
+// and picking reads the map only after all of them.
+__global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
+  __shared__ int s_need[SV_CACHE_MAX_SEQS];  // pages a sequence needs, then where its share starts
+  __shared__ unsigned s_w[RZ_NW];
+  __shared__ int s_ncopy, s_served;
+  const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
+  const int sh = a.page_shift, page = 1 << sh;
+  if (tid == 0) s_ncopy = s_served = 0;
+
+  // ---- checks, and pages behind the wanted length given back
+  for (int b = wid; b < a.S; b += RZ_NW) {
+    const int keep = a.keep_len[b], want = a.want_len[b], held = a.seq_pages[b];
+    int32_t *row = a.page_table + (size_t)b * a.W;
+    int code = 0;
+    const int goal = (int)(((long long)want + page - 1) >> sh);
+    if (want >= 0) {
+      if (held < 0 || held > a.W || goal > a.W || keep < 0 || (long long)keep > ((long long)held << sh)) {
+        code = SV_ROW_BAD_LENGTH;
+      } else {  // the entries this call reads: those to give back, and those at or behind keep_len
+        bool bad = false;
+        for (int i = min(goal, keep >> sh) + lane; i < held; i += WAVE) {
+          const unsigned p = (unsigned)row[i];
+          bad |= p >= (unsigned)a.P || ld_ref(&a.ref_count[p]) <= 0;
+        }
+        if (__any(bad)) code = SV_ROW_BAD_PAGE;
+      }
+    }
+    if (lane == 0) {
+      a.row_status[b] = code;
+      s_need[b] = (want >= 0 && code == 0) ? 0 : -1;  // -1: left as it is
+    }
+  }
+  __threadfence_block();
+  __syncthreads();
+  for (int b = wid; b < a.S; b += RZ_NW) {
+    if (s_need[b] < 0) continue;
+    const int held = a.seq_pages[b], goal = (int)(((long long)a.want_len[b] + page - 1) >> sh);
+    int32_t *row = a.page_table + (size_t)b * a.W;
+    for (int i = goal + lane; i < held; i += WAVE) {
+      give_back(a, row[i]);
+      row[i] = -1;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+
+  // ---- needs: entries to replace (held by others too, at or behind keep_len) and to add
+  auto needs = [&](const int32_t *row, int i, int held) { return i >= held || ld_ref(&a.ref_count[row[i]]) > 1; };
+  for (int b = wid; b < a.S; b += RZ_NW) {
+    if (s_need[b] < 0) continue;
+    const int held = a.seq_pages[b], goal = (int)(((long long)a.want_len[b] + page - 1) >> sh);
+    const int32_t *row = a.page_table + (size_t)b * a.W;
+    int n = 0;
+    if (a.want_len[b] > a.keep_len[b]) {
+      const int first = a.keep_len[b] >> sh;
+      n = max(0, goal - held);
+      for (int i0 = first; i0 < min(held, goal); i0 += WAVE)
+        n += __popcll(__ballot(i0 + lane < min(held, goal) && needs(row, i0 + lane, held)));
+    }
+    if (lane == 0) s_need[b] = n;
+  }
+  __syncthreads();
+  unsigned need_all = 0;
+  {
+    for (int b0 = 0; b0 < a.S; b0 += RZ_NT) {
+      const int b = b0 + tid;
+      unsigned tot;
+      const unsigned ex = rz_scan(b < a.S && s_need[b] > 0 ? (unsigned)s_need[b] : 0u, s_w, tot) + need_all;
+      // where the share starts; a sequence that needs nothing has -2, one left alone -1
+      if (b < a.S && s_need[b] >= 0) s_need[b] = s_need[b] > 0 ? (int)ex : -2;
+      need_all += tot;
+    }
+  }
+  __syncthreads();
+
+  // ---- the lowest free pages, need_all of them or as many as there are
+  unsigned found = 0;
+  const int words = (a.P + 31) >> 5;
+  for (int w0 = 0; w0 < words && found < need_all; w0 += RZ_NT) {
+    unsigned bits = (w0 + tid < words) ? ld_map(&a.free_map[w0 + tid]) : 0u;
+    if (w0 + tid == words - 1 && (a.P & 31)) bits &= (1u << (a.P & 31)) - 1u;
+    unsigned tot;
+    unsigned at = found + rz_scan((unsigned)__popc(bits), s_w, tot);
+    for (; bits && at < need_all; bits &= bits - 1, ++at) a.alloc[at] = (w0 + tid) * 32 + __ffs((int)bits) - 1;
+    found += tot;
+  }
+  found = min(found, need_all);
+  __threadfence_block();
+  __syncthreads();
+
+  // ---- handed out, sequence by sequence; the replaced page takes the fresh one's place in alloc
+  for (int b = wid; b < a.S; b += RZ_NW) {
+    const int start = s_need[b];
+    if (start == -1) continue;
+    const int held = a.seq_pages[b], goal = (int)(((long long)a.want_len[b] + page - 1) >> sh);
+    int32_t *row = a.page_table + (size_t)b * a.W;
+    if (start == -2) {
+      if (lane == 0) a.seq_pages[b] = goal;
+      continue;
+    }
+    const int keep = a.keep_len[b], first = keep >> sh;
+    int n = 0;
+    for (int i0 = first; i0 < goal; i0 += WAVE) n += __popcll(__ballot(i0 + lane < goal && needs(row, i0 + lane, held)));
+    if ((unsigned)(start + n) > found) {  // then the shares behind it do not fit either
+      if (lane == 0) {
+        a.row_status[b] = SV_ROW_NO_PAGES;
+        a.seq_pages[b] = min(held, goal);
+      }
+      continue;
+    }
+    if (lane == 0) atomicMax(&s_served, start + n);
+    int at = start;
+    for (int i0 = first; i0 < goal; i0 += WAVE) {
+      const int i = i0 + lane;
+      const bool take = i < goal && needs(row, i, held);
+      const unsigned long long who = __ballot(take);
+      if (take) {
+        const int s = at + __popcll(who & ((1ull << lane) - 1ull));
+        const int fresh = a.alloc[s], old = i < held ? row[i] : -1;
+        row[i] = fresh;
+        a.alloc[s] = old;
+        if (old >= 0 && i == first && (keep & (page - 1))) a.copies[atomicAdd(&s_ncopy, 1)] = make_int4(old, fresh, keep & (page - 1), 0);
+        atomicAnd(&a.free_map[fresh >> 5], ~(1u << (fresh & 31)));
+        __hip_atomic_store(&a.ref_count[fresh], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      at += __popcll(who);
+    }
+    if (lane == 0) a.seq_pages[b] = goal;
+  }
+  __threadfence();
+  __syncthreads();
+  // ---- replaced pages lose a holder (only now: the counts above are those after giving back)
+  for (int k = tid; k < s_served; k += RZ_NT)
+    if (a.alloc[k] >= 0) give_back(a, a.alloc[k]);
+  if (tid == 0) *a.n_copy = s_ncopy;
+}
+
+struct CopyArgs {
+  char *k_pages, *v_pages;
+  const int4 *copies;
+  const int32_t *n_copy;
+  unsigned L;
+  Pool pool;
+};
+
+constexpr int COPY_WGS = 2048;  // 8 a CU; the host does not know how many copies there are
+
+// The kept slots of a page into another: a workgroup moves one head of one layer at a time,
+// COPY_STEP 16-byte units a thread in flight.  Keys: t runs fastest, kept * 16 bytes together.
+// Values: whole units lie together; of the last one only the kept elements are written.
+constexpr int COPY_STEP = 4;
+
+template <typename T>
+__global__ __launch_bounds__(NT) void k_cache_copy(const CopyArgs a) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const unsigned per = a.L * a.pool.Hkv;
+  const unsigned long long items = (unsigned long long)*a.n_copy * per;
+  const int tid = threadIdx.x, page = 1 << a.pool.page_shift, D = (int)a.pool.D, U = D / E;
+  const size_t hb = head_bytes<T>(a.pool);
+  for (unsigned long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int4 c = a.copies[it / per];
+    const unsigned lh = (unsigned)(it % per), l = lh / a.pool.Hkv, h = lh % a.pool.Hkv;
+    const size_t src = (((size_t)l * a.pool.P + c.x) * a.pool.Hkv + h) * hb, dst = (((size_t)l * a.pool.P + c.y) * a.pool.Hkv + h) * hb;
+    const int kept = c.z, nk = U * kept, nv = (kept / E) * D;
+    for (int x0 = tid; x0 < nk + nv; x0 += COPY_STEP * NT) {
+      u32x4 w[COPY_STEP];
+      size_t at[COPY_STEP];
+#pragma unroll
+      for (int j = 0; j < COPY_STEP; ++j) {
+        const int x = min(x0 + j * NT, nk + nv - 1);
+        at[j] = (x < nk) ? ((size_t)(x / kept) * page + x % kept) * 16 : (size_t)(x - nk) * 16;
+        w[j] = *reinterpret_cast<const u32x4 *>((x < nk ? a.k_pages : a.v_pages) + src + at[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < COPY_STEP; ++j)
+        if (x0 + j * NT < nk + nv) *reinterpret_cast<u32x4 *>((x0 + j * NT < nk ? a.k_pages : a.v_pages) + dst + at[j]) = w[j];
+    }
+    if (kept % E)
+      for (int d = tid; d < D; d += NT) {
+        const size_t o = ((size_t)(kept / E) * D + d) * 16;
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(a.v_pages + src + o);
+        T e[E];
+        __builtin_memcpy(e, &w, 16);
+        T *out = reinterpret_cast<T *>(a.v_pages + dst + o);
+#pragma unroll
+        for (int j = 0; j < E - 1; ++j)
+          if (j < kept % E) out[j] = e[j];
+      }
+  }
+}
+
+// ---------------------------------------------------------------- fork
+
+struct ForkArgs {
+  int32_t *page_table, *seq_pages, *ref_count, *cache_len;
+  const int32_t *src, *dst;
+  int F, S, P, W;
+  int32_t *pair_status;
+};
+
+// One wave a pair.  Pairs do not touch what other pairs read: a target holds no pages, is no
+// pair's source, and of pairs with one target only the first is made.  (A target's own row
+// may be read by the checks of a pair that is refused whatever they find.)
+__global__ __launch_bounds__(NT) void k_cache_fork(const ForkArgs a) {
+  const int lane = lane_id(), f = (int)(blockIdx.x * NW) + (int)threadIdx.x / WAVE;
+  if (f >= a.F) return;
+  const int s = a.src[f], d = a.dst[f];
+  int code = 0, held = 0;
+  bool bad = (unsigned)s >= (unsigned)a.S || (unsigned)d >= (unsigned)a.S;
+  for (int i = lane; i < a.F; i += WAVE) bad |= a.src[i] == d || (i < f && a.dst[i] == d);
+  if (__any(bad)) {
+    code = SV_ROW_BAD_FORK;
+  } else if (a.seq_pages[d] != 0) {
+    code = SV_ROW_BAD_FORK;
+  } else {
+    held = a.seq_pages[s];
+    const int32_t *row = a.page_table + (size_t)s * a.W;
+    if (held < 0 || held > a.W) {
+      code = SV_ROW_BAD_LENGTH;
+    } else {
+      bool off = false;
+      for (int i = lane; i < held; i += WAVE) {
+        const unsigned p = (unsigned)row[i];
+        off |= p >= (unsigned)a.P || ld_ref(&a.ref_count[p]) <= 0;
+      }
+      if (__any(off)) code = SV_ROW_BAD_PAGE;
+    }
+  }
+  if (lane == 0) a.pair_status[f] = code;
+  if (code != 0) return;
+  const int32_t *row = a.page_table + (size_t)s * a.W;
+  int32_t *to = a.page_table + (size_t)d * a.W;
+  for (int i = lane; i < held; i += WAVE) {
+    const int p = row[i];
+    to[i] = p;
+    atomicAdd(&a.ref_count[p], 1);
+  }
+  if (lane == 0) {
+    a.seq_pages[d] = held;
+    a.cache_len[d] = a.cache_len[s];
+  }
+}
+
+}  // namespace sv
+
+// ======================================================================== host side
+
+namespace {
+
+using namespace sv;
+using sv_host::align256;
+
+bool pool_ok(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) {
+  return Hkv >= 1 && D >= 16 && D <= 1024 && D % 16 == 0 && page >= 16 && page <= 256 && (page & (page - 1)) == 0 &&
+         P >= 1 && W >= 1 && (long long)W * page <= 0x7fffffffLL - 4096;
+}
+
+Pool pool_of(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) {
+  return Pool{__builtin_ctz((unsigned)page), P, W, (unsigned)Hkv, (unsigned)D};
+}
+
+template <typename A>
+sv_status launch(const void *fn, A &a, long long grid, int block, void *stream) {
+  sv_host::Launcher L{(hipStream_t)stream, nullptr, 0};
+  L.block = block;
+  void *args[] = {&a};
+  L.go(fn, (unsigned)grid, args);
+  return L.e == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
+}
+
+struct ResizePlan {
+  size_t alloc, copies, n_copy, total;
+};
+ResizePlan resize_plan(int32_t S, int32_t P) {
+  ResizePlan p;
+  size_t o = 0;
+  p.alloc = o; o = align256(o + (size_t)P * 4);
+  p.copies = o; o = align256(o + (size_t)S * 16);
+  p.n_copy = o; o = align256(o + 4);
+  p.total = o;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_n, const void *v, int64_t v_stride_b,
+                            int64_t v_stride_n, sv_dtype dtype, void *k_pages, void *v_pages,
+                            const int32_t *page_table, const int32_t *cache_len, const int32_t *n_new, int32_t B,
+                            int32_t N, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                            int32_t table_width, int32_t *row_status, void *stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  const int esz = dtype == SV_BF16 ? 2 : 4;
+  if (B < 1 || N < 1 || N > SV_CACHE_MAX_NEW || !pool_ok(Hkv, D, page_size, num_pages, table_width)) return SV_ERR_SHAPE;
+  AppendArgs a = {};
+  a.chunks = (N + APPEND_SLOTS - 2) / APPEND_SLOTS + 1;  // the first may begin anywhere in a chunk
+  const long long grid = (long long)B * Hkv * a.chunks;
+  if (grid > 0x7fffffffLL) return SV_ERR_SHAPE;
+  if (!k || !v || !k_pages || !v_pages || !page_table || !cache_len || !row_status) return SV_ERR_NULL;
+  a.k = static_cast<const char *>(k);
+  a.v = static_cast<const char *>(v);
+  a.k_sb = k_stride_b * esz;
+  a.k_sn = k_stride_n * esz;
+  a.v_sb = v_stride_b * esz;
+  a.v_sn = v_stride_n * esz;
+  if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)a.k_sb | (uintptr_t)a.k_sn |
+       (uintptr_t)a.v_sb | (uintptr_t)a.v_sn) & 15)
+    return SV_ERR_ALIGN;
+  a.k_pages = static_cast<char *>(k_pages);
+  a.v_pages = static_cast<char *>(v_pages);
+  a.page_table = page_table;
+  a.cache_len = cache_len;
+  a.n_new = n_new;
+  a.N = N;
+  a.row_status = row_status;
+  a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
+  return launch(esz == 2 ? (const void *)&k_cache_append<uint16_t> : (const void *)&k_cache_append<float>, a, grid, NT, stream);
+}
+
+sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype, const int32_t *page_table,
+                            const int32_t *cache_len, const int32_t *accepted_len, const int32_t *path_nodes, int32_t L,
+                            int32_t B, int32_t N, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                            int32_t table_width, int32_t *new_len, int32_t *row_status, void *stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (B < 1 || L < 1 || N < 1 || N > SV_CACHE_MAX_NEW || !pool_ok(Hkv, D, page_size, num_pages, table_width)) return SV_ERR_SHAPE;
+  const long long LH = (long long)L * Hkv;
+  if (LH > 0x7fffffffLL || LH * B > 0x7fffffffLL) return SV_ERR_SHAPE;
+  if (!k_pages || !v_pages || !page_table || !cache_len || !accepted_len || !new_len || !row_status) return SV_ERR_NULL;
+  if (((uintptr_t)k_pages | (uintptr_t)v_pages) & 15) return SV_ERR_ALIGN;
+  // With paths several workgroups read a sequence's lengths: what they read is not written here.
+  for (const int32_t *in : {cache_len, accepted_len})
+    for (const int32_t *to : {(const int32_t *)new_len, (const int32_t *)row_status})
+      if (path_nodes && (uintptr_t)in < (uintptr_t)(to + B) && (uintptr_t)to < (uintptr_t)(in + B)) return SV_ERR_PARAM;
+  CommitArgs a = {};
+  a.k_pages = static_cast<char *>(k_pages);
+  a.v_pages = static_cast<char *>(v_pages);
+  a.page_table = page_table;
+  a.cache_len = cache_len;
+  a.accepted_len = accepted_len;
+  a.path = path_nodes;
+  a.N = N;
+  a.B = (unsigned)B;
+  a.LH = (unsigned)LH;
+  a.new_len = new_len;
+  a.row_status = row_status;
+  a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
+  // chains move nothing: one workgroup a sequence writes the lengths
+  return launch(dtype == SV_BF16 ? (const void *)&k_cache_commit<uint16_t> : (const void *)&k_cache_commit<float>, a,
+                path_nodes ? LH * B : B, NT, stream);
+}
+
+size_t sv_resize_workspace_bytes(int32_t S, int32_t num_pages) {
+  if (S < 1 || S > SV_CACHE_MAX_SEQS || num_pages < 1) return 256;
+  return resize_plan(S, num_pages).total;
+}
+
+sv_status spec_cache_resize(int32_t *page_table, int32_t *seq_pages, int32_t *ref_count, int32_t *free_map,
+                            const int32_t *keep_len, const int32_t *want_len, void *k_pages, void *v_pages,
+                            sv_dtype dtype, int32_t L, int32_t S, int32_t Hkv, int32_t D, int32_t page_size,
+                            int32_t num_pages, int32_t table_width, int32_t *row_status, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (S < 1 || S > SV_CACHE_MAX_SEQS || L < 0 || !pool_ok(L ? Hkv : 1, L ? D : 16, page_size, num_pages, table_width) ||
+      (long long)L * Hkv > 0x7fffffffLL)
+    return SV_ERR_SHAPE;
+  if (!page_table || !seq_pages || !ref_count || !free_map || !keep_len || !want_len || !row_status || !workspace ||
+      (L > 0 && (!k_pages || !v_pages)))
+    return SV_ERR_NULL;
+  if (L > 0 && (((uintptr_t)k_pages | (uintptr_t)v_pages) & 15)) return SV_ERR_ALIGN;
+  const ResizePlan p = resize_plan(S, num_pages);
+  if (workspace_bytes < p.total || ((uintptr_t)workspace & 255)) return SV_ERR_WORKSPACE;
+  char *base = static_cast<char *>(workspace);
+  ResizeArgs a = {page_table, seq_pages, ref_count, (unsigned *)free_map, keep_len, want_len, S, num_pages, table_width,
+                  __builtin_ctz((unsigned)page_size), row_status, (int32_t *)(base + p.alloc), (int4 *)(base + p.copies),
+                  (int32_t *)(base + p.n_copy)};
+  const sv_status st = launch((const void *)&k_cache_resize, a, 1, RZ_NT, stream);
+  if (st != SV_OK || L == 0) return st;
+  CopyArgs c = {static_cast<char *>(k_pages), static_cast<char *>(v_pages), a.copies, a.n_copy, (unsigned)L,
+                pool_of(Hkv, D, page_size, num_pages, table_width)};
+  return launch(dtype == SV_BF16 ? (const void *)&k_cache_copy<uint16_t> : (const void *)&k_cache_copy<float>, c, COPY_WGS,
+                NT, stream);
+}
+
+sv_status spec_cache_fork(int32_t *page_table, int32_t *seq_pages, int32_t *ref_count, int32_t *cache_len,
+                          const int32_t *src, const int32_t *dst, int32_t F, int32_t S, int32_t num_pages,
+                          int32_t table_width, int32_t *pair_status, void *stream) {
+  if (F < 1 || F > SV_CACHE_MAX_SEQS || S < 1 || S > SV_CACHE_MAX_SEQS || num_pages < 1 || table_width < 1) return SV_ERR_SHAPE;
+  if (!page_table || !seq_pages || !ref_count || !cache_len || !src || !dst || !pair_status) return SV_ERR_NULL;
+  ForkArgs a = {page_table, seq_pages, ref_count, cache_len, src, dst, F, S, num_pages, table_width, pair_status};
+  return launch((const void *)&k_cache_fork, a, (F + NW - 1) / NW, NT, stream);
+}
+
+}  // extern "C"

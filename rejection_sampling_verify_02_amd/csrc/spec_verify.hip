@@ -1661,13 +1661,13 @@ const char *sv_status_string(sv_status status) {
   switch (status) {
     case SV_OK: return "ok";
     case SV_ERR_NULL: return "a required pointer is NULL";
-    case SV_ERR_SHAPE: return "invalid shape (B < 1, G < 0, V < 1, or too large for one launch)";
+    case SV_ERR_SHAPE: return "invalid shape (B < 1, G < 0, V < 1, a size the call does not take, or too large for one launch)";
     case SV_ERR_DTYPE: return "unsupported logit dtype";
     case SV_ERR_TEMPERATURE: return "temperature must be finite and >= 0";
     case SV_ERR_WORKSPACE: return "workspace too small or not 256-byte aligned";
-    case SV_ERR_ALIGN: return "logit pointer not aligned to its element size";
+    case SV_ERR_ALIGN: return "a pointer or stride is not aligned (logits: element size; cache, its rows and the attention's output: 16 bytes)";
     case SV_ERR_LAUNCH: return "kernel launch failed";
-    case SV_ERR_PARAM: return "epsilon and delta must be finite and >= 0";
+    case SV_ERR_PARAM: return "a parameter is out of its range (epsilon, delta, window and sinks >= 0, sinks only with a window, all finite)";
     case SV_ERR_SCRATCH: return "the arguments need more scratch memory than spec_verify_noalloc holds";
   }
   return "unknown status";
