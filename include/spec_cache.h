@@ -108,7 +108,7 @@ sv_status spec_paged_attention_timed(const void *q, int64_t q_stride_b, int64_t 
                                      int32_t n_events, int32_t *n_launched);
 
 /* Names of the kernels spec_paged_attention launches, ';'-separated (static storage). */
-const char *sv_attention_launch_plan(void);
+const char *sv_attention_launch_plan(int32_t N, int32_t Hq, int32_t Hkv, int32_t D, sv_dtype dtype);
 
 /* ---- the new tokens' keys and values into the cache ----
  *

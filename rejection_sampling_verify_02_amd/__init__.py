@@ -128,7 +128,7 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
     lib.sv_attention_workspace_bytes.restype = SZ
     lib.sv_resize_workspace_bytes.argtypes = [I32, I32]
     lib.sv_resize_workspace_bytes.restype = SZ
-    lib.sv_attention_launch_plan.argtypes = []
+    lib.sv_attention_launch_plan.argtypes = [I32] * 5
     lib.sv_attention_launch_plan.restype = ctypes.c_char_p
     if path is None:
         _lib = lib

@@ -155,8 +155,9 @@ def sv_resize_workspace_bytes(S: int, num_pages: int) -> int:
     return int(load_library().sv_resize_workspace_bytes(S, num_pages))
 
 
-def sv_attention_launch_plan() -> list[str]:
-    return load_library().sv_attention_launch_plan().decode().split(";")
+def sv_attention_launch_plan(N: int, Hq: int, Hkv: int, D: int, dtype: int) -> list[str]:
+    s = load_library().sv_attention_launch_plan(N, Hq, Hkv, D, dtype).decode()
+    return s.split(";") if s else []
 
 
 def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=None, n_new=None, scale: float | None = None,

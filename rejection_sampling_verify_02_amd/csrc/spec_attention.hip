@@ -3,24 +3,25 @@
 // For node i of sequence b and query head h: out = softmax(scale q.k) v over the slots the
 // node sees (include/spec_cache.h).  All query rows of one key head, row r = node * group +
 // head in group, read the same keys and values, so a unit of work is (sequence, key head,
-// row tile of RT = 16 R rows) and streams the sequence's slots once, 32 at a time:
+// row tile) and streams the sequence's slots once, 32 at a time:
 //   S^T = K Q^T   keys as the matrix instruction's A operand, query rows as its columns
 //   O^T += V^T P^T
 // With rows as columns a lane owns one query row of each 16-row tile, in both products:
 // the row's running maximum and sum live in that lane's registers, rescaling is one factor
 // a lane, and the weights leave the first product in exactly the lanes and order in which
-// the second one takes them, so nothing goes through LDS inside the loop (the order of the
-// 16 slots of a score tile is chosen for that: SlotMap).  The cache's layout puts the 16
-// bytes each lane needs together, so keys and values go from HBM to the lanes that multiply
-// them with no staging either.
+// the second one takes them (the order of the slots in a score tile is chosen for that).
 //
-// Bound: with few rows the cache's bytes (2 D Hkv element sizes a token), read once; every
-// wave keeps the next tile's keys and this tile's values in flight.  The tiles of all units
-// are laid end to end and cut into equal shares, one a workgroup, whatever the lengths of
-// the sequences (a share may end in the middle of one unit and go on with the next); the
-// four waves of a workgroup take tiles in turn and join in LDS, and units that more than one
-// workgroup streamed are joined by k_attn_join.  Sums run in a fixed order: same call, same
-// bits.
+// Two kernels, by the rows of a unit (attn_plan):
+//   k_attn       up to 32 rows: bound by the cache's bytes.  The cache's layout puts the 16
+//                bytes a lane multiplies together, so keys and values go from HBM to the lanes
+//                that use them with no staging; each of the four waves takes every fourth tile,
+//                and they join through LDS at the end.
+//   k_attn_wide  more rows: the waves own rows instead, and share each tile through LDS, so
+//                that the L2 and L1 are read once for 64 or 128 rows.
+// The tiles of all units are laid end to end and cut into equal shares, one a workgroup,
+// whatever the lengths of the sequences (a share may end in the middle of one unit and go on
+// with the next); units that several workgroups streamed are joined by k_attn_join.  Sums run
+// in a fixed order: same call, same bits.
 
 #include "sv_common.h"
 
@@ -102,18 +103,23 @@ SVD unsigned seq_tiles(const AttnArgs &a, int b) {
   return t * (unsigned)a.Hkv;
 }
 
-SVD float xor_max(float x) {  // over the four lanes of a column (lane % 16 equal)
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+// Over the four lanes of a column (lane % 16 equal): the swaps exchange halves of lane rows
+// between two registers, which leaves both operands of each step in every lane.
+SVD float col_max(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned v = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-SVD float xor_sum(float x) {
+SVD float col_sum(float x) {
   x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
 }
-SVD unsigned xor_or(unsigned x) {
-  x |= (unsigned)__shfl_xor((int)x, 16);
-  return x | (unsigned)__shfl_xor((int)x, 32);
-}
+// Page ids by scalar loads: they do not queue behind the keys and values in flight.  (No
+// kernel here writes the table.)
+typedef const __attribute__((address_space(4))) int32_t *TablePtr;
+SVD int page_at(TablePtr t, int i) { return t[i]; }
 
 // Bits of the slots [a, b) among the 32 from t0 on.
 SVD unsigned slots32(int t0, int a, int b) {
@@ -137,6 +143,7 @@ template <>
 struct Mma<uint16_t> {
   static constexpr int E = 8, VT = 1;  // elements a unit; value units a lane needs per 16 d
   SVD static int key_slot(int t2, int m) { return 8 * (m >> 2) + 4 * t2 + (m & 3); }
+  SVD static int key_place(int slot) { return ((slot >> 2) & 1) * 16 + (slot >> 3) * 4 + (slot & 3); }  // 16 t2 + m of it
   SVD static int val_slot(int, int g) { return 8 * g; }           // first slot of the lane's unit
   SVD static unsigned lane_bits(unsigned x, int g) { return (x >> (8 * g)) & 0xffu; }  // a tile's bits to score order
   SVD static f32x4 qk(u32x4 k, u32x4 q, f32x4 c) {
@@ -164,6 +171,13 @@ struct Mma<uint16_t> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) bad |= (v[j] & 0x7f800000u) == 0x7f800000u || (v[j] & 0x7f80u) == 0x7f80u;
     return bad;
+  }
+  // The unit with elements that are not finite set to zero.
+  SVD static u32x4 finite(u32x4 v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] &= ((v[j] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((v[j] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+    return v;
   }
   // Elements e >= n of the unit become zero.
   SVD static u32x4 cut(u32x4 v, int n) {
@@ -193,6 +207,7 @@ template <>
 struct Mma<float> {
   static constexpr int E = 4, VT = 2;
   SVD static int key_slot(int t2, int m) { return 16 * t2 + m; }
+  SVD static int key_place(int slot) { return slot; }
   SVD static int val_slot(int t2, int g) { return 16 * t2 + 4 * g; }
   SVD static unsigned lane_bits(unsigned x, int g) { return ((x >> (4 * g)) & 0xfu) | (((x >> (16 + 4 * g)) & 0xfu) << 4); }
   SVD static f32x4 qk(u32x4 k, u32x4 q, f32x4 c) {
@@ -219,6 +234,11 @@ struct Mma<float> {
     for (int j = 0; j < 4; ++j) bad |= (v[j] & 0x7f800000u) == 0x7f800000u;
     return bad;
   }
+  SVD static u32x4 finite(u32x4 v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (v[j] & 0x7f800000u) == 0x7f800000u ? 0u : v[j];
+    return v;
+  }
   SVD static u32x4 cut(u32x4 v, int n) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = (n > j) ? v[j] : 0u;
@@ -236,45 +256,122 @@ struct Mma<float> {
   }
 };
 
-// Workgroups resident on a CU (their waves' registers bound them: the output tile, the query
-// rows, one tile of keys and one of values), which is also how many the grid has per CU.
-template <typename T, int D, int R>
-constexpr int attn_occ() {
-  constexpr int regs = R * (D / 4) + R * (D * (int)sizeof(T) / 16) + 2 * (D * (int)sizeof(T) / 8) + 8 * R + 48;
-  return regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+// ---------------------------------------------------------------- a workgroup's share
+
+constexpr unsigned MIN_SHARE = 4;  // tiles: one for each wave of k_attn
+
+// One unit's part of a share, and what the whole workgroup knows about it.
+struct Segment {
+  Seq sq;
+  Span sp;
+  int b, h, rt, l0, l1;  // the segment is the unit's tiles [l0, l1)
+  TablePtr table;
+  const int32_t *par;
+  int words;   // of a node's bit string
+  bool masks;  // some tile of the segment is not seen whole by every row
+
+  SVD int tile(int l) const { return (l < sp.n_sink ? l : l - sp.n_sink + sp.first) * TILE; }
+  SVD int end() const { return sq.len + sq.m; }
+  // Every row of the unit sees the whole tile.
+  SVD bool plain(const AttnArgs &a, int t0) const {
+    return t0 + TILE <= sq.len && (a.window <= 0 || t0 + TILE <= a.sinks || (long long)sq.len + sq.m - 1 - t0 < a.window);
+  }
+  // The pages of a tile's two halves (a page has at least 16 slots).  A half that no row sees
+  // may have no page any more (behind the sequence, or left of the window): the other half's
+  // page stands in for it.
+  SVD void pages(const AttnArgs &a, int t0, int &pa, int &pb) const {
+    const int t1 = t0 + TILE / 2;
+    const bool ha = t0 < a.sinks || t1 > sp.from;
+    const bool hb = t1 < end() && (t1 < a.sinks || t1 + TILE / 2 > sp.from);
+    const int ia = t0 >> a.page_shift, ib = t1 >> a.page_shift;
+    pa = page_at(table, ha ? ia : ib);
+    pb = (hb && ib != ia) ? page_at(table, ib) : pa;
+  }
+  // The slots of a tile that a row sees, as bits.
+  SVD unsigned sees(const AttnArgs &a, int t0, int dep, const unsigned *anc) const {
+    const int pos = sq.len + dep, lo = (a.window > 0) ? pos - a.window + 1 : 0;
+    const int head = par ? sq.len : pos + 1;  // slots that window and sinks alone decide
+    unsigned see = slots32(t0, lo, head) | slots32(t0, 0, min(a.sinks, head));
+    if (par) see |= anc32(anc, words, t0 - sq.len);
+    return see;
+  }
+};
+
+// LDS of either kernel: the tree, and what the prologue needs.
+template <int RT>
+struct SharedBooks {
+  int par[SV_CACHE_MAX_NEW];
+  uint16_t dep[RT];                          // depths of the row tile's nodes
+  unsigned anc[RT * (SV_CACHE_MAX_NEW / 32)];  // the nodes each of them sees
+  unsigned w[NW], at[2];
+  int bad;
+};
+
+// The code of a sequence: the same test in every workgroup that streams a part of it, so that
+// all its rows agree.
+template <int RT>
+SVD int seq_code(const AttnArgs &a, const Seq &sq, int b, SharedBooks<RT> &s) {
+  const int tid = threadIdx.x, page = 1 << a.page_shift;
+  const int32_t *table = a.page_table + (size_t)b * a.W;
+  if (!sq.ok) return SV_ROW_BAD_LENGTH;
+  if (sq.m == 0) return 0;
+  int bad = 0;
+  if (a.parent)
+    for (int i = tid; i < sq.m; i += NT) {
+      const int p = a.parent[(size_t)b * a.N + i];
+      s.par[i] = p;
+      if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 2;
+    }
+  // pages of the sinks, then from the window on
+  const int first = (a.window > 0) ? max(0, sq.len - a.window + 1) : 0;
+  const int p0 = first >> a.page_shift;
+  const int ps = min((min(a.sinks, first) + page - 1) >> a.page_shift, p0);
+  const int np = ((sq.len + sq.m + page - 1) >> a.page_shift) - p0 + ps;
+  for (int i = tid; i < np; i += NT)
+    if ((unsigned)table[i < ps ? i : i - ps + p0] >= (unsigned)a.P) bad |= 1;
+  if (tid == 0) s.bad = 0;
+  __syncthreads();
+  if (bad) atomicOr(&s.bad, bad);
+  __syncthreads();
+  const int x = s.bad;
+  return (x & 2) ? SV_ROW_BAD_TREE : (x & 1) ? SV_ROW_BAD_PAGE : 0;
 }
 
-template <typename T, int D, int R>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, D, R>()))) void k_attn(const AttnArgs a) {
+// Depths of the row tile's nodes and the nodes each sees, window and sinks included.
+template <int RT>
+SVD void tree_books(const AttnArgs &a, const Segment &g, SharedBooks<RT> &s) {
+  const int tid = threadIdx.x, i0 = g.sp.i0, n = g.sp.i1 - i0 + 1;
+  for (int i = tid; i < n * g.words; i += NT) s.anc[i] = 0u;
+  __syncthreads();
+  for (int i = tid; i < n; i += NT) {
+    int dep = 0;
+    for (int j = s.par[i0 + i]; j >= 0; j = s.par[j]) ++dep;
+    s.dep[i] = (uint16_t)dep;
+    int d = dep;  // of node j
+    for (int j = i0 + i; j >= 0; j = s.par[j], --d)
+      if (a.window <= 0 || dep - d < a.window || g.sq.len + d < a.sinks) s.anc[i * g.words + (j >> 5)] |= 1u << (j & 31);
+  }
+  __syncthreads();
+}
+
+// Walks the workgroup's share, a segment at a time.  stream(segment, code) computes the rows'
+// sums over the segment's slots (nothing for code != 0 or without live rows) and calls
+// emit(row, c4, sum, max, total) for every row of the tile and four elements d = 4 c4 ..;
+// emit is passed in so that the writing is one piece of code.
+template <typename T, int D, int RT, typename Stream>
+SVD void attn_share(const AttnArgs &a, SharedBooks<RT> &s, Stream stream) {
   typedef Mma<T> M;
-  constexpr int RT = 16 * R, E = M::E, ESZ = (int)sizeof(T);
-  constexpr int KS = D / (4 * E);  // key units a lane holds of a 16-slot score tile
-  constexpr int DT = D / 16;       // 16-wide tiles of the output's d
-  constexpr int PADD = D + 4;      // rows of the LDS join tile, padded against bank conflicts
-  constexpr unsigned MIN_SHARE = 4;  // a tile for each wave
-
-  __shared__ float s_o[NW * RT * PADD];
-  __shared__ float s_m[NW * RT], s_l[NW * RT];
-  __shared__ int s_par[SV_CACHE_MAX_NEW];
-  __shared__ uint16_t s_dep[RT];
-  __shared__ unsigned s_anc[RT * (SV_CACHE_MAX_NEW / 32)];
-  __shared__ unsigned s_w[NW];
-  __shared__ unsigned s_at[2];
-  __shared__ int s_bad;
-
-  const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
-  const int m = lane & 15, g = lane >> 4;
-  const int page = 1 << a.page_shift;
+  constexpr int ESZ = (int)sizeof(T);
+  const int tid = threadIdx.x;
   // Consecutive shares on one XCD: the row tiles of a key head read the same keys and values
   // through that XCD's L2.
   const unsigned w = (blockIdx.x % LANES) * (a.grid / LANES) + blockIdx.x / LANES;
 
-  // ---- this workgroup's share of all tiles
   unsigned T_all = 0, v = 0, ex = 0;
   for (int b0 = 0; b0 < a.B; b0 += NT) {
     v = (b0 + tid < a.B) ? seq_tiles<RT>(a, b0 + tid) : 0u;
     unsigned tot;
-    ex = block_excl_scan(v, s_w, tot);
+    ex = block_excl_scan(v, s.w, tot);
     T_all += tot;
   }
   const unsigned share = max((T_all + a.grid - 1) / a.grid, MIN_SHARE);
@@ -283,83 +380,95 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
   const unsigned pos_end = min(T_all, pos + share);
   if (a.B <= NT) {
     if (pos >= ex && pos < ex + v) {
-      s_at[0] = (unsigned)tid;
-      s_at[1] = pos - ex;
+      s.at[0] = (unsigned)tid;
+      s.at[1] = pos - ex;
     }
   } else {
     unsigned run = 0;
     for (int b0 = 0; run <= pos; b0 += NT) {
       v = (b0 + tid < a.B) ? seq_tiles<RT>(a, b0 + tid) : 0u;
       unsigned tot;
-      ex = run + block_excl_scan(v, s_w, tot);
+      ex = run + block_excl_scan(v, s.w, tot);
       if (pos >= ex && pos < ex + v) {
-        s_at[0] = (unsigned)(b0 + tid);
-        s_at[1] = pos - ex;
+        s.at[0] = (unsigned)(b0 + tid);
+        s.at[1] = pos - ex;
       }
       run += tot;
     }
   }
   __syncthreads();
-  int b = (int)s_at[0];
-  unsigned off = s_at[1];  // tiles of sequence b before pos
-
-  const unsigned long long page_bytes = (unsigned long long)a.Hkv * page * D * ESZ;
-  const unsigned head_bytes = (unsigned)page * D * ESZ;
-
-  Seq sq = seq_of(a, b);
-  int tree_b = -1;  // the sequence whose parents and depths are in LDS
+  Segment g;
+  g.b = __builtin_amdgcn_readfirstlane((int)s.at[0]);
+  unsigned off = (unsigned)__builtin_amdgcn_readfirstlane((int)s.at[1]);  // tiles of the sequence before pos
+  g.sq = seq_of(a, g.b);
+  int code = 0, code_b = -1;  // the code of sequence code_b
   while (pos < pos_end) {
-    // ---- the unit and the tiles of it that are this workgroup's
     unsigned per_head = 0;
-    for (int rt = 0; rt < a.n_rt; ++rt) per_head += (unsigned)span_of<RT>(a, sq, rt).tiles;
+    for (int rt = 0; rt < a.n_rt; ++rt) per_head += (unsigned)span_of<RT>(a, g.sq, rt).tiles;
     if (off >= per_head * (unsigned)a.Hkv) {
       off -= per_head * (unsigned)a.Hkv;
-      sq = seq_of(a, ++b);
+      g.sq = seq_of(a, ++g.b);
       continue;
     }
-    const int h = (int)(off / per_head);
-    unsigned l0 = off - (unsigned)h * per_head;
-    int rt = 0;
-    Span sp = span_of<RT>(a, sq, 0);
-    while (l0 >= (unsigned)sp.tiles) {
-      l0 -= (unsigned)sp.tiles;
-      sp = span_of<RT>(a, sq, ++rt);
+    g.h = (int)(off / per_head);
+    g.l0 = (int)(off - (unsigned)g.h * per_head);
+    g.rt = 0;
+    g.sp = span_of<RT>(a, g.sq, 0);
+    while (g.l0 >= g.sp.tiles) {
+      g.l0 -= g.sp.tiles;
+      g.sp = span_of<RT>(a, g.sq, ++g.rt);
     }
-    const int l1 = (int)min((unsigned)sp.tiles, l0 + (pos_end - pos));
-    const bool whole = l0 == 0 && l1 == sp.tiles;
-    const int unit = (b * a.Hkv + h) * a.n_rt + rt;
-    const int32_t *table = a.page_table + (size_t)b * a.W;
-    const int32_t *par = a.parent ? a.parent + (size_t)b * a.N : nullptr;
-    const bool live = sp.i0 <= sp.i1;
-    const int end_all = sq.len + sq.m;
+    g.l1 = (int)min((unsigned)g.sp.tiles, (unsigned)g.l0 + (pos_end - pos));
+    g.table = (TablePtr)(a.page_table + (size_t)g.b * a.W);
+    g.par = a.parent ? a.parent + (size_t)g.b * a.N : nullptr;
+    g.words = (g.sq.m + 31) >> 5;
+    g.masks = a.window > 0 || g.tile(g.l1 - 1) + TILE > g.sq.len;
+    const bool whole = g.l0 == 0 && g.l1 == g.sp.tiles;
 
-    // ---- what makes the whole sequence invalid: the same test in every workgroup of it
     __syncthreads();  // the previous segment is done with the LDS
-    if (tid == 0) s_bad = sq.ok ? 0 : -SV_ROW_BAD_LENGTH;
-    if (par && sq.ok && tree_b != b)
-      for (int i = tid; i < sq.m; i += NT) s_par[i] = par[i];
-    __syncthreads();
-    if (sq.ok && sq.m > 0) {
-      if (par) {
-        bool bad = false;
-        for (int i = tid; i < sq.m; i += NT) bad |= (i == 0) ? s_par[0] != -1 : (s_par[i] < 0 || s_par[i] >= i);
-        if (bad) atomicMax(&s_bad, 64 - SV_ROW_BAD_TREE);
-      }
-      int p0 = 0, np = 0;  // pages of the sinks, then from the window on
-      const int first = (a.window > 0) ? max(0, sq.len - a.window + 1) : 0;
-      p0 = first >> a.page_shift;
-      const int ps = min((min(a.sinks, first) + page - 1) >> a.page_shift, p0);
-      np = ((end_all + page - 1) >> a.page_shift) - p0 + ps;
-      bool bad = false;
-      for (int i = tid; i < np; i += NT) bad |= (unsigned)table[i < ps ? i : i - ps + p0] >= (unsigned)a.P;
-      if (bad) atomicMax(&s_bad, -SV_ROW_BAD_PAGE);
+    if (code_b != g.b) {
+      code = seq_code<RT>(a, g.sq, g.b, s);
+      code_b = g.b;
     }
-    __syncthreads();
-    const int code = s_bad > 64 ? 64 - s_bad : -s_bad;  // a bad tree before a bad page
-    if (tid == 0 && h == 0 && rt == 0 && l0 == 0) a.row_status[b] = code;
+    if (tid == 0 && g.h == 0 && g.rt == 0 && g.l0 == 0) a.row_status[g.b] = code;
+    if (tid == 0 && g.l0 == 0) {
+      const unsigned last = (pos + (unsigned)g.sp.tiles - 1) / share;
+      a.desc[(g.b * a.Hkv + g.h) * a.n_rt + g.rt] =
+          make_uint4(w, last - w + 1, (code ? 0x80000000u : 0u) | (unsigned)(g.sq.ok ? g.sq.m : 0), 0u);
+    }
+    if (code == 0 && g.par && g.masks && g.sp.i0 <= g.sp.i1) tree_books<RT>(a, g, s);
 
-    f32x4 o[R][DT];
-    float rm[R], rl[R];
+    const unsigned slot = 2 * w + (g.l0 == 0 ? 1u : 0u);
+    auto emit = [&](int row, int c4, f32x4 acc, float mt, float ls) {
+      const int rg = g.rt * RT + row, i = rg / a.group, hh = rg - i * a.group;
+      if (whole) {
+        if (i >= a.N) return;
+        f32x4 y = acc * (1.0f / ls);
+        if (i >= g.sq.m) y = f32x4{0, 0, 0, 0};
+        if (code != 0) y = f32x4{NAN, NAN, NAN, NAN};
+        M::store4(a.out + ((((size_t)g.b * a.N + i) * a.Hq + g.h * a.group + hh) * D + 4 * c4) * ESZ, y[0], y[1], y[2], y[3]);
+      } else {
+        *reinterpret_cast<f32x4 *>(&a.part_o[((size_t)slot * RT + row) * D + 4 * c4]) = acc;
+        if (c4 == 0) a.part_ml[(size_t)slot * RT + row] = make_float2(mt, ls);
+      }
+    };
+    stream(g, code, emit);
+    pos += (unsigned)(g.l1 - g.l0);
+    off += (unsigned)(g.l1 - g.l0);
+  }
+}
+
+// A wave's rows over one tile of scores: masks, running maximum and sum, weights.
+template <typename T, int D, int R>
+struct Rows {
+  typedef Mma<T> M;
+  static constexpr int KS = D / (4 * M::E), DT = D / 16;
+  f32x4 o[R][DT];
+  float rm[R], rl[R];
+  u32x4 q[R][KS];
+  int node[R], dep[R];  // clamped to the segment's nodes
+
+  SVD void clear() {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       rm[r] = -INFINITY;
@@ -367,72 +476,125 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[r][d] = f32x4{0, 0, 0, 0};
     }
-
-    if (live && code == 0) {
-      // ---- depths of the rows' nodes and the nodes they see, where tiles of this segment need them
-      const int i0 = sp.i0, words = (sq.m + 31) >> 5;
-      const int last_tile = (l1 - 1 < sp.n_sink) ? l1 - 1 : l1 - 1 - sp.n_sink + sp.first;
-      const bool masks = a.window > 0 || (last_tile + 1) * TILE > sq.len;
-      if (par && masks) {
-        const int n_nodes = sp.i1 - i0 + 1;
-        for (int i = tid; i < n_nodes * words; i += NT) s_anc[i] = 0u;
-        __syncthreads();
-        for (int i = tid; i < n_nodes; i += NT) {
-          int dep_i = 0;
-          for (int j = s_par[i0 + i]; j >= 0; j = s_par[j]) ++dep_i;
-          s_dep[i] = (uint16_t)dep_i;
-          int d = dep_i;  // depth of j
-          for (int j = i0 + i; j >= 0; j = s_par[j], --d)
-            if (a.window <= 0 || dep_i - d < a.window || sq.len + d < a.sinks) s_anc[i * words + (j >> 5)] |= 1u << (j & 31);
-        }
-        __syncthreads();
-        tree_b = b;
-      }
-
-      // ---- query rows
-      u32x4 qf[R][KS];
-      int node[R], dep[R];
+  }
+  // Rows row0 + 16 r + m of the unit; rows that are no new token's get zeros.
+  template <int RT>
+  SVD void load(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int row0, int m, int g) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int row = rt * RT + 16 * r + m;
-        const int i = row / a.group, hh = row - i * a.group;
-        const bool in = i < sq.m;
-        node[r] = in ? i : sp.i1;
-        dep[r] = (par && masks) ? (int)s_dep[node[r] - i0] : node[r];
-        const char *qp = a.q + (long long)b * a.q_sb + (long long)(in ? i : 0) * a.q_sn + (size_t)(h * a.group + hh) * D * ESZ;
+    for (int r = 0; r < R; ++r) {
+      const int row = row0 + 16 * r + m, i = row / a.group, hh = row - i * a.group;
+      const bool in = i < sg.sq.m;
+      node[r] = min(i, sg.sp.i1);
+      dep[r] = (sg.par && sg.masks) ? (int)s.dep[node[r] - sg.sp.i0] : node[r];
+      const char *qp = a.q + (long long)sg.b * a.q_sb + (long long)(in ? i : 0) * a.q_sn + (size_t)(sg.h * a.group + hh) * D * sizeof(T);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const u32x4 x = *reinterpret_cast<const u32x4 *>(qp + (4 * s + g) * 16);
-          qf[r][s] = in ? x : u32x4{0, 0, 0, 0};
-        }
+      for (int k = 0; k < KS; ++k) {
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(qp + (4 * k + g) * 16);
+        q[r][k] = in ? x : u32x4{0, 0, 0, 0};
       }
+    }
+  }
+  template <int RT>
+  SVD unsigned view(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int t0, int r, int g) const {
+    return M::lane_bits(sg.sees(a, t0, dep[r], &s.anc[(node[r] - sg.sp.i0) * sg.words]), g);
+  }
+  template <int RT>
+  SVD void mask(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int t0, int g, f32x4 (&sc)[R][2]) const {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const unsigned vis = view(a, sg, s, t0, r, g);
+#pragma unroll
+      for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[r][t2][i] = ((vis >> (4 * t2 + i)) & 1u) ? sc[r][t2][i] : -INFINITY;
+    }
+  }
+  // Scores (as powers of two) to weights, against the running maximum.
+  SVD typename M::P soften(int r, f32x4 (&sc)[2]) {
+    float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])), fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+    mx = fmaxf(rm[r], col_max(mx));
+    if (__any(mx > rm[r])) {  // a new maximum in some row: all sums so far to the new scale
+      const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(rm[r] - mx);
+      rl[r] *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
+      rm[r] = mx;
+    }
+    const float mu = (mx == -INFINITY) ? 0.0f : mx;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t2 = 0; t2 < 2; ++t2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[t2][i] = fast_exp2(sc[t2][i] - mu);
+      sum += (sc[t2][0] + sc[t2][1]) + (sc[t2][2] + sc[t2][3]);
+    }
+    rl[r] += sum;
+    return M::weights(sc);
+  }
+  // What values that are not finite are to each row that sees them (they are left out of the
+  // products, where a weight of zero would not keep them from the other rows): flags of the
+  // values times flags of the view, both 0 or 1, count the sightings.
+  SVD void odd_values(int r, int d, const u32x4 (&v)[M::VT], unsigned vis) {
+    f32x4 one[2];
+#pragma unroll
+    for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) one[t2][i] = ((vis >> (4 * t2 + i)) & 1u) ? 1.0f : 0.0f;
+    const typename M::P see = M::weights(one);
+    u32x4 fn[M::VT], fp[M::VT], fm[M::VT];
+#pragma unroll
+    for (int t2 = 0; t2 < M::VT; ++t2) {
+      fn[t2] = M::flags(v[t2], [](float x) { return !(x == x); });
+      fp[t2] = M::flags(v[t2], [](float x) { return x == INFINITY; });
+      fm[t2] = M::flags(v[t2], [](float x) { return x == -INFINITY; });
+    }
+    const f32x4 z = {0, 0, 0, 0};
+    const f32x4 cn = M::pv(fn, see, z), cp = M::pv(fp, see, z), cm = M::pv(fm, see, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[r][d][i] += (cn[i] > 0.0f || (cp[i] > 0.0f && cm[i] > 0.0f)) ? NAN : cp[i] > 0.0f ? INFINITY : cm[i] > 0.0f ? -INFINITY : 0.0f;
+  }
+};
 
-      const char *kh = a.k_pages + (size_t)h * head_bytes;
-      const char *vh = a.v_pages + (size_t)h * head_bytes;
-      auto tile_of = [&](int l) { return l < sp.n_sink ? l : l - sp.n_sink + sp.first; };
-      // The pages of a tile's two halves (a page has at least 16 slots).  A half that no row
-      // sees may have no page any more (behind the sequence, or left of the window): the
-      // other half's page stands in for it.
-      auto pages_of = [&](int l, int &pa, int &pb) {
-        const int t0 = tile_of(l) * TILE, t1 = t0 + TILE / 2;
-        const bool ha = t0 < a.sinks || t1 > sp.from;
-        const bool hb = t1 < end_all && (t1 < a.sinks || t1 + TILE / 2 > sp.from);
-        const int ia = t0 >> a.page_shift, ib = t1 >> a.page_shift;
-        pa = table[ha ? ia : ib];
-        pb = (hb && ib != ia) ? table[ib] : pa;
-      };
-      auto load_k = [&](int l, int pa, int pb, u32x4 (&k)[2][KS]) {
-        const int t0 = tile_of(l) * TILE;
+// ---------------------------------------------------------------- few rows
+
+// Workgroups resident on a CU, which is also how many the grid has per CU.
+template <typename T, int D, int R>
+constexpr int attn_occ() { return (R * D * (int)sizeof(T) <= 128) ? 3 : (D * (int)sizeof(T) <= 256 ) ? 2 : (D * (int)sizeof(T) <= 512 && R == 1) ? 2 : 1; }
+
+template <typename T, int D, int R>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, D, R>()))) void k_attn(const AttnArgs a) {
+  typedef Mma<T> M;
+  constexpr int RT = 16 * R, E = M::E, ESZ = (int)sizeof(T);
+  constexpr int KS = D / (4 * E);  // key units a lane holds of a 16-slot score tile
+  constexpr int DT = D / 16;       // 16-wide tiles of the output's d
+  constexpr int PADD = D + 4;      // rows of the LDS join tile, padded against bank conflicts
+  __shared__ SharedBooks<RT> s;
+  __shared__ float s_o[NW * RT * PADD];
+  __shared__ float s_m[NW * RT], s_l[NW * RT];
+
+  const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
+  const int m = lane & 15, g = lane >> 4;
+  const int page = 1 << a.page_shift;
+  const unsigned long long page_bytes = (unsigned long long)a.Hkv * page * D * ESZ;
+  const unsigned head_bytes = (unsigned)page * D * ESZ;
+
+  attn_share<T, D, RT>(a, s, [&](const Segment &sg, int code, auto emit) {
+    Rows<T, D, R> rows;
+    rows.clear();
+    if (sg.sp.i0 <= sg.sp.i1 && code == 0) {
+      const char *kh = a.k_pages + (size_t)sg.h * head_bytes;
+      const char *vh = a.v_pages + (size_t)sg.h * head_bytes;
+      auto load_k = [&](int t0, int pa, int pb, u32x4 (&k)[2][KS]) {
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
           const int sl = M::key_slot(t2, m);
           const char *p = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)((t0 + sl) & (page - 1)) + (unsigned)(g * page)) * 16u;
 #pragma unroll
-          for (int s = 0; s < KS; ++s) k[t2][s] = *reinterpret_cast<const u32x4 *>(p + (size_t)s * (4 * 16) * page);
+          for (int k4 = 0; k4 < KS; ++k4) k[t2][k4] = *reinterpret_cast<const u32x4 *>(p + (size_t)k4 * (4 * 16) * page);
         }
       };
-      auto load_v = [&](int l, int pa, int pb, u32x4 (&v)[DT][M::VT]) {
-        const int t0 = tile_of(l) * TILE;
+      auto load_v = [&](int t0, int pa, int pb, u32x4 (&v)[DT][M::VT]) {
 #pragma unroll
         for (int t2 = 0; t2 < M::VT; ++t2) {
           const int sl = M::val_slot(t2, g);
@@ -441,164 +603,97 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
           for (int d = 0; d < DT; ++d) v[d][t2] = *reinterpret_cast<const u32x4 *>(p + d * 256);
         }
       };
+      auto cut_v = [&](int t0, u32x4 (&v)[DT][M::VT]) {  // slots behind the sequence hold anything
+        if (t0 + TILE > sg.end())
+#pragma unroll
+          for (int t2 = 0; t2 < M::VT; ++t2)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) v[d][t2] = M::cut(v[d][t2], sg.end() - t0 - M::val_slot(t2, g));
+      };
 
-      int l = (int)l0 + wid;
-      u32x4 kf[2][KS];
-      int pa = 0, pb = 0, na = 0, nb = 0;
-      if (l < l1) {
-        pages_of(l, pa, pb);
-        load_k(l, pa, pb, kf);
-        if (l + NW < l1) pages_of(l + NW, na, nb);
+      u32x4 kf[2][KS], vf[DT][M::VT];
+      int l = sg.l0 + wid, pa = 0, pb = 0;
+      if (l < sg.l1) {
+        sg.pages(a, sg.tile(l), pa, pb);
+        load_k(sg.tile(l), pa, pb, kf);
       }
-      for (; l < l1; l += NW) {
-        const int t0 = tile_of(l) * TILE;
-        u32x4 vf[DT][M::VT];
-        load_v(l, pa, pb, vf);
-        f32x4 s[R][2];
+      rows.load(a, sg, s, sg.rt * RT, m, g);
+      bool odd_any = false;
+      for (; l < sg.l1; l += NW) {
+        const int t0 = sg.tile(l);
+        const bool more = l + NW < sg.l1;
+        int na = 0, nb = 0;
+        if (more) sg.pages(a, sg.tile(l + NW), na, nb);
+        load_v(t0, pa, pb, vf);
+        f32x4 sc[R][2];
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4{0, 0, 0, 0};
+        for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int k4 = 0; k4 < KS; ++k4)
 #pragma unroll
           for (int t2 = 0; t2 < 2; ++t2)
 #pragma unroll
-            for (int r = 0; r < R; ++r) s[r][t2] = M::qk(kf[t2][k], qf[r][k], s[r][t2]);
+            for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(kf[t2][k4], rows.q[r][k4], sc[r][t2]);
         pa = na;
         pb = nb;
-        if (l + NW < l1) {
-          load_k(l + NW, pa, pb, kf);
-          if (l + 2 * NW < l1) pages_of(l + 2 * NW, na, nb);
-        }
+        if (more) load_k(sg.tile(l + NW), pa, pb, kf);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) s[r][t2] = s[r][t2] * a.c2;
-
-        // Tiles that every row of the unit sees whole need no mask.
-        const bool plain = t0 + TILE <= sq.len &&
-                           (a.window <= 0 || t0 + TILE <= a.sinks || (long long)sq.len + sq.m - 1 - t0 < a.window);
-        unsigned vis[R];  // the row's view of this lane's slots, bit 4 t2 + i
-#pragma unroll
-        for (int r = 0; r < R; ++r) vis[r] = 0u;
-        if (!plain) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int pos_r = sq.len + dep[r], lo = (a.window > 0) ? pos_r - a.window + 1 : 0;
-            const int head = par ? sq.len : pos_r + 1;  // slots that window and sinks alone decide
-            unsigned see = slots32(t0, lo, head) | slots32(t0, 0, min(a.sinks, head));
-            if (par) see |= anc32(&s_anc[(node[r] - i0) * words], words, t0 - sq.len);
-            vis[r] = M::lane_bits(see, g);
-#pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[r][t2][i] = ((vis[r] >> (4 * t2 + i)) & 1u) ? s[r][t2][i] : -INFINITY;
-          }
-          if (t0 + TILE > end_all)  // slots behind the sequence hold anything
-#pragma unroll
-            for (int t2 = 0; t2 < M::VT; ++t2)
-#pragma unroll
-              for (int d = 0; d < DT; ++d) vf[d][t2] = M::cut(vf[d][t2], end_all - t0 - M::val_slot(t2, g));
-        }
-
-        typename M::P pw[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float mx = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                           fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-          mx = fmaxf(rm[r], xor_max(mx));
-          if (__any(mx > rm[r])) {  // a new maximum in some row: all sums so far to the new scale
-            const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(rm[r] - mx);
-            rl[r] *= f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
-            rm[r] = mx;
-          }
-          const float mu = (mx == -INFINITY) ? 0.0f : mx;
-          float sum = 0.0f;
-#pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[r][t2][i] = fast_exp2(s[r][t2][i] - mu);
-            sum += (s[r][t2][0] + s[r][t2][1]) + (s[r][t2][2] + s[r][t2][3]);
-          }
-          rl[r] += sum;
-          pw[r] = M::weights(s[r]);
-        }
-
-        // A value that is not finite must reach the rows that see it and no others, and a
-        // zero weight does not keep it away (0 * inf): such values are taken out of the
-        // product, and what they are to each row follows from products of flags.
-        bool odd = false;
-        if (!plain) {
+          for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = sc[r][t2] * a.c2;
+        if (!sg.plain(a, t0)) {
+          rows.mask(a, sg, s, t0, g, sc);
+          cut_v(t0, vf);
+          bool odd = false;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int t2 = 0; t2 < M::VT; ++t2) odd |= M::non_finite(vf[d][t2]);
-        }
-        if (!plain && __any(odd)) {
-          typename M::P sees[R];
+          if (__any(odd)) {
+            odd_any = true;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            f32x4 one[2];
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) one[t2][i] = ((vis[r] >> (4 * t2 + i)) & 1u) ? 1.0f : 0.0f;
-            sees[r] = M::weights(one);
+              for (int t2 = 0; t2 < M::VT; ++t2) vf[d][t2] = M::finite(vf[d][t2]);
           }
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            u32x4 fn[M::VT], fp[M::VT], fm[M::VT];
-#pragma unroll
-            for (int t2 = 0; t2 < M::VT; ++t2) {
-              fn[t2] = M::flags(vf[d][t2], [](float x) { return !(x == x); });
-              fp[t2] = M::flags(vf[d][t2], [](float x) { return x == INFINITY; });
-              fm[t2] = M::flags(vf[d][t2], [](float x) { return x == -INFINITY; });
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const f32x4 z = {0, 0, 0, 0};
-              const f32x4 cn = M::pv(fn, sees[r], z), cp = M::pv(fp, sees[r], z), cm = M::pv(fm, sees[r], z);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o[r][d][i] += (cn[i] > 0.0f || (cp[i] > 0.0f && cm[i] > 0.0f)) ? NAN
-                              : cp[i] > 0.0f ? INFINITY : cm[i] > 0.0f ? -INFINITY : 0.0f;
-            }
-          }
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int t2 = 0; t2 < M::VT; ++t2) {
-              const u32x4 ok = M::flags(vf[d][t2], [](float x) { return x - x == 0.0f; });
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const unsigned keep = (sizeof(T) == 2) ? ((ok[j] & 0xffffu ? 0xffffu : 0u) | (ok[j] >> 16 ? 0xffff0000u : 0u))
-                                                       : (ok[j] ? 0xffffffffu : 0u);
-                vf[d][t2][j] &= keep;
-              }
-            }
         }
+        typename M::P pw[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) pw[r] = rows.soften(r, sc[r]);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int r = 0; r < R; ++r) o[r][d] = M::pv(vf[d], pw[r], o[r][d]);
+          for (int r = 0; r < R; ++r) rows.o[r][d] = M::pv(vf[d], pw[r], rows.o[r][d]);
       }
+      if (odd_any)
+        for (l = sg.l0 + wid; l < sg.l1; l += NW) {
+          const int t0 = sg.tile(l);
+          if (sg.plain(a, t0)) continue;
+          sg.pages(a, t0, pa, pb);
+          load_v(t0, pa, pb, vf);
+          cut_v(t0, vf);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const unsigned vis = rows.view(a, sg, s, t0, r, g);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) rows.odd_values(r, d, vf[d], vis);
+          }
+        }
     }
 
-    // ---- the four waves joined: rows' maxima and sums, then the output tiles
+    // the four waves joined: rows' maxima and sums, then the output tiles
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float l_row = xor_sum(rl[r]);
+      const float l_row = col_sum(rows.rl[r]);
       if (g == 0) {
-        s_m[wid * RT + 16 * r + m] = rm[r];
+        s_m[wid * RT + 16 * r + m] = rows.rm[r];
         s_l[wid * RT + 16 * r + m] = l_row;
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        *reinterpret_cast<f32x4 *>(&s_o[(wid * RT + 16 * r + m) * PADD + 16 * d + 4 * g]) = o[r][d];
+        *reinterpret_cast<f32x4 *>(&s_o[(wid * RT + 16 * r + m) * PADD + 16 * d + 4 * g]) = rows.o[r][d];
     }
     __syncthreads();
-    const unsigned slot = 2 * w + (l0 == 0 ? 1u : 0u);
     for (int x = tid; x < RT * (D / 4); x += NT) {
       const int row = x / (D / 4), c4 = x - row * (D / 4);
       float mt = -INFINITY;
@@ -608,40 +703,185 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
       float ls = 0.0f;
 #pragma unroll
       for (int k = 0; k < NW; ++k) {
-        const float mk = s_m[k * RT + row];
-        if (mk == -INFINITY && s_l[k * RT + row] == 0.0f) continue;  // a wave without a tile
+        const float mk = s_m[k * RT + row], lk = s_l[k * RT + row];
+        if (mk == -INFINITY && lk == 0.0f) continue;  // a wave that saw nothing
         const float f = fast_exp2(mk - mt);
-        ls += f * s_l[k * RT + row];
+        ls += f * lk;
         acc += *reinterpret_cast<const f32x4 *>(&s_o[(k * RT + row) * PADD + 4 * c4]) * f;
       }
-      const int rg = rt * RT + row, i = rg / a.group, hh = rg - i * a.group;
-      if (whole) {
-        if (i >= a.N) continue;
-        float inv = 1.0f / ls;
-        if (code != 0) inv = NAN;
-        f32x4 y = acc * inv;
-        if (code == 0 && i >= sq.m) y = f32x4{0, 0, 0, 0};
-        M::store4(a.out + ((((size_t)b * a.N + i) * a.Hq + h * a.group + hh) * D + 4 * c4) * ESZ, y[0], y[1], y[2], y[3]);
-      } else {
-        *reinterpret_cast<f32x4 *>(&a.part_o[((size_t)slot * RT + row) * D + 4 * c4]) = acc;
-        if (c4 == 0) a.part_ml[(size_t)slot * RT + row] = make_float2(mt, ls);
+      emit(row, c4, acc, mt, ls);
+    }
+  });
+}
+
+// ---------------------------------------------------------------- many rows
+
+// A tile's keys and values lie in LDS in the order in which the lanes read them, 16 lanes
+// 256 bytes: keys [unit of d][score tile, row of it], values [unit of slots][d].  While the
+// waves work on one buffer the next tile's units are in flight in registers; they go to the
+// other buffer when the work is done: one barrier a tile.
+template <typename T, int D, int R>
+constexpr int wide_occ() { return (R * D * (int)sizeof(T) <= 512) ? 2 : 1; }
+
+template <typename T, int D, int R>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, D, R>()))) void k_attn_wide(const AttnArgs a) {
+  typedef Mma<T> M;
+  constexpr int RT = 16 * R * NW, E = M::E, ESZ = (int)sizeof(T);
+  constexpr int KS = D / (4 * E), DT = D / 16;
+  constexpr int UNITS = TILE * D / E, PT = UNITS / NT;  // 16-byte units of a tile's keys (or values), and a thread's
+  __shared__ SharedBooks<RT> s;
+  __shared__ u32x4 s_k[2][UNITS], s_v[2][UNITS];
+  __shared__ int s_odd;
+
+  const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
+  const int m = lane & 15, g = lane >> 4;
+  const int page = 1 << a.page_shift;
+  const unsigned long long page_bytes = (unsigned long long)a.Hkv * page * D * ESZ;
+  const unsigned head_bytes = (unsigned)page * D * ESZ;
+
+  attn_share<T, D, RT>(a, s, [&](const Segment &sg, int code, auto emit) {
+    Rows<T, D, R> rows;
+    rows.clear();
+    if (sg.sp.i0 <= sg.sp.i1 && code == 0) {
+      const char *kh = a.k_pages + (size_t)sg.h * head_bytes;
+      const char *vh = a.v_pages + (size_t)sg.h * head_bytes;
+      auto load_k = [&](int t0, int pa, int pb, u32x4 (&k)[PT]) {
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          const int x = tid + j * NT, u = x / TILE, sl = x % TILE;
+          k[j] = *reinterpret_cast<const u32x4 *>(kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + (size_t)(u * page + ((t0 + sl) & (page - 1))) * 16);
+        }
+      };
+      auto load_v = [&](int t0, int pa, int pb, u32x4 (&v)[PT]) {
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          const int x = tid + j * NT, sl = x / D * E, d = x % D;
+          v[j] = *reinterpret_cast<const u32x4 *>(vh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + (size_t)(((t0 + sl) & (page - 1)) / E * D + d) * 16);
+        }
+      };
+      auto put_k = [&](int buf, const u32x4 (&k)[PT]) {
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          const int x = tid + j * NT;
+          s_k[buf][x / TILE * TILE + M::key_place(x % TILE)] = k[j];
+        }
+      };
+      auto cut_v = [&](int t0, u32x4 (&v)[PT]) {  // slots behind the sequence hold anything
+        if (t0 + TILE > sg.end())
+#pragma unroll
+          for (int j = 0; j < PT; ++j) v[j] = M::cut(v[j], sg.end() - t0 - (tid + j * NT) / D * E);
+      };
+      auto put_v = [&](int t0, int buf, u32x4 (&v)[PT]) {
+        if (!sg.plain(a, t0)) {
+          cut_v(t0, v);
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < PT; ++j) odd |= M::non_finite(v[j]);
+          if (odd) {
+            s_odd = 1;
+#pragma unroll
+            for (int j = 0; j < PT; ++j) v[j] = M::finite(v[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < PT; ++j) s_v[buf][tid + j * NT] = v[j];
+      };
+
+      u32x4 kf[PT], vf[PT];
+      int pa, pb, l = sg.l0, buf = 0;
+      sg.pages(a, sg.tile(l), pa, pb);
+      load_k(sg.tile(l), pa, pb, kf);
+      load_v(sg.tile(l), pa, pb, vf);
+      if (tid == 0) s_odd = 0;
+      rows.load(a, sg, s, sg.rt * RT + wid * 16 * R, m, g);
+      __syncthreads();  // s_odd, before the first put_v may set it
+      put_k(0, kf);
+      put_v(sg.tile(l), 0, vf);
+      if (l + 1 < sg.l1) {
+        sg.pages(a, sg.tile(l + 1), pa, pb);
+        load_k(sg.tile(l + 1), pa, pb, kf);
+        load_v(sg.tile(l + 1), pa, pb, vf);
       }
+      __syncthreads();
+      for (; l < sg.l1; ++l, buf ^= 1) {
+        const int t0 = sg.tile(l);
+        f32x4 sc[R][2];
+#pragma unroll
+        for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k4 = 0; k4 < KS; ++k4)
+#pragma unroll
+          for (int t2 = 0; t2 < 2; ++t2) {
+            const u32x4 k = s_k[buf][(4 * k4 + g) * TILE + 16 * t2 + m];
+#pragma unroll
+            for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(k, rows.q[r][k4], sc[r][t2]);
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = sc[r][t2] * a.c2;
+        if (!sg.plain(a, t0)) rows.mask(a, sg, s, t0, g, sc);
+        typename M::P pw[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) pw[r] = rows.soften(r, sc[r]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          u32x4 v[M::VT];
+#pragma unroll
+          for (int t2 = 0; t2 < M::VT; ++t2) v[t2] = s_v[buf][M::val_slot(t2, g) / E * D + 16 * d + m];
+#pragma unroll
+          for (int r = 0; r < R; ++r) rows.o[r][d] = M::pv(v, pw[r], rows.o[r][d]);
+        }
+        if (l + 1 < sg.l1) {
+          put_k(buf ^ 1, kf);
+          put_v(sg.tile(l + 1), buf ^ 1, vf);
+          if (l + 2 < sg.l1) {
+            sg.pages(a, sg.tile(l + 2), pa, pb);
+            load_k(sg.tile(l + 2), pa, pb, kf);
+            load_v(sg.tile(l + 2), pa, pb, vf);
+          }
+        }
+        __syncthreads();
+      }
+      if (s_odd)  // the same for the whole workgroup: set before the loop's last barrier
+        for (l = sg.l0; l < sg.l1; ++l) {
+          const int t0 = sg.tile(l);
+          if (sg.plain(a, t0)) continue;
+          sg.pages(a, t0, pa, pb);
+          load_v(t0, pa, pb, vf);
+          cut_v(t0, vf);
+#pragma unroll
+          for (int j = 0; j < PT; ++j) s_v[0][tid + j * NT] = vf[j];
+          __syncthreads();
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const unsigned vis = rows.view(a, sg, s, t0, r, g);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              u32x4 v[M::VT];
+#pragma unroll
+              for (int t2 = 0; t2 < M::VT; ++t2) v[t2] = s_v[0][M::val_slot(t2, g) / E * D + 16 * d + m];
+              rows.odd_values(r, d, v, vis);
+            }
+          }
+          __syncthreads();
+        }
     }
-    if (tid == 0 && l0 == 0) {
-      const unsigned last = (pos + (unsigned)sp.tiles - 1) / share;
-      a.desc[unit] = make_uint4(w, last - w + 1, (unsigned)(code ? 0x80000000u : 0u) | (unsigned)max(0, sq.ok ? sq.m : 0), 0u);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float l_row = col_sum(rows.rl[r]);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) emit(wid * 16 * R + 16 * r + m, 4 * d + g, rows.o[r][d], rows.rm[r], l_row);
     }
-    pos += (unsigned)l1 - l0;
-    off += (unsigned)l1 - l0;
-  }
+  });
 }
 
 // Units that several workgroups streamed: one wave a row, its partial tiles in the order of
 // the slots.
-template <typename T, int D, int R>
+template <typename T, int D, int RT>
 __global__ __launch_bounds__(NT) void k_attn_join(const AttnArgs a) {
   typedef Mma<T> M;
-  constexpr int RT = 16 * R, ESZ = (int)sizeof(T), PL = D / 4;  // lanes that hold a row
+  constexpr int ESZ = (int)sizeof(T), PL = D / 4;  // lanes that hold a row
   const int lane = lane_id(), wid = threadIdx.x / WAVE;
   const int unit = blockIdx.x / (RT / NW), row = (blockIdx.x % (RT / NW)) * NW + wid;
   const uint4 ds = a.desc[unit];
@@ -666,8 +906,8 @@ __global__ __launch_bounds__(NT) void k_attn_join(const AttnArgs a) {
     const size_t s = (size_t)slot_of(k) * RT + row;
     const float2 ml = a.part_ml[s];
     const f32x4 x = *reinterpret_cast<const f32x4 *>(&a.part_o[s * D + 4 * c4]);
-    const float f = (ml.x == -INFINITY && ml.y == 0.0f) ? 0.0f : fast_exp2(ml.x - mt);
-    const bool none = ml.x == -INFINITY && ml.y == 0.0f;
+    const bool none = ml.x == -INFINITY && ml.y == 0.0f;  // it saw nothing of the row
+    const float f = fast_exp2(ml.x - mt);
     ls += none ? 0.0f : f * ml.y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] += none ? 0.0f : f * x[j];
@@ -693,36 +933,48 @@ __global__ __launch_bounds__(NT) void k_attn_join(const AttnArgs a) {
 namespace {
 
 using namespace sv;
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 using sv_host::align256;
 
 struct AttnPlan {
-  int R, RT, n_rt, occ;
+  bool wide;
+  int R, RT, n_rt;
   unsigned grid;
   long long units;
   size_t part_o, part_ml, desc, total;
 };
 
-// Row tiles a wave holds: as many as the rows need, up to what its registers take.
-int rows_R(long long rows, int D, int esz) {
-  const int most = (esz == 2) ? (D == 256 ? 2 : 4) : (D == 64 ? 4 : D == 128 ? 2 : 1);
-  const int need = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  return need < most ? need : most;
-}
-
 bool pow2_page(int32_t page) { return page >= 16 && page <= 256 && (page & (page - 1)) == 0; }
 
 template <typename T, int D, int R>
-constexpr int occ_of() { return attn_occ<T, D, R>(); }
-
-int plan_occ(int D, int esz, int R) {
-  if (esz == 2) {
-    if (D == 64) return R == 1 ? occ_of<uint16_t, 64, 1>() : R == 2 ? occ_of<uint16_t, 64, 2>() : occ_of<uint16_t, 64, 4>();
-    if (D == 128) return R == 1 ? occ_of<uint16_t, 128, 1>() : R == 2 ? occ_of<uint16_t, 128, 2>() : occ_of<uint16_t, 128, 4>();
-    return R == 1 ? occ_of<uint16_t, 256, 1>() : occ_of<uint16_t, 256, 2>();
+void attn_go(sv_host::Launcher &L, AttnArgs &a, const AttnPlan &p) {
+  void *args[] = {&a};
+  if (p.wide) {
+    L.go((const void *)&k_attn_wide<T, D, R>, p.grid, args);
+    L.go((const void *)&k_attn_join<T, D, 16 * R * NW>, (unsigned)(p.units * (p.RT / NW)), args);
+  } else if constexpr (D <= 128 || R == 1) {
+    L.go((const void *)&k_attn<T, D, R>, p.grid, args);
+    L.go((const void *)&k_attn_join<T, D, 16 * R>, (unsigned)(p.units * (p.RT / NW)), args);
   }
-  if (D == 64) return R == 1 ? occ_of<float, 64, 1>() : R == 2 ? occ_of<float, 64, 2>() : occ_of<float, 64, 4>();
-  if (D == 128) return R == 1 ? occ_of<float, 128, 1>() : occ_of<float, 128, 2>();
-  return occ_of<float, 256, 1>();
+}
+
+// The kernel for a head size and type: f is called with the constants.
+template <typename F>
+auto attn_pick(int esz, int D, int R, F f) {
+  typedef uint16_t h;
+  if (esz == 2) {
+    if (D == 64) return R == 1 ? f(h{}, Int<64>{}, Int<1>{}) : f(h{}, Int<64>{}, Int<2>{});
+    if (D == 128) return R == 1 ? f(h{}, Int<128>{}, Int<1>{}) : f(h{}, Int<128>{}, Int<2>{});
+    return R == 1 ? f(h{}, Int<256>{}, Int<1>{}) : f(h{}, Int<256>{}, Int<2>{});
+  }
+  if (D == 64) return R == 1 ? f(0.0f, Int<64>{}, Int<1>{}) : f(0.0f, Int<64>{}, Int<2>{});
+  if (D == 128) return R == 1 ? f(0.0f, Int<128>{}, Int<1>{}) : f(0.0f, Int<128>{}, Int<2>{});
+  return f(0.0f, Int<256>{}, Int<1>{});
 }
 
 bool attn_shape_ok(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page, int32_t W) {
@@ -730,17 +982,24 @@ bool attn_shape_ok(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int
          (D == 64 || D == 128 || D == 256) && pow2_page(page) && W >= 1 && (long long)W * page <= 0x7fffffffLL - 4096;
 }
 
+// Up to 16 rows of a key head, or 32 up to D = 128: one wave holds them in its registers; more go to
+// the kernel whose waves share them.
 bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page, int32_t W, int esz, AttnPlan &p) {
   const long long rows = (long long)N * (Hq / Hkv);
-  p.R = rows_R(rows, D, esz);
-  p.RT = 16 * p.R;
+  const bool two = D <= 128;  // the registers take two row tiles of k_attn
+  p.wide = rows > (two ? 32 : 16);
+  p.R = p.wide ? (rows <= 64 || D * esz == 1024 ? 1 : 2) : (rows <= 16 ? 1 : 2);
+  p.RT = 16 * p.R * (p.wide ? NW : 1);
   const long long n_rt = (rows + p.RT - 1) / p.RT;
   p.units = (long long)B * Hkv * n_rt;
   const long long most = ((long long)W * page + TILE - 1) / TILE + 1;  // tiles of a unit
   if (p.units * most > 0x7fffffffLL || p.units * p.RT > 0x7fffffffLL) return false;
   p.n_rt = (int)n_rt;
-  p.occ = plan_occ(D, esz, p.R);
-  long long grid = 256LL * p.occ;  // one resident set of the device's 256 CUs
+  const int occ = attn_pick(esz, D, p.R, [&](auto t, auto d, auto r) {
+    typedef decltype(t) T;
+    return p.wide ? wide_occ<T, decltype(d)::value, decltype(r)::value>() : attn_occ<T, decltype(d)::value, decltype(r)::value>();
+  });
+  long long grid = 256LL * occ;  // one resident set of the device's 256 CUs
   const long long need = (p.units * most + 3) / 4;
   if (need < grid) grid = need;
   p.grid = (unsigned)((grid + LANES - 1) / LANES * LANES);
@@ -750,13 +1009,6 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
   p.desc = o; o = align256(o + (size_t)p.units * 16);
   p.total = o;
   return true;
-}
-
-template <typename T, int D, int R>
-void attn_go(sv_host::Launcher &L, AttnArgs &a, const AttnPlan &p) {
-  void *args[] = {&a};
-  L.go((const void *)&k_attn<T, D, R>, p.grid, args);
-  L.go((const void *)&k_attn_join<T, D, R>, (unsigned)(p.units * (p.RT / NW)), args);
 }
 
 sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_pages, const void *v_pages, sv_dtype dt,
@@ -805,15 +1057,10 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   a.part_ml = (float2 *)(base + p.part_ml);
   a.desc = (uint4 *)(base + p.desc);
   sv_host::Launcher L{(hipStream_t)stream, ev, nev};
-  if (esz == 2) {
-    if (D == 64) p.R == 1 ? attn_go<uint16_t, 64, 1>(L, a, p) : p.R == 2 ? attn_go<uint16_t, 64, 2>(L, a, p) : attn_go<uint16_t, 64, 4>(L, a, p);
-    else if (D == 128) p.R == 1 ? attn_go<uint16_t, 128, 1>(L, a, p) : p.R == 2 ? attn_go<uint16_t, 128, 2>(L, a, p) : attn_go<uint16_t, 128, 4>(L, a, p);
-    else p.R == 1 ? attn_go<uint16_t, 256, 1>(L, a, p) : attn_go<uint16_t, 256, 2>(L, a, p);
-  } else {
-    if (D == 64) p.R == 1 ? attn_go<float, 64, 1>(L, a, p) : p.R == 2 ? attn_go<float, 64, 2>(L, a, p) : attn_go<float, 64, 4>(L, a, p);
-    else if (D == 128) p.R == 1 ? attn_go<float, 128, 1>(L, a, p) : attn_go<float, 128, 2>(L, a, p);
-    else attn_go<float, 256, 1>(L, a, p);
-  }
+  attn_pick(esz, D, p.R, [&](auto t, auto d, auto r) {
+    attn_go<decltype(t), decltype(d)::value, decltype(r)::value>(L, a, p);
+    return 0;
+  });
   if (nl) *nl = L.n;
   return L.e == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
 }
@@ -854,6 +1101,12 @@ sv_status spec_paged_attention_timed(const void *q, int64_t q_stride_b, int64_t 
                   stream, events, n_events, n_launched);
 }
 
-const char *sv_attention_launch_plan(void) { return "k_attn;k_attn_join"; }
+const char *sv_attention_launch_plan(int32_t N, int32_t Hq, int32_t Hkv, int32_t D, sv_dtype dtype) {
+  AttnPlan p;
+  if ((dtype != SV_F32 && dtype != SV_BF16) || !attn_shape_ok(1, N, Hq, Hkv, D, 16, 1) ||
+      !attn_plan(1, N, Hq, Hkv, D, 16, 1, dtype == SV_BF16 ? 2 : 4, p))
+    return "";
+  return p.wide ? "k_attn_wide;k_attn_join" : "k_attn;k_attn_join";
+}
 
 }  // extern "C"

@@ -48,7 +48,9 @@ def test_attention_workspace_and_plan(lib):
     large = sv.sv_attention_workspace_bytes(64, 32, 32, 8, 128, 64, 1000, sv.SV_BF16)
     assert 256 < small < large and small % 256 == 0 and large % 256 == 0
     assert sv.sv_attention_workspace_bytes(64, 32, 32, 8, 100, 64, 1000, sv.SV_BF16) == 256  # a call that is refused
-    assert sv.sv_attention_launch_plan() == ["k_attn", "k_attn_join"]
+    assert sv.sv_attention_launch_plan(1, 32, 8, 128, sv.SV_BF16) == ["k_attn", "k_attn_join"]
+    assert sv.sv_attention_launch_plan(32, 32, 8, 128, sv.SV_BF16) == ["k_attn_wide", "k_attn_join"]
+    assert sv.sv_attention_launch_plan(1, 32, 8, 96, sv.SV_BF16) == []
 
 
 def append(lib, **kw):
