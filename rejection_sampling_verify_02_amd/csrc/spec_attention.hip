@@ -136,32 +136,38 @@ SVD unsigned anc32(const unsigned *w, int words, int j0) {
 template <typename T>
 struct Mma;
 
-// bf16: a 16-byte unit is 8 elements, one operand of a 16x16x32 instruction.  Score tile t2
-// (0, 1) holds slots 8 (m / 4) + 4 t2 + m % 4, m its row: lane group g then has slots 8 g ..
-// 8 g + 7 in the order of a value unit.
+// Score tile t2 (0, 1) of a tile holds its slots 16 t2 + m, m the row: 16 lanes read 256 bytes
+// of keys together (in pieces of 64 a tile took a fifth longer).  Lane group g then has the
+// scores of slots 16 t2 + 4 g + i, i < 4.
+
+// bf16: a 16-byte unit is 8 elements, one operand of a 16x16x32 instruction.
 template <>
 struct Mma<uint16_t> {
   static constexpr int E = 8, VT = 1;  // elements a unit; value units a lane needs per 16 d
-  SVD static int key_slot(int t2, int m) { return 8 * (m >> 2) + 4 * t2 + (m & 3); }
-  SVD static int key_place(int slot) { return ((slot >> 2) & 1) * 16 + (slot >> 3) * 4 + (slot & 3); }  // 16 t2 + m of it
   SVD static int val_slot(int, int g) { return 8 * g; }           // first slot of the lane's unit
-  SVD static unsigned lane_bits(unsigned x, int g) { return (x >> (8 * g)) & 0xffu; }  // a tile's bits to score order
   SVD static f32x4 qk(u32x4 k, u32x4 q, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q), c, 0, 0, 0);
   }
   struct P {
     bf16x8 w;
   };
-  // The weights are rounded to bf16 (at most 2^-9 relative each, as the inputs themselves
-  // are); their sum is taken in f32 before the rounding.
+  // The weights are rounded to bf16 (by at most 2^-8 relative each, as the inputs themselves
+  // were); their sum is taken in f32 before the rounding.  A lane of the second product wants
+  // slots 8 g .. 8 g + 7, a value unit: with the two score tiles' pairs of weights by lane group
+  // as a0 a1 a2 a3 and b0 b1 b2 b3, the swaps make a0 a2 b0 b2 and a1 a3 b1 b3 of them.
   SVD static P weights(const f32x4 (&s)[2]) {
-    P p;
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p.w[i] = (__bf16)s[0][i];
-      p.w[4 + i] = (__bf16)s[1][i];
+    for (int j = 0; j < 2; ++j) {
+      const unsigned x = __builtin_bit_cast(unsigned, bf16x2{(__bf16)s[0][2 * j], (__bf16)s[0][2 * j + 1]});
+      const unsigned y = __builtin_bit_cast(unsigned, bf16x2{(__bf16)s[1][2 * j], (__bf16)s[1][2 * j + 1]});
+      const auto h = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+      const auto q = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+      w[j] = q[0];
+      w[2 + j] = q[1];
     }
-    return p;
+    return P{__builtin_bit_cast(bf16x8, w)};
   }
   SVD static f32x4 pv(const u32x4 (&v)[1], const P &p, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v[0]), p.w, c, 0, 0, 0);
@@ -201,15 +207,12 @@ struct Mma<uint16_t> {
 };
 
 // f32: a unit is 4 elements, one element each for four 16x16x4 instructions (instruction j
-// of a step contracts over element j of every lane group's unit).  Score tile t2 holds slots
-// 16 t2 + m; the value unit of lane group g for it is slots 16 t2 + 4 g .. + 3.
+// of a step contracts over element j of every lane group's unit); the lane's value units are
+// slots 16 t2 + 4 g .. + 3, as its scores are.
 template <>
 struct Mma<float> {
   static constexpr int E = 4, VT = 2;
-  SVD static int key_slot(int t2, int m) { return 16 * t2 + m; }
-  SVD static int key_place(int slot) { return slot; }
   SVD static int val_slot(int t2, int g) { return 16 * t2 + 4 * g; }
-  SVD static unsigned lane_bits(unsigned x, int g) { return ((x >> (4 * g)) & 0xfu) | (((x >> (16 + 4 * g)) & 0xfu) << 4); }
   SVD static f32x4 qk(u32x4 k, u32x4 q, f32x4 c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -496,7 +499,8 @@ struct Rows {
   }
   template <int RT>
   SVD unsigned view(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int t0, int r, int g) const {
-    return M::lane_bits(sg.sees(a, t0, dep[r], &s.anc[(node[r] - sg.sp.i0) * sg.words]), g);
+    const unsigned see = sg.sees(a, t0, dep[r], &s.anc[(node[r] - sg.sp.i0) * sg.words]);
+    return ((see >> (4 * g)) & 0xfu) | (((see >> (16 + 4 * g)) & 0xfu) << 4);  // bit 4 t2 + i
   }
   template <int RT>
   SVD void mask(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int t0, int g, f32x4 (&sc)[R][2]) const {
@@ -588,10 +592,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
       auto load_k = [&](int t0, int pa, int pb, u32x4 (&k)[2][KS]) {
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
-          const int sl = M::key_slot(t2, m);
+          const int sl = 16 * t2 + m;
           const char *p = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)((t0 + sl) & (page - 1)) + (unsigned)(g * page)) * 16u;
 #pragma unroll
-          for (int k4 = 0; k4 < KS; ++k4) k[t2][k4] = *reinterpret_cast<const u32x4 *>(p + (size_t)k4 * (4 * 16) * page);
+          for (int k4 = 0; k4 < KS; ++k4) k[t2][k4] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + (size_t)k4 * (4 * 16) * page));
         }
       };
       auto load_v = [&](int t0, int pa, int pb, u32x4 (&v)[DT][M::VT]) {
@@ -600,7 +604,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
           const int sl = M::val_slot(t2, g);
           const char *p = vh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)(((t0 + sl) & (page - 1)) / E) * D + m) * 16u;
 #pragma unroll
-          for (int d = 0; d < DT; ++d) v[d][t2] = *reinterpret_cast<const u32x4 *>(p + d * 256);
+          for (int d = 0; d < DT; ++d) v[d][t2] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + d * 256));
         }
       };
       auto cut_v = [&](int t0, u32x4 (&v)[DT][M::VT]) {  // slots behind the sequence hold anything
@@ -620,10 +624,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
       rows.load(a, sg, s, sg.rt * RT, m, g);
       bool odd_any = false;
       for (; l < sg.l1; l += NW) {
-        const int t0 = sg.tile(l);
-        const bool more = l + NW < sg.l1;
-        int na = 0, nb = 0;
-        if (more) sg.pages(a, sg.tile(l + NW), na, nb);
+        // The next tile's keys are loaded whether there is one or not (the last tile's again
+        // then), so that the waits below count loads and do not drain them.
+        const int t0 = sg.tile(l), tn = sg.tile(l + NW < sg.l1 ? l + NW : l);
+        int na, nb;
+        sg.pages(a, tn, na, nb);
         load_v(t0, pa, pb, vf);
         f32x4 sc[R][2];
 #pragma unroll
@@ -636,7 +641,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
             for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(kf[t2][k4], rows.q[r][k4], sc[r][t2]);
         pa = na;
         pb = nb;
-        if (more) load_k(sg.tile(l + NW), pa, pb, kf);
+        load_k(tn, pa, pb, kf);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -763,7 +768,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
           const int x = tid + j * NT;
-          s_k[buf][x / TILE * TILE + M::key_place(x % TILE)] = k[j];
+          s_k[buf][x] = k[j];
         }
       };
       auto cut_v = [&](int t0, u32x4 (&v)[PT]) {  // slots behind the sequence hold anything
