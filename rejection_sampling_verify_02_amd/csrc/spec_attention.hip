@@ -39,7 +39,9 @@ struct AttnArgs {
   long long q_sb, q_sn;  // bytes
   const int32_t *page_table, *cache_len, *n_new, *parent;
   int B, N, Hq, Hkv, group, page_shift, P, W;
-  float c2;  // scale * log2 e: scores are kept as powers of two
+  float c2;        // |scale| log2 e: weights are powers of two
+  unsigned flip;   // the sign bits of q, for a negative scale
+  float slack;     // 8 / c2: see Rows::soften
   int window, sinks;
   char *out;
   int32_t *row_status;
@@ -300,20 +302,38 @@ struct Segment {
   }
 };
 
-// LDS of either kernel: the tree, and what the prologue needs.
-template <int RT>
+// LDS of either kernel besides its tiles: the tree, sized by the call (books_bytes), and what
+// the prologue needs.
 struct SharedBooks {
-  int par[SV_CACHE_MAX_NEW];
-  uint16_t dep[RT];                          // depths of the row tile's nodes
-  unsigned anc[RT * (SV_CACHE_MAX_NEW / 32)];  // the nodes each of them sees
-  unsigned w[NW], at[2];
-  int bad;
+  uint16_t *par;   // [N] parents (node 0's is not kept)
+  uint16_t *dep;   // [nodes of a row tile] their depths
+  unsigned *anc;   // [nodes of a row tile][words] the nodes each of them sees
+  unsigned *w, *at;  // [NW], [2]
+  int *bad;
 };
+SV_HD int tile_nodes(int RT, int N, int group) {
+  const int n = (RT - 1) / group + 2;  // a tile may begin and end inside a node's heads
+  return n < N ? n : N;
+}
+SV_HD unsigned books_bytes(int RT, int N, int group, bool tree) {
+  const unsigned n = tree ? (unsigned)tile_nodes(RT, N, group) : 0u;
+  return (NW + 4) * 4 + n * ((N + 31) / 32) * 4 + ((n + (tree ? (unsigned)N : 0u) + 1) / 2) * 4;
+}
+SVD SharedBooks books_at(unsigned *p, int RT, int N, int group) {
+  const int n = tile_nodes(RT, N, group);
+  SharedBooks s;
+  s.w = p;
+  s.at = p + NW;
+  s.bad = reinterpret_cast<int *>(p + NW + 2);
+  s.anc = p + NW + 4;
+  s.dep = reinterpret_cast<uint16_t *>(s.anc + n * ((N + 31) / 32));
+  s.par = s.dep + n;
+  return s;
+}
 
 // The code of a sequence: the same test in every workgroup that streams a part of it, so that
 // all its rows agree.
-template <int RT>
-SVD int seq_code(const AttnArgs &a, const Seq &sq, int b, SharedBooks<RT> &s) {
+SVD int seq_code(const AttnArgs &a, const Seq &sq, int b, const SharedBooks &s) {
   const int tid = threadIdx.x, page = 1 << a.page_shift;
   const int32_t *table = a.page_table + (size_t)b * a.W;
   if (!sq.ok) return SV_ROW_BAD_LENGTH;
@@ -322,7 +342,7 @@ SVD int seq_code(const AttnArgs &a, const Seq &sq, int b, SharedBooks<RT> &s) {
   if (a.parent)
     for (int i = tid; i < sq.m; i += NT) {
       const int p = a.parent[(size_t)b * a.N + i];
-      s.par[i] = p;
+      s.par[i] = (uint16_t)p;
       if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 2;
     }
   // pages of the sinks, then from the window on
@@ -332,27 +352,27 @@ SVD int seq_code(const AttnArgs &a, const Seq &sq, int b, SharedBooks<RT> &s) {
   const int np = ((sq.len + sq.m + page - 1) >> a.page_shift) - p0 + ps;
   for (int i = tid; i < np; i += NT)
     if ((unsigned)table[i < ps ? i : i - ps + p0] >= (unsigned)a.P) bad |= 1;
-  if (tid == 0) s.bad = 0;
+  if (tid == 0) *s.bad = 0;
   __syncthreads();
-  if (bad) atomicOr(&s.bad, bad);
+  if (bad) atomicOr(s.bad, bad);
   __syncthreads();
-  const int x = s.bad;
+  const int x = *s.bad;
   return (x & 2) ? SV_ROW_BAD_TREE : (x & 1) ? SV_ROW_BAD_PAGE : 0;
 }
 
 // Depths of the row tile's nodes and the nodes each sees, window and sinks included.
-template <int RT>
-SVD void tree_books(const AttnArgs &a, const Segment &g, SharedBooks<RT> &s) {
+SVD void tree_books(const AttnArgs &a, const Segment &g, const SharedBooks &s) {
   const int tid = threadIdx.x, i0 = g.sp.i0, n = g.sp.i1 - i0 + 1;
   for (int i = tid; i < n * g.words; i += NT) s.anc[i] = 0u;
   __syncthreads();
   for (int i = tid; i < n; i += NT) {
     int dep = 0;
-    for (int j = s.par[i0 + i]; j >= 0; j = s.par[j]) ++dep;
+    for (int j = i0 + i; j > 0; j = s.par[j]) ++dep;
     s.dep[i] = (uint16_t)dep;
-    int d = dep;  // of node j
-    for (int j = i0 + i; j >= 0; j = s.par[j], --d)
+    for (int j = i0 + i, d = dep; d >= 0; --d) {  // d: the depth of j
       if (a.window <= 0 || dep - d < a.window || g.sq.len + d < a.sinks) s.anc[i * g.words + (j >> 5)] |= 1u << (j & 31);
+      if (d > 0) j = s.par[j];
+    }
   }
   __syncthreads();
 }
@@ -362,7 +382,7 @@ SVD void tree_books(const AttnArgs &a, const Segment &g, SharedBooks<RT> &s) {
 // emit(row, c4, sum, max, total) for every row of the tile and four elements d = 4 c4 ..;
 // emit is passed in so that the writing is one piece of code.
 template <typename T, int D, int RT, typename Stream>
-SVD void attn_share(const AttnArgs &a, SharedBooks<RT> &s, Stream stream) {
+SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Stream stream) {
   typedef Mma<T> M;
   constexpr int ESZ = (int)sizeof(T);
   const int tid = threadIdx.x;
@@ -430,7 +450,7 @@ SVD void attn_share(const AttnArgs &a, SharedBooks<RT> &s, Stream stream) {
 
     __syncthreads();  // the previous segment is done with the LDS
     if (code_b != g.b) {
-      code = seq_code<RT>(a, g.sq, g.b, s);
+      code = seq_code(a, g.sq, g.b, s);
       code_b = g.b;
     }
     if (tid == 0 && g.h == 0 && g.rt == 0 && g.l0 == 0) a.row_status[g.b] = code;
@@ -439,7 +459,7 @@ SVD void attn_share(const AttnArgs &a, SharedBooks<RT> &s, Stream stream) {
       a.desc[(g.b * a.Hkv + g.h) * a.n_rt + g.rt] =
           make_uint4(w, last - w + 1, (code ? 0x80000000u : 0u) | (unsigned)(g.sq.ok ? g.sq.m : 0), 0u);
     }
-    if (code == 0 && g.par && g.masks && g.sp.i0 <= g.sp.i1) tree_books<RT>(a, g, s);
+    if (code == 0 && g.par && g.masks && g.sp.i0 <= g.sp.i1) tree_books(a, g, s);
 
     const unsigned slot = 2 * w + (g.l0 == 0 ? 1u : 0u);
     auto emit = [&](int row, int c4, f32x4 acc, float mt, float ls) {
@@ -467,22 +487,22 @@ struct Rows {
   typedef Mma<T> M;
   static constexpr int KS = D / (4 * M::E), DT = D / 16;
   f32x4 o[R][DT];
-  float rm[R], rl[R];
+  float rm[R], rl[R];   // the largest score nm stands for, the sum of weights
+  float nm[R], lim[R];  // see soften
   u32x4 q[R][KS];
   int node[R], dep[R];  // clamped to the segment's nodes
 
   SVD void clear() {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      rm[r] = -INFINITY;
-      rl[r] = 0.0f;
+      rm[r] = lim[r] = -INFINITY;
+      rl[r] = nm[r] = 0.0f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[r][d] = f32x4{0, 0, 0, 0};
     }
   }
   // Rows row0 + 16 r + m of the unit; rows that are no new token's get zeros.
-  template <int RT>
-  SVD void load(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int row0, int m, int g) {
+  SVD void load(const AttnArgs &a, const Segment &sg, const SharedBooks &s, int row0, int m, int g) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = row0 + 16 * r + m, i = row / a.group, hh = row - i * a.group;
@@ -493,17 +513,22 @@ struct Rows {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const u32x4 x = *reinterpret_cast<const u32x4 *>(qp + (4 * k + g) * 16);
-        q[r][k] = in ? x : u32x4{0, 0, 0, 0};
+        q[r][k] = in ? x ^ a.flip : u32x4{0, 0, 0, 0};
       }
     }
   }
-  template <int RT>
-  SVD unsigned view(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int t0, int r, int g) const {
+  // The query rows are waited for here, not in a loop that counts what is on its way.
+  SVD void arrived() {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(q[r][k]));
+  }
+  SVD unsigned view(const AttnArgs &a, const Segment &sg, const SharedBooks &s, int t0, int r, int g) const {
     const unsigned see = sg.sees(a, t0, dep[r], &s.anc[(node[r] - sg.sp.i0) * sg.words]);
     return ((see >> (4 * g)) & 0xfu) | (((see >> (16 + 4 * g)) & 0xfu) << 4);  // bit 4 t2 + i
   }
-  template <int RT>
-  SVD void mask(const AttnArgs &a, const Segment &sg, const SharedBooks<RT> &s, int t0, int g, f32x4 (&sc)[R][2]) const {
+  SVD void mask(const AttnArgs &a, const Segment &sg, const SharedBooks &s, int t0, int g, f32x4 (&sc)[R][2]) const {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const unsigned vis = view(a, sg, s, t0, r, g);
@@ -513,28 +538,35 @@ struct Rows {
         for (int i = 0; i < 4; ++i) sc[r][t2][i] = ((vis >> (4 * t2 + i)) & 1u) ? sc[r][t2][i] : -INFINITY;
     }
   }
-  // Scores (as powers of two) to weights, against the running maximum.
-  SVD typename M::P soften(int r, f32x4 (&sc)[2]) {
-    float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])), fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-    mx = fmaxf(rm[r], col_max(mx));
-    if (__any(mx > rm[r])) {  // a new maximum in some row: all sums so far to the new scale
-      const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(rm[r] - mx);
+  // Scores to weights 2^(c2 score - nm).  nm follows the row's maximum loosely: it moves only
+  // when a score passes it by a factor of 2^8, so that after the first tiles no sum has to be
+  // rescaled and the four lanes of a row need not compare notes (weights up to 2^8 keep their
+  // relative rounding, and the quotient of the sums is the same).
+  SVD typename M::P soften(const AttnArgs &a, int r, f32x4 (&sc)[2]) {
+    const float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])), fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+    if (__any(top > lim[r])) {
+      const float mx = fmaxf(rm[r], col_max(top));
+      const float nm2 = (mx == -INFINITY) ? 0.0f : mx * a.c2;
+      const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(nm[r] - nm2);
       rl[r] *= f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
       rm[r] = mx;
+      nm[r] = nm2;
+      lim[r] = mx + a.slack;
     }
-    const float mu = (mx == -INFINITY) ? 0.0f : mx;
     float sum = 0.0f;
 #pragma unroll
     for (int t2 = 0; t2 < 2; ++t2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[t2][i] = fast_exp2(sc[t2][i] - mu);
+      for (int i = 0; i < 4; ++i) sc[t2][i] = fast_exp2(fmaf(sc[t2][i], a.c2, -nm[r]));
       sum += (sc[t2][0] + sc[t2][1]) + (sc[t2][2] + sc[t2][3]);
     }
     rl[r] += sum;
     return M::weights(sc);
   }
+  // The exponent that a row's sums are relative to (-inf: nothing seen so far).
+  SVD float scale(int r) const { return (rm[r] == -INFINITY) ? -INFINITY : nm[r]; }
   // What values that are not finite are to each row that sees them (they are left out of the
   // products, where a weight of zero would not keep them from the other rows): flags of the
   // values times flags of the view, both 0 or 1, count the sightings.
@@ -573,7 +605,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
   constexpr int KS = D / (4 * E);  // key units a lane holds of a 16-slot score tile
   constexpr int DT = D / 16;       // 16-wide tiles of the output's d
   constexpr int PADD = D + 4;      // rows of the LDS join tile, padded against bank conflicts
-  __shared__ SharedBooks<RT> s;
+  extern __shared__ unsigned s_books[];
+  const SharedBooks s = books_at(s_books, RT, a.N, a.group);
   __shared__ float s_o[NW * RT * PADD];
   __shared__ float s_m[NW * RT], s_l[NW * RT];
 
@@ -642,10 +675,6 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
         pa = na;
         pb = nb;
         load_k(tn, pa, pb, kf);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = sc[r][t2] * a.c2;
         if (!sg.plain(a, t0)) {
           rows.mask(a, sg, s, t0, g, sc);
           cut_v(t0, vf);
@@ -664,7 +693,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
         }
         typename M::P pw[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) pw[r] = rows.soften(r, sc[r]);
+        for (int r = 0; r < R; ++r) pw[r] = rows.soften(a, r, sc[r]);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -691,7 +720,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
     for (int r = 0; r < R; ++r) {
       const float l_row = col_sum(rows.rl[r]);
       if (g == 0) {
-        s_m[wid * RT + 16 * r + m] = rows.rm[r];
+        s_m[wid * RT + 16 * r + m] = rows.scale(r);
         s_l[wid * RT + 16 * r + m] = l_row;
       }
 #pragma unroll
@@ -722,20 +751,43 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
 // ---------------------------------------------------------------- many rows
 
 // A tile's keys and values lie in LDS in the order in which the lanes read them, 16 lanes
-// 256 bytes: keys [unit of d][score tile, row of it], values [unit of slots][d].  While the
-// waves work on one buffer the next tile's units are in flight in registers; they go to the
-// other buffer when the work is done: one barrier a tile.
+// 256 bytes: keys [unit of d][slot], values [unit of slots][d].  They come there straight from
+// memory, without registers in between, into a ring of buffers: while the waves work on one
+// tile the next ones are on their way, and one barrier a tile both hands a tile over and frees
+// the buffer before it.  (With the next tile alone in flight, in registers, 16 trees of 32
+// nodes took 110 us.)  The buffers are variables of their own and the loop is unrolled over
+// them, so that the compiler sees that a tile's reads do not wait for later tiles.
+typedef __attribute__((address_space(3))) void *LdsPtr;
+typedef const __attribute__((address_space(1))) void *GlobalPtr;
+
 template <typename T, int D, int R>
 constexpr int wide_occ() { return (R * D * (int)sizeof(T) <= 512) ? 2 : 1; }
+// Buffers of the ring: what two resident workgroups' LDS takes.
+template <typename T, int D>
+constexpr int wide_ring() { return D * (int)sizeof(T) <= 256 ? 4 : 2; }
+
+// Waits until at most n of the wave's vector memory operations and none of its LDS operations
+// are on their way, then for the other waves; no memory access moves across.
+template <int n>
+SVD void hand_over() {
+  static_assert(n < 64, "six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x70);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 template <typename T, int D, int R>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, D, R>()))) void k_attn_wide(const AttnArgs a) {
   typedef Mma<T> M;
   constexpr int RT = 16 * R * NW, E = M::E, ESZ = (int)sizeof(T);
   constexpr int KS = D / (4 * E), DT = D / 16;
-  constexpr int UNITS = TILE * D / E, PT = UNITS / NT;  // 16-byte units of a tile's keys (or values), and a thread's
-  __shared__ SharedBooks<RT> s;
-  __shared__ u32x4 s_k[2][UNITS], s_v[2][UNITS];
+  constexpr int UNITS = TILE * D / E;                 // 16-byte units of a tile's keys, and of its values
+  constexpr int PW = UNITS / NT;                      // of each, 64-unit pieces that a wave fetches
+  constexpr int NB = wide_ring<T, D>();
+  extern __shared__ unsigned s_books[];
+  const SharedBooks s = books_at(s_books, RT, a.N, a.group);
+  __shared__ u32x4 s_t0[2 * UNITS], s_t1[2 * UNITS], s_t2[NB > 2 ? 2 * UNITS : 1], s_t3[NB > 2 ? 2 * UNITS : 1];
   __shared__ int s_odd;
 
   const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -750,66 +802,47 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     if (sg.sp.i0 <= sg.sp.i1 && code == 0) {
       const char *kh = a.k_pages + (size_t)sg.h * head_bytes;
       const char *vh = a.v_pages + (size_t)sg.h * head_bytes;
-      auto load_k = [&](int t0, int pa, int pb, u32x4 (&k)[PT]) {
-#pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          const int x = tid + j * NT, u = x / TILE, sl = x % TILE;
-          k[j] = *reinterpret_cast<const u32x4 *>(kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + (size_t)(u * page + ((t0 + sl) & (page - 1))) * 16);
-        }
-      };
-      auto load_v = [&](int t0, int pa, int pb, u32x4 (&v)[PT]) {
-#pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          const int x = tid + j * NT, sl = x / D * E, d = x % D;
-          v[j] = *reinterpret_cast<const u32x4 *>(vh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + (size_t)(((t0 + sl) & (page - 1)) / E * D + d) * 16);
-        }
-      };
-      auto put_k = [&](int buf, const u32x4 (&k)[PT]) {
-#pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          const int x = tid + j * NT;
-          s_k[buf][x] = k[j];
-        }
-      };
-      auto cut_v = [&](int t0, u32x4 (&v)[PT]) {  // slots behind the sequence hold anything
-        if (t0 + TILE > sg.end())
-#pragma unroll
-          for (int j = 0; j < PT; ++j) v[j] = M::cut(v[j], sg.end() - t0 - (tid + j * NT) / D * E);
-      };
-      auto put_v = [&](int t0, int buf, u32x4 (&v)[PT]) {
-        if (!sg.plain(a, t0)) {
-          cut_v(t0, v);
-          bool odd = false;
-#pragma unroll
-          for (int j = 0; j < PT; ++j) odd |= M::non_finite(v[j]);
-          if (odd) {
-            s_odd = 1;
-#pragma unroll
-            for (int j = 0; j < PT; ++j) v[j] = M::finite(v[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < PT; ++j) s_v[buf][tid + j * NT] = v[j];
-      };
-
-      u32x4 kf[PT], vf[PT];
-      int pa, pb, l = sg.l0, buf = 0;
-      sg.pages(a, sg.tile(l), pa, pb);
-      load_k(sg.tile(l), pa, pb, kf);
-      load_v(sg.tile(l), pa, pb, vf);
-      if (tid == 0) s_odd = 0;
       rows.load(a, sg, s, sg.rt * RT + wid * 16 * R, m, g);
-      __syncthreads();  // s_odd, before the first put_v may set it
-      put_k(0, kf);
-      put_v(sg.tile(l), 0, vf);
-      if (l + 1 < sg.l1) {
-        sg.pages(a, sg.tile(l + 1), pa, pb);
-        load_k(sg.tile(l + 1), pa, pb, kf);
-        load_v(sg.tile(l + 1), pa, pb, vf);
-      }
-      __syncthreads();
-      for (; l < sg.l1; ++l, buf ^= 1) {
+      if (tid == 0) s_odd = 0;
+
+      auto fetch = [&](int l, u32x4 *buf) {
         const int t0 = sg.tile(l);
+        int pa, pb;
+        sg.pages(a, t0, pa, pb);
+        const int sl = lane % TILE;
+        const char *kp = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes +
+                         (size_t)((2 * wid + lane / TILE) * page + ((t0 + sl) & (page - 1))) * 16;
+#pragma unroll
+        for (int j = 0; j < PW; ++j)
+          __builtin_amdgcn_global_load_lds((GlobalPtr)(kp + (size_t)j * (2 * NW * 16) * page), (LdsPtr)(buf + (j * NW + wid) * WAVE), 16, 0, 2);
+#pragma unroll
+        for (int j = 0; j < PW; ++j) {
+          const int x = (j * NW + wid) * WAVE, vs = x / D * E;  // D units a value unit's slots: a piece lies in one of them
+          const char *vp = vh + (unsigned long long)(unsigned)(vs < 16 ? pa : pb) * page_bytes +
+                           (size_t)(((t0 + vs) & (page - 1)) / E * D + x % D + lane) * 16;
+          __builtin_amdgcn_global_load_lds((GlobalPtr)vp, (LdsPtr)(buf + UNITS + x), 16, 0, 2);
+        }
+      };
+      // Slots behind the sequence hold anything, and values that are not finite are left out of
+      // the products where not every row sees them.
+      auto clean = [&](int t0, u32x4 *vb) {
+        bool odd = false;
+#pragma unroll
+        for (int j = 0; j < PW; ++j) {
+          u32x4 v = M::cut(vb[tid + j * NT], sg.end() - t0 - (tid + j * NT) / D * E);
+          odd |= M::non_finite(v);
+          vb[tid + j * NT] = M::finite(v);
+        }
+        if (odd) s_odd = 1;
+        __syncthreads();
+      };
+      auto work = [&](int l, u32x4 *buf, u32x4 *last) {
+        const int t0 = sg.tile(l), left = sg.l1 - 1 - l;
+        if (NB > 2 && left >= 2) hand_over<(NB - 2) * 2 * PW>();
+        else if (NB > 2 && left == 1) hand_over<2 * PW>();
+        else hand_over<0>();
+        const bool plain = sg.plain(a, t0);
+        if (!plain) clean(t0, buf + UNITS);
         f32x4 sc[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = f32x4{0, 0, 0, 0};
@@ -817,47 +850,49 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
         for (int k4 = 0; k4 < KS; ++k4)
 #pragma unroll
           for (int t2 = 0; t2 < 2; ++t2) {
-            const u32x4 k = s_k[buf][(4 * k4 + g) * TILE + 16 * t2 + m];
+            const u32x4 k = buf[(4 * k4 + g) * TILE + 16 * t2 + m];
 #pragma unroll
             for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(k, rows.q[r][k4], sc[r][t2]);
           }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = sc[r][t2] * a.c2;
-        if (!sg.plain(a, t0)) rows.mask(a, sg, s, t0, g, sc);
+        if (left >= NB - 1) fetch(l + NB - 1, last);
+        if (!plain) rows.mask(a, sg, s, t0, g, sc);
         typename M::P pw[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) pw[r] = rows.soften(r, sc[r]);
+        for (int r = 0; r < R; ++r) pw[r] = rows.soften(a, r, sc[r]);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           u32x4 v[M::VT];
 #pragma unroll
-          for (int t2 = 0; t2 < M::VT; ++t2) v[t2] = s_v[buf][M::val_slot(t2, g) / E * D + 16 * d + m];
+          for (int t2 = 0; t2 < M::VT; ++t2) v[t2] = buf[UNITS + M::val_slot(t2, g) / E * D + 16 * d + m];
 #pragma unroll
           for (int r = 0; r < R; ++r) rows.o[r][d] = M::pv(v, pw[r], rows.o[r][d]);
         }
-        if (l + 1 < sg.l1) {
-          put_k(buf ^ 1, kf);
-          put_v(sg.tile(l + 1), buf ^ 1, vf);
-          if (l + 2 < sg.l1) {
-            sg.pages(a, sg.tile(l + 2), pa, pb);
-            load_k(sg.tile(l + 2), pa, pb, kf);
-            load_v(sg.tile(l + 2), pa, pb, vf);
-          }
-        }
-        __syncthreads();
+      };
+
+      fetch(sg.l0, s_t0);
+      if (NB > 2) {
+        if (sg.l0 + 1 < sg.l1) fetch(sg.l0 + 1, s_t1);
+        if (sg.l0 + 2 < sg.l1) fetch(sg.l0 + 2, s_t2);
       }
-      if (s_odd)  // the same for the whole workgroup: set before the loop's last barrier
-        for (l = sg.l0; l < sg.l1; ++l) {
+      rows.arrived();
+      for (int l = sg.l0; l < sg.l1; l += NB) {
+        if (NB > 2) {
+          work(l, s_t0, s_t3);
+          if (l + 1 < sg.l1) work(l + 1, s_t1, s_t0);
+          if (l + 2 < sg.l1) work(l + 2, s_t2, s_t1);
+          if (l + 3 < sg.l1) work(l + 3, s_t3, s_t2);
+        } else {
+          work(l, s_t0, s_t1);
+          if (l + 1 < sg.l1) work(l + 1, s_t1, s_t0);
+        }
+      }
+      __syncthreads();
+      if (s_odd)
+        for (int l = sg.l0; l < sg.l1; ++l) {
           const int t0 = sg.tile(l);
           if (sg.plain(a, t0)) continue;
-          sg.pages(a, t0, pa, pb);
-          load_v(t0, pa, pb, vf);
-          cut_v(t0, vf);
-#pragma unroll
-          for (int j = 0; j < PT; ++j) s_v[0][tid + j * NT] = vf[j];
-          __syncthreads();
+          fetch(l, s_t0);
+          hand_over<0>();
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const unsigned vis = rows.view(a, sg, s, t0, r, g);
@@ -865,7 +900,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
             for (int d = 0; d < DT; ++d) {
               u32x4 v[M::VT];
 #pragma unroll
-              for (int t2 = 0; t2 < M::VT; ++t2) v[t2] = s_v[0][M::val_slot(t2, g) / E * D + 16 * d + m];
+              for (int t2 = 0; t2 < M::VT; ++t2)
+                v[t2] = M::cut(s_t0[UNITS + M::val_slot(t2, g) / E * D + 16 * d + m], sg.end() - t0 - M::val_slot(t2, g));
               rows.odd_values(r, d, v, vis);
             }
           }
@@ -876,7 +912,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     for (int r = 0; r < R; ++r) {
       const float l_row = col_sum(rows.rl[r]);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) emit(wid * 16 * R + 16 * r + m, 4 * d + g, rows.o[r][d], rows.rm[r], l_row);
+      for (int d = 0; d < DT; ++d) emit(wid * 16 * R + 16 * r + m, 4 * d + g, rows.o[r][d], rows.scale(r), l_row);
     }
   });
 }
@@ -959,11 +995,14 @@ bool pow2_page(int32_t page) { return page >= 16 && page <= 256 && (page & (page
 template <typename T, int D, int R>
 void attn_go(sv_host::Launcher &L, AttnArgs &a, const AttnPlan &p) {
   void *args[] = {&a};
+  L.lds = books_bytes(p.RT, a.N, a.group, a.parent != nullptr);
   if (p.wide) {
     L.go((const void *)&k_attn_wide<T, D, R>, p.grid, args);
+    L.lds = 0;
     L.go((const void *)&k_attn_join<T, D, 16 * R * NW>, (unsigned)(p.units * (p.RT / NW)), args);
   } else if constexpr (D <= 128 || R == 1) {
     L.go((const void *)&k_attn<T, D, R>, p.grid, args);
+    L.lds = 0;
     L.go((const void *)&k_attn_join<T, D, 16 * R>, (unsigned)(p.units * (p.RT / NW)), args);
   }
 }
@@ -1051,7 +1090,10 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   a.page_shift = __builtin_ctz((unsigned)page);
   a.P = P;
   a.W = W;
-  a.c2 = (float)((double)scale * LOG2E);
+  // A scale of zero becomes one too small to matter, so that 0 times -inf need not be met.
+  a.c2 = fmaxf((float)(fabs((double)scale) * LOG2E), 1e-30f);
+  a.flip = scale < 0.0f ? (esz == 2 ? 0x80008000u : 0x80000000u) : 0u;
+  a.slack = fminf(8.0f / a.c2, 1e30f);
   a.window = window;
   a.sinks = sinks;
   a.out = static_cast<char *>(out);

@@ -820,14 +820,15 @@ struct Launcher {
   int n = 0;
   hipError_t e = hipSuccess;
   int block = sv::NT;  // threads per workgroup of the next launches
+  unsigned lds = 0;    // and their dynamic LDS bytes
   void go(const void *fn, unsigned grid, void **args) {
     if (e != hipSuccess) return;
     const dim3 blk(block);
     if (ev && 2 * n + 1 < nev)
-      e = hipExtLaunchKernel(fn, dim3(grid), blk, args, 0, st, (hipEvent_t)ev[2 * n],
+      e = hipExtLaunchKernel(fn, dim3(grid), blk, args, lds, st, (hipEvent_t)ev[2 * n],
                              (hipEvent_t)ev[2 * n + 1], 0);
     else
-      e = hipLaunchKernel(fn, dim3(grid), blk, args, 0, st);
+      e = hipLaunchKernel(fn, dim3(grid), blk, args, lds, st);
     if (e == hipSuccess) ++n;
   }
 };
