@@ -71,6 +71,7 @@ SVD Seq seq_of(const AttnArgs &a, int b) {
   s.len = a.cache_len[b];
   s.m = a.n_new ? a.n_new[b] : a.N;
   s.ok = s.len >= 0 && s.m >= 0 && s.m <= a.N && (long long)s.len + s.m <= ((long long)a.W << a.page_shift);
+  if (!s.ok) s.len = s.m = 0;
   return s;
 }
 
@@ -263,8 +264,6 @@ struct Mma<float> {
 
 // ---------------------------------------------------------------- a workgroup's share
 
-constexpr unsigned MIN_SHARE = 4;  // tiles: one for each wave of k_attn
-
 // One unit's part of a share, and what the whole workgroup knows about it.
 struct Segment {
   Seq sq;
@@ -291,6 +290,10 @@ struct Segment {
     const int ia = t0 >> a.page_shift, ib = t1 >> a.page_shift;
     pa = page_at(table, ha ? ia : ib);
     pb = (hb && ib != ia) ? page_at(table, ib) : pa;
+    // Tiles are fetched before the sequence's pages have been checked: a page of no pool is
+    // page 0 here (and the sequence's rows become NaN).
+    pa = (unsigned)pa < (unsigned)a.P ? pa : 0;
+    pb = (unsigned)pb < (unsigned)a.P ? pb : 0;
   }
   // The slots of a tile that a row sees, as bits.
   SVD unsigned sees(const AttnArgs &a, int t0, int dep, const unsigned *anc) const {
@@ -366,24 +369,51 @@ SVD void tree_books(const AttnArgs &a, const Segment &g, const SharedBooks &s) {
   for (int i = tid; i < n * g.words; i += NT) s.anc[i] = 0u;
   __syncthreads();
   for (int i = tid; i < n; i += NT) {
-    int dep = 0;
-    for (int j = i0 + i; j > 0; j = s.par[j]) ++dep;
-    s.dep[i] = (uint16_t)dep;
-    for (int j = i0 + i, d = dep; d >= 0; --d) {  // d: the depth of j
-      if (a.window <= 0 || dep - d < a.window || g.sq.len + d < a.sinks) s.anc[i * g.words + (j >> 5)] |= 1u << (j & 31);
-      if (d > 0) j = s.par[j];
+    // up from the node, then down in depth again where the window cuts ancestors off
+    unsigned *anc = s.anc + i * g.words;
+    int dep = 0, j = i0 + i;
+    for (;; j = s.par[j], ++dep) {
+      anc[j >> 5] |= 1u << (j & 31);
+      if (j == 0) break;
     }
+    s.dep[i] = (uint16_t)dep;
+    if (a.window > 0 && dep >= a.window)
+      for (int d = dep, k = i0 + i;; k = s.par[k], --d) {  // d: the depth of k
+        if (dep - d >= a.window && g.sq.len + d >= a.sinks) anc[k >> 5] &= ~(1u << (k & 31));
+        if (d == 0) break;
+      }
   }
   __syncthreads();
 }
 
-// Walks the workgroup's share, a segment at a time.  stream(segment, code) computes the rows'
-// sums over the segment's slots (nothing for code != 0 or without live rows) and calls
-// emit(row, c4, sum, max, total) for every row of the tile and four elements d = 4 c4 ..;
-// emit is passed in so that the writing is one piece of code.
-template <typename T, int D, int RT, typename Stream>
-SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Stream stream) {
-  typedef Mma<T> M;
+// Where a row of a segment goes: to the output if the segment is the whole unit, else to the
+// segment's partial tile.
+template <typename T, int D>
+struct RowSink {
+  enum { SKIP, OUT, ZERO, BAD, PART } kind;
+  char *p;
+  float inv;
+  SVD void put(int c4, f32x4 acc) const {  // elements 4 c4 .. 4 c4 + 3
+    if (kind == SKIP) return;
+    if (kind == PART) {
+      reinterpret_cast<f32x4 *>(p)[c4] = acc;
+      return;
+    }
+    f32x4 y = acc * inv;
+    if (kind == ZERO) y = f32x4{0, 0, 0, 0};
+    if (kind == BAD) y = f32x4{NAN, NAN, NAN, NAN};
+    Mma<T>::store4(p + c4 * 4 * sizeof(T), y[0], y[1], y[2], y[3]);
+  }
+};
+
+// Walks the workgroup's share, a segment at a time: begin(segment) sends for the first tiles,
+// and while they come the sequence is checked and its tree laid out; run(segment, code, sink)
+// then computes the rows' sums over the segment's slots and puts every row of the tile into
+// sink(row, exponent, sum of weights).  begin is called for every segment, also one whose rows
+// are no new tokens (its tile 0 is then some page's, and not used): what it leaves in registers
+// would have to be kept from segment to segment otherwise.
+template <typename T, int D, int RT, unsigned MIN_SHARE, typename Begin, typename Run>
+SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run run) {
   constexpr int ESZ = (int)sizeof(T);
   const int tid = threadIdx.x;
   // Consecutive shares on one XCD: the row tiles of a key head read the same keys and values
@@ -407,16 +437,16 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Stream stream) {
       s.at[1] = pos - ex;
     }
   } else {
-    unsigned run = 0;
-    for (int b0 = 0; run <= pos; b0 += NT) {
+    unsigned seen = 0;
+    for (int b0 = 0; seen <= pos; b0 += NT) {
       v = (b0 + tid < a.B) ? seq_tiles<RT>(a, b0 + tid) : 0u;
       unsigned tot;
-      ex = run + block_excl_scan(v, s.w, tot);
+      ex = seen + block_excl_scan(v, s.w, tot);
       if (pos >= ex && pos < ex + v) {
         s.at[0] = (unsigned)(b0 + tid);
         s.at[1] = pos - ex;
       }
-      run += tot;
+      seen += tot;
     }
   }
   __syncthreads();
@@ -449,6 +479,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Stream stream) {
     const bool whole = g.l0 == 0 && g.l1 == g.sp.tiles;
 
     __syncthreads();  // the previous segment is done with the LDS
+    begin(g);
     if (code_b != g.b) {
       code = seq_code(a, g.sq, g.b, s);
       code_b = g.b;
@@ -462,20 +493,22 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Stream stream) {
     if (code == 0 && g.par && g.masks && g.sp.i0 <= g.sp.i1) tree_books(a, g, s);
 
     const unsigned slot = 2 * w + (g.l0 == 0 ? 1u : 0u);
-    auto emit = [&](int row, int c4, f32x4 acc, float mt, float ls) {
+    auto sink = [&](int row, float mt, float ls) {
+      RowSink<T, D> to;
       const int rg = g.rt * RT + row, i = rg / a.group, hh = rg - i * a.group;
       if (whole) {
-        if (i >= a.N) return;
-        f32x4 y = acc * (1.0f / ls);
-        if (i >= g.sq.m) y = f32x4{0, 0, 0, 0};
-        if (code != 0) y = f32x4{NAN, NAN, NAN, NAN};
-        M::store4(a.out + ((((size_t)g.b * a.N + i) * a.Hq + g.h * a.group + hh) * D + 4 * c4) * ESZ, y[0], y[1], y[2], y[3]);
+        to.kind = i >= a.N ? to.SKIP : code != 0 ? to.BAD : i >= g.sq.m ? to.ZERO : to.OUT;
+        to.p = a.out + (((size_t)g.b * a.N + i) * a.Hq + g.h * a.group + hh) * D * ESZ;
+        to.inv = 1.0f / ls;
       } else {
-        *reinterpret_cast<f32x4 *>(&a.part_o[((size_t)slot * RT + row) * D + 4 * c4]) = acc;
-        if (c4 == 0) a.part_ml[(size_t)slot * RT + row] = make_float2(mt, ls);
+        to.kind = to.PART;
+        to.p = reinterpret_cast<char *>(a.part_o + ((size_t)slot * RT + row) * D);
+        to.inv = 1.0f;
+        a.part_ml[(size_t)slot * RT + row] = make_float2(mt, ls);  // by every lane that asks: the same
       }
+      return to;
     };
-    stream(g, code, emit);
+    run(g, code, sink);
     pos += (unsigned)(g.l1 - g.l0);
     off += (unsigned)(g.l1 - g.l0);
   }
@@ -502,13 +535,12 @@ struct Rows {
     }
   }
   // Rows row0 + 16 r + m of the unit; rows that are no new token's get zeros.
-  SVD void load(const AttnArgs &a, const Segment &sg, const SharedBooks &s, int row0, int m, int g) {
+  SVD void load(const AttnArgs &a, const Segment &sg, int row0, int m, int g) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = row0 + 16 * r + m, i = row / a.group, hh = row - i * a.group;
       const bool in = i < sg.sq.m;
       node[r] = min(i, sg.sp.i1);
-      dep[r] = (sg.par && sg.masks) ? (int)s.dep[node[r] - sg.sp.i0] : node[r];
       const char *qp = a.q + (long long)sg.b * a.q_sb + (long long)(in ? i : 0) * a.q_sn + (size_t)(sg.h * a.group + hh) * D * sizeof(T);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -516,6 +548,10 @@ struct Rows {
         q[r][k] = in ? x ^ a.flip : u32x4{0, 0, 0, 0};
       }
     }
+  }
+  SVD void depths(const Segment &sg, const SharedBooks &s) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) dep[r] = (sg.par && sg.masks) ? (int)s.dep[node[r] - sg.sp.i0] : node[r];
   }
   // The query rows are waited for here, not in a loop that counts what is on its way.
   SVD void arrived() {
@@ -616,53 +652,58 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
   const unsigned long long page_bytes = (unsigned long long)a.Hkv * page * D * ESZ;
   const unsigned head_bytes = (unsigned)page * D * ESZ;
 
-  attn_share<T, D, RT>(a, s, [&](const Segment &sg, int code, auto emit) {
-    Rows<T, D, R> rows;
-    rows.clear();
-    if (sg.sp.i0 <= sg.sp.i1 && code == 0) {
-      const char *kh = a.k_pages + (size_t)sg.h * head_bytes;
-      const char *vh = a.v_pages + (size_t)sg.h * head_bytes;
-      auto load_k = [&](int t0, int pa, int pb, u32x4 (&k)[2][KS]) {
+  Rows<T, D, R> rows;
+  u32x4 kf[2][KS], vf[DT][M::VT];
+  // `last`: there is no such tile; one unit stands in for all of them, so that the loop's waits
+  // can count loads instead of draining them.
+  auto load_k = [&](const Segment &sg, int t0, int pa, int pb, bool last) {
+    const char *kh = a.k_pages + (size_t)sg.h * head_bytes;
+    const size_t step = last ? 0 : (size_t)(4 * 16) * page;
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {
-          const int sl = 16 * t2 + m;
-          const char *p = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)((t0 + sl) & (page - 1)) + (unsigned)(g * page)) * 16u;
+    for (int t2 = 0; t2 < 2; ++t2) {
+      const int sl = 16 * t2 + m;
+      const char *p = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)((t0 + sl) & (page - 1)) + (unsigned)(g * page)) * 16u;
 #pragma unroll
-          for (int k4 = 0; k4 < KS; ++k4) k[t2][k4] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + (size_t)k4 * (4 * 16) * page));
-        }
-      };
-      auto load_v = [&](int t0, int pa, int pb, u32x4 (&v)[DT][M::VT]) {
+      for (int k4 = 0; k4 < KS; ++k4) kf[t2][k4] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + k4 * step));
+    }
+  };
+  auto load_v = [&](const Segment &sg, int t0, int pa, int pb) {
+    const char *vh = a.v_pages + (size_t)sg.h * head_bytes;
 #pragma unroll
-        for (int t2 = 0; t2 < M::VT; ++t2) {
-          const int sl = M::val_slot(t2, g);
-          const char *p = vh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)(((t0 + sl) & (page - 1)) / E) * D + m) * 16u;
+    for (int t2 = 0; t2 < M::VT; ++t2) {
+      const int sl = M::val_slot(t2, g);
+      const char *p = vh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes + ((unsigned)(((t0 + sl) & (page - 1)) / E) * D + m) * 16u;
 #pragma unroll
-          for (int d = 0; d < DT; ++d) v[d][t2] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + d * 256));
-        }
-      };
-      auto cut_v = [&](int t0, u32x4 (&v)[DT][M::VT]) {  // slots behind the sequence hold anything
-        if (t0 + TILE > sg.end())
+      for (int d = 0; d < DT; ++d) vf[d][t2] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + d * 256));
+    }
+  };
+  auto cut_v = [&](const Segment &sg, int t0) {  // slots behind the sequence hold anything
+    if (t0 + TILE > sg.end())
 #pragma unroll
-          for (int t2 = 0; t2 < M::VT; ++t2)
+      for (int t2 = 0; t2 < M::VT; ++t2)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) v[d][t2] = M::cut(v[d][t2], sg.end() - t0 - M::val_slot(t2, g));
-      };
+        for (int d = 0; d < DT; ++d) vf[d][t2] = M::cut(vf[d][t2], sg.end() - t0 - M::val_slot(t2, g));
+  };
+  auto begin = [&](const Segment &sg) {
+    const int t0 = sg.tile(min(sg.l0 + wid, sg.l1 - 1));
+    int pa, pb;
+    sg.pages(a, t0, pa, pb);
+    load_k(sg, t0, pa, pb, false);
+    load_v(sg, t0, pa, pb);
+    rows.load(a, sg, sg.rt * RT, m, g);
+  };
 
-      u32x4 kf[2][KS], vf[DT][M::VT];
-      int l = sg.l0 + wid, pa = 0, pb = 0;
-      if (l < sg.l1) {
-        sg.pages(a, sg.tile(l), pa, pb);
-        load_k(sg.tile(l), pa, pb, kf);
-      }
-      rows.load(a, sg, s, sg.rt * RT, m, g);
+  attn_share<T, D, RT, NW>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+    rows.clear();
+    int l = sg.l0 + wid;
+    if (sg.sp.i0 <= sg.sp.i1 && code == 0 && l < sg.l1) {
+      rows.depths(sg, s);
       bool odd_any = false;
-      for (; l < sg.l1; l += NW) {
-        // The next tile's keys are loaded whether there is one or not (the last tile's again
-        // then), so that the waits below count loads and do not drain them.
-        const int t0 = sg.tile(l), tn = sg.tile(l + NW < sg.l1 ? l + NW : l);
-        int na, nb;
-        sg.pages(a, tn, na, nb);
-        load_v(t0, pa, pb, vf);
+      for (;;) {
+        const bool last = l + NW >= sg.l1;
+        const int t0 = sg.tile(l), tn = sg.tile(last ? l : l + NW);
+        int pa, pb;
+        sg.pages(a, tn, pa, pb);
         f32x4 sc[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r) sc[r][0] = sc[r][1] = f32x4{0, 0, 0, 0};
@@ -672,12 +713,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
           for (int t2 = 0; t2 < 2; ++t2)
 #pragma unroll
             for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(kf[t2][k4], rows.q[r][k4], sc[r][t2]);
-        pa = na;
-        pb = nb;
-        load_k(tn, pa, pb, kf);
+        load_k(sg, tn, pa, pb, last);
         if (!sg.plain(a, t0)) {
           rows.mask(a, sg, s, t0, g, sc);
-          cut_v(t0, vf);
+          cut_v(sg, t0);
           bool odd = false;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
@@ -698,14 +737,18 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int r = 0; r < R; ++r) rows.o[r][d] = M::pv(vf[d], pw[r], rows.o[r][d]);
+        if (last) break;
+        l += NW;
+        load_v(sg, tn, pa, pb);
       }
       if (odd_any)
         for (l = sg.l0 + wid; l < sg.l1; l += NW) {
           const int t0 = sg.tile(l);
           if (sg.plain(a, t0)) continue;
+          int pa, pb;
           sg.pages(a, t0, pa, pb);
-          load_v(t0, pa, pb, vf);
-          cut_v(t0, vf);
+          load_v(sg, t0, pa, pb);
+          cut_v(sg, t0);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const unsigned vis = rows.view(a, sg, s, t0, r, g);
@@ -743,7 +786,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
         ls += f * lk;
         acc += *reinterpret_cast<const f32x4 *>(&s_o[(k * RT + row) * PADD + 4 * c4]) * f;
       }
-      emit(row, c4, acc, mt, ls);
+      sink(row, mt, ls).put(c4, acc);
     }
   });
 }
@@ -796,33 +839,43 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
   const unsigned long long page_bytes = (unsigned long long)a.Hkv * page * D * ESZ;
   const unsigned head_bytes = (unsigned)page * D * ESZ;
 
-  attn_share<T, D, RT>(a, s, [&](const Segment &sg, int code, auto emit) {
-    Rows<T, D, R> rows;
-    rows.clear();
-    if (sg.sp.i0 <= sg.sp.i1 && code == 0) {
-      const char *kh = a.k_pages + (size_t)sg.h * head_bytes;
-      const char *vh = a.v_pages + (size_t)sg.h * head_bytes;
-      rows.load(a, sg, s, sg.rt * RT + wid * 16 * R, m, g);
-      if (tid == 0) s_odd = 0;
+  Rows<T, D, R> rows;
+  auto fetch = [&](const Segment &sg, int l, u32x4 *buf) {
+    const char *kh = a.k_pages + (size_t)sg.h * head_bytes, *vh = a.v_pages + (size_t)sg.h * head_bytes;
+    const int t0 = sg.tile(l);
+    int pa, pb;
+    sg.pages(a, t0, pa, pb);
+    const int sl = lane % TILE;
+    const char *kp = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes +
+                     (size_t)((2 * wid + lane / TILE) * page + ((t0 + sl) & (page - 1))) * 16;
+#pragma unroll
+    for (int j = 0; j < PW; ++j)
+      __builtin_amdgcn_global_load_lds((GlobalPtr)(kp + (size_t)j * (2 * NW * 16) * page), (LdsPtr)(buf + (j * NW + wid) * WAVE), 16, 0, 2);
+#pragma unroll
+    for (int j = 0; j < PW; ++j) {
+      const int x = (j * NW + wid) * WAVE, vs = x / D * E;  // D units a value unit's slots: a piece lies in one of them
+      const char *vp = vh + (unsigned long long)(unsigned)(vs < 16 ? pa : pb) * page_bytes +
+                       (size_t)(((t0 + vs) & (page - 1)) / E * D + x % D + lane) * 16;
+      __builtin_amdgcn_global_load_lds((GlobalPtr)vp, (LdsPtr)(buf + UNITS + x), 16, 0, 2);
+    }
+  };
+  auto begin = [&](const Segment &sg) {
+    rows.load(a, sg, sg.rt * RT + wid * 16 * R, m, g);
+    if (tid == 0) s_odd = 0;
+    fetch(sg, sg.l0, s_t0);
+    if (NB > 2) {
+      if (sg.l0 + 1 < sg.l1) fetch(sg, sg.l0 + 1, s_t1);
+      if (sg.l0 + 2 < sg.l1) fetch(sg, sg.l0 + 2, s_t2);
+    }
+  };
 
-      auto fetch = [&](int l, u32x4 *buf) {
-        const int t0 = sg.tile(l);
-        int pa, pb;
-        sg.pages(a, t0, pa, pb);
-        const int sl = lane % TILE;
-        const char *kp = kh + (unsigned long long)(unsigned)(sl < 16 ? pa : pb) * page_bytes +
-                         (size_t)((2 * wid + lane / TILE) * page + ((t0 + sl) & (page - 1))) * 16;
-#pragma unroll
-        for (int j = 0; j < PW; ++j)
-          __builtin_amdgcn_global_load_lds((GlobalPtr)(kp + (size_t)j * (2 * NW * 16) * page), (LdsPtr)(buf + (j * NW + wid) * WAVE), 16, 0, 2);
-#pragma unroll
-        for (int j = 0; j < PW; ++j) {
-          const int x = (j * NW + wid) * WAVE, vs = x / D * E;  // D units a value unit's slots: a piece lies in one of them
-          const char *vp = vh + (unsigned long long)(unsigned)(vs < 16 ? pa : pb) * page_bytes +
-                           (size_t)(((t0 + vs) & (page - 1)) / E * D + x % D + lane) * 16;
-          __builtin_amdgcn_global_load_lds((GlobalPtr)vp, (LdsPtr)(buf + UNITS + x), 16, 0, 2);
-        }
-      };
+  attn_share<T, D, RT, 1>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+    rows.clear();
+    if (sg.sp.i0 > sg.sp.i1 || code != 0) {
+      hand_over<0>();  // what begin sent for has come before the buffers are used again
+    } else {
+      rows.depths(sg, s);
+      rows.arrived();
       // Slots behind the sequence hold anything, and values that are not finite are left out of
       // the products where not every row sees them.
       auto clean = [&](int t0, u32x4 *vb) {
@@ -854,7 +907,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
 #pragma unroll
             for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(k, rows.q[r][k4], sc[r][t2]);
           }
-        if (left >= NB - 1) fetch(l + NB - 1, last);
+        if (left >= NB - 1) fetch(sg, l + NB - 1, last);
         if (!plain) rows.mask(a, sg, s, t0, g, sc);
         typename M::P pw[R];
 #pragma unroll
@@ -869,12 +922,6 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
         }
       };
 
-      fetch(sg.l0, s_t0);
-      if (NB > 2) {
-        if (sg.l0 + 1 < sg.l1) fetch(sg.l0 + 1, s_t1);
-        if (sg.l0 + 2 < sg.l1) fetch(sg.l0 + 2, s_t2);
-      }
-      rows.arrived();
       for (int l = sg.l0; l < sg.l1; l += NB) {
         if (NB > 2) {
           work(l, s_t0, s_t3);
@@ -891,7 +938,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
         for (int l = sg.l0; l < sg.l1; ++l) {
           const int t0 = sg.tile(l);
           if (sg.plain(a, t0)) continue;
-          fetch(l, s_t0);
+          fetch(sg, l, s_t0);
           hand_over<0>();
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -910,9 +957,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float l_row = col_sum(rows.rl[r]);
+      const auto to = sink(wid * 16 * R + 16 * r + m, rows.scale(r), col_sum(rows.rl[r]));
 #pragma unroll
-      for (int d = 0; d < DT; ++d) emit(wid * 16 * R + 16 * r + m, 4 * d + g, rows.o[r][d], rows.scale(r), l_row);
+      for (int d = 0; d < DT; ++d) to.put(4 * d + g, rows.o[r][d]);
     }
   });
 }
