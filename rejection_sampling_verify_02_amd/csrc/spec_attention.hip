@@ -390,19 +390,24 @@ SVD void tree_books(const AttnArgs &a, const Segment &g, const SharedBooks &s) {
 // segment's partial tile.
 template <typename T, int D>
 struct RowSink {
-  enum { SKIP, OUT, ZERO, BAD, PART } kind;
+  enum { SKIP, OUT, ZERO, PART } kind;
   char *p;
   float inv;
-  SVD void put(int c4, f32x4 acc) const {  // elements 4 c4 .. 4 c4 + 3
-    if (kind == SKIP) return;
+  // Elements 4 c4 .. 4 c4 + 3 for c4 = first, first + step, ...: acc[0], acc[1], ...
+  template <int n>
+  SVD void put(int first, int step, const f32x4 (&acc)[n]) const {
     if (kind == PART) {
-      reinterpret_cast<f32x4 *>(p)[c4] = acc;
-      return;
+#pragma unroll
+      for (int k = 0; k < n; ++k) reinterpret_cast<f32x4 *>(p)[first + k * step] = acc[k];
+    } else if (kind != SKIP) {
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        f32x4 y = acc[k] * inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (kind == ZERO) ? 0.0f : y[i];
+        Mma<T>::store4(p + (first + k * step) * 4 * sizeof(T), y[0], y[1], y[2], y[3]);
+      }
     }
-    f32x4 y = acc * inv;
-    if (kind == ZERO) y = f32x4{0, 0, 0, 0};
-    if (kind == BAD) y = f32x4{NAN, NAN, NAN, NAN};
-    Mma<T>::store4(p + c4 * 4 * sizeof(T), y[0], y[1], y[2], y[3]);
   }
 };
 
@@ -497,9 +502,9 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
       RowSink<T, D> to;
       const int rg = g.rt * RT + row, i = rg / a.group, hh = rg - i * a.group;
       if (whole) {
-        to.kind = i >= a.N ? to.SKIP : code != 0 ? to.BAD : i >= g.sq.m ? to.ZERO : to.OUT;
+        to.kind = i >= a.N ? to.SKIP : (code == 0 && i >= g.sq.m) ? to.ZERO : to.OUT;
         to.p = a.out + (((size_t)g.b * a.N + i) * a.Hq + g.h * a.group + hh) * D * ESZ;
-        to.inv = 1.0f / ls;
+        to.inv = code != 0 ? NAN : 1.0f / ls;
       } else {
         to.kind = to.PART;
         to.p = reinterpret_cast<char *>(a.part_o + ((size_t)slot * RT + row) * D);
@@ -786,7 +791,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
         ls += f * lk;
         acc += *reinterpret_cast<const f32x4 *>(&s_o[(k * RT + row) * PADD + 4 * c4]) * f;
       }
-      sink(row, mt, ls).put(c4, acc);
+      const f32x4 one[1] = {acc};
+      sink(row, mt, ls).put(c4, 0, one);
     }
   });
 }
@@ -795,27 +801,27 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
 
 // A tile's keys and values lie in LDS in the order in which the lanes read them, 16 lanes
 // 256 bytes: keys [unit of d][slot], values [unit of slots][d].  They come there straight from
-// memory, without registers in between, into a ring of buffers: while the waves work on one
-// tile the next ones are on their way, and one barrier a tile both hands a tile over and frees
-// the buffer before it.  (With the next tile alone in flight, in registers, 16 trees of 32
-// nodes took 110 us.)  The buffers are variables of their own and the loop is unrolled over
-// them, so that the compiler sees that a tile's reads do not wait for later tiles.
+// memory, without registers in between, a stage of ST tiles at a time: while the waves work on
+// one stage the next is on its way, and one barrier hands a stage over and frees the other.
+// (With the next tile alone in flight, in registers, 16 trees of 32 nodes took 110 us.)  The
+// two stages are variables of their own, so that the compiler sees that reads of one do not
+// wait for the other; four of one tile each, one more in flight, made the code twice as long,
+// and a workgroup spends its first microseconds fetching code.
 typedef __attribute__((address_space(3))) void *LdsPtr;
 typedef const __attribute__((address_space(1))) void *GlobalPtr;
 
 template <typename T, int D, int R>
 constexpr int wide_occ() { return (R * D * (int)sizeof(T) <= 512) ? 2 : 1; }
-// Buffers of the ring: what two resident workgroups' LDS takes.
+// Tiles of a stage: as many as let two workgroups' stages fit a CU's LDS (two f32 heads of 256
+// fill it alone).
 template <typename T, int D>
-constexpr int wide_ring() { return D * (int)sizeof(T) <= 256 ? 4 : 2; }
+constexpr int wide_stage() { return D * (int)sizeof(T) <= 256 ? 2 : 1; }
 
-// Waits until at most n of the wave's vector memory operations and none of its LDS operations
-// are on their way, then for the other waves; no memory access moves across.
-template <int n>
+// Waits until none of the wave's memory operations is on its way, then for the other waves; no
+// memory access moves across.
 SVD void hand_over() {
-  static_assert(n < 64, "six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x70);
+  __builtin_amdgcn_s_waitcnt(0x70);  // vmcnt 0, lgkmcnt 0
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -827,10 +833,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
   constexpr int KS = D / (4 * E), DT = D / 16;
   constexpr int UNITS = TILE * D / E;                 // 16-byte units of a tile's keys, and of its values
   constexpr int PW = UNITS / NT;                      // of each, 64-unit pieces that a wave fetches
-  constexpr int NB = wide_ring<T, D>();
+  constexpr int ST = wide_stage<T, D>();
   extern __shared__ unsigned s_books[];
   const SharedBooks s = books_at(s_books, RT, a.N, a.group);
-  __shared__ u32x4 s_t0[2 * UNITS], s_t1[2 * UNITS], s_t2[NB > 2 ? 2 * UNITS : 1], s_t3[NB > 2 ? 2 * UNITS : 1];
+  __shared__ u32x4 s_a[ST][2 * UNITS], s_b[ST][2 * UNITS];
   __shared__ int s_odd;
 
   const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -859,20 +865,21 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
       __builtin_amdgcn_global_load_lds((GlobalPtr)vp, (LdsPtr)(buf + UNITS + x), 16, 0, 2);
     }
   };
+  auto fetch_stage = [&](const Segment &sg, int l, u32x4 (&st)[ST][2 * UNITS]) {
+#pragma unroll 1
+    for (int k = 0; k < ST; ++k)
+      if (l + k < sg.l1) fetch(sg, l + k, st[k]);
+  };
   auto begin = [&](const Segment &sg) {
     rows.load(a, sg, sg.rt * RT + wid * 16 * R, m, g);
     if (tid == 0) s_odd = 0;
-    fetch(sg, sg.l0, s_t0);
-    if (NB > 2) {
-      if (sg.l0 + 1 < sg.l1) fetch(sg, sg.l0 + 1, s_t1);
-      if (sg.l0 + 2 < sg.l1) fetch(sg, sg.l0 + 2, s_t2);
-    }
+    fetch_stage(sg, sg.l0, s_a);
   };
 
   attn_share<T, D, RT, 1>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
     rows.clear();
     if (sg.sp.i0 > sg.sp.i1 || code != 0) {
-      hand_over<0>();  // what begin sent for has come before the buffers are used again
+      hand_over();  // what begin sent for has come before the buffers are used again
     } else {
       rows.depths(sg, s);
       rows.arrived();
@@ -889,11 +896,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
         if (odd) s_odd = 1;
         __syncthreads();
       };
-      auto work = [&](int l, u32x4 *buf, u32x4 *last) {
-        const int t0 = sg.tile(l), left = sg.l1 - 1 - l;
-        if (NB > 2 && left >= 2) hand_over<(NB - 2) * 2 * PW>();
-        else if (NB > 2 && left == 1) hand_over<2 * PW>();
-        else hand_over<0>();
+      auto work = [&](int l, u32x4 *buf) {
+        const int t0 = sg.tile(l);
         const bool plain = sg.plain(a, t0);
         if (!plain) clean(t0, buf + UNITS);
         f32x4 sc[R][2];
@@ -907,7 +911,6 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
 #pragma unroll
             for (int r = 0; r < R; ++r) sc[r][t2] = M::qk(k, rows.q[r][k4], sc[r][t2]);
           }
-        if (left >= NB - 1) fetch(sg, l + NB - 1, last);
         if (!plain) rows.mask(a, sg, s, t0, g, sc);
         typename M::P pw[R];
 #pragma unroll
@@ -921,25 +924,25 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
           for (int r = 0; r < R; ++r) rows.o[r][d] = M::pv(v, pw[r], rows.o[r][d]);
         }
       };
+      auto stage = [&](int l, u32x4 (&now)[ST][2 * UNITS], u32x4 (&next)[ST][2 * UNITS]) {
+        hand_over();
+        fetch_stage(sg, l + ST, next);
+#pragma unroll 1
+        for (int k = 0; k < ST; ++k)
+          if (l + k < sg.l1) work(l + k, now[k]);
+      };
 
-      for (int l = sg.l0; l < sg.l1; l += NB) {
-        if (NB > 2) {
-          work(l, s_t0, s_t3);
-          if (l + 1 < sg.l1) work(l + 1, s_t1, s_t0);
-          if (l + 2 < sg.l1) work(l + 2, s_t2, s_t1);
-          if (l + 3 < sg.l1) work(l + 3, s_t3, s_t2);
-        } else {
-          work(l, s_t0, s_t1);
-          if (l + 1 < sg.l1) work(l + 1, s_t1, s_t0);
-        }
+      for (int l = sg.l0; l < sg.l1; l += 2 * ST) {
+        stage(l, s_a, s_b);
+        if (l + ST < sg.l1) stage(l + ST, s_b, s_a);
       }
       __syncthreads();
       if (s_odd)
         for (int l = sg.l0; l < sg.l1; ++l) {
           const int t0 = sg.tile(l);
           if (sg.plain(a, t0)) continue;
-          fetch(sg, l, s_t0);
-          hand_over<0>();
+          fetch(sg, l, s_a[0]);
+          hand_over();
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const unsigned vis = rows.view(a, sg, s, t0, r, g);
@@ -948,7 +951,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
               u32x4 v[M::VT];
 #pragma unroll
               for (int t2 = 0; t2 < M::VT; ++t2)
-                v[t2] = M::cut(s_t0[UNITS + M::val_slot(t2, g) / E * D + 16 * d + m], sg.end() - t0 - M::val_slot(t2, g));
+                v[t2] = M::cut(s_a[0][UNITS + M::val_slot(t2, g) / E * D + 16 * d + m], sg.end() - t0 - M::val_slot(t2, g));
               rows.odd_values(r, d, v, vis);
             }
           }
@@ -957,9 +960,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const auto to = sink(wid * 16 * R + 16 * r + m, rows.scale(r), col_sum(rows.rl[r]));
-#pragma unroll
-      for (int d = 0; d < DT; ++d) to.put(4 * d + g, rows.o[r][d]);
+      sink(wid * 16 * R + 16 * r + m, rows.scale(r), col_sum(rows.rl[r])).put(g, 4, rows.o[r]);
     }
   });
 }
