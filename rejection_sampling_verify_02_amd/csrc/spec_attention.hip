@@ -421,10 +421,6 @@ template <typename T, int D, int RT, unsigned MIN_SHARE, typename Begin, typenam
 SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run run) {
   constexpr int ESZ = (int)sizeof(T);
   const int tid = threadIdx.x;
-  // Consecutive shares on one XCD: the row tiles of a key head read the same keys and values
-  // through that XCD's L2.
-  const unsigned w = (blockIdx.x % LANES) * (a.grid / LANES) + blockIdx.x / LANES;
-
   unsigned T_all = 0, v = 0, ex = 0;
   for (int b0 = 0; b0 < a.B; b0 += NT) {
     v = (b0 + tid < a.B) ? seq_tiles<RT>(a, b0 + tid) : 0u;
@@ -433,7 +429,11 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     T_all += tot;
   }
   const unsigned share = max((T_all + a.grid - 1) / a.grid, MIN_SHARE);
-  if ((unsigned long long)w * share >= T_all) return;
+  // Consecutive shares on one XCD (block p runs on XCD p % LANES), as many on each: the row
+  // tiles of a key head read the same keys and values through that XCD's L2.
+  const unsigned shares = (T_all + share - 1) / share, per_xcd = (shares + LANES - 1) / LANES;
+  const unsigned w = (blockIdx.x % LANES) * per_xcd + blockIdx.x / LANES;
+  if (blockIdx.x / LANES >= per_xcd || w >= shares) return;
   unsigned pos = w * share;
   const unsigned pos_end = min(T_all, pos + share);
   if (a.B <= NT) {
@@ -459,7 +459,8 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   g.b = __builtin_amdgcn_readfirstlane((int)s.at[0]);
   unsigned off = (unsigned)__builtin_amdgcn_readfirstlane((int)s.at[1]);  // tiles of the sequence before pos
   g.sq = seq_of(a, g.b);
-  int code = 0, code_b = -1;  // the code of sequence code_b
+  int code = 0, code_b = -1;           // the code of sequence code_b
+  int books_b = -1, books_rt = -1;     // the row tile whose books are in LDS
   while (pos < pos_end) {
     unsigned per_head = 0;
     for (int rt = 0; rt < a.n_rt; ++rt) per_head += (unsigned)span_of<RT>(a, g.sq, rt).tiles;
@@ -495,7 +496,11 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
       a.desc[(g.b * a.Hkv + g.h) * a.n_rt + g.rt] =
           make_uint4(w, last - w + 1, (code ? 0x80000000u : 0u) | (unsigned)(g.sq.ok ? g.sq.m : 0), 0u);
     }
-    if (code == 0 && g.par && g.masks && g.sp.i0 <= g.sp.i1) tree_books(a, g, s);
+    if (code == 0 && g.par && g.masks && g.sp.i0 <= g.sp.i1 && (books_b != g.b || books_rt != g.rt)) {
+      tree_books(a, g, s);  // the same for every key head
+      books_b = g.b;
+      books_rt = g.rt;
+    }
 
     const unsigned slot = 2 * w + (g.l0 == 0 ? 1u : 0u);
     auto sink = [&](int row, float mt, float ls) {
@@ -1092,7 +1097,8 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
     return p.wide ? wide_occ<T, decltype(d)::value, decltype(r)::value>() : attn_occ<T, decltype(d)::value, decltype(r)::value>();
   });
   long long grid = 256LL * occ;  // one resident set of the device's 256 CUs
-  const long long need = (p.units * most + 3) / 4;
+  const long long least = p.wide ? 1 : NW;  // tiles of a share
+  const long long need = (p.units * most + least - 1) / least;
   if (need < grid) grid = need;
   p.grid = (unsigned)((grid + LANES - 1) / LANES * LANES);
   size_t o = 0;
