@@ -57,7 +57,7 @@ extern "C" {
 #define SV_ROW_BAD_FORK (-10)   /* spec_cache_fork: not a pair it can make                    */
 
 #define SV_CACHE_MAX_NEW 1024   /* most new tokens N of a sequence in one call                */
-#define SV_CACHE_MAX_SEQS 8192  /* most sequences of spec_cache_resize and spec_cache_fork    */
+#define SV_CACHE_MAX_SEQS 4096  /* most sequences of spec_cache_resize and spec_cache_fork    */
 
 /* ---- attention of the new tokens over a paged cache ----
  *
@@ -116,7 +116,7 @@ const char *sv_attention_launch_plan(int32_t N, int32_t Hq, int32_t Hkv, int32_t
  *   k, v         [B, N, Hkv, D] dtype; strides as for q above, 16-byte aligned
  *   row_status   [B] int32 out: 0, SV_ROW_BAD_LENGTH or SV_ROW_BAD_PAGE; nothing of the
  *                sequence is then written
- * D is a multiple of 16 up to 1024.  The slots' pages must be the sequence's own (as
+ * D is a multiple of 16 up to 512.  The slots' pages must be the sequence's own (as
  * spec_cache_resize leaves them): two sequences that write to one page race. */
 sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_n, const void *v,
                             int64_t v_stride_b, int64_t v_stride_n, sv_dtype dtype, void *k_pages,
@@ -141,7 +141,7 @@ sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_
  *                beyond N - 1, or slots beyond the table), SV_ROW_BAD_TREE (path_nodes not
  *                increasing in 1 .. N-1) or SV_ROW_BAD_PAGE; new_len is then cache_len and
  *                nothing of the sequence is moved
- * D is a multiple of 16 up to 1024.  The slots' pages must be the sequence's own. */
+ * D is a multiple of 16 up to 512.  The slots' pages must be the sequence's own. */
 sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype,
                             const int32_t *page_table, const int32_t *cache_len,
                             const int32_t *accepted_len, const int32_t *path_nodes, int32_t L,

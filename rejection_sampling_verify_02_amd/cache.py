@@ -23,7 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import math
-from contextlib import nullcontext
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -31,7 +31,7 @@ import torch
 from . import SV_BF16, SV_F32, SpecVerifyError, load_library, sv_status_string
 
 ROW_BAD_PAGE, ROW_BAD_LENGTH, ROW_NO_PAGES, ROW_BAD_FORK = -7, -8, -9, -10
-CACHE_MAX_NEW, CACHE_MAX_SEQS = 1024, 8192
+CACHE_MAX_NEW, CACHE_MAX_SEQS = 1024, 4096
 
 
 class PagePool(NamedTuple):
@@ -58,92 +58,123 @@ def empty_pages(layers: int, num_pages: int, kv_heads: int, head_dim: int, page_
             torch.zeros((layers, num_pages, kv_heads, page_size // E, head_dim, E), dtype=dtype, device=device))
 
 
+# The checks below take the usual case in one expression and look for the reason only when it
+# fails: a call's host time is a few microseconds, and shows where its kernels take no longer.
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _code(t: torch.Tensor, name: str) -> int:
-    if t.dtype is torch.bfloat16:
+    dt = t.dtype
+    if dt is _BF16:
         return SV_BF16
-    if t.dtype is torch.float32:
+    if dt is _F32:
         return SV_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {dt}")
 
 
-def _ints(t, name: str, shape: tuple, dev, optional: bool = False):
+def _ints(t, name: str, shape: tuple, dev: int, optional: bool = False):
     """The address of a contiguous int32 tensor of that shape (None where it may be left out)."""
     if t is None:
         if optional:
             return None
         raise TypeError(f"{name} must be an int32 tensor, got None")
-    if t.dtype is not torch.int32:
+    if t.dtype is _I32 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not _I32:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _pages(k_pages, v_pages, dims: int, dtype, dev):
+def _pages(k_pages, v_pages, dims: int, dtype, dev: int):
     """(P, Hkv, D, page_size) of a cache of `dims` dimensions (5: a layer, 6: all of them)."""
-    if k_pages.dim() != dims or v_pages.dim() != dims:
+    ks, vs = k_pages.shape, v_pages.shape
+    E = 8 if dtype is _BF16 else 4
+    if len(ks) == len(vs) == dims and k_pages.dtype is dtype and v_pages.dtype is dtype and k_pages.get_device() == dev \
+            and v_pages.get_device() == dev and k_pages.is_contiguous() and v_pages.is_contiguous():
+        P, H, U, page, e = ks[-5:]
+        if e == E and page % E == 0 and vs == ks[:-3] + (page // E, U * E, E):
+            return P, H, U * E, page
+    if len(ks) != dims or len(vs) != dims:
         raise ValueError(f"k_pages and v_pages must have {dims} dimensions")
     if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
         raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")
-    if k_pages.device != dev or v_pages.device != dev:
-        raise ValueError(f"k_pages and v_pages must be on {dev}")
+    if k_pages.get_device() != dev or v_pages.get_device() != dev:
+        raise ValueError(f"k_pages and v_pages must be on device {dev}, got {k_pages.device} and {v_pages.device}")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    P, H, U, page, E = k_pages.shape[-5:]
-    if E != 16 // k_pages.element_size() or page % E:
-        raise ValueError(f"k_pages must be [..., P, Hkv, D / {16 // k_pages.element_size()}, page_size, "
-                         f"{16 // k_pages.element_size()}], got {tuple(k_pages.shape)}")
-    if v_pages.shape != k_pages.shape[:-3] + (page // E, U * E, E):
-        raise ValueError(f"v_pages must have shape {tuple(k_pages.shape[:-3]) + (page // E, U * E, E)}, "
-                         f"got {tuple(v_pages.shape)}")
-    return P, H, U * E, page
+    raise ValueError(f"k_pages must be [..., P, Hkv, D / {E}, page_size, {E}] and v_pages [..., P, Hkv, page_size / {E}, D, {E}], "
+                     f"got {tuple(ks)} and {tuple(vs)}")
 
 
-def _rows(t, name: str, B: int, N: int, H: int, D: int, dtype, dev):
+def _rows(t, name: str, shape: tuple, dtype, dev: int):
     """Address and strides (sequence, node) of a [B, N, H, D] tensor whose heads lie together."""
-    if t.shape != (B, N, H, D):
-        raise ValueError(f"{name} must have shape {(B, N, H, D)}, got {tuple(t.shape)}")
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        B, N, H, D = shape
+        sb, sn, sh, sd = t.stride()
+        if (sd == 1 or D <= 1) and (sh == D or H <= 1):
+            # a dimension of one entry may carry any stride: it is never stepped
+            return t.data_ptr(), sb if B > 1 else 0, sn if N > 1 else 0
+        raise ValueError(f"{name}'s heads must lie together (strides D and 1), got strides {t.stride()}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    sb, sn, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}'s heads must lie together (strides D and 1), got strides {t.stride()}")
-    # a dimension of one entry may carry any stride: it is never stepped
-    return t.data_ptr(), sb if B > 1 else 0, sn if N > 1 else 0
+    raise ValueError(f"{name} must be on device {dev}, got {t.device}")
 
 
-def _device(t, name: str):
-    if t.device.type != "cuda":
+def _table(t, dev: int, rows: int | None = None):
+    """Address and width of a page table."""
+    if t.dim() != 2:
+        raise ValueError("page_table must have two dimensions, sequences and pages")
+    B, W = t.shape
+    return _ints(t, "page_table", (B if rows is None else rows, W), dev), W
+
+
+def _device(t, name: str) -> int:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.device
+    return t.get_device()
 
 
-def _on(dev, stream):
-    """The context to allocate and launch in, and the raw stream."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return nullcontext(), torch.cuda.current_stream(dev).cuda_stream
+def _launch(dev: int, stream, call, *args):
+    """call(raw stream, *args) with the tensors' device current and, given a raw stream of the
+    caller's, that stream current too: what the call allocates then belongs to it."""
     if stream is None:
-        return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)), stream
+        if dev == _current_device():
+            return call(_raw_stream(dev), *args)
+        with torch.cuda.device(dev):
+            return call(_raw_stream(dev), *args)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+        return call(stream, *args)
 
 
-def _work(workspace, nbytes: int, dev):
+def _work(workspace, nbytes: int, dev: int):
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if workspace.dtype is not torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on device {dev}")
     return workspace
 
 
 def _raise(rc: int):
     if rc != 0:
         raise SpecVerifyError(rc, sv_status_string(rc))
+
+
+@lru_cache(maxsize=None)
+def _attention_bytes(*sizes) -> int:
+    return int(load_library().sv_attention_workspace_bytes(*sizes))
+
+
+@lru_cache(maxsize=None)
+def _resize_bytes(*sizes) -> int:
+    return int(load_library().sv_resize_workspace_bytes(*sizes))
 
 
 def sv_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, page_size: int, table_width: int,
@@ -171,41 +202,43 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
     ``out`` may supply the two tensors.  ``events`` as for spec_verify: the number of kernels is
     then returned last.
     """
-    lib = load_library()
     dev = _device(q, "q")
     dt = _code(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [B, N, Hq, D]")
-    B, N, Hq, D = q.shape
+    shape = q.shape
+    B, N, Hq, D = shape
     P, Hkv, Dk, page = _pages(k_pages, v_pages, 5, q.dtype, dev)
     if Dk != D:
         raise ValueError(f"the cache's heads have {Dk} elements, q's {D}")
-    qp, qb, qn = _rows(q, "q", B, N, Hq, D, q.dtype, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, table_width]")
-    W = page_table.shape[1]
-    ints = (_ints(page_table, "page_table", (B, W), dev), _ints(cache_len, "cache_len", (B,), dev),
-            _ints(n_new, "n_new", (B,), dev, True), _ints(parent, "parent", (B, N), dev, True))
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if out is None:
-            o, st = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
-        else:
-            o, st = out
-            if not o.is_contiguous():
-                raise ValueError("out must be contiguous")
-            _rows(o, "out", B, N, Hq, D, q.dtype, dev)
-            _ints(st, "row_status", (B,), dev)
-        ws = _work(workspace, lib.sv_attention_workspace_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
-        args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, *ints, B, N, Hq, Hkv, D, page, P, W,
-                1.0 / math.sqrt(D) if scale is None else scale, window, sinks, o.data_ptr(), st.data_ptr(),
-                ws.data_ptr(), ws.numel(), raw)
+    qp, qb, qn = _rows(q, "q", shape, q.dtype, dev)
+    table, W = _table(page_table, dev, B)
+    seqs = (B,)
+    lens, news = _ints(cache_len, "cache_len", seqs, dev), _ints(n_new, "n_new", seqs, dev, True)
+    par = _ints(parent, "parent", (B, N), dev, True)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is not None:
+        if not out[0].is_contiguous():
+            raise ValueError("out must be contiguous")
+        _rows(out[0], "out", shape, q.dtype, dev)
+        _ints(out[1], "row_status", seqs, dev)
+
+    def call(raw):
+        o, st = out or (torch.empty(shape, dtype=q.dtype, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
+        ws = _work(workspace, _attention_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
+        args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, news, par, B, N, Hq, Hkv, D, page, P, W,
+                scale, window, sinks, o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel(), raw)
         if events is None:
-            _raise(lib.spec_paged_attention(*args))
+            rc = load_library().spec_paged_attention(*args)
+            if rc:
+                _raise(rc)
             return o, st
         n = ctypes.c_int32(0)
-        _raise(lib.spec_paged_attention_timed(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
+        _raise(load_library().spec_paged_attention_timed(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
         return o, st, n.value
+
+    return _launch(dev, stream, call)
 
 
 def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=None, stream=None, out=None):
@@ -213,29 +246,32 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=No
     between sequences and nodes) into slots cache_len .. cache_len + n_new - 1 of one layer's
     k_pages and v_pages (see include/spec_cache.h).  Returns row_status [B] int32, which ``out``
     may supply."""
-    lib = load_library()
     dev = _device(k, "k")
     dt = _code(k, "k")
     if k.dim() != 4:
         raise ValueError("k must be [B, N, Hkv, D]")
-    B, N, Hkv, D = k.shape
+    shape = k.shape
+    B, N, Hkv, D = shape
     P, Hc, Dk, page = _pages(k_pages, v_pages, 5, k.dtype, dev)
-    if (Hc, Dk) != (Hkv, D):
+    if Hc != Hkv or Dk != D:
         raise ValueError(f"the cache has {Hc} heads of {Dk} elements, k {Hkv} of {D}")
-    kp, kb, kn = _rows(k, "k", B, N, Hkv, D, k.dtype, dev)
-    vp, vb, vn = _rows(v, "v", B, N, Hkv, D, k.dtype, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, table_width]")
-    W = page_table.shape[1]
-    ints = (_ints(page_table, "page_table", (B, W), dev), _ints(cache_len, "cache_len", (B,), dev),
-            _ints(n_new, "n_new", (B,), dev, True))
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        st = torch.empty(B, dtype=torch.int32, device=dev) if out is None else out
-        sp = _ints(st, "row_status", (B,), dev)
-        _raise(lib.spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), *ints, B, N, Hkv, D,
-                                     page, P, W, sp, raw))
-    return st
+    kp, kb, kn = _rows(k, "k", shape, k.dtype, dev)
+    vp, vb, vn = _rows(v, "v", shape, k.dtype, dev)
+    table, W = _table(page_table, dev, B)
+    seqs = (B,)
+    lens, news = _ints(cache_len, "cache_len", seqs, dev), _ints(n_new, "n_new", seqs, dev, True)
+    if out is not None:
+        _ints(out, "row_status", seqs, dev)
+
+    def call(raw):
+        st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
+        rc = load_library().spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens, news,
+                                              B, N, Hkv, D, page, P, W, st.data_ptr(), raw)
+        if rc:
+            _raise(rc)
+        return st
+
+    return _launch(dev, stream, call)
 
 
 def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes=None, *, max_new: int | None = None,
@@ -245,13 +281,11 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
     path_nodes [B, N] int32 as spec_tree_verify returns them, or for chains accepted_len alone
     and ``max_new``, the N = G + 1 new tokens that were verified.  Returns (new_len [B],
     row_status [B]) int32; ``out`` may supply them (for chains new_len may be cache_len itself)."""
-    lib = load_library()
     dev = _device(k_pages, "k_pages")
     dt = _code(k_pages, "k_pages")
     P, Hkv, D, page = _pages(k_pages, v_pages, 6, k_pages.dtype, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, table_width]")
-    B, W = page_table.shape
+    table, W = _table(page_table, dev)
+    B = page_table.shape[0]
     if path_nodes is not None:
         N = path_nodes.shape[1] if path_nodes.dim() == 2 else 0
         if max_new is not None and max_new != N:
@@ -260,27 +294,28 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
         raise ValueError("chains need max_new, the new tokens N = G + 1 of the verification")
     else:
         N = max_new
-    ints = (_ints(page_table, "page_table", (B, W), dev), _ints(cache_len, "cache_len", (B,), dev),
-            _ints(accepted_len, "accepted_len", (B,), dev), _ints(path_nodes, "path_nodes", (B, N), dev, True))
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if out is None:
-            n, st = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
-        else:
-            n, st = out
-        np_, sp = _ints(n, "new_len", (B,), dev), _ints(st, "row_status", (B,), dev)
-        _raise(lib.spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, *ints, k_pages.shape[0], B, N, Hkv, D, page, P,
-                                     W, np_, sp, raw))
-    return n, st
+    seqs = (B,)
+    lens, acc = _ints(cache_len, "cache_len", seqs, dev), _ints(accepted_len, "accepted_len", seqs, dev)
+    path = _ints(path_nodes, "path_nodes", (B, N), dev, True)
+    if out is not None:
+        _ints(out[0], "new_len", seqs, dev)
+        _ints(out[1], "row_status", seqs, dev)
+
+    def call(raw):
+        n, st = out or (torch.empty(seqs, dtype=_I32, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
+        rc = load_library().spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, k_pages.shape[0],
+                                              B, N, Hkv, D, page, P, W, n.data_ptr(), st.data_ptr(), raw)
+        if rc:
+            _raise(rc)
+        return n, st
+
+    return _launch(dev, stream, call)
 
 
-def _books(pool: PagePool, dev):
-    if pool.page_table.dim() != 2:
-        raise ValueError("page_table must be [S, table_width]")
-    S, W = pool.page_table.shape
-    P = pool.ref_count.numel()
-    return S, W, P, (_ints(pool.page_table, "page_table", (S, W), dev), _ints(pool.seq_pages, "seq_pages", (S,), dev),
-                     _ints(pool.ref_count, "ref_count", (P,), dev))
+def _books(pool: PagePool, dev: int):
+    table, W = _table(pool.page_table, dev)
+    S, P = pool.page_table.shape[0], pool.ref_count.numel()
+    return S, W, P, (table, _ints(pool.seq_pages, "seq_pages", (S,), dev), _ints(pool.ref_count, "ref_count", (P,), dev))
 
 
 def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=None, *, page_size: int | None = None,
@@ -290,7 +325,6 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
     keep_len [S] is replaced by the sequence's own, its kept slots copied in all layers of k_pages
     [L, P, Hkv, D/E, page, E] and v_pages.  Without them nothing is copied and ``page_size`` is
     needed.  Returns row_status [S] int32, which ``out`` may supply."""
-    lib = load_library()
     dev = _device(pool.page_table, "page_table")
     S, W, P, books = _books(pool, dev)
     free = _ints(pool.free_map, "free_map", ((P + 31) // 32,), dev)
@@ -306,29 +340,41 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
         raise ValueError("page_size is needed without k_pages and v_pages")
     else:
         dt, L, Hkv, D, page, kp, vp = SV_BF16, 0, 1, 16, page_size, None, None
-    keep, want = _ints(keep_len, "keep_len", (S,), dev), _ints(want_len, "want_len", (S,), dev)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        st = torch.empty(S, dtype=torch.int32, device=dev) if out is None else out
-        sp = _ints(st, "row_status", (S,), dev)
-        ws = _work(workspace, lib.sv_resize_workspace_bytes(S, P), dev)
-        _raise(lib.spec_cache_resize(*books, free, keep, want, kp, vp, dt, L, S, Hkv, D, page, P, W, sp, ws.data_ptr(),
-                                     ws.numel(), raw))
-    return st
+    seqs = (S,)
+    keep, want = _ints(keep_len, "keep_len", seqs, dev), _ints(want_len, "want_len", seqs, dev)
+    if out is not None:
+        _ints(out, "row_status", seqs, dev)
+
+    def call(raw):
+        st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
+        ws = _work(workspace, _resize_bytes(S, P), dev)
+        rc = load_library().spec_cache_resize(*books, free, keep, want, kp, vp, dt, L, S, Hkv, D, page, P, W, st.data_ptr(),
+                                              ws.data_ptr(), ws.numel(), raw)
+        if rc:
+            _raise(rc)
+        return st
+
+    return _launch(dev, stream, call)
 
 
 def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=None):
     """Makes sequences dst [F] continuations of sequences src [F] (int32) that share their pages
     (see include/spec_cache.h); cache_len [S] is written at dst.  Returns pair_status [F] int32,
     which ``out`` may supply."""
-    lib = load_library()
     dev = _device(pool.page_table, "page_table")
     S, W, P, books = _books(pool, dev)
     F = src.numel()
-    n, s, d = _ints(cache_len, "cache_len", (S,), dev), _ints(src, "src", (F,), dev), _ints(dst, "dst", (F,), dev)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        st = torch.empty(F, dtype=torch.int32, device=dev) if out is None else out
-        sp = _ints(st, "pair_status", (F,), dev)
-        _raise(lib.spec_cache_fork(*books, n, s, d, F, S, P, W, sp, raw))
-    return st
+    pairs = (F,)
+    lens = _ints(cache_len, "cache_len", (S,), dev)
+    s, d = _ints(src, "src", pairs, dev), _ints(dst, "dst", pairs, dev)
+    if out is not None:
+        _ints(out, "pair_status", pairs, dev)
+
+    def call(raw):
+        st = torch.empty(pairs, dtype=_I32, device=dev) if out is None else out
+        rc = load_library().spec_cache_fork(*books, lens, s, d, F, S, P, W, st.data_ptr(), raw)
+        if rc:
+            _raise(rc)
+        return st
+
+    return _launch(dev, stream, call)

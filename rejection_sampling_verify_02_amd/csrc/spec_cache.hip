@@ -111,16 +111,20 @@ struct CommitArgs {
   Pool pool;
 };
 
-// One workgroup moves one head's entries of one sequence in one layer, path position by path
-// position.  Sources lie behind their targets (path_nodes[j] >= j + 1, increasing), so a
-// thread that owns its d and goes up the path never overwrites what it has still to read, and
-// no thread needs another's: COMMIT_STEP entries are read before they are written.
-constexpr int COMMIT_STEP = 8;
+// One workgroup moves one head's entries of one sequence in one layer, in batches of whole
+// target units of values (COMMIT_R * NT / D of them): everything a batch moves is read before
+// any of it is written.  Later batches read nothing that earlier ones wrote, since sources lie
+// behind their targets (path_nodes[j] >= j + 1, increasing).  A value unit is put together in
+// registers and written whole, slots that are no targets as they were: 16-byte stores in place
+// of single elements 16 bytes apart (which took 43 us where this takes 15: 16 trees, 32
+// layers).
+constexpr int COMMIT_R = 2;  // units of keys, and of values, that a thread holds
 
 template <typename T>
 __global__ __launch_bounds__(NT) void k_cache_commit(const CommitArgs a) {
   constexpr int E = 16 / (int)sizeof(T);
-  __shared__ int s_path[SV_CACHE_MAX_NEW];
+  __shared__ int s_slot[SV_CACHE_MAX_NEW], s_page[SV_CACHE_MAX_NEW];  // of the sources
+  __shared__ int s_first;
   const int tid = threadIdx.x;
   const int b = (int)(blockIdx.x % a.B);
   const unsigned lh = blockIdx.x / a.B;
@@ -128,6 +132,7 @@ __global__ __launch_bounds__(NT) void k_cache_commit(const CommitArgs a) {
   const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D;
   const int32_t *table = a.page_table + (size_t)b * a.pool.W;
 
+  if (tid == 0) s_first = acc;
   int code = 0, top = 0;  // top: the last node kept
   if (acc < 0) {
     code = acc;
@@ -136,14 +141,14 @@ __global__ __launch_bounds__(NT) void k_cache_commit(const CommitArgs a) {
   } else {
     top = acc;
     if (a.path && acc > 0) {
+      const int32_t *path = a.path + (size_t)b * a.N;
       bool bad = false;
       for (int j = tid; j < acc; j += NT) {
-        const int x = a.path[(size_t)b * a.N + j], y = j ? a.path[(size_t)b * a.N + j - 1] : 0;
-        s_path[j] = x;
+        const int x = path[j], y = j ? path[j - 1] : 0;
         bad |= x <= y || x >= a.N;
       }
+      top = path[acc - 1];
       if (__syncthreads_or(bad)) code = SV_ROW_BAD_TREE;
-      else top = s_path[acc - 1];
     }
     if (code == 0 && (long long)len + top + 1 > ((long long)a.pool.W << sh)) code = SV_ROW_BAD_LENGTH;
     if (code == 0) {
@@ -157,43 +162,63 @@ __global__ __launch_bounds__(NT) void k_cache_commit(const CommitArgs a) {
     a.new_len[b] = (code == 0) ? len + 1 + acc : len;
   }
   if (code != 0 || !a.path || top == acc) return;  // entries that lie together already
+  for (int j = tid; j < acc; j += NT) {
+    const int x = a.path[(size_t)b * a.N + j];
+    s_slot[j] = len + x;
+    s_page[j] = table[(len + x) >> sh];
+    if (x != j + 1) atomicMin(&s_first, j);
+  }
+  __syncthreads();
 
   const size_t hb = head_bytes<T>(a.pool);
   const unsigned l = lh / a.pool.Hkv, h = lh % a.pool.Hkv;
   const size_t lay = (size_t)l * a.pool.P;
-  auto base = [&](int s) { return ((lay + (size_t)table[s >> sh]) * a.pool.Hkv + h) * hb; };
-  const int U = D / E;
-  // thread x < U owns key unit x, threads behind it own the values of one d each
-  for (int x = tid; x < U + D; x += NT) {
-    for (int j0 = 0; j0 < acc; j0 += COMMIT_STEP) {
-      if (x < U) {
-        u32x4 w[COMMIT_STEP];
+  auto base = [&](int p) { return ((lay + (size_t)p) * a.pool.Hkv + h) * hb; };
+  const int U = D / E, per = COMMIT_R * NT / D;  // target units a batch
+  const int t_end = len + 1 + acc;               // targets are slots len + 1 + j
+  for (int u0 = (len + 1 + s_first) / E; u0 * E < t_end; u0 += per) {
+    const int lo = max(u0 * E, len + 1 + s_first), hi = min((u0 + per) * E, t_end);
+    u32x4 kw[COMMIT_R], vw[COMMIT_R];
 #pragma unroll
-        for (int j = 0; j < COMMIT_STEP; ++j) {
-          const int s = len + s_path[min(j0 + j, acc - 1)];
-          w[j] = *reinterpret_cast<const u32x4 *>(a.k_pages + base(s) + ((size_t)x * page + (s & (page - 1))) * 16);
-        }
+    for (int r = 0; r < COMMIT_R; ++r) {
+      const int x = tid + r * NT;
+      if (x < (hi - lo) * U) {
+        const int j = lo + x / U - (len + 1), s = s_slot[j];
+        kw[r] = *reinterpret_cast<const u32x4 *>(a.k_pages + base(s_page[j]) + ((size_t)(x % U) * page + (s & (page - 1))) * 16);
+      }
+      if (x < per * D) {
+        const int u = u0 + x / D, d = x % D, f = u * E;
+        if (f < hi) {
+          const size_t o = ((size_t)((f & (page - 1)) / E) * D + d) * 16;
+          u32x4 w = *reinterpret_cast<const u32x4 *>(a.v_pages + base(table[f >> sh]) + o);
+          T e[E];
+          __builtin_memcpy(e, &w, 16);
 #pragma unroll
-        for (int j = 0; j < COMMIT_STEP; ++j) {
-          const int s = len + 1 + j0 + j;
-          if (j0 + j < acc) *reinterpret_cast<u32x4 *>(a.k_pages + base(s) + ((size_t)x * page + (s & (page - 1))) * 16) = w[j];
-        }
-      } else {
-        const int d = x - U;
-        T w[COMMIT_STEP];
-#pragma unroll
-        for (int j = 0; j < COMMIT_STEP; ++j) {
-          const int s = len + s_path[min(j0 + j, acc - 1)], t = s & (page - 1);
-          w[j] = *reinterpret_cast<const T *>(a.v_pages + base(s) + ((size_t)(t / E) * D + d) * 16 + (size_t)(t % E) * sizeof(T));
-        }
-#pragma unroll
-        for (int j = 0; j < COMMIT_STEP; ++j) {
-          const int s = len + 1 + j0 + j, t = s & (page - 1);
-          if (j0 + j < acc)
-            *reinterpret_cast<T *>(a.v_pages + base(s) + ((size_t)(t / E) * D + d) * 16 + (size_t)(t % E) * sizeof(T)) = w[j];
+          for (int i = 0; i < E; ++i)
+            if (f + i >= lo && f + i < hi) {
+              const int j = f + i - (len + 1), t = s_slot[j] & (page - 1);
+              e[i] = *reinterpret_cast<const T *>(a.v_pages + base(s_page[j]) + ((size_t)(t / E) * D + d) * 16 + (size_t)(t % E) * sizeof(T));
+            }
+          __builtin_memcpy(&w, e, 16);
+          vw[r] = w;
         }
       }
     }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < COMMIT_R; ++r) {
+      const int x = tid + r * NT;
+      if (x < (hi - lo) * U) {
+        const int s = lo + x / U;
+        *reinterpret_cast<u32x4 *>(a.k_pages + base(table[s >> sh]) + ((size_t)(x % U) * page + (s & (page - 1))) * 16) = kw[r];
+      }
+      if (x < per * D) {
+        const int u = u0 + x / D, d = x % D, f = u * E;
+        if (f < hi)
+          *reinterpret_cast<u32x4 *>(a.v_pages + base(table[f >> sh]) + ((size_t)((f & (page - 1)) / E) * D + d) * 16) = vw[r];
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -229,6 +254,30 @@ SVD unsigned rz_scan(unsigned v, unsigned *s_w, unsigned &total) {
   total = tot;
   return before + inc - v;
 }
+// In place, x[0 .. n) becomes its exclusive prefix and x[n] the total.
+SVD unsigned rz_prefix(unsigned *x, int n, unsigned *s_w) {
+  unsigned run = 0;
+  for (int i0 = 0; i0 < n; i0 += RZ_NT) {
+    const int i = i0 + (int)threadIdx.x;
+    unsigned tot;
+    const unsigned ex = rz_scan(i < n ? x[i] : 0u, s_w, tot);
+    if (i < n) x[i] = run + ex;
+    run += tot;
+  }
+  if (threadIdx.x == 0) x[n] = run;
+  __syncthreads();
+  return run;
+}
+// The i with x[i] <= e < x[i + 1] in a prefix over n.
+SVD int rz_find(const unsigned *x, int n, unsigned e) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (x[m] <= e) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
 SVD int ld_ref(const int32_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 SVD unsigned ld_map(const unsigned *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
@@ -238,83 +287,88 @@ SVD void give_back(const ResizeArgs &a, int p) {
 }
 
 // The pool's books are a few kilobytes and every sequence's pages depend on those of the
-// sequences before it, so one workgroup does them, a wave a sequence at a time where rows
-// are walked: give back, count needs, pick the lowest free pages, hand them out.  Which
-// pages are picked does not depend on the order in which atomics land: the counts are sums,
-// and picking reads the map only after all of them.
+// sequences before it, so one workgroup does them.  Bound: a chain of about ten rounds to
+// memory.  Each round runs over the table entries it concerns laid end to end, whoever's they
+// are, a thread an entry (a wave a sequence, 16 sequences after one another, took 50 us for
+// 256 sequences where this takes 12).  Which pages are picked does not depend on the order in
+// which atomics land: the counts are sums, and picking reads the map only after all of them.
 __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
-  __shared__ int s_need[SV_CACHE_MAX_SEQS];  // pages a sequence needs, then where its share starts
+  extern __shared__ unsigned s_dyn[];
   __shared__ unsigned s_w[RZ_NW];
   __shared__ int s_ncopy, s_served;
-  const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
+  const int tid = threadIdx.x, S = a.S;
   const int sh = a.page_shift, page = 1 << sh;
+  // per sequence: the first entry this call reads (to give back, or at or behind keep_len), the
+  // pages it is to hold (-1: it is left as it is), and prefixes of its entries read, entries to
+  // replace and entries to add
+  int *s_lo = (int *)s_dyn, *s_goal = s_lo + S;
+  unsigned *s_ent = s_dyn + 2 * S, *s_swap = s_ent + S + 1, *s_add = s_swap + S + 1;
+  int *s_bad = (int *)(s_add + S + 1);
   if (tid == 0) s_ncopy = s_served = 0;
 
-  // ---- checks, and pages behind the wanted length given back
-  for (int b = wid; b < a.S; b += RZ_NW) {
+  for (int b = tid; b < S; b += RZ_NT) {
     const int keep = a.keep_len[b], want = a.want_len[b], held = a.seq_pages[b];
-    int32_t *row = a.page_table + (size_t)b * a.W;
-    int code = 0;
     const int goal = (int)(((long long)want + page - 1) >> sh);
+    int lo = 0, g = -1, ent = 0, add = 0, code = 0;
     if (want >= 0) {
       if (held < 0 || held > a.W || goal > a.W || keep < 0 || (long long)keep > ((long long)held << sh)) {
         code = SV_ROW_BAD_LENGTH;
-      } else {  // the entries this call reads: those to give back, and those at or behind keep_len
-        bool bad = false;
-        for (int i = min(goal, keep >> sh) + lane; i < held; i += WAVE) {
-          const unsigned p = (unsigned)row[i];
-          bad |= p >= (unsigned)a.P || ld_ref(&a.ref_count[p]) <= 0;
-        }
-        if (__any(bad)) code = SV_ROW_BAD_PAGE;
+      } else {
+        g = goal;
+        lo = min(goal, keep >> sh);
+        ent = held - lo;
+        add = max(0, goal - held);  // none for want <= keep: goal <= held then
       }
     }
-    if (lane == 0) {
-      a.row_status[b] = code;
-      s_need[b] = (want >= 0 && code == 0) ? 0 : -1;  // -1: left as it is
+    s_lo[b] = lo;
+    s_goal[b] = g;
+    s_ent[b] = (unsigned)ent;
+    s_add[b] = (unsigned)add;
+    s_swap[b] = 0u;
+    s_bad[b] = code;
+  }
+  __syncthreads();
+  const unsigned n_ent = rz_prefix(s_ent, S, s_w);
+  auto row_of = [&](int b) { return a.page_table + (size_t)b * a.W; };
+
+  // ---- the entries' pages
+  for (unsigned e = tid; e < n_ent; e += RZ_NT) {
+    const int b = rz_find(s_ent, S, e);
+    const unsigned p = (unsigned)row_of(b)[s_lo[b] + (int)(e - s_ent[b])];
+    if (p >= (unsigned)a.P || ld_ref(&a.ref_count[p]) <= 0) s_bad[b] = SV_ROW_BAD_PAGE;  // whoever writes: the same
+  }
+  __syncthreads();
+  for (int b = tid; b < S; b += RZ_NT) {
+    a.row_status[b] = s_bad[b];
+    if (s_bad[b]) {
+      s_goal[b] = -1;
+      s_add[b] = 0u;
     }
   }
-  __threadfence_block();
   __syncthreads();
-  for (int b = wid; b < a.S; b += RZ_NW) {
-    if (s_need[b] < 0) continue;
-    const int held = a.seq_pages[b], goal = (int)(((long long)a.want_len[b] + page - 1) >> sh);
-    int32_t *row = a.page_table + (size_t)b * a.W;
-    for (int i = goal + lane; i < held; i += WAVE) {
-      give_back(a, row[i]);
-      row[i] = -1;
+
+  // ---- pages behind the goal given back
+  for (unsigned e = tid; e < n_ent; e += RZ_NT) {
+    const int b = rz_find(s_ent, S, e), i = s_lo[b] + (int)(e - s_ent[b]);
+    if (s_goal[b] >= 0 && i >= s_goal[b]) {
+      give_back(a, row_of(b)[i]);
+      row_of(b)[i] = -1;
     }
   }
   __threadfence();
   __syncthreads();
 
-  // ---- needs: entries to replace (held by others too, at or behind keep_len) and to add
-  auto needs = [&](const int32_t *row, int i, int held) { return i >= held || ld_ref(&a.ref_count[row[i]]) > 1; };
-  for (int b = wid; b < a.S; b += RZ_NW) {
-    if (s_need[b] < 0) continue;
-    const int held = a.seq_pages[b], goal = (int)(((long long)a.want_len[b] + page - 1) >> sh);
-    const int32_t *row = a.page_table + (size_t)b * a.W;
-    int n = 0;
-    if (a.want_len[b] > a.keep_len[b]) {
-      const int first = a.keep_len[b] >> sh;
-      n = max(0, goal - held);
-      for (int i0 = first; i0 < min(held, goal); i0 += WAVE)
-        n += __popcll(__ballot(i0 + lane < min(held, goal) && needs(row, i0 + lane, held)));
-    }
-    if (lane == 0) s_need[b] = n;
+  // ---- entries to replace: others hold the page too, and the sequence is to write behind keep_len
+  auto swaps = [&](int b, int i) {
+    return i < s_goal[b] && a.want_len[b] > a.keep_len[b] && ld_ref(&a.ref_count[row_of(b)[i]]) > 1;
+  };
+  for (unsigned e = tid; e < n_ent; e += RZ_NT) {
+    const int b = rz_find(s_ent, S, e);
+    if (swaps(b, s_lo[b] + (int)(e - s_ent[b]))) atomicAdd(&s_swap[b], 1u);
   }
   __syncthreads();
-  unsigned need_all = 0;
-  {
-    for (int b0 = 0; b0 < a.S; b0 += RZ_NT) {
-      const int b = b0 + tid;
-      unsigned tot;
-      const unsigned ex = rz_scan(b < a.S && s_need[b] > 0 ? (unsigned)s_need[b] : 0u, s_w, tot) + need_all;
-      // where the share starts; a sequence that needs nothing has -2, one left alone -1
-      if (b < a.S && s_need[b] >= 0) s_need[b] = s_need[b] > 0 ? (int)ex : -2;
-      need_all += tot;
-    }
-  }
-  __syncthreads();
+  const unsigned n_add = rz_prefix(s_add, S, s_w), n_swap = rz_prefix(s_swap, S, s_w);
+  const unsigned need_all = n_add + n_swap;
 
   // ---- the lowest free pages, need_all of them or as many as there are
   unsigned found = 0;
@@ -331,52 +385,67 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
   __threadfence_block();
   __syncthreads();
 
-  // ---- handed out, sequence by sequence; the replaced page takes the fresh one's place in alloc
-  for (int b = wid; b < a.S; b += RZ_NW) {
-    const int start = s_need[b];
-    if (start == -1) continue;
-    const int held = a.seq_pages[b], goal = (int)(((long long)a.want_len[b] + page - 1) >> sh);
-    int32_t *row = a.page_table + (size_t)b * a.W;
-    if (start == -2) {
-      if (lane == 0) a.seq_pages[b] = goal;
-      continue;
-    }
-    const int keep = a.keep_len[b], first = keep >> sh;
-    int n = 0;
-    for (int i0 = first; i0 < goal; i0 += WAVE) n += __popcll(__ballot(i0 + lane < goal && needs(row, i0 + lane, held)));
-    if ((unsigned)(start + n) > found) {  // then the shares behind it do not fit either
-      if (lane == 0) {
-        a.row_status[b] = SV_ROW_NO_PAGES;
-        a.seq_pages[b] = min(held, goal);
+  // ---- handed out: a sequence's pages are those from s_swap + s_add on, replaced entries first,
+  // if the free pages reach to its last one (then they reach all sequences before it)
+  auto end_of = [&](int b) { return s_swap[b + 1] + s_add[b + 1]; };
+  auto fits = [&](int b) { return end_of(b) <= found; };
+  auto take = [&](int b, int i, unsigned at, int old) {
+    const int fresh = a.alloc[at];
+    row_of(b)[i] = fresh;
+    a.alloc[at] = old;
+    atomicAnd(&a.free_map[fresh >> 5], ~(1u << (fresh & 31)));
+    __hip_atomic_store(&a.ref_count[fresh], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return fresh;
+  };
+  if (n_swap > 0) {
+    unsigned seen = 0;  // entries replaced so far, in the order of all entries
+    for (unsigned e0 = 0; e0 < n_ent; e0 += RZ_NT) {
+      const unsigned e = e0 + tid;
+      int b = 0, i = 0;
+      bool it = false;
+      if (e < n_ent) {
+        b = rz_find(s_ent, S, e);
+        i = s_lo[b] + (int)(e - s_ent[b]);
+        it = swaps(b, i);
       }
-      continue;
-    }
-    if (lane == 0) atomicMax(&s_served, start + n);
-    int at = start;
-    for (int i0 = first; i0 < goal; i0 += WAVE) {
-      const int i = i0 + lane;
-      const bool take = i < goal && needs(row, i, held);
-      const unsigned long long who = __ballot(take);
-      if (take) {
-        const int s = at + __popcll(who & ((1ull << lane) - 1ull));
-        const int fresh = a.alloc[s], old = i < held ? row[i] : -1;
-        row[i] = fresh;
-        a.alloc[s] = old;
-        if (old >= 0 && i == first && (keep & (page - 1))) a.copies[atomicAdd(&s_ncopy, 1)] = make_int4(old, fresh, keep & (page - 1), 0);
-        atomicAnd(&a.free_map[fresh >> 5], ~(1u << (fresh & 31)));
-        __hip_atomic_store(&a.ref_count[fresh], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      unsigned tot;
+      const unsigned at = seen + rz_scan(it ? 1u : 0u, s_w, tot);
+      if (it && fits(b)) {
+        const int old = row_of(b)[i], keep = a.keep_len[b];
+        const int fresh = take(b, i, at + s_add[b], old);
+        if (i == keep >> sh && (keep & (page - 1))) a.copies[atomicAdd(&s_ncopy, 1)] = make_int4(old, fresh, keep & (page - 1), 0);
       }
-      at += __popcll(who);
+      seen += tot;
     }
-    if (lane == 0) a.seq_pages[b] = goal;
+  }
+  for (unsigned e = tid; e < n_add; e += RZ_NT) {
+    const int b = rz_find(s_add, S, e);
+    if (fits(b)) take(b, a.seq_pages[b] + (int)(e - s_add[b]), s_swap[b + 1] + e, -1);
+  }
+  __syncthreads();
+  for (int b = tid; b < S; b += RZ_NT) {
+    const int goal = s_goal[b];
+    if (goal < 0) continue;
+    const bool some = s_swap[b + 1] + s_add[b + 1] > s_swap[b] + s_add[b];
+    if (some && !fits(b)) {
+      a.row_status[b] = SV_ROW_NO_PAGES;
+      a.seq_pages[b] = min(a.seq_pages[b], goal);
+    } else {
+      a.seq_pages[b] = goal;
+      if (some) atomicMax(&s_served, (int)end_of(b));
+    }
   }
   __threadfence();
   __syncthreads();
   // ---- replaced pages lose a holder (only now: the counts above are those after giving back)
-  for (int k = tid; k < s_served; k += RZ_NT)
-    if (a.alloc[k] >= 0) give_back(a, a.alloc[k]);
+  if (n_swap > 0)
+    for (int k = tid; k < s_served; k += RZ_NT)
+      if (a.alloc[k] >= 0) give_back(a, a.alloc[k]);
   if (tid == 0) *a.n_copy = s_ncopy;
 }
+
+// Dynamic LDS of k_cache_resize.
+inline unsigned resize_lds(int S) { return (unsigned)(6 * S + 3) * 4; }
 
 struct CopyArgs {
   char *k_pages, *v_pages;
@@ -386,7 +455,7 @@ struct CopyArgs {
   Pool pool;
 };
 
-constexpr int COPY_WGS = 2048;  // 8 a CU; the host does not know how many copies there are
+constexpr int COPY_WGS = 1024;  // 4 a CU, whatever there is to copy: the host does not know
 
 // The kept slots of a page into another: a workgroup moves one head of one layer at a time,
 // COPY_STEP 16-byte units a thread in flight.  Keys: t runs fastest, kept * 16 bytes together.
@@ -494,7 +563,7 @@ using namespace sv;
 using sv_host::align256;
 
 bool pool_ok(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) {
-  return Hkv >= 1 && D >= 16 && D <= 1024 && D % 16 == 0 && page >= 16 && page <= 256 && (page & (page - 1)) == 0 &&
+  return Hkv >= 1 && D >= 16 && D <= COMMIT_R * NT && D % 16 == 0 && page >= 16 && page <= 256 && (page & (page - 1)) == 0 &&
          P >= 1 && W >= 1 && (long long)W * page <= 0x7fffffffLL - 4096;
 }
 
@@ -503,9 +572,10 @@ Pool pool_of(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) {
 }
 
 template <typename A>
-sv_status launch(const void *fn, A &a, long long grid, int block, void *stream) {
+sv_status launch(const void *fn, A &a, long long grid, int block, void *stream, unsigned lds = 0) {
   sv_host::Launcher L{(hipStream_t)stream, nullptr, 0};
   L.block = block;
+  L.lds = lds;
   void *args[] = {&a};
   L.go(fn, (unsigned)grid, args);
   return L.e == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
@@ -617,7 +687,7 @@ sv_status spec_cache_resize(int32_t *page_table, int32_t *seq_pages, int32_t *re
   ResizeArgs a = {page_table, seq_pages, ref_count, (unsigned *)free_map, keep_len, want_len, S, num_pages, table_width,
                   __builtin_ctz((unsigned)page_size), row_status, (int32_t *)(base + p.alloc), (int4 *)(base + p.copies),
                   (int32_t *)(base + p.n_copy)};
-  const sv_status st = launch((const void *)&k_cache_resize, a, 1, RZ_NT, stream);
+  const sv_status st = launch((const void *)&k_cache_resize, a, 1, RZ_NT, stream, resize_lds(S));
   if (st != SV_OK || L == 0) return st;
   CopyArgs c = {static_cast<char *>(k_pages), static_cast<char *>(v_pages), a.copies, a.n_copy, (unsigned)L,
                 pool_of(Hkv, D, page_size, num_pages, table_width)};

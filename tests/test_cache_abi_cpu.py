@@ -62,7 +62,7 @@ def append(lib, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dt=2), 3), (dict(B=0), 2), (dict(N=0), 2), (dict(N=1025), 2), (dict(Hkv=0), 2), (dict(D=8), 2), (dict(D=72), 2),
-    (dict(D=2048), 2), (dict(page=17), 2), (dict(P=0), 2), (dict(W=0), 2), (dict(B=1 << 30, Hkv=1 << 20), 2),
+    (dict(D=528), 2), (dict(page=17), 2), (dict(P=0), 2), (dict(W=0), 2), (dict(B=1 << 30, Hkv=1 << 20), 2),
     (dict(k=None), 1), (dict(v=None), 1), (dict(kp=None), 1), (dict(vp=None), 1), (dict(table=None), 1), (dict(lens=None), 1),
     (dict(st=None), 1), (dict(k=FAKE + 2), 6), (dict(v=FAKE + 8), 6), (dict(kp=FAKE + 4), 6), (dict(vn=255), 6), (dict(kb=3), 6),
 ])
@@ -96,7 +96,7 @@ def resize(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(dt=5), 3), (dict(S=0), 2), (dict(S=8193), 2), (dict(L=-1), 2), (dict(D=0), 2), (dict(page=100), 2), (dict(P=0), 2),
+    (dict(dt=5), 3), (dict(S=0), 2), (dict(S=4097), 2), (dict(L=-1), 2), (dict(D=0), 2), (dict(page=100), 2), (dict(P=0), 2),
     (dict(W=-3), 2), (dict(table=None), 1), (dict(held=None), 1), (dict(ref=None), 1), (dict(free=None), 1), (dict(keep=None), 1),
     (dict(want=None), 1), (dict(kp=None), 1), (dict(vp=None), 1), (dict(st=None), 1), (dict(ws=None), 1), (dict(vp=FAKE + 8), 6),
     (dict(nbytes=256), 5), (dict(ws=FAKE + 16), 5), (dict(L=0, kp=None, vp=None, Hkv=0, D=0, nbytes=0), 5),
@@ -112,7 +112,7 @@ def fork(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(F=0), 2), (dict(F=8193), 2), (dict(S=0), 2), (dict(S=8193), 2), (dict(P=0), 2), (dict(W=0), 2), (dict(table=None), 1),
+    (dict(F=0), 2), (dict(F=4097), 2), (dict(S=0), 2), (dict(S=4097), 2), (dict(P=0), 2), (dict(W=0), 2), (dict(table=None), 1),
     (dict(held=None), 1), (dict(ref=None), 1), (dict(lens=None), 1), (dict(src=None), 1), (dict(dst=None), 1), (dict(st=None), 1),
 ])
 def test_fork_refuses(lib, kw, status):
@@ -143,7 +143,7 @@ def test_checks_of_the_binding():
     """The checks themselves, on CPU tensors (a device tensor differs in its address alone)."""
     import torch
     from rejection_sampling_verify_02_amd import cache
-    cpu = torch.device("cpu")
+    cpu = -1  # what get_device() says of CPU tensors
     kp, vp = sv.empty_pages(2, 4, 3, 64, 32, torch.float32, "cpu")
     assert kp.shape == (2, 4, 3, 16, 32, 4) and vp.shape == (2, 4, 3, 8, 64, 4)
     assert cache._pages(kp, vp, 6, torch.float32, cpu) == (4, 3, 64, 32)
@@ -155,14 +155,14 @@ def test_checks_of_the_binding():
     with pytest.raises(TypeError):
         cache._pages(kp, vp, 6, torch.bfloat16, cpu)
     x = torch.zeros((2, 3, 8, 64))
-    assert cache._rows(x, "x", 2, 3, 8, 64, torch.float32, cpu)[1:] == (3 * 8 * 64, 8 * 64)
-    assert cache._rows(x[:, :1], "x", 2, 1, 8, 64, torch.float32, cpu)[1:] == (3 * 8 * 64, 0)
-    assert cache._rows(x[:, :, 2:4], "x", 2, 3, 2, 64, torch.float32, cpu)[1:] == (3 * 8 * 64, 8 * 64)
+    assert cache._rows(x, "x", (2, 3, 8, 64), torch.float32, cpu)[1:] == (3 * 8 * 64, 8 * 64)
+    assert cache._rows(x[:, :1], "x", (2, 1, 8, 64), torch.float32, cpu)[1:] == (3 * 8 * 64, 0)
+    assert cache._rows(x[:, :, 2:4], "x", (2, 3, 2, 64), torch.float32, cpu)[1:] == (3 * 8 * 64, 8 * 64)
     for bad in (x[:, :, ::2], x[..., ::2], x.transpose(1, 2)):
         with pytest.raises(ValueError):
-            cache._rows(bad, "x", *bad.shape, torch.float32, cpu)
+            cache._rows(bad, "x", bad.shape, torch.float32, cpu)
     with pytest.raises(TypeError):
-        cache._rows(x, "x", 2, 3, 8, 64, torch.bfloat16, cpu)
+        cache._rows(x, "x", (2, 3, 8, 64), torch.bfloat16, cpu)
     i = torch.zeros((2, 3), dtype=torch.int32)
     assert cache._ints(i, "i", (2, 3), cpu) == i.data_ptr() and cache._ints(None, "i", (2, 3), cpu, True) is None
     for bad, e in ((i.long(), TypeError), (None, TypeError), (i[:, ::2], ValueError), (i.t().contiguous().t(), ValueError)):

@@ -47,7 +47,7 @@ def to_dev(x, esz, dev):
     (3, 64, 64, 70, [0, 60, 61], None),
     (1, 256, 16, 200, [5, 0], [200, 123]),
     (2, 16, 256, 9, [250, 300], None),
-    (1, 1024, 16, 3, [14, 2], None),
+    (1, 512, 16, 3, [14, 2], None),
     (1, 64, 128, 1024, [1], None),
 ])
 def test_append(dev, esz, H, D, page, N, lens, news):
@@ -105,7 +105,7 @@ def test_append_codes(dev):
 
 @pytest.mark.parametrize("esz", [2, 4])
 @pytest.mark.parametrize("L,H,D,page,N,seed", [(1, 1, 64, 16, 2, 0), (3, 2, 128, 16, 40, 1), (2, 1, 64, 32, 33, 2),
-                                              (2, 3, 256, 64, 100, 3), (1, 1, 16, 16, 1024, 4), (1, 1, 1024, 128, 17, 5)])
+                                              (2, 3, 256, 64, 100, 3), (1, 1, 16, 16, 1024, 4), (1, 1, 512, 128, 17, 5), (1, 2, 48, 16, 25, 6)])
 def test_commit(dev, esz, L, H, D, page, N, seed):
     import rejection_sampling_verify_02_amd as sv
     pick, rng = random.Random(seed), np.random.default_rng(seed)
@@ -273,8 +273,8 @@ def test_books_of_a_large_pool(dev):
 
 
 def test_many_sequences(dev):
-    """More sequences than the workgroup has threads."""
-    S, P, W, page = 2500, 4000, 3, 16
+    """More sequences than the workgroup has threads: as many as a call takes."""
+    S, P, W, page = 4096, 6500, 3, 16
     x = Both(dev, P, S, W, page, L=1, H=1, D=16)
     want = [(7 * b) % 40 for b in range(S)]
     status = x.resize([0] * S, want)
