@@ -18,7 +18,8 @@
 //                and they join through LDS at the end.
 //   k_attn_wide  more rows: the waves own rows instead, and share each tile through LDS, so
 //                that the L2 and L1 are read once for 64 or 128 rows.
-// The tiles of all units are laid end to end and cut into equal shares, one a workgroup,
+// The tiles of all units are laid end to end, in rounds of what a workgroup takes at a time,
+// and cut into equal shares, one a workgroup,
 // whatever the lengths of the sequences (a share may end in the middle of one unit and go on
 // with the next); units that several workgroups streamed are joined by k_attn_join.  Sums run
 // in a fixed order: same call, same bits.
@@ -98,12 +99,15 @@ SVD Span span_of(const AttnArgs &a, const Seq &s, int rt) {
   p.tiles = p.n_sink + (end + TILE - 1) / TILE - p.first;
   return p;
 }
-template <int RT>
-SVD unsigned seq_tiles(const AttnArgs &a, int b) {
-  const Seq s = seq_of(a, b);
+// Shares are counted in rounds of ROUND tiles, what a workgroup takes at a time: a unit begins
+// with a round of its own.
+template <int ROUND>
+SVD unsigned rounds_of(const Span &p) { return (unsigned)(p.tiles + ROUND - 1) / ROUND; }
+template <int RT, int ROUND>
+SVD unsigned head_rounds(const AttnArgs &a, const Seq &s) {
   unsigned t = 0;
-  for (int rt = 0; rt < a.n_rt; ++rt) t += (unsigned)span_of<RT>(a, s, rt).tiles;
-  return t * (unsigned)a.Hkv;
+  for (int rt = 0; rt < a.n_rt; ++rt) t += rounds_of<ROUND>(span_of<RT>(a, s, rt));
+  return t;
 }
 
 // Over the four lanes of a column (lane % 16 equal): the swaps exchange halves of lane rows
@@ -417,18 +421,18 @@ struct RowSink {
 // sink(row, exponent, sum of weights).  begin is called for every segment, also one whose rows
 // are no new tokens (its tile 0 is then some page's, and not used): what it leaves in registers
 // would have to be kept from segment to segment otherwise.
-template <typename T, int D, int RT, unsigned MIN_SHARE, typename Begin, typename Run>
+template <typename T, int D, int RT, int ROUND, typename Begin, typename Run>
 SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run run) {
   constexpr int ESZ = (int)sizeof(T);
   const int tid = threadIdx.x;
   unsigned T_all = 0, v = 0, ex = 0;
   for (int b0 = 0; b0 < a.B; b0 += NT) {
-    v = (b0 + tid < a.B) ? seq_tiles<RT>(a, b0 + tid) : 0u;
+    v = (b0 + tid < a.B) ? head_rounds<RT, ROUND>(a, seq_of(a, b0 + tid)) * (unsigned)a.Hkv : 0u;
     unsigned tot;
     ex = block_excl_scan(v, s.w, tot);
     T_all += tot;
   }
-  const unsigned share = max((T_all + a.grid - 1) / a.grid, MIN_SHARE);
+  const unsigned share = (T_all + a.grid - 1) / a.grid;
   // Consecutive shares on one XCD (block p runs on XCD p % LANES), as many on each: the row
   // tiles of a key head read the same keys and values through that XCD's L2.
   const unsigned shares = (T_all + share - 1) / share, per_xcd = (shares + LANES - 1) / LANES;
@@ -444,7 +448,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   } else {
     unsigned seen = 0;
     for (int b0 = 0; seen <= pos; b0 += NT) {
-      v = (b0 + tid < a.B) ? seq_tiles<RT>(a, b0 + tid) : 0u;
+      v = (b0 + tid < a.B) ? head_rounds<RT, ROUND>(a, seq_of(a, b0 + tid)) * (unsigned)a.Hkv : 0u;
       unsigned tot;
       ex = seen + block_excl_scan(v, s.w, tot);
       if (pos >= ex && pos < ex + v) {
@@ -457,32 +461,33 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   __syncthreads();
   Segment g;
   g.b = __builtin_amdgcn_readfirstlane((int)s.at[0]);
-  unsigned off = (unsigned)__builtin_amdgcn_readfirstlane((int)s.at[1]);  // tiles of the sequence before pos
+  unsigned off = (unsigned)__builtin_amdgcn_readfirstlane((int)s.at[1]);  // rounds of the sequence before pos
   g.sq = seq_of(a, g.b);
   int code = 0, code_b = -1;           // the code of sequence code_b
   int books_b = -1, books_rt = -1;     // the row tile whose books are in LDS
   while (pos < pos_end) {
-    unsigned per_head = 0;
-    for (int rt = 0; rt < a.n_rt; ++rt) per_head += (unsigned)span_of<RT>(a, g.sq, rt).tiles;
+    const unsigned per_head = head_rounds<RT, ROUND>(a, g.sq);
     if (off >= per_head * (unsigned)a.Hkv) {
       off -= per_head * (unsigned)a.Hkv;
       g.sq = seq_of(a, ++g.b);
       continue;
     }
     g.h = (int)(off / per_head);
-    g.l0 = (int)(off - (unsigned)g.h * per_head);
+    unsigned r0 = off - (unsigned)g.h * per_head;
     g.rt = 0;
     g.sp = span_of<RT>(a, g.sq, 0);
-    while (g.l0 >= g.sp.tiles) {
-      g.l0 -= g.sp.tiles;
+    while (r0 >= rounds_of<ROUND>(g.sp)) {
+      r0 -= rounds_of<ROUND>(g.sp);
       g.sp = span_of<RT>(a, g.sq, ++g.rt);
     }
-    g.l1 = (int)min((unsigned)g.sp.tiles, (unsigned)g.l0 + (pos_end - pos));
+    const unsigned rounds = rounds_of<ROUND>(g.sp), r1 = min(rounds, r0 + (pos_end - pos));
+    g.l0 = (int)(r0 * ROUND);
+    g.l1 = min(g.sp.tiles, (int)(r1 * ROUND));
     g.table = (TablePtr)(a.page_table + (size_t)g.b * a.W);
     g.par = a.parent ? a.parent + (size_t)g.b * a.N : nullptr;
     g.words = (g.sq.m + 31) >> 5;
     g.masks = a.window > 0 || g.tile(g.l1 - 1) + TILE > g.sq.len;
-    const bool whole = g.l0 == 0 && g.l1 == g.sp.tiles;
+    const bool whole = r0 == 0 && r1 == rounds;
 
     __syncthreads();  // the previous segment is done with the LDS
     begin(g);
@@ -492,7 +497,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     }
     if (tid == 0 && g.h == 0 && g.rt == 0 && g.l0 == 0) a.row_status[g.b] = code;
     if (tid == 0 && g.l0 == 0) {
-      const unsigned last = (pos + (unsigned)g.sp.tiles - 1) / share;
+      const unsigned last = (pos + rounds - 1) / share;
       a.desc[(g.b * a.Hkv + g.h) * a.n_rt + g.rt] =
           make_uint4(w, last - w + 1, (code ? 0x80000000u : 0u) | (unsigned)(g.sq.ok ? g.sq.m : 0), 0u);
     }
@@ -519,8 +524,8 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
       return to;
     };
     run(g, code, sink);
-    pos += (unsigned)(g.l1 - g.l0);
-    off += (unsigned)(g.l1 - g.l0);
+    pos += r1 - r0;
+    off += r1 - r0;
   }
 }
 
@@ -881,7 +886,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     fetch_stage(sg, sg.l0, s_a);
   };
 
-  attn_share<T, D, RT, 1>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+  attn_share<T, D, RT, ST>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
     rows.clear();
     if (sg.sp.i0 > sg.sp.i1 || code != 0) {
       hand_over();  // what begin sent for has come before the buffers are used again
@@ -1097,8 +1102,8 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
     return p.wide ? wide_occ<T, decltype(d)::value, decltype(r)::value>() : attn_occ<T, decltype(d)::value, decltype(r)::value>();
   });
   long long grid = 256LL * occ;  // one resident set of the device's 256 CUs
-  const long long least = p.wide ? 1 : NW;  // tiles of a share
-  const long long need = (p.units * most + least - 1) / least;
+  const long long round = p.wide ? (D * esz <= 256 ? 2 : 1) : NW;  // tiles of a round, the least share
+  const long long need = p.units * ((most + round - 1) / round);
   if (need < grid) grid = need;
   p.grid = (unsigned)((grid + LANES - 1) / LANES * LANES);
   size_t o = 0;
