@@ -99,14 +99,17 @@ SVD Span span_of(const AttnArgs &a, const Seq &s, int rt) {
   p.tiles = p.n_sink + (end + TILE - 1) / TILE - p.first;
   return p;
 }
-// Shares are counted in rounds of ROUND tiles, what a workgroup takes at a time: a unit begins
-// with a round of its own.
+// Work is counted in rounds of ROUND tiles, what a workgroup takes at a time; a unit begins with
+// a round of its own.
 template <int ROUND>
 SVD unsigned rounds_of(const Span &p) { return (unsigned)(p.tiles + ROUND - 1) / ROUND; }
+// The parts that a unit of r rounds is cut into, at most `most` rounds each, and a head's row
+// tiles together (most = 1: its rounds).
+SVD unsigned parts_of(unsigned r, unsigned most) { return (r + most - 1) / most; }
 template <int RT, int ROUND>
-SVD unsigned head_rounds(const AttnArgs &a, const Seq &s) {
+SVD unsigned head_parts(const AttnArgs &a, const Seq &s, unsigned most) {
   unsigned t = 0;
-  for (int rt = 0; rt < a.n_rt; ++rt) t += rounds_of<ROUND>(span_of<RT>(a, s, rt));
+  for (int rt = 0; rt < a.n_rt; ++rt) t += parts_of(rounds_of<ROUND>(span_of<RT>(a, s, rt)), most);
   return t;
 }
 
@@ -315,7 +318,7 @@ struct SharedBooks {
   uint16_t *par;   // [N] parents (node 0's is not kept)
   uint16_t *dep;   // [nodes of a row tile] their depths
   unsigned *anc;   // [nodes of a row tile][words] the nodes each of them sees
-  unsigned *w, *at;  // [NW], [2]
+  unsigned *w, *at, *tries;  // [NW], [2], [4]
   int *bad;
 };
 SV_HD int tile_nodes(int RT, int N, int group) {
@@ -324,7 +327,7 @@ SV_HD int tile_nodes(int RT, int N, int group) {
 }
 SV_HD unsigned books_bytes(int RT, int N, int group, bool tree) {
   const unsigned n = tree ? (unsigned)tile_nodes(RT, N, group) : 0u;
-  return (NW + 4) * 4 + n * ((N + 31) / 32) * 4 + ((n + (tree ? (unsigned)N : 0u) + 1) / 2) * 4;
+  return (NW + 12) * 4 + n * ((N + 31) / 32) * 4 + ((n + (tree ? (unsigned)N : 0u) + 1) / 2) * 4;
 }
 SVD SharedBooks books_at(unsigned *p, int RT, int N, int group) {
   const int n = tile_nodes(RT, N, group);
@@ -332,7 +335,8 @@ SVD SharedBooks books_at(unsigned *p, int RT, int N, int group) {
   s.w = p;
   s.at = p + NW;
   s.bad = reinterpret_cast<int *>(p + NW + 2);
-  s.anc = p + NW + 4;
+  s.tries = p + NW + 4;
+  s.anc = p + NW + 12;
   s.dep = reinterpret_cast<uint16_t *>(s.anc + n * ((N + 31) / 32));
   s.par = s.dep + n;
   return s;
@@ -415,31 +419,81 @@ struct RowSink {
   }
 };
 
+// The least rounds of a part: a part's sums are written and read once more when its unit is
+// joined, and should be no more than half of the keys and values they come from.
+template <typename T, int RT, int ROUND>
+constexpr unsigned least_part() {
+  constexpr int n = RT * 4 / (ROUND * TILE * (int)sizeof(T));
+  return n > 1 ? n : 1;
+}
+
 // Walks the workgroup's share, a segment at a time: begin(segment) sends for the first tiles,
 // and while they come the sequence is checked and its tree laid out; run(segment, code, sink)
 // then computes the rows' sums over the segment's slots and puts every row of the tile into
 // sink(row, exponent, sum of weights).  begin is called for every segment, also one whose rows
 // are no new tokens (its tile 0 is then some page's, and not used): what it leaves in registers
 // would have to be kept from segment to segment otherwise.
-template <typename T, int D, int RT, int ROUND, typename Begin, typename Run>
+template <typename T, int D, int RT, int ROUND, bool WIDE, typename Begin, typename Run>
 SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run run) {
   constexpr int ESZ = (int)sizeof(T);
   const int tid = threadIdx.x;
-  unsigned T_all = 0, v = 0, ex = 0;
-  for (int b0 = 0; b0 < a.B; b0 += NT) {
-    v = (b0 + tid < a.B) ? head_rounds<RT, ROUND>(a, seq_of(a, b0 + tid)) * (unsigned)a.Hkv : 0u;
-    unsigned tot;
-    ex = block_excl_scan(v, s.w, tot);
-    T_all += tot;
+  // The parts' size.  Where a few rounds more than an equal share cut the units into no more
+  // parts than there are workgroups, every workgroup gets one part: one that goes on with a
+  // second unit begins anew there (in k_attn_wide about 6 us, 3 rounds' time: the 32 windowed
+  // sequences took 59 us with shares that run on where they take 52 so).  Otherwise parts are
+  // single rounds and shares of them as equal as can be (units of 257 to 16001 slots, one a
+  // workgroup: 392 us, so 343).
+  constexpr unsigned LEAST = least_part<T, RT, ROUND>();
+  const bool aligned = (unsigned)a.B * (unsigned)(a.Hkv * a.n_rt) <= a.grid && ((long long)a.W << a.page_shift) < (1 << 27);
+  unsigned v = 0, ex = 0, total = 0;
+  auto scan = [&](unsigned most) {  // of every sequence's parts; for the first NT (all of them, mostly) v and ex stay
+    total = 0;
+    for (int b0 = (a.B - 1) / NT * NT; b0 >= 0; b0 -= NT) {
+      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most) * (unsigned)a.Hkv : 0u;
+      unsigned tot;
+      ex = block_excl_scan(v, s.w, tot);
+      total += tot;
+    }
+  };
+  scan(1u);
+  unsigned share = (total + a.grid - 1) / a.grid, most = 1;  // rounds a share, rounds a part
+  if (aligned && share > 1u) {
+    constexpr int TRY = 4;
+    const unsigned tries = WIDE ? TRY : min(1u + share / 16, (unsigned)TRY);
+    unsigned n[TRY];
+#pragma unroll
+    for (int k = 0; k < TRY; ++k) n[k] = 0;
+    for (int b = tid; b < a.B; b += NT) {
+      const Seq sq = seq_of(a, b);
+#pragma unroll
+      for (int k = 0; k < TRY; ++k) n[k] += head_parts<RT, ROUND>(a, sq, max(share + k, LEAST)) * (unsigned)a.Hkv;
+    }
+    if (tid < TRY) s.tries[tid] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < TRY; ++k) {
+      const unsigned t = scan_add_u(n[k]);
+      if (lane_id() == WAVE - 1) atomicAdd(&s.tries[k], t);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = TRY - 1; k >= 0; --k)
+      if (k < (int)tries && s.tries[k] <= a.grid) most = max(share + k, LEAST);
+    if (most > 1u) {
+      scan(most);
+      share = 1;
+    }
+  } else if (aligned && LEAST > 1) {
+    most = LEAST;
+    scan(most);
   }
-  const unsigned share = (T_all + a.grid - 1) / a.grid;
   // Consecutive shares on one XCD (block p runs on XCD p % LANES), as many on each: the row
   // tiles of a key head read the same keys and values through that XCD's L2.
-  const unsigned shares = (T_all + share - 1) / share, per_xcd = (shares + LANES - 1) / LANES;
+  const unsigned shares = (total + share - 1) / share, per_xcd = (shares + LANES - 1) / LANES;
   const unsigned w = (blockIdx.x % LANES) * per_xcd + blockIdx.x / LANES;
   if (blockIdx.x / LANES >= per_xcd || w >= shares) return;
   unsigned pos = w * share;
-  const unsigned pos_end = min(T_all, pos + share);
+  const unsigned pos_end = min(total, pos + share);
   if (a.B <= NT) {
     if (pos >= ex && pos < ex + v) {
       s.at[0] = (unsigned)tid;
@@ -448,7 +502,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   } else {
     unsigned seen = 0;
     for (int b0 = 0; seen <= pos; b0 += NT) {
-      v = (b0 + tid < a.B) ? head_rounds<RT, ROUND>(a, seq_of(a, b0 + tid)) * (unsigned)a.Hkv : 0u;
+      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most) * (unsigned)a.Hkv : 0u;
       unsigned tot;
       ex = seen + block_excl_scan(v, s.w, tot);
       if (pos >= ex && pos < ex + v) {
@@ -461,12 +515,12 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   __syncthreads();
   Segment g;
   g.b = __builtin_amdgcn_readfirstlane((int)s.at[0]);
-  unsigned off = (unsigned)__builtin_amdgcn_readfirstlane((int)s.at[1]);  // rounds of the sequence before pos
+  unsigned off = (unsigned)__builtin_amdgcn_readfirstlane((int)s.at[1]);  // parts of the sequence before pos
   g.sq = seq_of(a, g.b);
   int code = 0, code_b = -1;           // the code of sequence code_b
   int books_b = -1, books_rt = -1;     // the row tile whose books are in LDS
   while (pos < pos_end) {
-    const unsigned per_head = head_rounds<RT, ROUND>(a, g.sq);
+    const unsigned per_head = head_parts<RT, ROUND>(a, g.sq, most);
     if (off >= per_head * (unsigned)a.Hkv) {
       off -= per_head * (unsigned)a.Hkv;
       g.sq = seq_of(a, ++g.b);
@@ -476,18 +530,22 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     unsigned r0 = off - (unsigned)g.h * per_head;
     g.rt = 0;
     g.sp = span_of<RT>(a, g.sq, 0);
-    while (r0 >= rounds_of<ROUND>(g.sp)) {
-      r0 -= rounds_of<ROUND>(g.sp);
+    unsigned rounds = rounds_of<ROUND>(g.sp), parts = parts_of(rounds, most);
+    while (r0 >= parts) {
+      r0 -= parts;
       g.sp = span_of<RT>(a, g.sq, ++g.rt);
+      rounds = rounds_of<ROUND>(g.sp);
+      parts = parts_of(rounds, most);
     }
-    const unsigned rounds = rounds_of<ROUND>(g.sp), r1 = min(rounds, r0 + (pos_end - pos));
-    g.l0 = (int)(r0 * ROUND);
-    g.l1 = min(g.sp.tiles, (int)(r1 * ROUND));
+    const unsigned r1 = min(parts, r0 + (pos_end - pos));
+    // parts of a unit differ by a round at most (parts <= grid and rounds < 2^22 where they are not the same)
+    g.l0 = (int)((parts == rounds ? r0 : r0 * rounds / parts) * ROUND);
+    g.l1 = min(g.sp.tiles, (int)((parts == rounds ? r1 : r1 * rounds / parts) * ROUND));
     g.table = (TablePtr)(a.page_table + (size_t)g.b * a.W);
     g.par = a.parent ? a.parent + (size_t)g.b * a.N : nullptr;
     g.words = (g.sq.m + 31) >> 5;
     g.masks = a.window > 0 || g.tile(g.l1 - 1) + TILE > g.sq.len;
-    const bool whole = r0 == 0 && r1 == rounds;
+    const bool whole = r0 == 0 && r1 == parts;
 
     __syncthreads();  // the previous segment is done with the LDS
     begin(g);
@@ -497,7 +555,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     }
     if (tid == 0 && g.h == 0 && g.rt == 0 && g.l0 == 0) a.row_status[g.b] = code;
     if (tid == 0 && g.l0 == 0) {
-      const unsigned last = (pos + rounds - 1) / share;
+      const unsigned last = (pos + parts - 1) / share;
       a.desc[(g.b * a.Hkv + g.h) * a.n_rt + g.rt] =
           make_uint4(w, last - w + 1, (code ? 0x80000000u : 0u) | (unsigned)(g.sq.ok ? g.sq.m : 0), 0u);
     }
@@ -708,7 +766,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
     rows.load(a, sg, sg.rt * RT, m, g);
   };
 
-  attn_share<T, D, RT, NW>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+  attn_share<T, D, RT, NW, false>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
     rows.clear();
     int l = sg.l0 + wid;
     if (sg.sp.i0 <= sg.sp.i1 && code == 0 && l < sg.l1) {
@@ -886,7 +944,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     fetch_stage(sg, sg.l0, s_a);
   };
 
-  attn_share<T, D, RT, ST>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+  attn_share<T, D, RT, ST, true>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
     rows.clear();
     if (sg.sp.i0 > sg.sp.i1 || code != 0) {
       hand_over();  // what begin sent for has come before the buffers are used again
