@@ -95,11 +95,11 @@ def _pages(k_pages, v_pages, dims: int, dtype, dev: int):
     """(P, Hkv, D, page_size) of a cache of `dims` dimensions (5: a layer, 6: all of them)."""
     ks, vs = k_pages.shape, v_pages.shape
     E = 8 if dtype is _BF16 else 4
-    if len(ks) == len(vs) == dims and k_pages.dtype is dtype and v_pages.dtype is dtype and k_pages.get_device() == dev \
-            and v_pages.get_device() == dev and k_pages.is_contiguous() and v_pages.is_contiguous():
-        P, H, U, page, e = ks[-5:]
-        if e == E and page % E == 0 and vs == ks[:-3] + (page // E, U * E, E):
-            return P, H, U * E, page
+    if len(ks) == dims:
+        *lead, U, page, e = ks
+        if e == E and page % E == 0 and vs == (*lead, page // E, U * E, E) and k_pages.dtype is dtype and v_pages.dtype is dtype \
+                and k_pages.get_device() == dev and v_pages.get_device() == dev and k_pages.is_contiguous() and v_pages.is_contiguous():
+            return lead[-2], lead[-1], U * E, page
     if len(ks) != dims or len(vs) != dims:
         raise ValueError(f"k_pages and v_pages must have {dims} dimensions")
     if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
@@ -142,16 +142,13 @@ def _device(t, name: str) -> int:
     return t.get_device()
 
 
-def _launch(dev: int, stream, call, *args):
-    """call(raw stream, *args) with the tensors' device current and, given a raw stream of the
-    caller's, that stream current too: what the call allocates then belongs to it."""
-    if stream is None:
-        if dev == _current_device():
-            return call(_raw_stream(dev), *args)
-        with torch.cuda.device(dev):
-            return call(_raw_stream(dev), *args)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
-        return call(stream, *args)
+def _elsewhere(dev: int, stream):
+    """None if a call may allocate and launch as things are; else the context to do it in: the
+    tensors' device current and, given a raw stream of the caller's, that stream current too, so
+    that what the call allocates belongs to it."""
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev))
+    return None if dev == _current_device() else torch.cuda.device(dev)
 
 
 def _work(workspace, nbytes: int, dev: int):
@@ -203,6 +200,11 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
     then returned last.
     """
     dev = _device(q, "q")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, parent=parent, n_new=n_new, scale=scale,
+                                        window=window, sinks=sinks, workspace=workspace, out=out, events=events)
     dt = _code(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [B, N, Hq, D]")
@@ -224,21 +226,18 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
         _rows(out[0], "out", shape, q.dtype, dev)
         _ints(out[1], "row_status", seqs, dev)
 
-    def call(raw):
-        o, st = out or (torch.empty(shape, dtype=q.dtype, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
-        ws = _work(workspace, _attention_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
-        args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, news, par, B, N, Hq, Hkv, D, page, P, W,
-                scale, window, sinks, o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel(), raw)
-        if events is None:
-            rc = load_library().spec_paged_attention(*args)
-            if rc:
-                _raise(rc)
-            return o, st
-        n = ctypes.c_int32(0)
-        _raise(load_library().spec_paged_attention_timed(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
-        return o, st, n.value
-
-    return _launch(dev, stream, call)
+    o, st = out or (torch.empty(shape, dtype=q.dtype, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
+    ws = _work(workspace, _attention_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
+    args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, news, par, B, N, Hq, Hkv, D, page, P, W,
+            scale, window, sinks, o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if events is None:
+        rc = load_library().spec_paged_attention(*args)
+        if rc:
+            _raise(rc)
+        return o, st
+    n = ctypes.c_int32(0)
+    _raise(load_library().spec_paged_attention_timed(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
+    return o, st, n.value
 
 
 def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=None, stream=None, out=None):
@@ -247,6 +246,10 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=No
     k_pages and v_pages (see include/spec_cache.h).  Returns row_status [B] int32, which ``out``
     may supply."""
     dev = _device(k, "k")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, n_new=n_new, out=out)
     dt = _code(k, "k")
     if k.dim() != 4:
         raise ValueError("k must be [B, N, Hkv, D]")
@@ -263,15 +266,12 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=No
     if out is not None:
         _ints(out, "row_status", seqs, dev)
 
-    def call(raw):
-        st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
-        rc = load_library().spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens, news,
-                                              B, N, Hkv, D, page, P, W, st.data_ptr(), raw)
-        if rc:
-            _raise(rc)
-        return st
-
-    return _launch(dev, stream, call)
+    st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
+    rc = load_library().spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens, news,
+                                          B, N, Hkv, D, page, P, W, st.data_ptr(), _raw_stream(dev))
+    if rc:
+        _raise(rc)
+    return st
 
 
 def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes=None, *, max_new: int | None = None,
@@ -282,6 +282,10 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
     and ``max_new``, the N = G + 1 new tokens that were verified.  Returns (new_len [B],
     row_status [B]) int32; ``out`` may supply them (for chains new_len may be cache_len itself)."""
     dev = _device(k_pages, "k_pages")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes, max_new=max_new, out=out)
     dt = _code(k_pages, "k_pages")
     P, Hkv, D, page = _pages(k_pages, v_pages, 6, k_pages.dtype, dev)
     table, W = _table(page_table, dev)
@@ -301,15 +305,12 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
         _ints(out[0], "new_len", seqs, dev)
         _ints(out[1], "row_status", seqs, dev)
 
-    def call(raw):
-        n, st = out or (torch.empty(seqs, dtype=_I32, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
-        rc = load_library().spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, k_pages.shape[0],
-                                              B, N, Hkv, D, page, P, W, n.data_ptr(), st.data_ptr(), raw)
-        if rc:
-            _raise(rc)
-        return n, st
-
-    return _launch(dev, stream, call)
+    n, st = out or (torch.empty(seqs, dtype=_I32, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
+    rc = load_library().spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, k_pages.shape[0],
+                                          B, N, Hkv, D, page, P, W, n.data_ptr(), st.data_ptr(), _raw_stream(dev))
+    if rc:
+        _raise(rc)
+    return n, st
 
 
 def _books(pool: PagePool, dev: int):
@@ -326,6 +327,10 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
     [L, P, Hkv, D/E, page, E] and v_pages.  Without them nothing is copied and ``page_size`` is
     needed.  Returns row_status [S] int32, which ``out`` may supply."""
     dev = _device(pool.page_table, "page_table")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return spec_cache_resize(pool, keep_len, want_len, k_pages, v_pages, page_size=page_size, workspace=workspace, out=out)
     S, W, P, books = _books(pool, dev)
     free = _ints(pool.free_map, "free_map", ((P + 31) // 32,), dev)
     if k_pages is not None:
@@ -345,16 +350,13 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
     if out is not None:
         _ints(out, "row_status", seqs, dev)
 
-    def call(raw):
-        st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
-        ws = _work(workspace, _resize_bytes(S, P), dev)
-        rc = load_library().spec_cache_resize(*books, free, keep, want, kp, vp, dt, L, S, Hkv, D, page, P, W, st.data_ptr(),
-                                              ws.data_ptr(), ws.numel(), raw)
-        if rc:
-            _raise(rc)
-        return st
-
-    return _launch(dev, stream, call)
+    st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
+    ws = _work(workspace, _resize_bytes(S, P), dev)
+    rc = load_library().spec_cache_resize(*books, free, keep, want, kp, vp, dt, L, S, Hkv, D, page, P, W, st.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if rc:
+        _raise(rc)
+    return st
 
 
 def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=None):
@@ -362,6 +364,10 @@ def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=Non
     (see include/spec_cache.h); cache_len [S] is written at dst.  Returns pair_status [F] int32,
     which ``out`` may supply."""
     dev = _device(pool.page_table, "page_table")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return spec_cache_fork(pool, cache_len, src, dst, out=out)
     S, W, P, books = _books(pool, dev)
     F = src.numel()
     pairs = (F,)
@@ -370,11 +376,8 @@ def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=Non
     if out is not None:
         _ints(out, "pair_status", pairs, dev)
 
-    def call(raw):
-        st = torch.empty(pairs, dtype=_I32, device=dev) if out is None else out
-        rc = load_library().spec_cache_fork(*books, lens, s, d, F, S, P, W, st.data_ptr(), raw)
-        if rc:
-            _raise(rc)
-        return st
-
-    return _launch(dev, stream, call)
+    st = torch.empty(pairs, dtype=_I32, device=dev) if out is None else out
+    rc = load_library().spec_cache_fork(*books, lens, s, d, F, S, P, W, st.data_ptr(), _raw_stream(dev))
+    if rc:
+        _raise(rc)
+    return st

@@ -285,6 +285,15 @@ SVD unsigned ld_map(const unsigned *p) { return __hip_atomic_load(p, __ATOMIC_RE
 SVD void give_back(const ResizeArgs &a, int p) {
   if (atomicSub(&a.ref_count[p], 1) == 1) atomicOr(&a.free_map[p >> 5], 1u << (p & 31));
 }
+// A barrier behind which the workgroup's own atomics and stores have been done.  (Its loads of
+// what it changes go past the L1; no other workgroup reads the books, so that nothing needs to
+// be written back beyond the L2.)
+SVD void rz_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x70);  // vmcnt 0, lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // The pool's books are a few kilobytes and every sequence's pages depend on those of the
 // sequences before it, so one workgroup does them.  Bound: a chain of about ten rounds to
@@ -331,11 +340,23 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
   const unsigned n_ent = rz_prefix(s_ent, S, s_w);
   auto row_of = [&](int b) { return a.page_table + (size_t)b * a.W; };
 
-  // ---- the entries' pages
+  // ---- the entries' pages.  A thread keeps its first entry; most calls have no more.
+  struct Entry {
+    int b, i, page;
+  };
+  auto entry_at = [&](unsigned e) {
+    Entry t;
+    t.b = rz_find(s_ent, S, e);
+    t.i = s_lo[t.b] + (int)(e - s_ent[t.b]);
+    t.page = row_of(t.b)[t.i];
+    return t;
+  };
+  Entry mine = {0, 0, 0};
+  if ((unsigned)tid < n_ent) mine = entry_at(tid);
+  auto entry = [&](unsigned e) { return e == (unsigned)tid ? mine : entry_at(e); };
   for (unsigned e = tid; e < n_ent; e += RZ_NT) {
-    const int b = rz_find(s_ent, S, e);
-    const unsigned p = (unsigned)row_of(b)[s_lo[b] + (int)(e - s_ent[b])];
-    if (p >= (unsigned)a.P || ld_ref(&a.ref_count[p]) <= 0) s_bad[b] = SV_ROW_BAD_PAGE;  // whoever writes: the same
+    const Entry t = entry(e);
+    if ((unsigned)t.page >= (unsigned)a.P || ld_ref(&a.ref_count[t.page]) <= 0) s_bad[t.b] = SV_ROW_BAD_PAGE;  // whoever writes: the same
   }
   __syncthreads();
   for (int b = tid; b < S; b += RZ_NT) {
@@ -349,22 +370,21 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
 
   // ---- pages behind the goal given back
   for (unsigned e = tid; e < n_ent; e += RZ_NT) {
-    const int b = rz_find(s_ent, S, e), i = s_lo[b] + (int)(e - s_ent[b]);
-    if (s_goal[b] >= 0 && i >= s_goal[b]) {
-      give_back(a, row_of(b)[i]);
-      row_of(b)[i] = -1;
+    const Entry t = entry(e);
+    if (s_goal[t.b] >= 0 && t.i >= s_goal[t.b]) {
+      give_back(a, t.page);
+      row_of(t.b)[t.i] = -1;
     }
   }
-  __threadfence();
-  __syncthreads();
+  rz_sync();
 
   // ---- entries to replace: others hold the page too, and the sequence is to write behind keep_len
-  auto swaps = [&](int b, int i) {
-    return i < s_goal[b] && a.want_len[b] > a.keep_len[b] && ld_ref(&a.ref_count[row_of(b)[i]]) > 1;
+  auto swaps = [&](const Entry &t) {
+    return t.i < s_goal[t.b] && a.want_len[t.b] > a.keep_len[t.b] && ld_ref(&a.ref_count[t.page]) > 1;
   };
   for (unsigned e = tid; e < n_ent; e += RZ_NT) {
-    const int b = rz_find(s_ent, S, e);
-    if (swaps(b, s_lo[b] + (int)(e - s_ent[b]))) atomicAdd(&s_swap[b], 1u);
+    const Entry t = entry(e);
+    if (swaps(t)) atomicAdd(&s_swap[t.b], 1u);
   }
   __syncthreads();
   const unsigned n_add = rz_prefix(s_add, S, s_w), n_swap = rz_prefix(s_swap, S, s_w);
@@ -382,8 +402,7 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
     found += tot;
   }
   found = min(found, need_all);
-  __threadfence_block();
-  __syncthreads();
+  rz_sync();
 
   // ---- handed out: a sequence's pages are those from s_swap + s_add on, replaced entries first,
   // if the free pages reach to its last one (then they reach all sequences before it)
@@ -401,19 +420,17 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
     unsigned seen = 0;  // entries replaced so far, in the order of all entries
     for (unsigned e0 = 0; e0 < n_ent; e0 += RZ_NT) {
       const unsigned e = e0 + tid;
-      int b = 0, i = 0;
+      Entry t = {0, 0, 0};
       bool it = false;
       if (e < n_ent) {
-        b = rz_find(s_ent, S, e);
-        i = s_lo[b] + (int)(e - s_ent[b]);
-        it = swaps(b, i);
+        t = entry(e);
+        it = swaps(t);
       }
       unsigned tot;
       const unsigned at = seen + rz_scan(it ? 1u : 0u, s_w, tot);
-      if (it && fits(b)) {
-        const int old = row_of(b)[i], keep = a.keep_len[b];
-        const int fresh = take(b, i, at + s_add[b], old);
-        if (i == keep >> sh && (keep & (page - 1))) a.copies[atomicAdd(&s_ncopy, 1)] = make_int4(old, fresh, keep & (page - 1), 0);
+      if (it && fits(t.b)) {
+        const int keep = a.keep_len[t.b], fresh = take(t.b, t.i, at + s_add[t.b], t.page);
+        if (t.i == keep >> sh && (keep & (page - 1))) a.copies[atomicAdd(&s_ncopy, 1)] = make_int4(t.page, fresh, keep & (page - 1), 0);
       }
       seen += tot;
     }
@@ -435,8 +452,7 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
       if (some) atomicMax(&s_served, (int)end_of(b));
     }
   }
-  __threadfence();
-  __syncthreads();
+  rz_sync();
   // ---- replaced pages lose a holder (only now: the counts above are those after giving back)
   if (n_swap > 0)
     for (int k = tid; k < s_served; k += RZ_NT)
