@@ -162,7 +162,9 @@ struct Mma<uint16_t> {
     bf16x8 w;
   };
   // The weights are rounded to bf16 (by at most 2^-8 relative each, as the inputs themselves
-  // were); their sum is taken in f32 before the rounding.  A lane of the second product wants
+  // were), and the sum they are divided by is that of the rounded weights, in f32: an error that
+  // the weights share cancels, and a row that sees one slot gets its value exactly.  The sum is
+  // one more product, with ones.  A lane of the second product wants
   // slots 8 g .. 8 g + 7, a value unit: with the two score tiles' pairs of weights by lane group
   // as a0 a1 a2 a3 and b0 b1 b2 b3, the swaps make a0 a2 b0 b2 and a1 a3 b1 b3 of them.
   SVD static P weights(const f32x4 (&s)[2]) {
@@ -182,6 +184,13 @@ struct Mma<uint16_t> {
   SVD static f32x4 pv(const u32x4 (&v)[1], const P &p, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v[0]), p.w, c, 0, 0, 0);
   }
+  // A row's sum of weights: all of it in every element.
+  typedef f32x4 Sum;
+  SVD static Sum add(const P &p, const f32x4 (&)[2], Sum c) {
+    const u32x4 ones[1] = {u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}};
+    return pv(ones, p, c);
+  }
+  SVD static float total(Sum c) { return c[0]; }
   SVD static bool non_finite(u32x4 v) {
     bool bad = false;
 #pragma unroll
@@ -233,6 +242,12 @@ struct Mma<float> {
     f32x4 w[2];
   };
   SVD static P weights(const f32x4 (&s)[2]) { return P{{s[0], s[1]}}; }
+  // A row's sum of weights: a part of it in each of its four lanes.
+  typedef float Sum;
+  SVD static Sum add(const P &, const f32x4 (&s)[2], Sum c) {
+    return c + (((s[0][0] + s[0][1]) + (s[0][2] + s[0][3])) + ((s[1][0] + s[1][1]) + (s[1][2] + s[1][3])));
+  }
+  SVD static float total(Sum c) { return col_sum(c); }
   SVD static f32x4 pv(const u32x4 (&v)[2], const P &p, f32x4 c) {
 #pragma unroll
     for (int t2 = 0; t2 < 2; ++t2)
@@ -593,7 +608,8 @@ struct Rows {
   typedef Mma<T> M;
   static constexpr int KS = D / (4 * M::E), DT = D / 16;
   f32x4 o[R][DT];
-  float rm[R], rl[R];   // the largest score nm stands for, the sum of weights
+  float rm[R];          // the largest score nm stands for
+  typename M::Sum rl[R];  // sums of weights
   float nm[R], lim[R];  // see soften
   u32x4 q[R][KS];
   int node[R], dep[R];  // clamped to the segment's nodes
@@ -602,7 +618,8 @@ struct Rows {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       rm[r] = lim[r] = -INFINITY;
-      rl[r] = nm[r] = 0.0f;
+      rl[r] = typename M::Sum{};
+      nm[r] = 0.0f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[r][d] = f32x4{0, 0, 0, 0};
     }
@@ -657,22 +674,20 @@ struct Rows {
       const float mx = fmaxf(rm[r], col_max(top));
       const float nm2 = (mx == -INFINITY) ? 0.0f : mx * a.c2;
       const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(nm[r] - nm2);
-      rl[r] *= f;
+      rl[r] = rl[r] * f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
       rm[r] = mx;
       nm[r] = nm2;
       lim[r] = mx + a.slack;
     }
-    float sum = 0.0f;
 #pragma unroll
-    for (int t2 = 0; t2 < 2; ++t2) {
+    for (int t2 = 0; t2 < 2; ++t2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[t2][i] = fast_exp2(fmaf(sc[t2][i], a.c2, -nm[r]));
-      sum += (sc[t2][0] + sc[t2][1]) + (sc[t2][2] + sc[t2][3]);
-    }
-    rl[r] += sum;
-    return M::weights(sc);
+    const typename M::P p = M::weights(sc);
+    rl[r] = M::add(p, sc, rl[r]);
+    return p;
   }
   // The exponent that a row's sums are relative to (-inf: nothing seen so far).
   SVD float scale(int r) const { return (rm[r] == -INFINITY) ? -INFINITY : nm[r]; }
@@ -834,7 +849,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
     // the four waves joined: rows' maxima and sums, then the output tiles
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float l_row = col_sum(rows.rl[r]);
+      const float l_row = M::total(rows.rl[r]);
       if (g == 0) {
         s_m[wid * RT + 16 * r + m] = rows.scale(r);
         s_l[wid * RT + 16 * r + m] = l_row;
@@ -1028,7 +1043,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      sink(wid * 16 * R + 16 * r + m, rows.scale(r), col_sum(rows.rl[r])).put(g, 4, rows.o[r]);
+      sink(wid * 16 * R + 16 * r + m, rows.scale(r), M::total(rows.rl[r])).put(g, 4, rows.o[r]);
     }
   });
 }
