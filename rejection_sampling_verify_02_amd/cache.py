@@ -115,9 +115,9 @@ def _pages(k_pages, v_pages, dims: int, dtype, dev: int):
 def _rows(t, name: str, shape: tuple, dtype, dev: int):
     """Address and strides (sequence, node) of a [B, N, H, D] tensor whose heads lie together."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        B, N, H, D = shape
         sb, sn, sh, sd = t.stride()
-        if (sd == 1 or D <= 1) and (sh == D or H <= 1):
+        B, N, H, D = shape
+        if sd == 1 and sh == D or (sd == 1 or D <= 1) and (sh == D or H <= 1):
             # a dimension of one entry may carry any stride: it is never stepped
             return t.data_ptr(), sb if B > 1 else 0, sn if N > 1 else 0
         raise ValueError(f"{name}'s heads must lie together (strides D and 1), got strides {t.stride()}")
@@ -153,7 +153,7 @@ def _elsewhere(dev: int, stream):
 
 def _work(workspace, nbytes: int, dev: int):
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=dev)
     if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on device {dev}")
     return workspace
@@ -226,7 +226,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
         _rows(out[0], "out", shape, q.dtype, dev)
         _ints(out[1], "row_status", seqs, dev)
 
-    o, st = out or (torch.empty(shape, dtype=q.dtype, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
+    o, st = out or (torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(cache_len))
     ws = _work(workspace, _attention_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
     args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, news, par, B, N, Hq, Hkv, D, page, P, W,
             scale, window, sinks, o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
@@ -266,7 +266,7 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=No
     if out is not None:
         _ints(out, "row_status", seqs, dev)
 
-    st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
+    st = torch.empty_like(cache_len) if out is None else out
     rc = load_library().spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens, news,
                                           B, N, Hkv, D, page, P, W, st.data_ptr(), _raw_stream(dev))
     if rc:
@@ -305,7 +305,7 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
         _ints(out[0], "new_len", seqs, dev)
         _ints(out[1], "row_status", seqs, dev)
 
-    n, st = out or (torch.empty(seqs, dtype=_I32, device=dev), torch.empty(seqs, dtype=_I32, device=dev))
+    n, st = out or (torch.empty_like(cache_len), torch.empty_like(cache_len))
     rc = load_library().spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, k_pages.shape[0],
                                           B, N, Hkv, D, page, P, W, n.data_ptr(), st.data_ptr(), _raw_stream(dev))
     if rc:
@@ -350,7 +350,7 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
     if out is not None:
         _ints(out, "row_status", seqs, dev)
 
-    st = torch.empty(seqs, dtype=_I32, device=dev) if out is None else out
+    st = torch.empty_like(keep_len) if out is None else out
     ws = _work(workspace, _resize_bytes(S, P), dev)
     rc = load_library().spec_cache_resize(*books, free, keep, want, kp, vp, dt, L, S, Hkv, D, page, P, W, st.data_ptr(),
                                           ws.data_ptr(), ws.numel(), _raw_stream(dev))
@@ -376,7 +376,7 @@ def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=Non
     if out is not None:
         _ints(out, "pair_status", pairs, dev)
 
-    st = torch.empty(pairs, dtype=_I32, device=dev) if out is None else out
+    st = torch.empty_like(src) if out is None else out
     rc = load_library().spec_cache_fork(*books, lens, s, d, F, S, P, W, st.data_ptr(), _raw_stream(dev))
     if rc:
         _raise(rc)
