@@ -1013,14 +1013,97 @@ def run_typical(args, dev, hev):
     return res
 
 
+def run_round(args, dev, hev):
+    """One round of speculative decoding around the verification, without the model's own
+    products: pages for the new tokens, per layer the append and the attention over the paged
+    cache, the tree verification, the commit of the accepted paths, the pages behind them given
+    back.  Drafted tree nodes scored and verified per second; per-kernel times of the attention."""
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    from rejection_sampling_verify_02_amd import workloads as wl
+
+    cfg = wl.ROUND_CONFIGS["round_bf16_b16_n32"]
+    tc = wl.TREE_CONFIGS[cfg.tree]
+    B, N, V, S, L = tc.B, tc.N, tc.V, tc.max_children, cfg.layers
+    H, Hq, D, page = cfg.kv_heads, cfg.kv_heads * cfg.group, cfg.head_dim, cfg.page_size
+    n_sets = args.sets or 2
+    log(f"[bench] round {cfg.name}: B={B} N={N} V={V}, {L} layers of {Hq}/{H} heads of {D}, pages of {page}, {n_sets} input sets")
+    i32 = dict(dtype=torch.int32, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(cfg.seed)
+    lens = torch.from_numpy(wl.round_lengths(cfg, B)).to(dev)
+    W = -(-(cfg.max_len + N) // page)
+    P = int((-(-(lens + N) // page)).sum().item()) + 64
+    sets = []
+    for s in range(n_sets):
+        raw = wl.make_tree(B, N, V, tc.dtype, tc.seed + 1000 * s, max_children=S, draft_noise=tc.draft_noise)
+        t, d = (torch.from_numpy(a).view(torch.bfloat16).to(dev) for a in (raw.target, raw.draft))
+        par = torch.from_numpy(raw.parent.copy()).to(dev)
+        rows = d[torch.arange(B, device=dev)[:, None], par[:, 1:].long()].reshape(B * (N - 1), V).contiguous()
+        tk, _ = sv.spec_sample(rows, torch.from_numpy(raw.u_draft[:, 1:].reshape(-1).copy()).to(dev), tc.temperature, tc.top_k)
+        tok = torch.zeros((B, N), **i32)
+        tok[:, 1:] = tk.reshape(B, N - 1)
+        pool = sv.PagePool.empty(P, B, W, dev)
+        kp, vp = sv.empty_pages(L, P, H, D, page, torch.bfloat16, dev)
+        kp.normal_(generator=gen)
+        vp.normal_(generator=gen)
+        bad = sv.spec_cache_resize(pool, torch.zeros_like(lens), lens, kp, vp)
+        if int(bad.abs().sum().item()):
+            raise RuntimeError(f"the pool does not hold the batch: {bad.tolist()}")
+        q, k, v = (torch.randn((L, B, N, h, D), generator=gen, device=dev).to(torch.bfloat16) for h in (Hq, H, H))
+        sets.append((t, d, tok, par, torch.from_numpy(raw.u_accept).to(dev), torch.from_numpy(raw.u_sample).to(dev), pool, kp, vp, q, k, v))
+    torch.cuda.synchronize(dev)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    ws = sv.Workspace()
+    status = []
+
+    def call(i, events=None):
+        t, d, tok, par, ua, us, pool, kp, vp, q, k, v = sets[i % n_sets]
+        sv.spec_cache_resize(pool, lens, lens + N, kp, vp)
+        for l in range(L):
+            sv.spec_cache_append(k[l], v[l], kp[l], vp[l], pool.page_table, lens)
+            out, st = sv.spec_paged_attention(q[l], kp[l], vp[l], pool.page_table, lens, parent=par)
+        acc, _, path = sv.spec_tree_verify(t, d, tok, par, ua, us, tc.temperature, tc.top_k, max_children=S, workspace=ws, stream=stream)
+        new, st2 = sv.spec_cache_commit(kp, vp, pool.page_table, lens, acc, path)
+        sv.spec_cache_resize(pool, new, new, kp, vp)
+        status[:] = [st, st2, acc]
+
+    def attend(i, events=None):
+        *_, par, _, _, pool, kp, vp, q, _, _ = sets[i % n_sets]
+        return sv.spec_paged_attention(q[i % L], kp[i % L], vp[i % L], pool.page_table, lens, parent=par, events=events)
+
+    K = args.steps
+    t = time_loop(call, [], K, args.warmup, stream, dev, hev, False, 0)
+    t_call = t["wall"] / K
+    if any(int(x.min().item()) < 0 for x in status):
+        raise RuntimeError(f"a round ended with row codes {[x.tolist() for x in status]}")
+    for s in sets:
+        sv.spec_cache_resize(s[6], lens, lens + N, s[7], s[8])
+    ta = time_loop(attend, sv.sv_attention_launch_plan(N, Hq, H, D, sv.SV_BF16), K, args.warmup, stream, dev, hev,
+                   not args.no_stage_events, args.flush_calls)
+    alg = int((lens + N).sum().item()) * H * D * 4 + 2 * B * N * Hq * D * 2  # keys and values once, queries, outputs
+    return {
+        "metric": "draft-tree nodes scored over the cache and verified per second (attention, verification and cache alone)",
+        "value": round(B * (N - 1) / t_call, 1), "unit": "nodes/s", "n_gpus": 1, "steps": K, "warmup": args.warmup,
+        "ms_per_step": round(t_call * 1e3, 5), "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+        "data": "synthetic",
+        "config": {"workload": "attention_" + cfg.name, "B": B, "N": N, "V": V, "layers": L, "query_heads": Hq, "key_heads": H,
+                   "head_dim": D, "page_size": page, "lengths": [cfg.min_len, cfg.max_len], "input_sets": n_sets},
+        "round_loops_ms": [round(w * 1e3, 4) for w in t["walls"]],
+        "attention_us_per_layer": round(ta["wall"] / K * 1e6, 3),
+        **timing_fields(ta, K, args.warmup),
+        "roofline": roofline(ta["per_kernel"], "k_attn_wide", alg, None),
+        "cpu_baseline": None,
+    }
+
+
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--warmup", type=int, default=20)
-    ap.add_argument("--op", default="verify", choices=["verify", "sample", "overlap", "tree", "typical"],
+    ap.add_argument("--op", default="verify", choices=["verify", "sample", "overlap", "tree", "typical", "round"],
                     help="verify (the default: B=64, G=4, V=128256 bf16), the batched sampler, the per-position overlap, "
-                         "tree verification, or typical acceptance")
+                         "tree verification, typical acceptance, or a round over a paged cache (attention, tree verification, commit)")
     ap.add_argument("--config", type=int, default=3, choices=[1, 2, 3, 4, 5],
                     help="verification workload (3, the default, is B=64, G=4, V=128256 bf16; 4 greedy and 5 top-k "
                          "are timed for the design notes)")
@@ -1070,7 +1153,7 @@ def main() -> int:
     dev = torch.device("cuda:0")
     hev = HipEvents()
     run = {"sample": run_sample, "overlap": run_overlap, "tree": run_tree,
-           "typical": run_typical}.get(args.op, run_verify)
+           "typical": run_typical, "round": run_round}.get(args.op, run_verify)
     res = run(args, dev, hev)
     print(json.dumps(res), flush=True)
     return 0

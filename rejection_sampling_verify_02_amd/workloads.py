@@ -300,6 +300,34 @@ def make_tree(B: int, N: int, V: int, dtype: str, seed: int, *, max_children: in
     return TreeRaw(target, draft, parents, uniforms(rng, (B, N)), uniforms(rng, (B, N)), uniforms(rng, (B,)))
 
 
+# ---------------------------------------------------------------- rounds over a paged cache
+
+@dataclass(frozen=True)
+class RoundConfig:
+    name: str
+    tree: str              # the draft trees (TREE_CONFIGS) that a round scores and verifies
+    layers: int
+    kv_heads: int
+    group: int             # query heads a key head
+    head_dim: int
+    page_size: int
+    min_len: int           # cached tokens, spread evenly over the batch
+    max_len: int
+    seed: int
+
+
+# The tree batch over caches of 2000 to 8111 tokens, four layers of 32 query and 8 key heads.
+ROUND_CONFIGS = {
+    "round_bf16_b16_n32": RoundConfig("round_bf16_b16_n32", "tree_bf16_b16_n32", 4, 8, 4, 128, 32, 2000, 8111, 4001),
+}
+
+
+def round_lengths(cfg: RoundConfig, B: int) -> np.ndarray:
+    """Cached tokens of every sequence: evenly spread, in a seeded order."""
+    rng = np.random.default_rng(cfg.seed)
+    return rng.permutation(np.linspace(cfg.min_len, cfg.max_len, B).astype(np.int32))
+
+
 # ---------------------------------------------------------------- degenerate residuals
 
 # A drafted token whose target logit sits far below the rest of the row (-460, so that
