@@ -319,7 +319,7 @@ struct Segment {
   }
   // The slots of a tile that a row sees, as bits.
   SVD unsigned sees(const AttnArgs &a, int t0, int dep, const unsigned *anc) const {
-    const int pos = sq.len + dep, lo = (a.window > 0) ? pos - a.window + 1 : 0;
+    const int pos = sq.len + dep, lo = (a.window > 0) ? max(0, pos - a.window + 1) : 0;
     const int head = par ? sq.len : pos + 1;  // slots that window and sinks alone decide
     unsigned see = slots32(t0, lo, head) | slots32(t0, 0, min(a.sinks, head));
     if (par) see |= anc32(anc, words, t0 - sq.len);
@@ -1166,9 +1166,11 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
   p.R = p.wide ? (rows <= 64 || D * esz == 1024 ? 1 : 2) : (rows <= 16 ? 1 : 2);
   p.RT = 16 * p.R * (p.wide ? NW : 1);
   const long long n_rt = (rows + p.RT - 1) / p.RT;
-  p.units = (long long)B * Hkv * n_rt;
   const long long most = ((long long)W * page + TILE - 1) / TILE + 1;  // tiles of a unit
-  if (p.units * most > 0x7fffffffLL || p.units * p.RT > 0x7fffffffLL) return false;
+  const long long heads = (long long)B * Hkv, limit = 0x7fffffffLL;
+  if (heads > limit || n_rt > limit / heads) return false;
+  p.units = heads * n_rt;
+  if (most > limit / p.units || p.RT > limit / p.units) return false;
   p.n_rt = (int)n_rt;
   const int occ = attn_pick(esz, D, p.R, [&](auto t, auto d, auto r) {
     typedef decltype(t) T;
@@ -1200,7 +1202,7 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   AttnPlan p;
   if (!attn_plan(B, N, Hq, Hkv, D, page, W, esz, p)) return SV_ERR_SHAPE;
   if (!q || !k_pages || !v_pages || !table || !cache_len || !out || !status || !ws) return SV_ERR_NULL;
-  if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out | (uintptr_t)(q_sb * esz) | (uintptr_t)(q_sn * esz)) & 15)
+  if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out | ((uintptr_t)q_sb * esz) | ((uintptr_t)q_sn * esz)) & 15)
     return SV_ERR_ALIGN;
   if (ws_bytes < p.total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
   char *base = static_cast<char *>(ws);
@@ -1208,8 +1210,8 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   a.q = static_cast<const char *>(q);
   a.k_pages = static_cast<const char *>(k_pages);
   a.v_pages = static_cast<const char *>(v_pages);
-  a.q_sb = q_sb * esz;
-  a.q_sn = q_sn * esz;
+  a.q_sb = (long long)((unsigned long long)q_sb * esz);
+  a.q_sn = (long long)((unsigned long long)q_sn * esz);
   a.page_table = table;
   a.cache_len = cache_len;
   a.n_new = n_new;

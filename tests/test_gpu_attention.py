@@ -126,7 +126,8 @@ def test_chain(dev, dtype, shape):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (3, 2), (16, 0), (33, 1), (40, 50), (500, 4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (3, 2), (16, 0), (33, 1), (40, 50), (500, 4), (2 ** 31 - 1, 2 ** 31 - 1),
+                                          (5, 2 ** 31 - 1)])
 @pytest.mark.parametrize("tree", [False, True])
 def test_window_and_sinks(dev, dtype, window, sinks, tree):
     c = Case(dev, dtype, 5, 9, 1, 2, 64, 16, [0, 3, 33, 90, 200], tree=tree, window=window, sinks=sinks, seed=window + sinks)
@@ -150,6 +151,43 @@ def test_long_contexts_split_over_workgroups(dev, dtype, Hkv, g, D):
     """Lengths far apart, so that a share spans several short sequences and a long one many shares."""
     c = Case(dev, dtype, 6, 2, Hkv, g, D, 64, [6000, 1, 40, 2500, 0, 333], seed=5)
     check(c, *run(c))
+
+
+@pytest.mark.parametrize("dtype,N,g,D,window", [("bf16", 24, 4, 128, 0), ("bf16", 12, 4, 64, 0), ("f32", 9, 8, 64, 0),
+                                                ("bf16", 40, 2, 256, 300), ("f32", 33, 2, 256, 0), ("f32", 20, 8, 128, 777)])
+def test_long_contexts_with_many_rows(dev, dtype, N, g, D, window):
+    """The kernel whose waves share tiles, with units cut into parts."""
+    c = Case(dev, dtype, 3, N, 1, g, D, 32, [3500, 10, 1777], tree=True, window=window, sinks=40 if window else 0, seed=N)
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,g,lens", [(1, 4, [1100] * 40), (20, 4, [1100] * 40), (3, 1, list(range(0, 2000, 50))), (1, 2, [5] * 300 + [900])])
+def test_every_way_to_cut_a_batch(dev, dtype, N, g, lens):
+    """Equal lengths (a part a workgroup), lengths that no such cut fits (shares that run on into
+    the next unit), and more units than workgroups."""
+    H = 4 if len(lens) <= 40 else 2
+    c = Case(dev, dtype, len(lens), N, H, g, 64, 64, lens, seed=len(lens) + N)
+    t = c.tensors()
+    import rejection_sampling_verify_02_amd as sv
+    out, st = sv.spec_paged_attention(**t)
+    assert st.tolist() == [0] * c.B
+    # the float64 reference for some sequences, and for all of them the same bits when asked again
+    some = sorted({0, 1, c.B // 2, c.B - 1})
+    part = Case.__new__(Case)
+    part.__dict__.update(c.__dict__)
+    part.B, part.q, part.lens, part.news = len(some), c.q[some], [c.lens[b] for b in some], [c.news[b] for b in some]
+    part.ks, part.vs = [c.ks[b] for b in some], [c.vs[b] for b in some]
+    check(part, out[some], st[some])
+    again, _ = sv.spec_paged_attention(**t)
+    assert (again == out).all()
+    # a sequence's rows do not depend on how the others cut the batch, but for the order of f32 sums
+    alone = {**t, "q": t["q"][:1].contiguous(), "page_table": t["page_table"][:1].contiguous(), "cache_len": t["cache_len"][:1].contiguous()}
+    one, _ = sv.spec_paged_attention(**alone)
+    first = Case.__new__(Case)
+    first.__dict__.update(part.__dict__)
+    first.B, first.q, first.lens, first.news, first.ks, first.vs = 1, c.q[:1], c.lens[:1], c.news[:1], c.ks[:1], c.vs[:1]
+    check(first, one, st[:1])
 
 
 def test_many_sequences(dev):
@@ -201,7 +239,8 @@ def test_scales(dev, dtype, scale):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("what", ["nan", "inf", "-inf", "both"])
-def test_values_that_are_not_finite_reach_only_rows_that_see_them(dev, dtype, what):
+@pytest.mark.parametrize("g,D", [(2, 64), (8, 64), (6, 128), (8, 256)])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(dev, dtype, what, g, D):
     """A tree's nodes whose keys or values are not finite: their descendants show it, other
     branches do not.  The same for a committed token at the window's edge."""
     import rejection_sampling_verify_02_amd as sv
@@ -209,7 +248,7 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(dev, dtype, wh
     N, n = 12, 37
     parents = np.array([[-1, 0, 0, 1, 1, 2, 2, 3, 5, 7, 8, 10]], np.int32)
     for window, where, slots in ((0, "v", [n + 3, n + 7]), (0, "v", [n + 2, n + 6]), (8, "v", [n - 7, n - 6]), (0, "k", [n + 3])):
-        c = Case(dev, dtype, 1, N, 1, 2, 64, 16, [n], tree=True, window=window, seed=21, evict=False)
+        c = Case(dev, dtype, 1, N, 1, g, D, 16, [n], tree=True, window=window, seed=21, evict=False)
         c.parents = parents
         for x, t in zip(bad * 2, slots):
             if where == "k" and not np.isnan(x):
@@ -267,10 +306,11 @@ def test_same_bits_every_time_and_on_other_streams(dev):
     assert all(torch.equal(x, first_c) and torch.equal(y, first_d) for x, y in got)
 
 
-def test_captured_and_replayed(dev):
+@pytest.mark.parametrize("N", [4, 30])
+def test_captured_and_replayed(dev, N):
     import torch
     import rejection_sampling_verify_02_amd as sv
-    c = Case(dev, "bf16", 3, 4, 2, 4, 64, 16, [700, 30, 1], seed=15)
+    c = Case(dev, "bf16", 3, N, 2, 4, 64, 16, [700, 30, 1], seed=15)
     t = c.tensors()
     plain, _ = sv.spec_paged_attention(**t)
     q0 = t["q"].clone()
