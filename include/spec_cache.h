@@ -34,11 +34,12 @@
  * (unless strides are given), the caller owns every buffer, nothing is allocated, kept or
  * synchronised, work is enqueued on `stream`, and a status other than SV_OK means that
  * nothing was enqueued.  Every call may be captured into a HIP graph: no kernel waits for
- * another workgroup, and workspaces need no particular contents.  Calls that overlap in
- * time need workspaces of their own, and calls that change a cache or its tables have to be
- * ordered with every other call on them.  Page indexes, lengths, trees and paths are checked
- * on the device: memory outside the pool is never touched, and a sequence with a code in
- * row_status has the outputs stated at each call.
+ * another workgroup, and workspaces need no particular contents.  Outputs do not overlap a
+ * call's inputs unless it is stated that they may.  Calls that overlap in time need
+ * workspaces of their own, and calls that change a cache or its tables have to be ordered
+ * with every other call on them.  Page indexes, lengths, trees and paths are checked on the
+ * device: memory outside the pool is never touched, and a sequence with a code in row_status
+ * has the outputs stated at each call.
  */
 #ifndef SPEC_CACHE_H
 #define SPEC_CACHE_H
@@ -173,7 +174,8 @@ sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype,
  *   k_pages, v_pages  L pools (NULL with L = 0: the caller copies, or shares no pages)
  *   row_status   [S] int32 out: 0, SV_ROW_BAD_LENGTH, SV_ROW_BAD_PAGE (neither changes the
  *                sequence's row) or SV_ROW_NO_PAGES
- *   workspace    sv_resize_workspace_bytes(S, num_pages) bytes, 256-byte aligned */
+ *   workspace    sv_resize_workspace_bytes(S, num_pages) bytes, 256-byte aligned
+ * S * table_width fits 31 bits (else SV_ERR_SHAPE). */
 size_t sv_resize_workspace_bytes(int32_t S, int32_t num_pages);
 sv_status spec_cache_resize(int32_t *page_table, int32_t *seq_pages, int32_t *ref_count,
                             int32_t *free_map, const int32_t *keep_len, const int32_t *want_len,

@@ -32,6 +32,7 @@ from . import SV_BF16, SV_F32, SpecVerifyError, load_library, sv_status_string
 
 ROW_BAD_PAGE, ROW_BAD_LENGTH, ROW_NO_PAGES, ROW_BAD_FORK = -7, -8, -9, -10
 CACHE_MAX_NEW, CACHE_MAX_SEQS = 1024, 4096
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 class PagePool(NamedTuple):
@@ -44,6 +45,8 @@ class PagePool(NamedTuple):
     @classmethod
     def empty(cls, num_pages: int, max_seqs: int, table_width: int, device) -> "PagePool":
         i32 = dict(dtype=torch.int32, device=device)
+        if num_pages < 1 or max_seqs < 1 or table_width < 1:
+            raise ValueError(f"a pool has at least one page, sequence and table entry, got {num_pages}, {max_seqs}, {table_width}")
         free = torch.full(((num_pages + 31) // 32,), -1, **i32)
         if num_pages % 32:
             free[-1] = (1 << num_pages % 32) - 1
@@ -53,7 +56,11 @@ class PagePool(NamedTuple):
 
 def empty_pages(layers: int, num_pages: int, kv_heads: int, head_dim: int, page_size: int, dtype, device):
     """Zeroed (k_pages, v_pages) of `layers` layers in the cache's layout."""
-    E = 16 // torch.empty((), dtype=dtype).element_size()
+    if dtype not in (_BF16, _F32):
+        raise TypeError(f"the cache must be bfloat16 or float32, got {dtype}")
+    if head_dim < 16 or head_dim % 16 or not 16 <= page_size <= 256 or page_size & (page_size - 1):
+        raise ValueError(f"head_dim must be a multiple of 16 and page_size a power of two from 16 to 256, got {head_dim} and {page_size}")
+    E = 8 if dtype is _BF16 else 4
     return (torch.zeros((layers, num_pages, kv_heads, head_dim // E, page_size, E), dtype=dtype, device=device),
             torch.zeros((layers, num_pages, kv_heads, page_size // E, head_dim, E), dtype=dtype, device=device))
 
@@ -61,7 +68,6 @@ def empty_pages(layers: int, num_pages: int, kv_heads: int, head_dim: int, page_
 # The checks below take the usual case in one expression and look for the reason only when it
 # fails: a call's host time is a few microseconds, and shows where its kernels take no longer.
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -72,6 +78,13 @@ def _code(t: torch.Tensor, name: str) -> int:
     if dt is _F32:
         return SV_F32
     raise TypeError(f"{name} must be bfloat16 or float32, got {dt}")
+
+
+def _int32(x: int, name: str) -> int:
+    """x, if it is one: ctypes would pass its low 32 bits."""
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
 
 
 def _ints(t, name: str, shape: tuple, dev: int, optional: bool = False):
@@ -220,6 +233,8 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
     par = _ints(parent, "parent", (B, N), dev, True)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    if window or sinks:
+        _int32(window, "window"), _int32(sinks, "sinks")
     if out is not None:
         if not out[0].is_contiguous():
             raise ValueError("out must be contiguous")
@@ -297,7 +312,7 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
     elif max_new is None:
         raise ValueError("chains need max_new, the new tokens N = G + 1 of the verification")
     else:
-        N = max_new
+        N = _int32(max_new, "max_new")
     seqs = (B,)
     lens, acc = _ints(cache_len, "cache_len", seqs, dev), _ints(accepted_len, "accepted_len", seqs, dev)
     path = _ints(path_nodes, "path_nodes", (B, N), dev, True)
@@ -344,7 +359,7 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
     elif page_size is None:
         raise ValueError("page_size is needed without k_pages and v_pages")
     else:
-        dt, L, Hkv, D, page, kp, vp = SV_BF16, 0, 1, 16, page_size, None, None
+        dt, L, Hkv, D, page, kp, vp = SV_BF16, 0, 1, 16, _int32(page_size, "page_size"), None, None
     seqs = (S,)
     keep, want = _ints(keep_len, "keep_len", seqs, dev), _ints(want_len, "want_len", seqs, dev)
     if out is not None:

@@ -454,8 +454,8 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   const int tid = threadIdx.x;
   // The parts' size.  Where a few rounds more than an equal share cut the units into no more
   // parts than there are workgroups, every workgroup gets one part: one that goes on with a
-  // second unit begins anew there (in k_attn_wide about 6 us, 3 rounds' time: the 32 windowed
-  // sequences took 59 us with shares that run on where they take 52 so).  Otherwise parts are
+  // second unit begins anew there (in k_attn_wide about 6 us, 3 rounds' time: 32
+  // sequences with window and sinks took 59 us with shares that run on, 50 so).  Otherwise parts are
   // single rounds and shares of them as equal as can be (units of 257 to 16001 slots, one a
   // workgroup: 392 us, so 343).
   constexpr unsigned LEAST = least_part<T, RT, ROUND>();
@@ -886,7 +886,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
 // 256 bytes: keys [unit of d][slot], values [unit of slots][d].  They come there straight from
 // memory, without registers in between, a stage of ST tiles at a time: while the waves work on
 // one stage the next is on its way, and one barrier hands a stage over and frees the other.
-// (With the next tile alone in flight, in registers, 16 trees of 32 nodes took 110 us.)  The
+// (16 trees of 32 nodes: 92 us; with the next tile alone in flight, in registers, 110.)  The
 // two stages are variables of their own, so that the compiler sees that reads of one do not
 // wait for the other; four of one tile each, one more in flight, made the code twice as long,
 // and a workgroup spends its first microseconds fetching code.

@@ -33,7 +33,9 @@ struct AppendArgs {
   Pool pool;
 };
 
-constexpr int APPEND_SLOTS = 32;  // slots a workgroup writes: whole value units (8 prompts of up to 1000 tokens: 16 11.6, 32 10.0, 64 11.4 us)
+// Slots a workgroup writes, whole value units (8 prompts of up to 1000 tokens, 36.9 MB read and
+// written: 16 slots 11.6, 32 10.0, 64 11.4 us; a copy of those bytes takes 7.7).
+constexpr int APPEND_SLOTS = 32;
 
 // One workgroup writes up to APPEND_SLOTS slots of one head.  Keys: a thread moves 16 bytes
 // (E values of d of one slot), neighbours along d in the source.  Values: a thread gathers
@@ -116,8 +118,8 @@ struct CommitArgs {
 // any of it is written.  Later batches read nothing that earlier ones wrote, since sources lie
 // behind their targets (path_nodes[j] >= j + 1, increasing).  A value unit is put together in
 // registers and written whole, slots that are no targets as they were: 16-byte stores in place
-// of single elements 16 bytes apart (which took 43 us where this takes 15: 16 trees, 32
-// layers).
+// of single elements 16 bytes apart (16 trees, 32 layers: 43 us, so 23, the
+// bytes' 4.4; every moved value element is 2 bytes of a 64-byte line that is read and written).
 constexpr int COMMIT_R = 2;  // units of keys, and of values, that a thread holds
 
 template <typename T>
@@ -298,8 +300,8 @@ SVD void rz_sync() {
 // The pool's books are a few kilobytes and every sequence's pages depend on those of the
 // sequences before it, so one workgroup does them.  Bound: a chain of about ten rounds to
 // memory.  Each round runs over the table entries it concerns laid end to end, whoever's they
-// are, a thread an entry (a wave a sequence, 16 sequences after one another, took 50 us for
-// 256 sequences where this takes 12).  Which pages are picked does not depend on the order in
+// are, a thread an entry, which it keeps in registers (256 sequences whose pages grow and
+// shrink: 8.6 us; a wave a sequence, 16 sequences after one another, 54).  Which pages are picked does not depend on the order in
 // which atomics land: the counts are sums, and picking reads the map only after all of them.
 __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
   extern __shared__ unsigned s_dyn[];
@@ -474,7 +476,8 @@ struct CopyArgs {
 constexpr int COPY_WGS = 1024;  // 4 a CU, whatever there is to copy: the host does not know
 
 // The kept slots of a page into another: a workgroup moves one head of one layer at a time,
-// COPY_STEP 16-byte units a thread in flight.  Keys: t runs fastest, kept * 16 bytes together.
+// COPY_STEP 16-byte units a thread in flight (504 pages' halves in 32 layers, 1.01 GB read and
+// written: 187 us, 5.4 TB/s; bound by memory).  Keys: t runs fastest, kept * 16 bytes together.
 // Values: whole units lie together; of the last one only the kept elements are written.
 constexpr int COPY_STEP = 4;
 
@@ -692,7 +695,7 @@ sv_status spec_cache_resize(int32_t *page_table, int32_t *seq_pages, int32_t *re
                             size_t workspace_bytes, void *stream) {
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (S < 1 || S > SV_CACHE_MAX_SEQS || L < 0 || !pool_ok(L ? Hkv : 1, L ? D : 16, page_size, num_pages, table_width) ||
-      (long long)L * Hkv > 0x7fffffffLL)
+      (long long)L * Hkv > 0x7fffffffLL || (long long)S * table_width > 0x7fffffffLL)  // entries are counted in 32 bits
     return SV_ERR_SHAPE;
   if (!page_table || !seq_pages || !ref_count || !free_map || !keep_len || !want_len || !row_status || !workspace ||
       (L > 0 && (!k_pages || !v_pages)))

@@ -386,3 +386,18 @@ def test_outputs_and_workspace_may_be_given(dev):
     check(c, *got)
     with pytest.raises(sv.SpecVerifyError, match="WORKSPACE"):
         sv.spec_paged_attention(**t, workspace=ws[:-256])
+
+
+def test_default_stream_by_its_handle_and_sizes_beyond_32_bits(dev):
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    c = Case(dev, "bf16", 2, 2, 1, 2, 64, 16, [300, 40], seed=21)
+    t = c.tensors()
+    torch.cuda.synchronize(dev)
+    with torch.cuda.stream(torch.cuda.Stream(dev)):
+        got = sv.spec_paged_attention(**t, stream=torch.cuda.default_stream(dev).cuda_stream)
+    torch.cuda.synchronize(dev)
+    check(c, *got)
+    for kw in (dict(window=2**32 + 5), dict(window=8, sinks=2**32)):  # ctypes would pass 5 and 0
+        with pytest.raises(ValueError, match="32 bits"):
+            sv.spec_paged_attention(**{**t, **kw})
