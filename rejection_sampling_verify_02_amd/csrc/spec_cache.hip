@@ -476,8 +476,8 @@ struct CopyArgs {
 constexpr int COPY_WGS = 1024;  // 4 a CU, whatever there is to copy: the host does not know
 
 // The kept slots of a page into another: a workgroup moves one head of one layer at a time,
-// COPY_STEP 16-byte units a thread in flight (504 pages' halves in 32 layers, 1.01 GB read and
-// written: 187 us, 5.4 TB/s; bound by memory).  Keys: t runs fastest, kept * 16 bytes together.
+// COPY_STEP 16-byte units a thread in flight (16 prompts continued seven ways in 32 layers,
+// 1.01 GB read and written: 186 us, 5.4 TB/s; bound by memory).  Keys: t runs fastest, kept * 16 bytes together.
 // Values: whole units lie together; of the last one only the kept elements are written.
 constexpr int COPY_STEP = 4;
 
