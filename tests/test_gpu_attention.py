@@ -401,3 +401,29 @@ def test_default_stream_by_its_handle_and_sizes_beyond_32_bits(dev):
     for kw in (dict(window=2**32 + 5), dict(window=8, sinks=2**32)):  # ctypes would pass 5 and 0
         with pytest.raises(ValueError, match="32 bits"):
             sv.spec_paged_attention(**{**t, **kw})
+
+
+@pytest.mark.parametrize("N", [2, 40])  # both kernels
+@pytest.mark.parametrize("D", [128, 256])
+def test_f32_scores_keep_their_bits(dev, N, D):
+    """The error over all outputs, which the rounding of the scores decides.  With u = 2^-24 and a
+    rounding's error u / sqrt(3) in the root mean square of a sum's size, products of variance 4:
+    a sum lengthened by four products at a time in K = D / 16 steps gathers (u / sqrt 3) * 2 *
+    sqrt(2) K, four of them twice that, and joining them (u / sqrt 3) * 2 sqrt(D) * sqrt 2; times
+    the scale 1 / sqrt D that is 3.3u + 1.6u (added in squares, 3.7u) at D = 256.  Weights (one rounding of
+    an argument up to 16 below, 4.6u, the power, u, sums and quotient, 2u) come to 5.1u: 6.3u =
+    3.8e-7 in all, and less for D = 128.  Twice that is allowed for the orders in which an
+    instruction may add its four products; a single sum of 256 is beyond it (measured 1.2e-6)."""
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    c = Case(dev, "f32", 4, N, 2, 1, D, 16, [250, 300, 331, 358], seed=23)
+    rng = np.random.default_rng(24)
+    t = c.tensors()
+    # full mantissas: values that bf16 holds too would make the products short
+    c.q = torch.from_numpy(2.0 * rng.standard_normal(c.q.shape)).float().double().numpy()
+    t["q"] = torch.from_numpy(c.q).float().to(dev)
+    out, st = sv.spec_paged_attention(**t)
+    want = c.expect()[0]
+    err = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert st.tolist() == [0] * 4
+    assert err <= 7.6e-7, err
