@@ -677,27 +677,40 @@ struct Rows {
   // Scores to weights 2^(c2 score - nm).  nm follows the row's maximum loosely: it moves only
   // when a score passes it by a factor of 2^8, so that after the first tiles no sum has to be
   // rescaled and the four lanes of a row need not compare notes (weights up to 2^8 keep their
-  // relative rounding, and the quotient of the sums is the same).
-  SVD typename M::P soften(const AttnArgs &a, int r, f32x4 (&sc)[2]) {
-    const float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])), fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-    if (__any(top > lim[r])) {
-      const float mx = fmaxf(rm[r], col_max(top));
-      const float nm2 = (mx == -INFINITY) ? 0.0f : mx * a.c2;
-      const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(nm[r] - nm2);
-      rl[r] = rl[r] * f;
+  // relative rounding, and the quotient of the sums is the same).  One test for all of a lane's
+  // rows, so that what follows is one stretch of code (16 trees of 32 nodes: 2 % off a test each).
+  SVD void soften(const AttnArgs &a, f32x4 (&sc)[R][2], typename M::P (&p)[R]) {
+    float top[R];
+    bool past = false;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
-      rm[r] = mx;
-      nm[r] = nm2;
-      lim[r] = mx + a.slack;
+    for (int r = 0; r < R; ++r) {
+      const f32x4 x = sc[r][0], y = sc[r][1];
+      top[r] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+      past |= top[r] > lim[r];
+    }
+    if (__any(past)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float mx = fmaxf(rm[r], col_max(top[r]));
+        const float nm2 = (mx == -INFINITY) ? 0.0f : mx * a.c2;
+        const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(nm[r] - nm2);
+        rl[r] = rl[r] * f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
+        rm[r] = mx;
+        nm[r] = nm2;
+        lim[r] = mx + a.slack;
+      }
     }
 #pragma unroll
-    for (int t2 = 0; t2 < 2; ++t2)
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[t2][i] = fast_exp2(fmaf(sc[t2][i], a.c2, -nm[r]));
-    const typename M::P p = M::weights(sc);
-    rl[r] = M::add(p, sc, rl[r]);
-    return p;
+      for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[r][t2][i] = fast_exp2(fmaf(sc[r][t2][i], a.c2, -nm[r]));
+      p[r] = M::weights(sc[r]);
+      rl[r] = M::add(p[r], sc[r], rl[r]);
+    }
   }
   // The exponent that a row's sums are relative to (-inf: nothing seen so far).
   SVD float scale(int r) const { return (rm[r] == -INFINITY) ? -INFINITY : nm[r]; }
@@ -845,8 +858,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
           }
         }
         typename M::P pw[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) pw[r] = rows.soften(a, r, sc[r]);
+        rows.soften(a, sc, pw);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -1025,8 +1037,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide_occ<T, 
           for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = M::score(dot[r][t2]);
         if (!plain) rows.mask(a, sg, s, t0, g, sc);
         typename M::P pw[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) pw[r] = rows.soften(a, r, sc[r]);
+        rows.soften(a, sc, pw);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           u32x4 v[M::VT];
