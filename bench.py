@@ -1058,14 +1058,14 @@ def run_round(args, dev, hev):
 
     def call(i, events=None):
         t, d, tok, par, ua, us, pool, kp, vp, q, k, v = sets[i % n_sets]
-        sv.spec_cache_resize(pool, lens, lens + N, kp, vp)
+        room = sv.spec_cache_resize(pool, lens, lens + N, kp, vp)
         for l in range(L):
-            sv.spec_cache_append(k[l], v[l], kp[l], vp[l], pool.page_table, lens)
-            out, st = sv.spec_paged_attention(q[l], kp[l], vp[l], pool.page_table, lens, parent=par)
+            sv.spec_cache_append(k[l], v[l], kp[l], vp[l], pool.page_table, lens, prior=room)
+            out, st = sv.spec_paged_attention(q[l], kp[l], vp[l], pool.page_table, lens, parent=par, prior=room)
         acc, _, path = sv.spec_tree_verify(t, d, tok, par, ua, us, tc.temperature, tc.top_k, max_children=S, workspace=ws, stream=stream)
-        new, st2 = sv.spec_cache_commit(kp, vp, pool.page_table, lens, acc, path)
+        new, st2 = sv.spec_cache_commit(kp, vp, pool.page_table, lens, acc, path, prior=room)
         sv.spec_cache_resize(pool, new, new, kp, vp)
-        status[:] = [st, st2, acc]
+        status[:] = [room, st, st2, acc]
 
     def attend(i, events=None):
         *_, par, _, _, pool, kp, vp, q, _, _ = sets[i % n_sets]

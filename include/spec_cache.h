@@ -40,6 +40,16 @@
  * with every other call on them.  Page indexes, lengths, trees and paths are checked on the
  * device: memory outside the pool is never touched, and a sequence with a code in row_status
  * has the outputs stated at each call.
+ *
+ * Refused sequences.  A sequence that spec_cache_resize refuses (SV_ROW_NO_PAGES, or another
+ * code) keeps the pages it has, and the last of them may be one that other sequences hold too:
+ * what is written to it is written to theirs.  The calls that follow in the round therefore
+ * take the resize's row_status as `prior` (the _after variants below, which are the calls
+ * themselves with prior == NULL): prior [B] int32, and a sequence with prior[b] < 0 is left
+ * alone, before anything else of it is tested.  Its row_status is prior[b]; nothing of it is
+ * written or moved, its attention rows are NaN, and it keeps its length.  prior does not
+ * overlap a call's outputs (SV_ERR_PARAM).  It is read on the device, so that a captured round
+ * follows refusals too.
  */
 #ifndef SPEC_CACHE_H
 #define SPEC_CACHE_H
@@ -108,6 +118,20 @@ sv_status spec_paged_attention_timed(const void *q, int64_t q_stride_b, int64_t 
                                      size_t workspace_bytes, void *stream, void *const *events,
                                      int32_t n_events, int32_t *n_launched);
 
+/* spec_paged_attention (with events as in spec_paged_attention_timed where they are given)
+ * behind a call that may have refused sequences: see `prior` above. */
+sv_status spec_paged_attention_after(const void *q, int64_t q_stride_b, int64_t q_stride_n,
+                                     const void *k_pages, const void *v_pages, sv_dtype dtype,
+                                     const int32_t *page_table, const int32_t *cache_len,
+                                     const int32_t *n_new, const int32_t *parent,
+                                     const int32_t *prior, int32_t B, int32_t N, int32_t Hq,
+                                     int32_t Hkv, int32_t D, int32_t page_size,
+                                     int32_t num_pages, int32_t table_width, float scale,
+                                     int32_t window, int32_t sinks, void *out,
+                                     int32_t *row_status, void *workspace,
+                                     size_t workspace_bytes, void *stream, void *const *events,
+                                     int32_t n_events, int32_t *n_launched);
+
 /* Names of the kernels spec_paged_attention launches, ';'-separated (static storage). */
 const char *sv_attention_launch_plan(int32_t N, int32_t Hq, int32_t Hkv, int32_t D, sv_dtype dtype);
 
@@ -118,13 +142,22 @@ const char *sv_attention_launch_plan(int32_t N, int32_t Hq, int32_t Hkv, int32_t
  *   row_status   [B] int32 out: 0, SV_ROW_BAD_LENGTH or SV_ROW_BAD_PAGE; nothing of the
  *                sequence is then written
  * D is a multiple of 16 up to 512.  The slots' pages must be the sequence's own (as
- * spec_cache_resize leaves them): two sequences that write to one page race. */
+ * spec_cache_resize leaves them for the sequences that it serves; the others are told by
+ * `prior` above): two sequences that write to one page race. */
 sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_n, const void *v,
                             int64_t v_stride_b, int64_t v_stride_n, sv_dtype dtype, void *k_pages,
                             void *v_pages, const int32_t *page_table, const int32_t *cache_len,
                             const int32_t *n_new, int32_t B, int32_t N, int32_t Hkv, int32_t D,
                             int32_t page_size, int32_t num_pages, int32_t table_width,
                             int32_t *row_status, void *stream);
+sv_status spec_cache_append_after(const void *k, int64_t k_stride_b, int64_t k_stride_n,
+                                  const void *v, int64_t v_stride_b, int64_t v_stride_n,
+                                  sv_dtype dtype, void *k_pages, void *v_pages,
+                                  const int32_t *page_table, const int32_t *cache_len,
+                                  const int32_t *n_new, const int32_t *prior, int32_t B,
+                                  int32_t N, int32_t Hkv, int32_t D, int32_t page_size,
+                                  int32_t num_pages, int32_t table_width, int32_t *row_status,
+                                  void *stream);
 
 /* ---- the accepted path's entries moved together, and the new lengths ----
  *
@@ -142,13 +175,21 @@ sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_
  *                beyond N - 1, or slots beyond the table), SV_ROW_BAD_TREE (path_nodes not
  *                increasing in 1 .. N-1) or SV_ROW_BAD_PAGE; new_len is then cache_len and
  *                nothing of the sequence is moved
- * D is a multiple of 16 up to 512.  The slots' pages must be the sequence's own. */
+ * D is a multiple of 16 up to 512.  The slots' pages must be the sequence's own, as for the
+ * append. */
 sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype,
                             const int32_t *page_table, const int32_t *cache_len,
                             const int32_t *accepted_len, const int32_t *path_nodes, int32_t L,
                             int32_t B, int32_t N, int32_t Hkv, int32_t D, int32_t page_size,
                             int32_t num_pages, int32_t table_width, int32_t *new_len,
                             int32_t *row_status, void *stream);
+sv_status spec_cache_commit_after(void *k_pages, void *v_pages, sv_dtype dtype,
+                                  const int32_t *page_table, const int32_t *cache_len,
+                                  const int32_t *accepted_len, const int32_t *path_nodes,
+                                  const int32_t *prior, int32_t L, int32_t B, int32_t N,
+                                  int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                                  int32_t table_width, int32_t *new_len, int32_t *row_status,
+                                  void *stream);
 
 /* ---- pages taken, given back and copied on write ----
  *

@@ -37,7 +37,8 @@ EXPORTED = ("spec_verify", "spec_verify_timed", "sv_workspace_bytes", "sv_worksp
             "sv_read_probe", "spec_verify_noalloc", "sv_timeline_stamps",
             "spec_paged_attention", "spec_paged_attention_timed", "sv_attention_workspace_bytes",
             "sv_attention_launch_plan", "spec_cache_append", "spec_cache_commit", "spec_cache_resize",
-            "sv_resize_workspace_bytes", "spec_cache_fork")
+            "sv_resize_workspace_bytes", "spec_cache_fork", "spec_paged_attention_after", "spec_cache_append_after",
+            "spec_cache_commit_after")
 
 
 class SpecVerifyError(RuntimeError):
@@ -117,9 +118,13 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
     lib.sv_launch_plan.restype = ctypes.c_char_p
     SI = ctypes.c_int64  # strides
     attn = [V, SI, SI, V, V, I32, V, V, V, V, *[I32] * 8, F32, I32, I32, V, V, V, SZ, V]
+    append, commit = [V, SI, SI, V, SI, SI, I32, *[V] * 5, *[I32] * 7, V, V], [V, V, I32, *[V] * 4, *[I32] * 8, V, V, V]
     for fn, args in ((lib.spec_paged_attention, attn), (lib.spec_paged_attention_timed, attn + [V, I32, V]),
-                     (lib.spec_cache_append, [V, SI, SI, V, SI, SI, I32, *[V] * 5, *[I32] * 7, V, V]),
-                     (lib.spec_cache_commit, [V, V, I32, *[V] * 4, *[I32] * 8, V, V, V]),
+                     (lib.spec_cache_append, append), (lib.spec_cache_commit, commit),
+                     # with the row codes of an earlier call before the sizes
+                     (lib.spec_paged_attention_after, attn[:10] + [V] + attn[10:] + [V, I32, V]),
+                     (lib.spec_cache_append_after, append[:12] + [V] + append[12:]),
+                     (lib.spec_cache_commit_after, commit[:7] + [V] + commit[7:]),
                      (lib.spec_cache_resize, [*[V] * 8, *[I32] * 8, V, V, SZ, V]),
                      (lib.spec_cache_fork, [*[V] * 6, *[I32] * 4, V, V])):
         fn.argtypes = args

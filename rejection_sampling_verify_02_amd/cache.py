@@ -6,13 +6,16 @@ here, every step runs in the library's HIP kernels, and nothing proceeds without
 
     pool = PagePool.empty(num_pages, max_seqs, table_width, device)
     k_pages, v_pages = empty_pages(L, num_pages, Hkv, D, page_size, torch.bfloat16, device)
-    spec_cache_resize(pool, cache_len, cache_len + N, k_pages, v_pages)
+    room = spec_cache_resize(pool, cache_len, cache_len + N, k_pages, v_pages)
     for l in range(L):
-        spec_cache_append(k, v, k_pages[l], v_pages[l], pool.page_table, cache_len)
-        out, status = spec_paged_attention(q, k_pages[l], v_pages[l], pool.page_table, cache_len, parent=parent)
+        spec_cache_append(k, v, k_pages[l], v_pages[l], pool.page_table, cache_len, prior=room)
+        out, status = spec_paged_attention(q, k_pages[l], v_pages[l], pool.page_table, cache_len, parent=parent, prior=room)
     acc, tokens, path = spec_tree_verify(target_logits, draft_logits, tokens, parent, ...)
-    cache_len, status = spec_cache_commit(k_pages, v_pages, pool.page_table, cache_len, acc, path)
+    cache_len, status = spec_cache_commit(k_pages, v_pages, pool.page_table, cache_len, acc, path, prior=room)
     spec_cache_resize(pool, cache_len, cache_len, k_pages, v_pages)
+
+``prior`` carries the resize's row codes on: a sequence that the pool had no pages left for may
+still share its last page with others, and is left alone by the calls that would write to it.
 
 Calls are enqueued on the current stream of the tensors' device, or on ``stream`` (a raw
 hipStream_t), and may be captured into a HIP graph.  Work memory is taken for each call from
@@ -202,13 +205,14 @@ def sv_attention_launch_plan(N: int, Hq: int, Hkv: int, D: int, dtype: int) -> l
 
 
 def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=None, n_new=None, scale: float | None = None,
-                         window: int = 0, sinks: int = 0, workspace=None, stream=None, out=None, events=None):
+                         window: int = 0, sinks: int = 0, prior=None, workspace=None, stream=None, out=None, events=None):
     """Attention of the new tokens over a paged cache (see include/spec_cache.h).
 
     q [B, N, Hq, D] bfloat16 or float32 (heads together, any strides between sequences and
     nodes), one layer's k_pages [P, Hkv, D/E, page, E] and v_pages [P, Hkv, page/E, D, E],
-    page_table [B, W], cache_len [B], n_new [B] (None: N each) and parent [B, N] (None: a
-    chain) int32.  scale defaults to 1 / sqrt(D).  Returns (out [B, N, Hq, D], row_status [B]);
+    page_table [B, W], cache_len [B], n_new [B] (None: N each), parent [B, N] (None: a chain)
+    and prior [B] (row codes of an earlier call: a sequence with one has it again and rows of
+    NaN) int32.  scale defaults to 1 / sqrt(D).  Returns (out [B, N, Hq, D], row_status [B]);
     ``out`` may supply the two tensors.  ``events`` as for spec_verify: the number of kernels is
     then returned last.
     """
@@ -217,7 +221,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
     if elsewhere is not None:
         with elsewhere:
             return spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, parent=parent, n_new=n_new, scale=scale,
-                                        window=window, sinks=sinks, workspace=workspace, out=out, events=events)
+                                        window=window, sinks=sinks, prior=prior, workspace=workspace, out=out, events=events)
     dt = _code(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [B, N, Hq, D]")
@@ -230,7 +234,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
     table, W = _table(page_table, dev, B)
     seqs = (B,)
     lens, news = _ints(cache_len, "cache_len", seqs, dev), _ints(n_new, "n_new", seqs, dev, True)
-    par = _ints(parent, "parent", (B, N), dev, True)
+    par, pri = _ints(parent, "parent", (B, N), dev, True), _ints(prior, "prior", seqs, dev, True)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if window or sinks:
@@ -243,28 +247,28 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
 
     o, st = out or (torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(cache_len))
     ws = _work(workspace, _attention_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
-    args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, news, par, B, N, Hq, Hkv, D, page, P, W,
+    args = (qp, qb, qn, k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, news, par, pri, B, N, Hq, Hkv, D, page, P, W,
             scale, window, sinks, o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if events is None:
-        rc = load_library().spec_paged_attention(*args)
+        rc = load_library().spec_paged_attention_after(*args, None, 0, None)
         if rc:
             _raise(rc)
         return o, st
     n = ctypes.c_int32(0)
-    _raise(load_library().spec_paged_attention_timed(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
+    _raise(load_library().spec_paged_attention_after(*args, (ctypes.c_void_p * len(events))(*events), len(events), ctypes.byref(n)))
     return o, st, n.value
 
 
-def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=None, stream=None, out=None):
+def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=None, prior=None, stream=None, out=None):
     """Writes the new tokens' keys and values k, v [B, N, Hkv, D] (heads together, any strides
     between sequences and nodes) into slots cache_len .. cache_len + n_new - 1 of one layer's
-    k_pages and v_pages (see include/spec_cache.h).  Returns row_status [B] int32, which ``out``
-    may supply."""
+    k_pages and v_pages (see include/spec_cache.h); nothing for a sequence with a row code of an
+    earlier call in prior [B] int32.  Returns row_status [B] int32, which ``out`` may supply."""
     dev = _device(k, "k")
     elsewhere = _elsewhere(dev, stream)
     if elsewhere is not None:
         with elsewhere:
-            return spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, n_new=n_new, out=out)
+            return spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, n_new=n_new, prior=prior, out=out)
     dt = _code(k, "k")
     if k.dim() != 4:
         raise ValueError("k must be [B, N, Hkv, D]")
@@ -278,29 +282,31 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=No
     table, W = _table(page_table, dev, B)
     seqs = (B,)
     lens, news = _ints(cache_len, "cache_len", seqs, dev), _ints(n_new, "n_new", seqs, dev, True)
+    pri = _ints(prior, "prior", seqs, dev, True)
     if out is not None:
         _ints(out, "row_status", seqs, dev)
 
     st = torch.empty_like(cache_len) if out is None else out
-    rc = load_library().spec_cache_append(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens, news,
-                                          B, N, Hkv, D, page, P, W, st.data_ptr(), _raw_stream(dev))
+    rc = load_library().spec_cache_append_after(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens,
+                                                news, pri, B, N, Hkv, D, page, P, W, st.data_ptr(), _raw_stream(dev))
     if rc:
         _raise(rc)
     return st
 
 
 def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes=None, *, max_new: int | None = None,
-                      stream=None, out=None):
+                      prior=None, stream=None, out=None):
     """Keeps node 0 and the accepted nodes of every sequence in all layers of k_pages
     [L, P, Hkv, D/E, page, E] and v_pages (see include/spec_cache.h): accepted_len [B] and
     path_nodes [B, N] int32 as spec_tree_verify returns them, or for chains accepted_len alone
-    and ``max_new``, the N = G + 1 new tokens that were verified.  Returns (new_len [B],
+    and ``max_new``, the N = G + 1 new tokens that were verified.  A sequence with a row code of
+    an earlier call in prior [B] int32 keeps its length and its entries.  Returns (new_len [B],
     row_status [B]) int32; ``out`` may supply them (for chains new_len may be cache_len itself)."""
     dev = _device(k_pages, "k_pages")
     elsewhere = _elsewhere(dev, stream)
     if elsewhere is not None:
         with elsewhere:
-            return spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes, max_new=max_new, out=out)
+            return spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, path_nodes, max_new=max_new, prior=prior, out=out)
     dt = _code(k_pages, "k_pages")
     P, Hkv, D, page = _pages(k_pages, v_pages, 6, k_pages.dtype, dev)
     table, W = _table(page_table, dev)
@@ -315,14 +321,15 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
         N = _int32(max_new, "max_new")
     seqs = (B,)
     lens, acc = _ints(cache_len, "cache_len", seqs, dev), _ints(accepted_len, "accepted_len", seqs, dev)
-    path = _ints(path_nodes, "path_nodes", (B, N), dev, True)
+    path, pri = _ints(path_nodes, "path_nodes", (B, N), dev, True), _ints(prior, "prior", seqs, dev, True)
     if out is not None:
         _ints(out[0], "new_len", seqs, dev)
         _ints(out[1], "row_status", seqs, dev)
 
     n, st = out or (torch.empty_like(cache_len), torch.empty_like(cache_len))
-    rc = load_library().spec_cache_commit(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, k_pages.shape[0],
-                                          B, N, Hkv, D, page, P, W, n.data_ptr(), st.data_ptr(), _raw_stream(dev))
+    rc = load_library().spec_cache_commit_after(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, pri,
+                                                k_pages.shape[0], B, N, Hkv, D, page, P, W, n.data_ptr(), st.data_ptr(),
+                                                _raw_stream(dev))
     if rc:
         _raise(rc)
     return n, st

@@ -38,7 +38,7 @@ constexpr int TILE = 32;  // slots a wave takes at a time
 struct AttnArgs {
   const char *q, *k_pages, *v_pages;
   long long q_sb, q_sn;  // bytes
-  const int32_t *page_table, *cache_len, *n_new, *parent;
+  const int32_t *page_table, *cache_len, *n_new, *parent, *prior;
   int B, N, Hq, Hkv, group, page_shift, P, W;
   float c2;        // |scale| log2 e: weights are powers of two
   unsigned flip;   // the sign bits of q, for a negative scale
@@ -64,14 +64,17 @@ struct Span {
 
 struct Seq {
   int len, m;
-  bool ok;  // lengths fit; the pages and the tree are checked elsewhere
+  bool ok;  // not refused before, and lengths fit; the pages and the tree are checked elsewhere
 };
+
+// The code of an earlier call that refused the sequence, or 0.
+SVD int prior_of(const AttnArgs &a, int b) { return a.prior ? min(a.prior[b], 0) : 0; }
 
 SVD Seq seq_of(const AttnArgs &a, int b) {
   Seq s;
   s.len = a.cache_len[b];
   s.m = a.n_new ? a.n_new[b] : a.N;
-  s.ok = s.len >= 0 && s.m >= 0 && s.m <= a.N && (long long)s.len + s.m <= ((long long)a.W << a.page_shift);
+  s.ok = prior_of(a, b) == 0 && s.len >= 0 && s.m >= 0 && s.m <= a.N && (long long)s.len + s.m <= ((long long)a.W << a.page_shift);
   if (!s.ok) s.len = s.m = 0;
   return s;
 }
@@ -372,7 +375,10 @@ SVD SharedBooks books_at(unsigned *p, int RT, int N, int group) {
 SVD int seq_code(const AttnArgs &a, const Seq &sq, int b, const SharedBooks &s) {
   const int tid = threadIdx.x, page = 1 << a.page_shift;
   const int32_t *table = a.page_table + (size_t)b * a.W;
-  if (!sq.ok) return SV_ROW_BAD_LENGTH;
+  if (!sq.ok) {
+    const int prior = prior_of(a, b);
+    return prior != 0 ? prior : SV_ROW_BAD_LENGTH;
+  }
   if (sq.m == 0) return 0;
   int bad = 0;
   if (a.parent)
@@ -1230,9 +1236,9 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
 }
 
 sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_pages, const void *v_pages, sv_dtype dt,
-                   const int32_t *table, const int32_t *cache_len, const int32_t *n_new, const int32_t *parent, int32_t B,
-                   int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W, float scale,
-                   int32_t window, int32_t sinks, void *out, int32_t *status, void *ws, size_t ws_bytes, void *stream,
+                   const int32_t *table, const int32_t *cache_len, const int32_t *n_new, const int32_t *parent,
+                   const int32_t *prior, int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page, int32_t P,
+                   int32_t W, float scale, int32_t window, int32_t sinks, void *out, int32_t *status, void *ws, size_t ws_bytes, void *stream,
                    void *const *ev, int32_t nev, int32_t *nl) {
   if (nl) *nl = 0;
   if (dt != SV_F32 && dt != SV_BF16) return SV_ERR_DTYPE;
@@ -1245,6 +1251,8 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out | ((uintptr_t)q_sb * esz) | ((uintptr_t)q_sn * esz)) & 15)
     return SV_ERR_ALIGN;
   if (ws_bytes < p.total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
+  // several workgroups read prior, and one writes the status
+  if (prior && (uintptr_t)prior < (uintptr_t)(status + B) && (uintptr_t)status < (uintptr_t)(prior + B)) return SV_ERR_PARAM;
   char *base = static_cast<char *>(ws);
   AttnArgs a = {};
   a.q = static_cast<const char *>(q);
@@ -1256,6 +1264,7 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   a.cache_len = cache_len;
   a.n_new = n_new;
   a.parent = parent;
+  a.prior = prior;
   a.B = B;
   a.N = N;
   a.Hq = Hq;
@@ -1305,7 +1314,7 @@ sv_status spec_paged_attention(const void *q, int64_t q_stride_b, int64_t q_stri
                                int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
                                int32_t table_width, float scale, int32_t window, int32_t sinks, void *out,
                                int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream) {
-  return attn_run(q, q_stride_b, q_stride_n, k_pages, v_pages, dtype, page_table, cache_len, n_new, parent, B, N, Hq, Hkv, D,
+  return attn_run(q, q_stride_b, q_stride_n, k_pages, v_pages, dtype, page_table, cache_len, n_new, parent, nullptr, B, N, Hq, Hkv, D,
                   page_size, num_pages, table_width, scale, window, sinks, out, row_status, workspace, workspace_bytes,
                   stream, nullptr, 0, nullptr);
 }
@@ -1317,7 +1326,20 @@ sv_status spec_paged_attention_timed(const void *q, int64_t q_stride_b, int64_t 
                                      int32_t num_pages, int32_t table_width, float scale, int32_t window, int32_t sinks,
                                      void *out, int32_t *row_status, void *workspace, size_t workspace_bytes,
                                      void *stream, void *const *events, int32_t n_events, int32_t *n_launched) {
-  return attn_run(q, q_stride_b, q_stride_n, k_pages, v_pages, dtype, page_table, cache_len, n_new, parent, B, N, Hq, Hkv, D,
+  return attn_run(q, q_stride_b, q_stride_n, k_pages, v_pages, dtype, page_table, cache_len, n_new, parent, nullptr, B, N, Hq, Hkv, D,
+                  page_size, num_pages, table_width, scale, window, sinks, out, row_status, workspace, workspace_bytes,
+                  stream, events, n_events, n_launched);
+}
+
+sv_status spec_paged_attention_after(const void *q, int64_t q_stride_b, int64_t q_stride_n, const void *k_pages,
+                                     const void *v_pages, sv_dtype dtype, const int32_t *page_table,
+                                     const int32_t *cache_len, const int32_t *n_new, const int32_t *parent,
+                                     const int32_t *prior, int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t page_size, int32_t num_pages, int32_t table_width, float scale, int32_t window,
+                                     int32_t sinks, void *out, int32_t *row_status, void *workspace,
+                                     size_t workspace_bytes, void *stream, void *const *events, int32_t n_events,
+                                     int32_t *n_launched) {
+  return attn_run(q, q_stride_b, q_stride_n, k_pages, v_pages, dtype, page_table, cache_len, n_new, parent, prior, B, N, Hq, Hkv, D,
                   page_size, num_pages, table_width, scale, window, sinks, out, row_status, workspace, workspace_bytes,
                   stream, events, n_events, n_launched);
 }

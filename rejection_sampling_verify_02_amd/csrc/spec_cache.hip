@@ -27,7 +27,7 @@ struct AppendArgs {
   const char *k, *v;
   long long k_sb, k_sn, v_sb, v_sn;  // bytes
   char *k_pages, *v_pages;
-  const int32_t *page_table, *cache_len, *n_new;
+  const int32_t *page_table, *cache_len, *n_new, *prior;
   int N, chunks;
   int32_t *row_status;
   Pool pool;
@@ -53,8 +53,10 @@ __global__ __launch_bounds__(NT) void k_cache_append(const AppendArgs a) {
   const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D;
   const int32_t *table = a.page_table + (size_t)b * a.pool.W;
 
-  int code = 0;
-  if (len < 0 || m < 0 || m > a.N || (long long)len + m > ((long long)a.pool.W << sh)) {
+  int code = a.prior ? min(a.prior[b], 0) : 0;
+  if (code != 0) {
+    // an earlier call refused the sequence: its pages may not be its own
+  } else if (len < 0 || m < 0 || m > a.N || (long long)len + m > ((long long)a.pool.W << sh)) {
     code = SV_ROW_BAD_LENGTH;
   } else if (m > 0) {
     const int p0 = len >> sh, p1 = (len + m - 1) >> sh;
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(NT) void k_cache_append(const AppendArgs a) {
 
 struct CommitArgs {
   char *k_pages, *v_pages;
-  const int32_t *page_table, *cache_len, *accepted_len, *path;
+  const int32_t *page_table, *cache_len, *accepted_len, *path, *prior;
   int N;
   unsigned B, LH;  // layers times heads
   int32_t *new_len, *row_status;
@@ -135,8 +137,10 @@ __global__ __launch_bounds__(NT) void k_cache_commit(const CommitArgs a) {
   const int32_t *table = a.page_table + (size_t)b * a.pool.W;
 
   if (tid == 0) s_first = acc;
-  int code = 0, top = 0;  // top: the last node kept
-  if (acc < 0) {
+  int code = a.prior ? min(a.prior[b], 0) : 0, top = 0;  // top: the last node kept
+  if (code != 0) {
+    // an earlier call refused the sequence: its pages may not be its own
+  } else if (acc < 0) {
     code = acc;
   } else if (len < 0 || acc > a.N - 1) {
     code = SV_ROW_BAD_LENGTH;
@@ -590,6 +594,11 @@ Pool pool_of(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) {
   return Pool{__builtin_ctz((unsigned)page), P, W, (unsigned)Hkv, (unsigned)D};
 }
 
+// Whether two arrays of n int32 share memory.
+bool overlap(const int32_t *x, const int32_t *y, int32_t n) {
+  return x && y && (uintptr_t)x < (uintptr_t)(y + n) && (uintptr_t)y < (uintptr_t)(x + n);
+}
+
 template <typename A>
 sv_status launch(const void *fn, A &a, long long grid, int block, void *stream, unsigned lds = 0) {
   sv_host::Launcher L{(hipStream_t)stream, nullptr, 0};
@@ -622,6 +631,15 @@ sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_
                             const int32_t *page_table, const int32_t *cache_len, const int32_t *n_new, int32_t B,
                             int32_t N, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
                             int32_t table_width, int32_t *row_status, void *stream) {
+  return spec_cache_append_after(k, k_stride_b, k_stride_n, v, v_stride_b, v_stride_n, dtype, k_pages, v_pages, page_table,
+                                 cache_len, n_new, nullptr, B, N, Hkv, D, page_size, num_pages, table_width, row_status, stream);
+}
+
+sv_status spec_cache_append_after(const void *k, int64_t k_stride_b, int64_t k_stride_n, const void *v,
+                                  int64_t v_stride_b, int64_t v_stride_n, sv_dtype dtype, void *k_pages, void *v_pages,
+                                  const int32_t *page_table, const int32_t *cache_len, const int32_t *n_new,
+                                  const int32_t *prior, int32_t B, int32_t N, int32_t Hkv, int32_t D, int32_t page_size,
+                                  int32_t num_pages, int32_t table_width, int32_t *row_status, void *stream) {
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   const int esz = dtype == SV_BF16 ? 2 : 4;
   if (B < 1 || N < 1 || N > SV_CACHE_MAX_NEW || !pool_ok(Hkv, D, page_size, num_pages, table_width)) return SV_ERR_SHAPE;
@@ -640,11 +658,13 @@ sv_status spec_cache_append(const void *k, int64_t k_stride_b, int64_t k_stride_
   if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)a.k_sb | (uintptr_t)a.k_sn |
        (uintptr_t)a.v_sb | (uintptr_t)a.v_sn) & 15)
     return SV_ERR_ALIGN;
+  if (overlap(prior, row_status, B)) return SV_ERR_PARAM;
   a.k_pages = static_cast<char *>(k_pages);
   a.v_pages = static_cast<char *>(v_pages);
   a.page_table = page_table;
   a.cache_len = cache_len;
   a.n_new = n_new;
+  a.prior = prior;
   a.N = N;
   a.row_status = row_status;
   a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
@@ -655,6 +675,15 @@ sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype, const 
                             const int32_t *cache_len, const int32_t *accepted_len, const int32_t *path_nodes, int32_t L,
                             int32_t B, int32_t N, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
                             int32_t table_width, int32_t *new_len, int32_t *row_status, void *stream) {
+  return spec_cache_commit_after(k_pages, v_pages, dtype, page_table, cache_len, accepted_len, path_nodes, nullptr, L, B, N, Hkv,
+                                 D, page_size, num_pages, table_width, new_len, row_status, stream);
+}
+
+sv_status spec_cache_commit_after(void *k_pages, void *v_pages, sv_dtype dtype, const int32_t *page_table,
+                                  const int32_t *cache_len, const int32_t *accepted_len, const int32_t *path_nodes,
+                                  const int32_t *prior, int32_t L, int32_t B, int32_t N, int32_t Hkv, int32_t D,
+                                  int32_t page_size, int32_t num_pages, int32_t table_width, int32_t *new_len,
+                                  int32_t *row_status, void *stream) {
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (B < 1 || L < 1 || N < 1 || N > SV_CACHE_MAX_NEW || !pool_ok(Hkv, D, page_size, num_pages, table_width)) return SV_ERR_SHAPE;
   const long long LH = (long long)L * Hkv;
@@ -664,7 +693,8 @@ sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype, const 
   // With paths several workgroups read a sequence's lengths: what they read is not written here.
   for (const int32_t *in : {cache_len, accepted_len})
     for (const int32_t *to : {(const int32_t *)new_len, (const int32_t *)row_status})
-      if (path_nodes && (uintptr_t)in < (uintptr_t)(to + B) && (uintptr_t)to < (uintptr_t)(in + B)) return SV_ERR_PARAM;
+      if (path_nodes && overlap(in, to, B)) return SV_ERR_PARAM;
+  if (overlap(prior, new_len, B) || overlap(prior, row_status, B)) return SV_ERR_PARAM;
   CommitArgs a = {};
   a.k_pages = static_cast<char *>(k_pages);
   a.v_pages = static_cast<char *>(v_pages);
@@ -672,6 +702,7 @@ sv_status spec_cache_commit(void *k_pages, void *v_pages, sv_dtype dtype, const 
   a.cache_len = cache_len;
   a.accepted_len = accepted_len;
   a.path = path_nodes;
+  a.prior = prior;
   a.N = N;
   a.B = (unsigned)B;
   a.LH = (unsigned)LH;

@@ -1,0 +1,208 @@
+"""Sequences that spec_cache_resize refuses, through the rest of the round: their last page may be
+one that others hold too, so with the resize's codes as `prior` nothing of theirs is written or
+moved, their rows are NaN, the code is handed on and they keep their length; a later round serves
+them.  The cache is compared entry by entry with every sequence's own tokens, kept here."""
+import numpy as np
+import pytest
+
+import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+NO_PAGES = -9
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import rejection_sampling_verify_02_amd as sv
+    sv.load_library()
+    return torch.device("cuda:0")
+
+
+def i32(x, dev):
+    import torch
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)
+
+
+class Forked:
+    """A prompt of n tokens and its forks: every sequence holds the prompt's pages, the pool has
+    `spare` pages besides.  The entries are small whole numbers, which every type holds."""
+
+    def __init__(self, dev, dtype, S, n, page, spare, L=2, H=2, D=64):
+        import torch
+        import rejection_sampling_verify_02_amd as sv
+        self.sv, self.dev, self.S, self.page, self.L, self.H, self.D = sv, dev, S, page, L, H, D
+        self.dt, self.esz = (torch.bfloat16, 2) if dtype == "bf16" else (torch.float32, 4)
+        self.rng = np.random.default_rng(n + S)
+        held = -(-n // page)
+        P, W = held + spare, held + 2
+        self.pool = sv.PagePool.empty(P, S, W, dev)
+        self.kp, self.vp = sv.empty_pages(L, P, H, D, page, self.dt, dev)
+        self.lens = i32([0] * S, dev)
+        want = i32([n] + [0] * (S - 1), dev)
+        assert sv.spec_cache_resize(self.pool, self.lens, want, self.kp, self.vp).tolist() == [0] * S
+        new = self.entries(n)
+        for l in range(L):
+            st = sv.spec_cache_append(self.tensor(new[l, 0]), self.tensor(new[l, 1]), self.kp[l], self.vp[l], self.pool.page_table,
+                                      self.lens, n_new=want)
+            assert st.tolist() == [0] * S
+        self.lens.copy_(want)
+        assert sv.spec_cache_fork(self.pool, self.lens, i32([0] * (S - 1), dev), i32(range(1, S), dev)).tolist() == [0] * (S - 1)
+        self.kept = [[new[:, :, 0, t] for t in range(n)] for _ in range(S)]
+
+    def entries(self, N):
+        return self.rng.integers(-99, 99, (self.L, 2, self.S, N, self.H, self.D)).astype(np.float64)
+
+    def tensor(self, x):
+        import torch
+        return torch.from_numpy(np.ascontiguousarray(x)).to(self.dt).to(self.dev)
+
+    def same(self):
+        """Every sequence's entries are its own tokens'."""
+        E = 16 // self.esz
+        table, hk, hv = self.pool.page_table.cpu().numpy(), self.kp.double().cpu().numpy(), self.vp.double().cpu().numpy()
+        assert self.lens.tolist() == [len(t) for t in self.kept]
+        for b in range(self.S):
+            for l in range(self.L if self.kept[b] else 0):
+                k, v = ref.unpack(hk[l], hv[l], table[b], len(self.kept[b]), self.page, E)
+                assert np.array_equal(k, np.stack([t[l, 0] for t in self.kept[b]], 1)), b
+                assert np.array_equal(v, np.stack([t[l, 1] for t in self.kept[b]], 1)), b
+
+    def round(self, N, path, g=2):
+        """One round in which every sequence's `path` (None: a chain of N - 1 drafts, all accepted)
+        is accepted; returns the resize's codes."""
+        import torch
+        sv = self.sv
+        room = sv.spec_cache_resize(self.pool, self.lens, self.lens + N, self.kp, self.vp)
+        codes = room.tolist()
+        new = self.entries(N)
+        parent = i32([np.arange(-1, N - 1)] * self.S, self.dev)
+        q = self.tensor(0.01 * self.rng.standard_normal((self.S, N, self.H * g, self.D)))
+        held = [c == 0 for c in codes]
+        for l in range(self.L):
+            st = sv.spec_cache_append(self.tensor(new[l, 0]), self.tensor(new[l, 1]), self.kp[l], self.vp[l], self.pool.page_table,
+                                      self.lens, prior=room)
+            assert st.tolist() == codes
+            for par in (None, parent):
+                out, st = sv.spec_paged_attention(q, self.kp[l], self.vp[l], self.pool.page_table, self.lens, parent=par, prior=room)
+                assert st.tolist() == codes
+                nan = torch.isnan(out)
+                assert [bool(nan[b].all()) for b in range(self.S)] == [not h for h in held]
+                assert not nan[[b for b in range(self.S) if held[b]]].any()
+        acc = i32([len(path) if path is not None else N - 1] * self.S, self.dev)
+        nodes = i32([list(path) + [-1] * (N - len(path))] * self.S, self.dev) if path is not None else None
+        more = {"max_new": N} if path is None else {}
+        self.lens, st = sv.spec_cache_commit(self.kp, self.vp, self.pool.page_table, self.lens, acc, nodes, prior=room, **more)
+        assert st.tolist() == codes
+        for b in range(self.S):
+            if held[b]:
+                self.kept[b] += [new[:, :, b, n] for n in [0, *(path if path is not None else range(1, N))]]
+        assert sv.spec_cache_resize(self.pool, self.lens, self.lens, self.kp, self.vp).tolist() == [0] * self.S
+        self.same()
+        return codes
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("path", [None, (1, 2, 3, 4), (2, 4), ()])
+@pytest.mark.parametrize("n,page", [(100, 64), (37, 16)])
+def test_new_tokens_that_fit_a_shared_page(dev, dtype, path, n, page):
+    """The new tokens fit the shared last page, and the pool has pages for one of the four: the
+    others are refused, and nothing reaches their siblings' entries.  Then the pool grows by the
+    pages of a sequence that ends, and those that were refused are served."""
+    x = Forked(dev, dtype, 4, n, page, spare=1)
+    assert x.round(5, path) == [0, NO_PAGES, NO_PAGES, NO_PAGES]
+    assert x.lens.tolist()[1:] == [n] * 3
+    # sequence 0 ends: its own page is free again
+    x.sv.spec_cache_resize(x.pool, i32([0] * 4, dev), i32([0, -1, -1, -1], dev), x.kp, x.vp)
+    x.lens[0] = 0
+    x.kept[0] = []
+    room = x.sv.spec_cache_resize(x.pool, x.lens, x.lens + i32([-1, 5, 5, 5], dev), x.kp, x.vp)
+    assert room.tolist() == [0, 0, NO_PAGES, NO_PAGES]
+    x.same()
+
+
+def test_every_sequence_is_refused(dev):
+    x = Forked(dev, "bf16", 3, 20, 16, spare=0)
+    assert x.round(4, (1, 3)) == [NO_PAGES] * 3
+    assert x.round(4, None) == [NO_PAGES] * 3
+
+
+@pytest.mark.parametrize("N", [3, 40])  # both attention kernels
+def test_codes_of_any_call_come_first(dev, N):
+    """A code in prior is handed on whatever else is wrong with the sequence; 0 and positive numbers
+    are no codes; sequences without one give the bits they give alone."""
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    from test_gpu_attention import Case
+    c = Case(dev, "bf16", 6, N, 2, 2, 64, 16, [40, 41, 300, 43, 44, 45], tree=True, news=[N] * 6, seed=12)
+    t = c.tensors()
+    good, _ = sv.spec_paged_attention(**t)
+    t["cache_len"][0] = -1
+    t["parent"][1, N - 1] = N - 1
+    t["page_table"][2, 2] = -1
+    prior = i32([-10, -7, -9, 0, 5, -1], dev)
+    out, st = sv.spec_paged_attention(**t, prior=prior)
+    assert st.tolist() == [-10, -7, -9, 0, 0, -1]
+    assert torch.isnan(out[[0, 1, 2, 5]]).all() and torch.equal(out[3:5], good[3:5])
+    before = t["k_pages"].clone(), t["v_pages"].clone()
+    k = torch.ones((6, N, 2, 64), dtype=torch.bfloat16, device=dev)
+    st = sv.spec_cache_append(k, k, t["k_pages"], t["v_pages"], t["page_table"], t["cache_len"], prior=i32([-10, -7, -9, -2, -3, -1], dev))
+    assert st.tolist() == [-10, -7, -9, -2, -3, -1]
+    acc, path = i32([-4, 1, 1, N, 1, 2], dev), i32([[2] + [-1] * (N - 1)] * 6, dev)
+    new, st = sv.spec_cache_commit(t["k_pages"][None], t["v_pages"][None], t["page_table"], t["cache_len"], acc, path,
+                                   prior=i32([-10, -7, -9, -2, -3, -1], dev))
+    assert st.tolist() == [-10, -7, -9, -2, -3, -1] and torch.equal(new, t["cache_len"])
+    assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) for a, b in zip(before, (t["k_pages"], t["v_pages"])))
+
+
+def test_a_captured_round_follows_refusals(dev):
+    """One graph of a round, replayed while the pool's room changes: what each replay refuses is
+    decided on the device."""
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    x = Forked(dev, "bf16", 3, 21, 16, spare=2, L=1)
+    N = 4
+    new = x.entries(N)
+    k, v = x.tensor(new[0, 0]), x.tensor(new[0, 1])
+    q = x.tensor(0.01 * x.rng.standard_normal((3, N, 4, 64)))
+    acc = i32([N - 1] * 3, dev)
+
+    def step(pool, kp, vp, lens):
+        room = sv.spec_cache_resize(pool, lens, lens + N, kp, vp)
+        st = [sv.spec_cache_append(k, v, kp[0], vp[0], pool.page_table, lens, prior=room)]
+        out, s = sv.spec_paged_attention(q, kp[0], vp[0], pool.page_table, lens, prior=room)
+        n, s2 = sv.spec_cache_commit(kp, vp, pool.page_table, lens, acc, max_new=N, prior=room)
+        lens.copy_(n)
+        sv.spec_cache_resize(pool, lens, lens, kp, vp)
+        return room, [*st, s, s2], out
+
+    def twin():
+        return sv.PagePool(*(t.clone() for t in x.pool)), x.kp.clone(), x.vp.clone(), x.lens.clone()
+
+    warm = twin()
+    step(*warm)
+    torch.cuda.synchronize(dev)
+    a, b = twin(), twin()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        room, codes, out = step(*a)
+    refused = served = 0
+    for turn in range(6):
+        if turn == 3:  # sequence 0 ends in both: its pages are free
+            for y in (a, b):
+                sv.spec_cache_resize(y[0], i32([0] * 3, dev), i32([0, -1, -1], dev), y[1], y[2])
+                y[3][0] = 0
+        g.replay()
+        want = step(*b)
+        torch.cuda.synchronize(dev)
+        assert room.tolist() == want[0].tolist() and all(c.tolist() == room.tolist() for c in codes + want[1])
+        assert torch.equal(out.nan_to_num(9.0), want[2].nan_to_num(9.0))
+        assert torch.isnan(out).flatten(1).all(1).tolist() == [r != 0 for r in room.tolist()]
+        for p, r in zip((*a[0], *a[1:]), (*b[0], *b[1:])):
+            assert torch.equal(p, r)
+        refused += sum(r == NO_PAGES for r in room.tolist())
+        served += sum(r == 0 for r in room.tolist())
+    assert refused and served
