@@ -237,7 +237,8 @@ struct ResizeArgs {
   int S, P, W, page_shift;
   int32_t *row_status;
   // workspace
-  int32_t *alloc;   // [P] the fresh pages in order, then the pages they replaced (-1: none)
+  int32_t *alloc;   // [P] the fresh pages in order
+  int32_t *old;     // [P] the pages they replaced (-1: none)
   int4 *copies;     // [S] page to copy from, page to copy to, slots to copy
   int32_t *n_copy;
 };
@@ -305,8 +306,9 @@ SVD void rz_sync() {
 // sequences before it, so one workgroup does them.  Bound: a chain of about ten rounds to
 // memory.  Each round runs over the table entries it concerns laid end to end, whoever's they
 // are, a thread an entry, which it keeps in registers (256 sequences whose pages grow and
-// shrink: 8.6 us; a wave a sequence, 16 sequences after one another, 54).  Which pages are picked does not depend on the order in
-// which atomics land: the counts are sums, and picking reads the map only after all of them.
+// shrink: 9.4 us; a wave a sequence, 16 sequences after one another, 54).  Which pages are
+// picked does not depend on the order in which atomics land: the counts are sums, and picking
+// reads the map only after all of them.
 __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
   extern __shared__ unsigned s_dyn[];
   __shared__ unsigned s_w[RZ_NW];
@@ -408,18 +410,23 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
     found += tot;
   }
   found = min(found, need_all);
+  // A sequence's pages are those from s_swap + s_add on, replaced entries first, if the free
+  // pages reach to its last one (then they reach all sequences before it).
+  auto end_of = [&](int b) { return s_swap[b + 1] + s_add[b + 1]; };
+  auto some = [&](int b) { return end_of(b) > s_swap[b] + s_add[b]; };
+  auto fits = [&](int b) { return end_of(b) <= found; };
+  for (int b = tid; b < S; b += RZ_NT)
+    if (some(b) && fits(b)) atomicMax(&s_served, (int)end_of(b));
   rz_sync();
 
-  // ---- handed out: a sequence's pages are those from s_swap + s_add on, replaced entries first,
-  // if the free pages reach to its last one (then they reach all sequences before it)
-  auto end_of = [&](int b) { return s_swap[b + 1] + s_add[b + 1]; };
-  auto fits = [&](int b) { return end_of(b) <= found; };
+  // ---- handed out.  The books of the fresh pages are kept back until all of it is done: what
+  // swaps says of an entry must be what was counted, also where the map calls a page free that
+  // has holders (counted pages and taken ones would be different ones then, and a page that is
+  // already gone could be taken again).
   auto take = [&](int b, int i, unsigned at, int old) {
     const int fresh = a.alloc[at];
     row_of(b)[i] = fresh;
-    a.alloc[at] = old;
-    atomicAnd(&a.free_map[fresh >> 5], ~(1u << (fresh & 31)));
-    __hip_atomic_store(&a.ref_count[fresh], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.old[at] = old;
     return fresh;
   };
   if (n_swap > 0) {
@@ -446,23 +453,26 @@ __global__ __launch_bounds__(RZ_NT) void k_cache_resize(const ResizeArgs a) {
     if (fits(b)) take(b, a.seq_pages[b] + (int)(e - s_add[b]), s_swap[b + 1] + e, -1);
   }
   __syncthreads();
+  for (int k = tid; k < s_served; k += RZ_NT) {
+    const int fresh = a.alloc[k];
+    atomicAnd(&a.free_map[fresh >> 5], ~(1u << (fresh & 31)));
+    __hip_atomic_store(&a.ref_count[fresh], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
   for (int b = tid; b < S; b += RZ_NT) {
     const int goal = s_goal[b];
     if (goal < 0) continue;
-    const bool some = s_swap[b + 1] + s_add[b + 1] > s_swap[b] + s_add[b];
-    if (some && !fits(b)) {
+    if (some(b) && !fits(b)) {
       a.row_status[b] = SV_ROW_NO_PAGES;
       a.seq_pages[b] = min(a.seq_pages[b], goal);
     } else {
       a.seq_pages[b] = goal;
-      if (some) atomicMax(&s_served, (int)end_of(b));
     }
   }
   rz_sync();
   // ---- replaced pages lose a holder (only now: the counts above are those after giving back)
   if (n_swap > 0)
     for (int k = tid; k < s_served; k += RZ_NT)
-      if (a.alloc[k] >= 0) give_back(a, a.alloc[k]);
+      if (a.old[k] >= 0) give_back(a, a.old[k]);
   if (tid == 0) *a.n_copy = s_ncopy;
 }
 
@@ -610,12 +620,13 @@ sv_status launch(const void *fn, A &a, long long grid, int block, void *stream, 
 }
 
 struct ResizePlan {
-  size_t alloc, copies, n_copy, total;
+  size_t alloc, old, copies, n_copy, total;
 };
 ResizePlan resize_plan(int32_t S, int32_t P) {
   ResizePlan p;
   size_t o = 0;
   p.alloc = o; o = align256(o + (size_t)P * 4);
+  p.old = o; o = align256(o + (size_t)P * 4);
   p.copies = o; o = align256(o + (size_t)S * 16);
   p.n_copy = o; o = align256(o + 4);
   p.total = o;
@@ -736,8 +747,8 @@ sv_status spec_cache_resize(int32_t *page_table, int32_t *seq_pages, int32_t *re
   if (workspace_bytes < p.total || ((uintptr_t)workspace & 255)) return SV_ERR_WORKSPACE;
   char *base = static_cast<char *>(workspace);
   ResizeArgs a = {page_table, seq_pages, ref_count, (unsigned *)free_map, keep_len, want_len, S, num_pages, table_width,
-                  __builtin_ctz((unsigned)page_size), row_status, (int32_t *)(base + p.alloc), (int4 *)(base + p.copies),
-                  (int32_t *)(base + p.n_copy)};
+                  __builtin_ctz((unsigned)page_size), row_status, (int32_t *)(base + p.alloc), (int32_t *)(base + p.old),
+                  (int4 *)(base + p.copies), (int32_t *)(base + p.n_copy)};
   const sv_status st = launch((const void *)&k_cache_resize, a, 1, RZ_NT, stream, resize_lds(S));
   if (st != SV_OK || L == 0) return st;
   CopyArgs c = {static_cast<char *>(k_pages), static_cast<char *>(v_pages), a.copies, a.n_copy, (unsigned)L,
