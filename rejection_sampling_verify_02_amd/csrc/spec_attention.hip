@@ -461,7 +461,7 @@ constexpr unsigned least_part() {
 // Walks the workgroup's share, a segment at a time: begin(segment) sends for the first tiles,
 // and while they come the sequence is checked and its tree laid out; run(segment, code, sink)
 // then computes the rows' sums over the segment's slots and puts every row of the tile into
-// sink(row, exponent, sum of weights).  begin is called for every segment, also one whose rows
+// sink(row, reference, sum of weights).  begin is called for every segment, also one whose rows
 // are no new tokens (its tile 0 is then some page's, and not used): what it leaves in registers
 // would have to be kept from segment to segment otherwise.
 template <typename T, int D, int RT, int ROUND, bool WIDE, typename Begin, typename Run>
@@ -624,9 +624,9 @@ struct Rows {
   typedef Mma<T> M;
   static constexpr int KS = D / (4 * M::E), DT = D / 16;
   f32x4 o[R][DT];
-  float rm[R];          // the largest score nm stands for
+  float rm[R];          // the largest score that ref stands for
   typename M::Sum rl[R];  // sums of weights
-  float nm[R], lim[R];  // see soften
+  float ref[R], lim[R];  // see soften
   u32x4 q[R][KS];
   int node[R], dep[R];  // clamped to the segment's nodes
 
@@ -635,7 +635,7 @@ struct Rows {
     for (int r = 0; r < R; ++r) {
       rm[r] = lim[r] = -INFINITY;
       rl[r] = typename M::Sum{};
-      nm[r] = 0.0f;
+      ref[r] = 0.0f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[r][d] = f32x4{0, 0, 0, 0};
     }
@@ -680,11 +680,13 @@ struct Rows {
         for (int i = 0; i < 4; ++i) sc[r][t2][i] = ((vis >> (4 * t2 + i)) & 1u) ? sc[r][t2][i] : -INFINITY;
     }
   }
-  // Scores to weights 2^(c2 score - nm).  nm follows the row's maximum loosely: it moves only
+  // Scores to weights 2^(c2 (score - ref)).  ref follows the row's maximum loosely: it moves only
   // when a score passes it by a factor of 2^8, so that after the first tiles no sum has to be
   // rescaled and the four lanes of a row need not compare notes (weights up to 2^8 keep their
   // relative rounding, and the quotient of the sums is the same).  One test for all of a lane's
   // rows, so that what follows is one stretch of code (16 trees of 32 nodes: 2 % off a test each).
+  // The difference is taken first: c2 score - c2 ref in one instruction has the rounding of c2 ref
+  // in it, which for scores around 10^9 is more than 2^7, and the weights were infinite or none.
   SVD void soften(const AttnArgs &a, f32x4 (&sc)[R][2], typename M::P (&p)[R]) {
     float top[R];
     bool past = false;
@@ -698,13 +700,12 @@ struct Rows {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float mx = fmaxf(rm[r], col_max(top[r]));
-        const float nm2 = (mx == -INFINITY) ? 0.0f : mx * a.c2;
-        const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2(nm[r] - nm2);
+        const float f = (rm[r] == -INFINITY) ? 0.0f : fast_exp2((rm[r] - mx) * a.c2);
         rl[r] = rl[r] * f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[r][d] = o[r][d] * f;
         rm[r] = mx;
-        nm[r] = nm2;
+        ref[r] = (mx == -INFINITY) ? 0.0f : mx;
         lim[r] = mx + a.slack;
       }
     }
@@ -713,13 +714,13 @@ struct Rows {
 #pragma unroll
       for (int t2 = 0; t2 < 2; ++t2)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[r][t2][i] = fast_exp2(fmaf(sc[r][t2][i], a.c2, -nm[r]));
+        for (int i = 0; i < 4; ++i) sc[r][t2][i] = fast_exp2((sc[r][t2][i] - ref[r]) * a.c2);
       p[r] = M::weights(sc[r]);
       rl[r] = M::add(p[r], sc[r], rl[r]);
     }
   }
-  // The exponent that a row's sums are relative to (-inf: nothing seen so far).
-  SVD float scale(int r) const { return (rm[r] == -INFINITY) ? -INFINITY : nm[r]; }
+  // The score that a row's sums are relative to (-inf: nothing seen so far).
+  SVD float scale(int r) const { return rm[r]; }
   // What values that are not finite are to each row that sees them (they are left out of the
   // products, where a weight of zero would not keep them from the other rows): flags of the
   // values times flags of the view, both 0 or 1, count the sightings.
@@ -914,7 +915,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn_occ<T, 
       for (int k = 0; k < NW; ++k) {
         const float mk = s_m[k * RT + row], lk = s_l[k * RT + row];
         if (mk == -INFINITY && lk == 0.0f) continue;  // a wave that saw nothing
-        const float f = fast_exp2(mk - mt);
+        const float f = fast_exp2((mk - mt) * a.c2);
         ls += f * lk;
         acc += *reinterpret_cast<const f32x4 *>(&s_o[(k * RT + row) * PADD + 4 * c4]) * f;
       }
@@ -1125,7 +1126,7 @@ __global__ __launch_bounds__(NT) void k_attn_join(const AttnArgs a) {
     const float2 ml = a.part_ml[s];
     const f32x4 x = *reinterpret_cast<const f32x4 *>(&a.part_o[s * D + 4 * c4]);
     const bool none = ml.x == -INFINITY && ml.y == 0.0f;  // it saw nothing of the row
-    const float f = fast_exp2(ml.x - mt);
+    const float f = fast_exp2((ml.x - mt) * a.c2);
     ls += none ? 0.0f : f * ml.y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] += none ? 0.0f : f * x[j];
