@@ -1274,8 +1274,9 @@ sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_page
   a.page_shift = __builtin_ctz((unsigned)page);
   a.P = P;
   a.W = W;
-  // A scale of zero becomes one too small to matter, so that 0 times -inf need not be met.
-  a.c2 = fmaxf((float)(fabs((double)scale) * LOG2E), 1e-30f);
+  // A scale of zero becomes one too small for any finite score to matter (2^-149 times 2^128), so
+  // that 0 times -inf need not be met; the largest one stays finite for the same reason.
+  a.c2 = (float)fmin(fmax(fabs((double)scale) * LOG2E, (double)__FLT_DENORM_MIN__), (double)__FLT_MAX__);
   a.flip = scale < 0.0f ? (esz == 2 ? 0x80008000u : 0x80000000u) : 0u;
   a.slack = fminf(8.0f / a.c2, 1e30f);
   a.window = window;

@@ -70,3 +70,36 @@ def test_huge_scores(dev, dtype, N, g, D, n, sign):
         expected(out.double().cpu().numpy(), want, dtype)
         flipped, _ = sv.spec_paged_attention(**{**t, "q": -t["q"]}, scale=-1 / np.sqrt(D))
         expected(flipped.double().cpu().numpy(), want, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D,n", [(2, 64, 500), (40, 128, 100)])  # both kernels
+@pytest.mark.parametrize("power,scale", [(60, 0.0), (105, 0.0), (110, 2.0 ** -122), (112, -2.0 ** -124), (110, 2.0 ** -140)])
+def test_scales_down_to_nothing(dev, dtype, N, D, n, power, scale):
+    """Scores up to 2^126 under scales that bring them back to ordinary sizes, or to nothing."""
+    import rejection_sampling_verify_02_amd as sv
+    t, _ = one_hot_case(dev, dtype, N, 1, D, n, power, 1, seed=n + power)
+    out, st = sv.spec_paged_attention(**t, scale=scale)
+    assert st.tolist() == [0]
+    # the same products at an ordinary size, which are exact: queries 2^power smaller, the scale larger
+    q = t["q"].double().cpu().numpy() * 2.0 ** -power
+    ks, vs = ref.unpack(t["k_pages"].double().cpu().numpy(), t["v_pages"].double().cpu().numpy(), t["page_table"][0].tolist(), n + N, 16,
+                        8 if dtype == "bf16" else 4)
+    want, tol = ref.attention(q, [ks], [vs], [n], [N], None, scale * 2.0 ** power, 0, 0, 2 if dtype == "bf16" else 4)
+    # scales below 2^-126 are held with fewer bits: half of 2^-149, relative to the largest score
+    z = abs(scale) * 2.0 ** power * 95 * D
+    tol = tol + (2 * z * min(1.0, 2.0 ** -149 / abs(scale)) if scale else 0.0) * np.abs(vs).max()
+    # what stands for a scale of zero: 2^-149 times the largest difference of scores
+    tol = tol + (0.0 if scale else 2 * 2.0 ** (power - 149) * 190 * D) * np.abs(vs).max()
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D,n", [(2, 64, 500), (40, 128, 100)])
+def test_the_largest_scale(dev, dtype, N, D, n):
+    import rejection_sampling_verify_02_amd as sv
+    t, want = one_hot_case(dev, dtype, N, 2, D, n, 0, 1, seed=n)
+    for scale in (1e30, float(np.finfo(np.float32).max)):
+        out, st = sv.spec_paged_attention(**t, scale=scale)
+        assert st.tolist() == [0]
+        expected(out.double().cpu().numpy(), want, dtype)
