@@ -84,7 +84,9 @@ extern "C" {
  *   cache_len    [B] int32 committed tokens; cache_len + n_new <= table_width * page_size
  *   n_new        [B] int32 new tokens of each sequence, 0 .. N (NULL: N)
  *   parent       [B, N] int32 or NULL, see above (entries behind n_new are not read)
- *   D            64, 128 or 256;  Hq a multiple of Hkv;  N at most SV_CACHE_MAX_NEW
+ *   D            64, 128 or 256;  Hq a multiple of Hkv;  N at most SV_CACHE_MAX_NEW;  rows
+ *                B * N * Hq, those of a sequence and key head padded to a multiple of 128 at
+ *                most, fewer than 2^26
  *   scale        finite;  window >= 0 (0: none);  sinks >= 0 (needs window)
  *   out          [B, N, Hq, D] dtype out; rows of nodes behind n_new are zero
  *   row_status   [B] int32 out: 0, or SV_ROW_BAD_LENGTH, SV_ROW_BAD_TREE, SV_ROW_BAD_PAGE

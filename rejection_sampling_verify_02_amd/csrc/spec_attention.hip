@@ -1217,7 +1217,8 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
   const long long heads = (long long)B * Hkv, limit = 0x7fffffffLL;
   if (heads > limit || n_rt > limit / heads) return false;
   p.units = heads * n_rt;
-  if (most > limit / p.units || p.RT > limit / p.units) return false;
+  // the join has a wave a row, and a launch fewer than 2^32 threads
+  if (most > limit / p.units || p.RT > 0xffffffffLL / WAVE / p.units) return false;
   p.n_rt = (int)n_rt;
   const int occ = attn_pick(esz, D, p.R, [&](auto t, auto d, auto r) {
     typedef decltype(t) T;

@@ -595,6 +595,9 @@ namespace {
 using namespace sv;
 using sv_host::align256;
 
+// Most workgroups of NT threads: a launch has fewer than 2^32 threads.
+constexpr long long MAX_WGS = 0xffffffffLL / NT;
+
 bool pool_ok(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) {
   return Hkv >= 1 && D >= 16 && D <= COMMIT_R * NT && D % 16 == 0 && page >= 16 && page <= 256 && (page & (page - 1)) == 0 &&
          P >= 1 && W >= 1 && (long long)W * page <= 0x7fffffffLL - 4096;
@@ -657,7 +660,7 @@ sv_status spec_cache_append_after(const void *k, int64_t k_stride_b, int64_t k_s
   AppendArgs a = {};
   a.chunks = (N + APPEND_SLOTS - 2) / APPEND_SLOTS + 1;  // the first may begin anywhere in a chunk
   const long long heads = (long long)B * Hkv;
-  if (heads > 0x7fffffffLL / a.chunks) return SV_ERR_SHAPE;
+  if (heads > MAX_WGS / a.chunks) return SV_ERR_SHAPE;
   const long long grid = heads * a.chunks;
   if (!k || !v || !k_pages || !v_pages || !page_table || !cache_len || !row_status) return SV_ERR_NULL;
   a.k = static_cast<const char *>(k);
@@ -698,7 +701,7 @@ sv_status spec_cache_commit_after(void *k_pages, void *v_pages, sv_dtype dtype, 
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (B < 1 || L < 1 || N < 1 || N > SV_CACHE_MAX_NEW || !pool_ok(Hkv, D, page_size, num_pages, table_width)) return SV_ERR_SHAPE;
   const long long LH = (long long)L * Hkv;
-  if (LH > 0x7fffffffLL || LH * B > 0x7fffffffLL) return SV_ERR_SHAPE;
+  if (B > MAX_WGS || LH > 0x7fffffffLL || (path_nodes && LH * B > MAX_WGS)) return SV_ERR_SHAPE;  // chains: one a sequence
   if (!k_pages || !v_pages || !page_table || !cache_len || !accepted_len || !new_len || !row_status) return SV_ERR_NULL;
   if (((uintptr_t)k_pages | (uintptr_t)v_pages) & 15) return SV_ERR_ALIGN;
   // With paths several workgroups read a sequence's lengths: what they read is not written here.
