@@ -90,6 +90,12 @@ def _int32(x: int, name: str) -> int:
     return x
 
 
+def _sizes(name: str, *sizes) -> None:
+    """The same for a tensor's sizes; an expanded one can have any."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"{name}'s sizes must fit 32 bits, got {sizes}")
+
+
 def _ints(t, name: str, shape: tuple, dev: int, optional: bool = False):
     """The address of a contiguous int32 tensor of that shape (None where it may be left out)."""
     if t is None:
@@ -133,6 +139,7 @@ def _rows(t, name: str, shape: tuple, dtype, dev: int):
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         sb, sn, sh, sd = t.stride()
         B, N, H, D = shape
+        _sizes(name, B, N, H)
         if sd == 1 and sh == D or (sd == 1 or D <= 1) and (sh == D or H <= 1):
             # a dimension of one entry may carry any stride: it is never stepped
             return t.data_ptr(), sb if B > 1 else 0, sn if N > 1 else 0
@@ -149,6 +156,7 @@ def _table(t, dev: int, rows: int | None = None):
     if t.dim() != 2:
         raise ValueError("page_table must have two dimensions, sequences and pages")
     B, W = t.shape
+    _sizes("page_table", B, W)
     return _ints(t, "page_table", (B if rows is None else rows, W), dev), W
 
 
@@ -312,7 +320,7 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
     table, W = _table(page_table, dev)
     B = page_table.shape[0]
     if path_nodes is not None:
-        N = path_nodes.shape[1] if path_nodes.dim() == 2 else 0
+        N = _int32(path_nodes.shape[1], "path_nodes' nodes") if path_nodes.dim() == 2 else 0
         if max_new is not None and max_new != N:
             raise ValueError(f"path_nodes has {N} nodes, max_new is {max_new}")
     elif max_new is None:
@@ -337,7 +345,7 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
 
 def _books(pool: PagePool, dev: int):
     table, W = _table(pool.page_table, dev)
-    S, P = pool.page_table.shape[0], pool.ref_count.numel()
+    S, P = pool.page_table.shape[0], _int32(pool.ref_count.numel(), "the pool's pages")
     return S, W, P, (table, _ints(pool.seq_pages, "seq_pages", (S,), dev), _ints(pool.ref_count, "ref_count", (P,), dev))
 
 
@@ -391,7 +399,7 @@ def spec_cache_fork(pool: PagePool, cache_len, src, dst, *, stream=None, out=Non
         with elsewhere:
             return spec_cache_fork(pool, cache_len, src, dst, out=out)
     S, W, P, books = _books(pool, dev)
-    F = src.numel()
+    F = _int32(src.numel(), "the pairs")
     pairs = (F,)
     lens = _ints(cache_len, "cache_len", (S,), dev)
     s, d = _ints(src, "src", pairs, dev), _ints(dst, "dst", pairs, dev)

@@ -44,3 +44,20 @@ def test_append(lib, B, N, Hkv, status):
                                                  (1, 1 << 24, 1, None, 2), (1, (1 << 24) - 1, 1, None, 1), (1, 1 << 24, 1, FAKE, 2)])
 def test_commit(lib, L, B, Hkv, path, status):
     assert lib.spec_cache_commit(None, FAKE, sv.SV_BF16, FAKE, FAKE, FAKE, path, L, B, 2, Hkv, 64, 16, 10, 4, FAKE, FAKE, None) == status
+
+
+def test_tensors_whose_sizes_do_not_fit_32_bits():
+    """Expanded tensors have any size for nothing; ctypes would pass the low 32 bits, here 3."""
+    import torch
+    from rejection_sampling_verify_02_amd import cache
+    n, cpu = 2**32 + 3, -1
+    x = torch.zeros((1, 1, 1, 64))
+    for shape in ((1, n, 1, 64), (n, 1, 1, 64), (1, 1, n, 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache._rows(x.expand(shape), "k", shape, torch.float32, cpu)
+    for shape in ((1, n), (n, 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache._table(torch.zeros((1, 1), dtype=torch.int32).expand(shape), cpu)
+    pool = sv.PagePool.empty(8, 2, 2, "cpu")
+    with pytest.raises(ValueError, match="32 bits"):
+        cache._books(pool._replace(ref_count=pool.ref_count[:1].expand(n)), cpu)
