@@ -113,6 +113,14 @@ def _ints(t, name: str, shape: tuple, dev: int, optional: bool = False):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _apart(outputs: dict, inputs: dict):
+    """Outputs of the caller's that several workgroups write while others read those inputs."""
+    for a, x in outputs.items():
+        for b, y in inputs.items():
+            if y is not None and x.data_ptr() < y.data_ptr() + 4 * y.numel() and y.data_ptr() < x.data_ptr() + 4 * x.numel():
+                raise ValueError(f"{a} must not share memory with {b}")
+
+
 def _pages(k_pages, v_pages, dims: int, dtype, dev: int):
     """(P, Hkv, D, page_size) of a cache of `dims` dimensions (5: a layer, 6: all of them)."""
     ks, vs = k_pages.shape, v_pages.shape
@@ -252,6 +260,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, cache_len, *, parent=N
             raise ValueError("out must be contiguous")
         _rows(out[0], "out", shape, q.dtype, dev)
         _ints(out[1], "row_status", seqs, dev)
+        _apart({"row_status": out[1]}, {"prior": prior})
 
     o, st = out or (torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(cache_len))
     ws = _work(workspace, _attention_bytes(B, N, Hq, Hkv, D, page, W, dt), dev)
@@ -293,6 +302,7 @@ def spec_cache_append(k, v, k_pages, v_pages, page_table, cache_len, *, n_new=No
     pri = _ints(prior, "prior", seqs, dev, True)
     if out is not None:
         _ints(out, "row_status", seqs, dev)
+        _apart({"row_status": out}, {"prior": prior})
 
     st = torch.empty_like(cache_len) if out is None else out
     rc = load_library().spec_cache_append_after(kp, kb, kn, vp, vb, vn, dt, k_pages.data_ptr(), v_pages.data_ptr(), table, lens,
@@ -333,6 +343,8 @@ def spec_cache_commit(k_pages, v_pages, page_table, cache_len, accepted_len, pat
     if out is not None:
         _ints(out[0], "new_len", seqs, dev)
         _ints(out[1], "row_status", seqs, dev)
+        _apart({"new_len": out[0], "row_status": out[1]},
+               {"prior": prior, **({"cache_len": cache_len, "accepted_len": accepted_len} if path_nodes is not None else {})})
 
     n, st = out or (torch.empty_like(cache_len), torch.empty_like(cache_len))
     rc = load_library().spec_cache_commit_after(k_pages.data_ptr(), v_pages.data_ptr(), dt, table, lens, acc, path, pri,

@@ -1667,7 +1667,7 @@ const char *sv_status_string(sv_status status) {
     case SV_ERR_WORKSPACE: return "workspace too small or not 256-byte aligned";
     case SV_ERR_ALIGN: return "a pointer or stride is not aligned (logits: element size; cache, its rows and the attention's output: 16 bytes)";
     case SV_ERR_LAUNCH: return "kernel launch failed";
-    case SV_ERR_PARAM: return "a parameter is out of its range (epsilon, delta, window and sinks >= 0, sinks only with a window, all finite)";
+    case SV_ERR_PARAM: return "a parameter is out of its range (epsilon, delta, scale finite; epsilon, delta, window and sinks >= 0; sinks only with a window), or an output overlaps an input";
     case SV_ERR_SCRATCH: return "the arguments need more scratch memory than spec_verify_noalloc holds";
   }
   return "unknown status";

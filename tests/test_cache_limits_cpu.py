@@ -61,3 +61,16 @@ def test_tensors_whose_sizes_do_not_fit_32_bits():
     pool = sv.PagePool.empty(8, 2, 2, "cpu")
     with pytest.raises(ValueError, match="32 bits"):
         cache._books(pool._replace(ref_count=pool.ref_count[:1].expand(n)), cpu)
+
+
+def test_outputs_that_overlap_inputs_are_named():
+    """In the binding by the two tensors' names, in the library's text as one of the reasons; the
+    text has the scale among the parameters too."""
+    import torch
+    from rejection_sampling_verify_02_amd import cache
+    x = torch.zeros(8, dtype=torch.int32)
+    cache._apart({"new_len": x[:4]}, {"cache_len": x[4:], "prior": None})
+    for a, b in ((x[:4], x[:4]), (x[:4], x[3:7]), (x[2:6], x[:3])):
+        with pytest.raises(ValueError, match="new_len.*cache_len"):
+            cache._apart({"row_status": torch.zeros(4, dtype=torch.int32), "new_len": a}, {"prior": None, "cache_len": b})
+    assert "overlap" in sv.sv_status_string(8) and "scale" in sv.sv_status_string(8)

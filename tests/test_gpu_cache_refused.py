@@ -206,3 +206,23 @@ def test_a_captured_round_follows_refusals(dev):
         refused += sum(r == NO_PAGES for r in room.tolist())
         served += sum(r == 0 for r in room.tolist())
     assert refused and served
+
+
+def test_calls_that_overlap_are_refused_by_name(dev):
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    kp, vp = sv.empty_pages(1, 4, 1, 64, 16, torch.bfloat16, dev)
+    table = i32([[0, 1], [2, 3]], dev)
+    lens, acc, st, q = i32([3, 4], dev), i32([1, 1], dev), i32([0, 0], dev), torch.zeros((2, 2, 1, 64), dtype=torch.bfloat16, device=dev)
+    path = i32([[1, -1], [1, -1]], dev)
+    for out, names in (((lens, st), "new_len.*cache_len"), ((st, acc), "row_status.*accepted_len"), ((acc, st), "new_len.*accepted_len")):
+        with pytest.raises(ValueError, match=names):
+            sv.spec_cache_commit(kp, vp, table, lens, acc, path, out=out)
+    new, _ = sv.spec_cache_commit(kp, vp, table, lens, acc, max_new=2, out=(lens, st))  # chains may
+    assert new is lens and lens.tolist() == [5, 6]
+    with pytest.raises(ValueError, match="row_status.*prior"):
+        sv.spec_cache_commit(kp, vp, table, lens, acc, max_new=2, prior=st, out=(lens, st))
+    with pytest.raises(ValueError, match="row_status.*prior"):
+        sv.spec_cache_append(q, q, kp[0], vp[0], table, lens, prior=st, out=st)
+    with pytest.raises(ValueError, match="row_status.*prior"):
+        sv.spec_paged_attention(q, kp[0], vp[0], table, lens, prior=st, out=(torch.empty_like(q), st))
