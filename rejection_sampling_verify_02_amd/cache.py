@@ -196,12 +196,13 @@ def _raise(rc: int):
         raise SpecVerifyError(rc, sv_status_string(rc))
 
 
-@lru_cache(maxsize=None)
+# Bounded: a server's batch sizes and table widths go on changing.
+@lru_cache(maxsize=1024)
 def _attention_bytes(*sizes) -> int:
     return int(load_library().sv_attention_workspace_bytes(*sizes))
 
 
-@lru_cache(maxsize=None)
+@lru_cache(maxsize=1024)
 def _resize_bytes(*sizes) -> int:
     return int(load_library().sv_resize_workspace_bytes(*sizes))
 

@@ -74,3 +74,14 @@ def test_outputs_that_overlap_inputs_are_named():
         with pytest.raises(ValueError, match="new_len.*cache_len"):
             cache._apart({"row_status": torch.zeros(4, dtype=torch.int32), "new_len": a}, {"prior": None, "cache_len": b})
     assert "overlap" in sv.sv_status_string(8) and "scale" in sv.sv_status_string(8)
+
+
+def test_remembered_workspace_sizes_are_bounded():
+    from rejection_sampling_verify_02_amd import cache
+    for f, size in ((cache._attention_bytes, lambda n: (1 + n % 7, 1, 8, 2, 64, 16, 1 + n, sv.SV_BF16)), (cache._resize_bytes, lambda n: (4, 1 + n))):
+        most = f.cache_info().maxsize
+        assert most is not None and most <= 4096
+        for n in range(most + 50):
+            f(*size(n))
+        assert f.cache_info().currsize == most
+        assert f(*size(0)) == getattr(sv, "sv" + f.__name__.replace("_bytes", "_workspace_bytes"))(*size(0))
