@@ -95,7 +95,9 @@ extern "C" {
  * q, k_pages, v_pages and out start at multiples of 16 bytes, and the strides of q are
  * multiples of 16 bytes (else SV_ERR_ALIGN).  Products are taken in matrix instructions of
  * the inputs' type with f32 sums; scores, softmax statistics and the output's sum are f32,
- * the weights are rounded to the inputs' type for the second product. */
+ * the weights are rounded to the inputs' type for the second product and divided by the sum
+ * of the rounded ones.  Weighted values are summed before that division, with weights of up to
+ * 2^8: values whose sum over the slots seen passes 2^119 in size may give infinities. */
 size_t sv_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
                                     int32_t page_size, int32_t table_width, sv_dtype dtype);
 sv_status spec_paged_attention(const void *q, int64_t q_stride_b, int64_t q_stride_n,

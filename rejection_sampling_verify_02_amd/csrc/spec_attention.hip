@@ -1205,7 +1205,15 @@ bool attn_shape_ok(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int
 }
 
 // Up to 16 rows of a key head, or 32 up to D = 128: one wave holds them in its registers; more go to
-// the kernel whose waves share them.
+// the kernel whose waves share them, with one row tile a wave up to 64 rows, else two.  Calls in us,
+// 16 sequences of 1000 to 4000 slots and 8 key heads, the rule's choice first:
+//   20 rows, k_attn with two row tiles against k_attn_wide with one: bf16 D = 64 27 / 32, D = 128
+//   46 / 45 (64 sequences 141 / 143); f32 D = 64 49 / 72, D = 128 91 / 122
+//   128 rows, two row tiles a wave against one: bf16 D = 64 48 / 55, D = 128 65 / 82, D = 256
+//   141 / 145; f32 D = 64 131 / 125 (256 rows 226 / 246), D = 128 237 / 224 (256 rows 463 / 434)
+// The rule looks at rows alone.  One row tile a wave would be faster for f32 at D = 128 (two need
+// 101 registers more than there are) and where little is to be read (2 sequences of up to 1000
+// slots, 128 rows: bf16 D = 128 24 / 20, D = 256 40 / 30).
 bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page, int32_t W, int esz, AttnPlan &p) {
   const long long rows = (long long)N * (Hq / Hkv);
   const bool two = D <= 128;  // the registers take two row tiles of k_attn
@@ -1240,8 +1248,8 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
 sv_status attn_run(const void *q, int64_t q_sb, int64_t q_sn, const void *k_pages, const void *v_pages, sv_dtype dt,
                    const int32_t *table, const int32_t *cache_len, const int32_t *n_new, const int32_t *parent,
                    const int32_t *prior, int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page, int32_t P,
-                   int32_t W, float scale, int32_t window, int32_t sinks, void *out, int32_t *status, void *ws, size_t ws_bytes, void *stream,
-                   void *const *ev, int32_t nev, int32_t *nl) {
+                   int32_t W, float scale, int32_t window, int32_t sinks, void *out, int32_t *status, void *ws,
+                   size_t ws_bytes, void *stream, void *const *ev, int32_t nev, int32_t *nl) {
   if (nl) *nl = 0;
   if (dt != SV_F32 && dt != SV_BF16) return SV_ERR_DTYPE;
   const int esz = dt == SV_BF16 ? 2 : 4;
