@@ -53,7 +53,9 @@ typedef enum {
   SV_ERR_WORKSPACE = 5,   /* workspace smaller than sv_workspace_bytes() or misaligned    */
   SV_ERR_ALIGN = 6,       /* a logit pointer is not aligned to its element size           */
   SV_ERR_LAUNCH = 7,      /* the HIP runtime refused a kernel launch                       */
-  SV_ERR_PARAM = 8,       /* spec_typical_verify: epsilon or delta negative or not finite   */
+  SV_ERR_PARAM = 8,       /* spec_typical_verify: epsilon or delta negative or not finite;  */
+                          /* spec_cache.h: scale, window or sinks out of range, or an       */
+                          /* output that overlaps an input                                  */
   SV_ERR_SCRATCH = 9      /* spec_verify_noalloc: the arguments need more scratch memory    */
                           /* than SV_NOALLOC_SCRATCH_BYTES                                   */
 } sv_status;

@@ -90,10 +90,9 @@ def _int32(x: int, name: str) -> int:
     return x
 
 
-def _sizes(name: str, *sizes) -> None:
-    """The same for a tensor's sizes; an expanded one can have any."""
-    if max(sizes) > 0x7FFFFFFF:
-        raise ValueError(f"{name}'s sizes must fit 32 bits, got {sizes}")
+def _too_large(name: str, *sizes):
+    """The same for a tensor's sizes (an expanded one can have any), once one is found not to fit."""
+    raise ValueError(f"{name}'s sizes must fit 32 bits, got {sizes}")
 
 
 def _ints(t, name: str, shape: tuple, dev: int, optional: bool = False):
@@ -147,7 +146,8 @@ def _rows(t, name: str, shape: tuple, dtype, dev: int):
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         sb, sn, sh, sd = t.stride()
         B, N, H, D = shape
-        _sizes(name, B, N, H)
+        if B | N | H > 0x7FFFFFFF:
+            _too_large(name, B, N, H)
         if sd == 1 and sh == D or (sd == 1 or D <= 1) and (sh == D or H <= 1):
             # a dimension of one entry may carry any stride: it is never stepped
             return t.data_ptr(), sb if B > 1 else 0, sn if N > 1 else 0
@@ -164,7 +164,8 @@ def _table(t, dev: int, rows: int | None = None):
     if t.dim() != 2:
         raise ValueError("page_table must have two dimensions, sequences and pages")
     B, W = t.shape
-    _sizes("page_table", B, W)
+    if B | W > 0x7FFFFFFF:
+        _too_large("page_table", B, W)
     return _ints(t, "page_table", (B if rows is None else rows, W), dev), W
 
 
@@ -368,7 +369,8 @@ def spec_cache_resize(pool: PagePool, keep_len, want_len, k_pages=None, v_pages=
     behind (see include/spec_cache.h); a page that others hold too and that lies at or behind slot
     keep_len [S] is replaced by the sequence's own, its kept slots copied in all layers of k_pages
     [L, P, Hkv, D/E, page, E] and v_pages.  Without them nothing is copied and ``page_size`` is
-    needed.  Returns row_status [S] int32, which ``out`` may supply."""
+    needed.  Returns row_status [S] int32, which ``out`` may supply; the calls that go on with the
+    same sequences take it as ``prior``."""
     dev = _device(pool.page_table, "page_table")
     elsewhere = _elsewhere(dev, stream)
     if elsewhere is not None:
