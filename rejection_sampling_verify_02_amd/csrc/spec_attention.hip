@@ -1232,7 +1232,9 @@ bool attn_plan(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t
     typedef decltype(t) T;
     return p.wide ? wide_occ<T, decltype(d)::value, decltype(r)::value>() : attn_occ<T, decltype(d)::value, decltype(r)::value>();
   });
-  long long grid = 256LL * occ;  // one resident set of the device's 256 CUs
+  // One resident set of the device's 256 CUs (trees of near 1024 nodes: their books leave room for
+  // one workgroup a CU of k_attn_wide, and the set comes in two turns; none waits for another).
+  long long grid = 256LL * occ;
   const long long round = p.wide ? (D * esz <= 256 ? 2 : 1) : NW;  // tiles of a round, the least share
   const long long need = p.units * ((most + round - 1) / round);
   if (need < grid) grid = need;
