@@ -245,6 +245,115 @@ sv_status spec_cache_fork(int32_t *page_table, int32_t *seq_pages, int32_t *ref_
                           int32_t S, int32_t num_pages, int32_t table_width,
                           int32_t *pair_status, void *stream);
 
+/* ---- a cache in 4 bits ----
+ *
+ * The microscaling format that the matrix cores' conversions take: 32 neighbouring elements of a
+ * head (a block) share a scale 2^(byte - 127), and each is a code of 4 bits, a sign (bit 3) and
+ * one of 0, 0.5, 1, 1.5, 2, 3, 4, 6: 4.25 bits an element.  A block's scale is the least power
+ * of two, from 2^-120 to 2^125, of which its largest element is at most six times; an element is
+ * the nearest value, a tie going to the even code (beyond 6 * 2^125: that).  A block with an
+ * element that is not finite has scale byte 255 and is NaN as a whole.  What a code stands for is
+ * a bf16 number.  With D 64, 128 or 256, two codes to a byte (the first of a pair in the low
+ * half), and S = 512 / D:
+ *   k_codes  [P, Hkv, D / 32, page_size, 16]         element d of slot t: [p, h, d / 32, t, d % 32 / 2]
+ *   v_codes  [P, Hkv, page_size / S, 16, S, D / 32]  [p, h, t / S, d / (D / 16), t % S, d % (D / 16) / 2]
+ *   k_scales, v_scales  [P, Hkv, D / 32, page_size]
+ * so that a lane's 16 bytes are what it multiplies with.  One layer's pool is one such set of
+ * arrays; the calls that work on every layer take L of each, one behind the other.  Codes start at
+ * multiples of 16 bytes, scales at multiples of 8.  Pages, tables, row codes and `prior` are as
+ * above. */
+
+/* ---- positions: queries and keys rotated, keys and values into the cache ----
+ *
+ * A token's position is cache_len[b] + its depth (positions[b, i] where they are given); pair j of
+ * the first rot_dim elements of a query's or key's head, elements j and j + rot_dim / 2, or 2 j and
+ * 2 j + 1 where interleaved, is (x, y) and becomes
+ *   factor * (x cos t - y sin t, y cos t + x sin t),  t = position * inv_freq[j]
+ * and the elements behind are left as they are.  Angles, cosines and the rotation are taken in
+ * 64 bits and rounded once.  Then k[b, i] and v[b, i] go to slot cache_len[b] + i of one layer's
+ * pool as in spec_cache_append, and the rotated queries to q_out.
+ *   q            [B, N, Hq, D] dtype, strides as in spec_paged_attention; NULL with q_out NULL
+ *                and Hq 0: keys and values alone
+ *   k, v         [B, N, Hkv, D] dtype, strides as in spec_cache_append
+ *   inv_freq     [rot_dim / 2] float32;  rot_dim even, 0 .. D (0: no rotation, inv_freq NULL)
+ *   k_pages, v_pages  one layer's pool, of dtype with k_scales == v_scales == NULL (D a multiple
+ *                of 16 up to 512), else the codes of a cache in 4 bits (dtype bf16; D 64, 128 or
+ *                256; keys are rounded to float32 after the rotation and then coded)
+ *   parent       [B, N] int32 or NULL (a chain), for the depths
+ *   positions    [B, N] int32 or NULL
+ *   q_out        [B, N, Hq, D] dtype out, not overlapping q: rows of nodes behind n_new are zero,
+ *                those of a sequence with a code NaN
+ *   row_status   [B] int32 out: 0, prior's code, SV_ROW_BAD_LENGTH, SV_ROW_BAD_TREE or
+ *                SV_ROW_BAD_PAGE; nothing of the sequence is then written to the cache
+ * q, k, v, their strides, the pages and q_out are multiples of 16 bytes.  The slots' pages must be
+ * the sequence's own, as for the append. */
+typedef struct {
+  const float *inv_freq;
+  int32_t rot_dim;
+  int32_t interleaved;
+  float factor;
+} sv_rotary;
+sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_stride_n,
+                                   const void *k, int64_t k_stride_b, int64_t k_stride_n,
+                                   const void *v, int64_t v_stride_b, int64_t v_stride_n,
+                                   sv_dtype dtype, void *k_pages, void *k_scales, void *v_pages,
+                                   void *v_scales, const sv_rotary *rotary,
+                                   const int32_t *page_table, const int32_t *cache_len,
+                                   const int32_t *n_new, const int32_t *parent,
+                                   const int32_t *positions, const int32_t *prior, int32_t B,
+                                   int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                                   int32_t page_size, int32_t num_pages, int32_t table_width,
+                                   void *q_out, int32_t *row_status, void *stream);
+
+/* ---- entries read back ----
+ *
+ * The keys and values in slots first[b] .. first[b] + count[b] - 1 of one layer, as dtype (bf16
+ * for a cache in 4 bits).
+ *   first        [B] int32;  count [B] int32, 0 .. N, or NULL (N)
+ *   k, v         [B, N, Hkv, D] dtype out; rows behind count are zero, those of a sequence with a
+ *                code NaN
+ *   row_status   [B] int32 out: 0, SV_ROW_BAD_LENGTH or SV_ROW_BAD_PAGE */
+sv_status spec_cache_read(const void *k_pages, const void *k_scales, const void *v_pages,
+                          const void *v_scales, sv_dtype dtype, const int32_t *page_table,
+                          const int32_t *first, const int32_t *count, int32_t B, int32_t N,
+                          int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                          int32_t table_width, void *k, void *v, int32_t *row_status,
+                          void *stream);
+
+/* ---- attention over a cache in 4 bits ----
+ *
+ * spec_paged_attention_after with such a cache: q and out are bf16, keys and values what their
+ * codes stand for. */
+size_t sv_attention4_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t page_size, int32_t table_width);
+sv_status spec_paged_attention4(const void *q, int64_t q_stride_b, int64_t q_stride_n,
+                                const void *k_codes, const void *k_scales, const void *v_codes,
+                                const void *v_scales, const int32_t *page_table,
+                                const int32_t *cache_len, const int32_t *n_new,
+                                const int32_t *parent, const int32_t *prior, int32_t B, int32_t N,
+                                int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                                int32_t num_pages, int32_t table_width, float scale,
+                                int32_t window, int32_t sinks, void *out, int32_t *row_status,
+                                void *workspace, size_t workspace_bytes, void *stream,
+                                void *const *events, int32_t n_events, int32_t *n_launched);
+const char *sv_attention4_launch_plan(int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
+
+/* ---- a cache in 4 bits: accepted paths, and copies on write ----
+ *
+ * spec_cache_commit_after and spec_cache_resize with such a cache (resize: L > 0). */
+sv_status spec_cache_commit4(void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                             const int32_t *page_table, const int32_t *cache_len,
+                             const int32_t *accepted_len, const int32_t *path_nodes,
+                             const int32_t *prior, int32_t L, int32_t B, int32_t N, int32_t Hkv,
+                             int32_t D, int32_t page_size, int32_t num_pages, int32_t table_width,
+                             int32_t *new_len, int32_t *row_status, void *stream);
+sv_status spec_cache_resize4(int32_t *page_table, int32_t *seq_pages, int32_t *ref_count,
+                             int32_t *free_map, const int32_t *keep_len, const int32_t *want_len,
+                             void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                             int32_t L, int32_t S, int32_t Hkv, int32_t D, int32_t page_size,
+                             int32_t num_pages, int32_t table_width, int32_t *row_status,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

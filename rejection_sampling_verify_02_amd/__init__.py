@@ -38,7 +38,8 @@ EXPORTED = ("spec_verify", "spec_verify_timed", "sv_workspace_bytes", "sv_worksp
             "spec_paged_attention", "spec_paged_attention_timed", "sv_attention_workspace_bytes",
             "sv_attention_launch_plan", "spec_cache_append", "spec_cache_commit", "spec_cache_resize",
             "sv_resize_workspace_bytes", "spec_cache_fork", "spec_paged_attention_after", "spec_cache_append_after",
-            "spec_cache_commit_after")
+            "spec_cache_commit_after", "spec_cache_append_rotary", "spec_cache_read", "spec_paged_attention4",
+            "sv_attention4_workspace_bytes", "sv_attention4_launch_plan", "spec_cache_commit4", "spec_cache_resize4")
 
 
 class SpecVerifyError(RuntimeError):
@@ -126,11 +127,21 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
                      (lib.spec_cache_append_after, append[:12] + [V] + append[12:]),
                      (lib.spec_cache_commit_after, commit[:7] + [V] + commit[7:]),
                      (lib.spec_cache_resize, [*[V] * 8, *[I32] * 8, V, V, SZ, V]),
-                     (lib.spec_cache_fork, [*[V] * 6, *[I32] * 4, V, V])):
+                     (lib.spec_cache_fork, [*[V] * 6, *[I32] * 4, V, V]),
+                     # positions, and a cache in 4 bits
+                     (lib.spec_cache_append_rotary, [*[V, SI, SI] * 3, I32, *[V] * 11, *[I32] * 8, V, V, V]),
+                     (lib.spec_cache_read, [V, V, V, V, I32, V, V, V, *[I32] * 7, V, V, V, V]),
+                     (lib.spec_paged_attention4, [V, SI, SI, *[V] * 9, *[I32] * 8, F32, I32, I32, V, V, V, SZ, V, V, I32, V]),
+                     (lib.spec_cache_commit4, [*[V] * 9, *[I32] * 8, V, V, V]),
+                     (lib.spec_cache_resize4, [*[V] * 10, *[I32] * 7, V, V, SZ, V])):
         fn.argtypes = args
         fn.restype = I32
     lib.sv_attention_workspace_bytes.argtypes = [I32] * 8
     lib.sv_attention_workspace_bytes.restype = SZ
+    lib.sv_attention4_workspace_bytes.argtypes = [I32] * 7
+    lib.sv_attention4_workspace_bytes.restype = SZ
+    lib.sv_attention4_launch_plan.argtypes = [I32] * 4
+    lib.sv_attention4_launch_plan.restype = ctypes.c_char_p
     lib.sv_resize_workspace_bytes.argtypes = [I32, I32]
     lib.sv_resize_workspace_bytes.restype = SZ
     lib.sv_attention_launch_plan.argtypes = [I32] * 5
@@ -573,7 +584,8 @@ def spec_verify_noalloc(target_logits, draft_logits, draft_tokens, u_accept, u_s
 _CACHE_NAMES = ("PagePool", "empty_pages", "spec_paged_attention", "spec_cache_append", "spec_cache_commit",
                 "spec_cache_resize", "spec_cache_fork", "sv_attention_workspace_bytes", "sv_resize_workspace_bytes",
                 "sv_attention_launch_plan", "ROW_BAD_PAGE", "ROW_BAD_LENGTH", "ROW_NO_PAGES", "ROW_BAD_FORK",
-                "CACHE_MAX_NEW", "CACHE_MAX_SEQS")
+                "CACHE_MAX_NEW", "CACHE_MAX_SEQS", "Pages4", "empty_pages4", "Rotary", "spec_cache_append_rotary", "spec_cache_read",
+                "sv_attention4_workspace_bytes", "sv_attention4_launch_plan")
 
 
 def __getattr__(name: str):

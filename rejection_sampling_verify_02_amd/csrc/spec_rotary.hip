@@ -1,0 +1,508 @@
+// spec_rotary.hip -- positions on the way into the cache: queries and keys rotated, keys and
+// values written to their slots, in the cache's type or in 4 bits (include/spec_cache.h), and
+// entries read back.
+//
+// Pair j of a head, (x, y), becomes factor * (x cos t - y sin t, y cos t + x sin t) with
+// t = position * inv_freq[j].  What a call has to move is its inputs once and its outputs once;
+// the angles are one for each token and pair, whatever the heads, so a workgroup takes a few
+// tokens, computes their cosines and sines once into LDS and streams the heads past them.
+
+#include "sv_fp4.h"
+
+namespace sv {
+
+struct RotaryArgs {
+  const char *q, *k, *v;
+  long long q_sb, q_sn, k_sb, k_sn, v_sb, v_sn;  // bytes
+  char *k_pages, *k_scales, *v_pages, *v_scales, *q_out;
+  const float *inv_freq;
+  const int32_t *page_table, *cache_len, *n_new, *parent, *positions, *prior;
+  int N, Hq, R, interleaved;
+  double factor;
+  int chunks, parts;  // workgroups of a sequence: chunks of tokens times parts of the heads
+  int32_t *row_status;
+  Pool pool;
+};
+
+// Tokens of a workgroup: whole units of values (8 slots of bf16, 4 of f32), so that a unit has
+// one writer.
+constexpr int ROT_TOKENS = 8;
+
+// cos t and sin t of t = n * f, in 64 bits: the product of a whole number and a float, rounded
+// once; a quarter turn's multiple taken off in two parts (the first exactly, in the fused
+// subtraction; below 2^31 * 2^8 turns what the two parts leave out is under 2^-60); and the
+// Taylor series on [-pi/4, pi/4], whose next terms are under 2^-54.
+SVD void turn_of(int n, float f, double factor, double &c, double &s) {
+  const double t = (double)n * (double)f;
+  const double k = rint(t * 0.63661977236758134308);
+  double r = fma(-k, 1.57079632679489655800, t);
+  r = fma(-k, 6.12323399573676603587e-17, r);
+  const double z = r * r;
+  double p = -1.0 / 1307674368000.0;
+  p = fma(p, z, 1.0 / 6227020800.0);
+  p = fma(p, z, -1.0 / 39916800.0);
+  p = fma(p, z, 1.0 / 362880.0);
+  p = fma(p, z, -1.0 / 5040.0);
+  p = fma(p, z, 1.0 / 120.0);
+  p = fma(p, z, -1.0 / 6.0);
+  const double sn = fma(p * z, r, r);
+  double h = 1.0 / 20922789888000.0;
+  h = fma(h, z, -1.0 / 87178291200.0);
+  h = fma(h, z, 1.0 / 479001600.0);
+  h = fma(h, z, -1.0 / 3628800.0);
+  h = fma(h, z, 1.0 / 40320.0);
+  h = fma(h, z, -1.0 / 720.0);
+  h = fma(h, z, 1.0 / 24.0);
+  h = fma(h, z, -0.5);
+  const double cs = fma(h, z, 1.0);
+  // k mod 4 quarter turns
+  const int m = (int)(k - 4.0 * floor(k * 0.25));
+  const double a = (m & 1) ? sn : cs, b = (m & 1) ? cs : sn;
+  c = ((m == 1 || m == 2) ? -a : a) * factor;
+  s = ((m >= 2) ? -b : b) * factor;
+}
+
+template <typename T>
+struct Unit {  // 16 bytes of elements
+  static constexpr int E = 16 / (int)sizeof(T);
+  float x[E];
+  SVD void load(const char *p) { Fmt<T>::unpack(*reinterpret_cast<const u32x4 *>(p), x); }
+  SVD u32x4 pack() const {
+    u32x4 w;
+    if constexpr (E == 8) {
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(unsigned, bf16x2{(__bf16)x[2 * j], (__bf16)x[2 * j + 1]});
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(x[j]);
+    }
+    return w;
+  }
+};
+
+// x and y of a pair turned.
+SVD void turned(float &x, float &y, const double2 cs) {
+  const double a = x, b = y;
+  x = (float)fma(a, cs.x, -(b * cs.y));
+  y = (float)fma(b, cs.x, a * cs.y);
+}
+
+// Element d of a head at p, turned: for heads whose pairs do not lie unit against unit.
+template <typename T>
+SVD float turned_one(const char *p, int d, int R, const double2 *cs) {
+  const T *x = reinterpret_cast<const T *>(p);
+  float a = Fmt<T>::at(x, d);
+  if (d >= R) return a;
+  const int h = R / 2;
+  const bool second = d >= h;
+  float b = Fmt<T>::at(x, second ? d - h : d + h);
+  if (second) {
+    turned(b, a, cs[d - h]);
+  } else {
+    turned(a, b, cs[d]);
+  }
+  return a;
+}
+
+// The code of a sequence (the same test in every workgroup of it), and its parents in LDS.
+SVD int rotary_code(const RotaryArgs &a, int b, int len, int m, uint16_t *s_par) {
+  const int sh = a.pool.page_shift, tid = threadIdx.x;
+  const int prior = a.prior ? min(a.prior[b], 0) : 0;
+  if (prior != 0) return prior;
+  if (len < 0 || m < 0 || m > a.N || (long long)len + m > ((long long)a.pool.W << sh)) return SV_ROW_BAD_LENGTH;
+  if (m == 0) return 0;
+  bool bad = false;
+  if (a.parent) {
+    for (int i = tid; i < m; i += NT) {
+      const int p = a.parent[(size_t)b * a.N + i];
+      s_par[i] = (uint16_t)p;
+      bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
+    }
+    if (__syncthreads_or(bad)) return SV_ROW_BAD_TREE;
+  }
+  const int32_t *table = a.page_table + (size_t)b * a.pool.W;
+  const int p0 = len >> sh, p1 = (len + m - 1) >> sh;
+  for (int i = p0 + tid; i <= p1; i += NT) bad |= (unsigned)table[i] >= (unsigned)a.pool.P;
+  return __syncthreads_or(bad) ? SV_ROW_BAD_PAGE : 0;
+}
+
+// T: the inputs' type; F4: the cache is in 4 bits; PAIRS: pairs lie unit against unit (neighbours
+// interleaved, or halves of whole units), so that a thread turns 16 bytes and their partners.
+template <typename T, bool F4, bool PAIRS>
+__global__ __launch_bounds__(NT) void k_append_rotary(const RotaryArgs a) {
+  constexpr int E = Unit<T>::E, ESZ = (int)sizeof(T);
+  extern __shared__ double2 s_cs[];  // [tokens][R / 2], then the parents
+  uint16_t *s_par = reinterpret_cast<uint16_t *>(s_cs + ROT_TOKENS * (a.R / 2));
+  const int tid = threadIdx.x;
+  const int part = (int)(blockIdx.x % (unsigned)a.parts);
+  const unsigned bc = blockIdx.x / (unsigned)a.parts;
+  const int chunk = (int)(bc % (unsigned)a.chunks), b = (int)(bc / (unsigned)a.chunks);
+  const int m = a.n_new ? a.n_new[b] : a.N;
+  int len = a.cache_len[b];
+  const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D, Hkv = (int)a.pool.Hkv, H2 = a.R / 2;
+  const int32_t *table = a.page_table + (size_t)b * a.pool.W;
+  const int code = rotary_code(a, b, len, m, s_par);
+  if (chunk == 0 && part == 0 && tid == 0) a.row_status[b] = code;
+  if (code != 0) len = 0;
+
+  const int c0 = (len / ROT_TOKENS + chunk) * ROT_TOKENS;
+  const int i0 = max(0, c0 - len), i1 = min(a.N, c0 + ROT_TOKENS - len);  // the workgroup's tokens
+  if (i0 >= i1) return;
+  const int live = code != 0 ? i0 : min(max(m, i0), i1);  // tokens from here on are not new
+  // The part's heads of the queries, and of the keys and values.
+  const int q0 = (int)((long long)a.Hq * part / a.parts), q1 = (int)((long long)a.Hq * (part + 1) / a.parts);
+  const int h0 = (int)((long long)Hkv * part / a.parts), h1 = (int)((long long)Hkv * (part + 1) / a.parts);
+  const int U = D / E;
+
+  if (live < i1) {  // queries of no token: zero, or NaN for a sequence with a code
+    const unsigned fill = code == 0 ? 0u : ESZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+    const int n = (q1 - q0) * U;
+    for (int x = tid; x < (i1 - live) * n; x += NT)
+      *reinterpret_cast<u32x4 *>(a.q_out + (((size_t)b * a.N + live + x / n) * a.Hq + q0) * D * ESZ + (size_t)(x % n) * 16) =
+          u32x4{fill, fill, fill, fill};
+  }
+  if (live <= i0) return;
+  const int nt = live - i0;
+
+  for (int x = tid; x < nt * H2; x += NT) {
+    const int t = x / H2, j = x - t * H2, i = i0 + t;
+    int pos = len + i;
+    if (a.positions) {
+      pos = a.positions[(size_t)b * a.N + i];
+    } else if (a.parent) {
+      pos = len;
+      for (int n = i; n > 0; n = s_par[n]) ++pos;
+    }
+    double2 cs;
+    turn_of(pos, a.inv_freq[j], a.factor, cs.x, cs.y);
+    s_cs[x] = cs;
+  }
+  __syncthreads();
+
+  // Queries, and the keys of a cache of the inputs' type: 16 bytes and, where the head's halves
+  // are turned against each other, their partners.  put(head, unit, bytes)
+  auto heads = [&](const char *src, int n_heads, const double2 *cs, auto put) {
+    const int HU = a.interleaved || H2 == 0 ? 0 : H2 / E;  // units of a half
+    const int items = PAIRS ? U - HU : U;
+    for (int x = tid; x < n_heads * items; x += NT) {
+      const int h = x / items, y = x - h * items;
+      const char *p = src + (size_t)h * D * ESZ;
+      if constexpr (!PAIRS) {
+        Unit<T> w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) w.x[e] = turned_one<T>(p, y * E + e, a.R, cs);
+        put(h, y, w.pack());
+      } else if (y < HU) {
+        Unit<T> w, v;
+        w.load(p + y * 16);
+        v.load(p + (y + HU) * 16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) turned(w.x[e], v.x[e], cs[y * E + e]);
+        put(h, y, w.pack());
+        put(h, y + HU, v.pack());
+      } else {
+        const int u = y + HU;
+        Unit<T> w;
+        w.load(p + u * 16);
+        if (a.interleaved)
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e)
+            if (u * E + 2 * e < a.R) turned(w.x[2 * e], w.x[2 * e + 1], cs[u * E / 2 + e]);
+        put(h, u, w.pack());
+      }
+    }
+  };
+  for (int t = 0; t < nt; ++t) {
+    const int i = i0 + t, s = len + i;
+    const double2 *cs = s_cs + t * H2;
+    char *qo = a.q_out + (((size_t)b * a.N + i) * a.Hq + q0) * D * ESZ;
+    heads(a.q + (long long)b * a.q_sb + (long long)i * a.q_sn + (size_t)q0 * D * ESZ, q1 - q0, cs, [&](int h, int u, u32x4 w) {
+      *reinterpret_cast<u32x4 *>(qo + (size_t)h * D * ESZ + u * 16) = w;
+    });
+    if constexpr (!F4) {
+      const size_t hb = head_bytes<T>(a.pool);
+      char *kp = a.k_pages + ((size_t)table[s >> sh] * Hkv + h0) * hb + (size_t)(s & (page - 1)) * 16;
+      heads(a.k + (long long)b * a.k_sb + (long long)i * a.k_sn + (size_t)h0 * D * ESZ, h1 - h0, cs, [&](int h, int u, u32x4 w) {
+        *reinterpret_cast<u32x4 *>(kp + (size_t)h * hb + (size_t)u * page * 16) = w;
+      });
+    }
+  }
+  if constexpr (!F4) {
+    // values: a thread gathers the E slots of one d (as k_cache_append does)
+    const int s0 = len + i0, s1 = len + live, u0 = s0 / E, u1 = (s1 - 1) / E;
+    const size_t hb = head_bytes<T>(a.pool);
+    for (int h = h0; h < h1; ++h)
+      for (int x = tid; x < (u1 - u0 + 1) * D; x += NT) {
+        const int u = u0 + x / D, d = x % D, f = u * E;
+        T e[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const int s = min(max(f + j, s0), s1 - 1);
+          e[j] = *reinterpret_cast<const T *>(a.v + (long long)b * a.v_sb + (long long)(s - len) * a.v_sn + ((size_t)h * D + d) * sizeof(T));
+        }
+        T *out = reinterpret_cast<T *>(a.v_pages + ((size_t)table[f >> sh] * Hkv + h) * hb + ((size_t)((f & (page - 1)) / E) * D + d) * 16);
+        if (f >= s0 && f + E <= s1) {
+          u32x4 w;
+          __builtin_memcpy(&w, e, 16);
+          *reinterpret_cast<u32x4 *>(out) = w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (f + j >= s0 && f + j < s1) out[j] = e[j];
+        }
+      }
+  } else {
+    // blocks of 32 elements, a thread each: keys, then values
+    const int G = D / F4_BLOCK, n = nt * (h1 - h0) * G, B = D / 32;
+    for (int x = tid; x < 2 * n; x += NT) {
+      const bool val = x >= n;
+      const int y = val ? x - n : x, u = y % G, th = y / G, t = th / (h1 - h0), h = h0 + th % (h1 - h0);
+      const int i = i0 + t, s = len + i, at = s & (page - 1);
+      const double2 *cs = s_cs + t * H2;
+      const char *p = val ? a.v + (long long)b * a.v_sb + (long long)i * a.v_sn + (size_t)h * D * ESZ
+                          : a.k + (long long)b * a.k_sb + (long long)i * a.k_sn + (size_t)h * D * ESZ;
+      float f[F4_BLOCK];
+      if (val || PAIRS || u * F4_BLOCK >= a.R) {
+#pragma unroll
+        for (int j = 0; j < F4_BLOCK / E; ++j) {
+          Unit<T> w;
+          w.load(p + (u * (F4_BLOCK / E) + j) * 16);
+#pragma unroll
+          for (int e = 0; e < E; ++e) f[j * E + e] = w.x[e];
+        }
+      }
+      if (!val && u * F4_BLOCK < a.R) {
+        if constexpr (PAIRS) {
+          if (a.interleaved) {
+#pragma unroll
+            for (int e = 0; e < F4_BLOCK / 2; ++e)
+              if (u * F4_BLOCK + 2 * e < a.R) turned(f[2 * e], f[2 * e + 1], cs[u * (F4_BLOCK / 2) + e]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < F4_BLOCK / E; ++j) {  // a unit lies in one half
+              const int d = u * F4_BLOCK + j * E;
+              if (d >= a.R) continue;
+              const bool second = d >= H2;
+              Unit<T> w;
+              w.load(p + (second ? d - H2 : d + H2) * ESZ);
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                float o = w.x[e];
+                if (second) turned(o, f[j * E + e], cs[d - H2 + e]);
+                else turned(f[j * E + e], o, cs[d + e]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < F4_BLOCK; ++e) f[e] = turned_one<T>(p, u * F4_BLOCK + e, a.R, cs);
+        }
+      }
+      unsigned w[4];
+      const unsigned byte = f4_encode(f, w);
+      const size_t ph = (size_t)table[s >> sh] * Hkv + h;
+      (val ? a.v_scales : a.k_scales)[ph * f4_scales(a.pool) + f4_scale(a.pool, u, at)] = (char)byte;
+      if (!val) {
+        *reinterpret_cast<u32x4 *>(a.k_pages + ph * f4_codes(a.pool) + f4_key(a.pool, u, at)) = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        char *o = a.v_pages + ph * f4_codes(a.pool);
+        const int pieces = 16 / B;  // of a block: its elements in D / 16 at a time
+        for (int r = 0; r < pieces; ++r) {
+          char *to = o + f4_value(a.pool, at, u * pieces + r);
+          if (B == 2) *reinterpret_cast<uint16_t *>(to) = (uint16_t)(w[r / 2] >> (16 * (r & 1)));
+          else if (B == 4) *reinterpret_cast<unsigned *>(to) = w[r];
+          else *reinterpret_cast<uint2 *>(to) = make_uint2(w[2 * r], w[2 * r + 1]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- entries read back
+
+struct ReadArgs {
+  const char *k_pages, *k_scales, *v_pages, *v_scales;
+  const int32_t *page_table, *first, *count;
+  int N, chunks;
+  char *k, *v;
+  int32_t *row_status;
+  Pool pool;
+};
+
+constexpr int READ_TOKENS = 8;
+
+template <typename T, bool F4>
+__global__ __launch_bounds__(NT) void k_cache_read(const ReadArgs a) {
+  constexpr int E = Unit<T>::E, ESZ = (int)sizeof(T);
+  const int tid = threadIdx.x;
+  const int chunk = (int)(blockIdx.x % (unsigned)a.chunks), b = (int)(blockIdx.x / (unsigned)a.chunks);
+  const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D, Hkv = (int)a.pool.Hkv;
+  const int first = a.first[b], m = a.count ? a.count[b] : a.N;
+  const int32_t *table = a.page_table + (size_t)b * a.pool.W;
+  int code = 0;
+  if (first < 0 || m < 0 || m > a.N || (long long)first + m > ((long long)a.pool.W << sh)) {
+    code = SV_ROW_BAD_LENGTH;
+  } else if (m > 0) {
+    bool bad = false;
+    for (int i = (first >> sh) + tid; i <= (first + m - 1) >> sh; i += NT) bad |= (unsigned)table[i] >= (unsigned)a.pool.P;
+    if (__syncthreads_or(bad)) code = SV_ROW_BAD_PAGE;
+  }
+  if (chunk == 0 && tid == 0) a.row_status[b] = code;
+  const int i0 = chunk * READ_TOKENS, i1 = min(a.N, i0 + READ_TOKENS);
+  const unsigned fill = code == 0 ? 0u : ESZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+  const int U = D / E, row = Hkv * U;
+  for (int x = tid; x < (i1 - i0) * row; x += NT) {
+    const int i = i0 + x / row, h = x % row / U, u = x % U;
+    u32x4 kw = {fill, fill, fill, fill}, vw = kw;
+    if (code == 0 && i < m) {
+      const int s = first + i, at = s & (page - 1);
+      const size_t ph = (size_t)table[s >> sh] * Hkv + h;
+      if constexpr (F4) {
+        const size_t sc = ph * f4_scales(a.pool) + f4_scale(a.pool, u / 4, at), co = ph * f4_codes(a.pool);
+        kw = f4_unit(*reinterpret_cast<const unsigned *>(a.k_pages + co + f4_key(a.pool, u / 4, at) + (u % 4) * 4),
+                     f4_factor((unsigned char)a.k_scales[sc]));
+        const int B = D / 32;  // 8 elements are two pieces, one, or half a one
+        unsigned w;
+        if (B == 2)
+          w = *reinterpret_cast<const uint16_t *>(a.v_pages + co + f4_value(a.pool, at, 2 * u)) |
+              (unsigned)*reinterpret_cast<const uint16_t *>(a.v_pages + co + f4_value(a.pool, at, 2 * u + 1)) << 16;
+        else
+          w = *reinterpret_cast<const unsigned *>(a.v_pages + co + f4_value(a.pool, at, u * 4 / B) + u * 4 % B);
+        vw = f4_unit(w, f4_factor((unsigned char)a.v_scales[sc]));
+      } else {
+        const size_t hb = head_bytes<T>(a.pool);
+        kw = *reinterpret_cast<const u32x4 *>(a.k_pages + ph * hb + ((size_t)u * page + at) * 16);
+        const T *vp = reinterpret_cast<const T *>(a.v_pages + ph * hb + ((size_t)(at / E) * D + u * E) * 16) + at % E;
+        T e[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) e[j] = vp[j * E];
+        __builtin_memcpy(&vw, e, 16);
+      }
+    }
+    const size_t o = (((size_t)b * a.N + i) * Hkv + h) * D * ESZ + (size_t)u * 16;
+    *reinterpret_cast<u32x4 *>(a.k + o) = kw;
+    *reinterpret_cast<u32x4 *>(a.v + o) = vw;
+  }
+}
+
+}  // namespace sv
+
+// ======================================================================== host side
+
+namespace {
+
+using namespace sv;
+using namespace sv_host;
+
+bool f4_dim(int32_t D) { return D == 64 || D == 128 || D == 256; }
+
+}  // namespace
+
+extern "C" {
+
+sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_stride_n, const void *k, int64_t k_stride_b,
+                                   int64_t k_stride_n, const void *v, int64_t v_stride_b, int64_t v_stride_n, sv_dtype dtype,
+                                   void *k_pages, void *k_scales, void *v_pages, void *v_scales, const sv_rotary *rotary,
+                                   const int32_t *page_table, const int32_t *cache_len, const int32_t *n_new,
+                                   const int32_t *parent, const int32_t *positions, const int32_t *prior, int32_t B, int32_t N,
+                                   int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                                   int32_t table_width, void *q_out, int32_t *row_status, void *stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  const bool f4 = k_scales || v_scales;
+  if (f4 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  const int esz = dtype == SV_BF16 ? 2 : 4, E = 16 / esz;
+  if (B < 1 || N < 1 || N > SV_CACHE_MAX_NEW || Hq < 0 || (Hq == 0) != (q == nullptr) || !pool_ok(Hkv, D, page_size, num_pages, table_width) ||
+      (f4 && !f4_dim(D)))
+    return SV_ERR_SHAPE;
+  const int R = rotary ? rotary->rot_dim : 0;
+  if (R < 0 || R > D || R % 2) return SV_ERR_SHAPE;
+  if (rotary && !(fabsf(rotary->factor) <= __FLT_MAX__)) return SV_ERR_PARAM;
+  RotaryArgs a = {};
+  a.chunks = (N + ROT_TOKENS - 2) / ROT_TOKENS + 1;  // the first may begin anywhere in a chunk
+  // Parts of the heads: so that small calls use more of the card (each part computes the tokens'
+  // angles anew).
+  const long long wgs = (long long)B * a.chunks;
+  a.parts = (int)(wgs >= 1024 ? 1 : (1024 + wgs - 1) / wgs);
+  if (a.parts > 8) a.parts = 8;
+  if (a.parts > Hkv) a.parts = Hkv;
+  if (wgs > MAX_WGS / a.parts) return SV_ERR_SHAPE;
+  if (!k || !v || !k_pages || !v_pages || (f4 && (!k_scales || !v_scales)) || !page_table || !cache_len || !row_status ||
+      (q && !q_out) || (R && !rotary->inv_freq))
+    return SV_ERR_NULL;
+  a.q = static_cast<const char *>(q);
+  a.k = static_cast<const char *>(k);
+  a.v = static_cast<const char *>(v);
+  const int64_t strides[6] = {q_stride_b, q_stride_n, k_stride_b, k_stride_n, v_stride_b, v_stride_n};
+  long long *to[6] = {&a.q_sb, &a.q_sn, &a.k_sb, &a.k_sn, &a.v_sb, &a.v_sn};
+  uintptr_t bits = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)q_out;
+  for (int i = 0; i < 6; ++i) {
+    *to[i] = (long long)((unsigned long long)strides[i] * esz);
+    if (i > 1 || q) bits |= (uintptr_t)*to[i];
+  }
+  if ((bits & 15) || (((uintptr_t)k_scales | (uintptr_t)v_scales) & 7) || (R && ((uintptr_t)rotary->inv_freq & 3))) return SV_ERR_ALIGN;
+  if (overlap(prior, row_status, B)) return SV_ERR_PARAM;
+  a.k_pages = static_cast<char *>(k_pages);
+  a.k_scales = static_cast<char *>(k_scales);
+  a.v_pages = static_cast<char *>(v_pages);
+  a.v_scales = static_cast<char *>(v_scales);
+  a.q_out = static_cast<char *>(q_out);
+  a.page_table = page_table;
+  a.cache_len = cache_len;
+  a.n_new = n_new;
+  a.parent = parent;
+  a.positions = positions;
+  a.prior = prior;
+  a.N = N;
+  a.Hq = Hq;
+  a.R = R;
+  if (R) {
+    a.inv_freq = rotary->inv_freq;
+    a.interleaved = rotary->interleaved != 0;
+    a.factor = rotary->factor;
+  }
+  a.row_status = row_status;
+  a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
+  const bool pairs = a.interleaved || (R / 2) % E == 0;
+  const unsigned lds = ROT_TOKENS * (R / 2) * 16 + (parent ? (unsigned)N * 2 : 0u);
+  const void *fn = f4 ? (pairs ? (const void *)&k_append_rotary<uint16_t, true, true> : (const void *)&k_append_rotary<uint16_t, true, false>)
+                 : esz == 2 ? (pairs ? (const void *)&k_append_rotary<uint16_t, false, true> : (const void *)&k_append_rotary<uint16_t, false, false>)
+                            : (pairs ? (const void *)&k_append_rotary<float, false, true> : (const void *)&k_append_rotary<float, false, false>);
+  return launch(fn, a, wgs * a.parts, NT, stream, lds);
+}
+
+sv_status spec_cache_read(const void *k_pages, const void *k_scales, const void *v_pages, const void *v_scales, sv_dtype dtype,
+                          const int32_t *page_table, const int32_t *first, const int32_t *count, int32_t B, int32_t N,
+                          int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages, int32_t table_width, void *k, void *v,
+                          int32_t *row_status, void *stream) {
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  const bool f4 = k_scales || v_scales;
+  if (f4 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (B < 1 || N < 1 || !pool_ok(Hkv, D, page_size, num_pages, table_width) || (f4 && !f4_dim(D)) ||
+      (long long)N > ((long long)table_width * page_size) || (long long)READ_TOKENS * Hkv * D > 0x7fffffffLL)
+    return SV_ERR_SHAPE;
+  ReadArgs a = {};
+  a.chunks = (N + READ_TOKENS - 1) / READ_TOKENS;
+  if (B > MAX_WGS / a.chunks) return SV_ERR_SHAPE;
+  if (!k_pages || !v_pages || (f4 && (!k_scales || !v_scales)) || !page_table || !first || !k || !v || !row_status) return SV_ERR_NULL;
+  if ((((uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)k | (uintptr_t)v) & 15) || (((uintptr_t)k_scales | (uintptr_t)v_scales) & 7))
+    return SV_ERR_ALIGN;
+  if (overlap(first, row_status, B) || overlap(count, row_status, B)) return SV_ERR_PARAM;
+  a.k_pages = static_cast<const char *>(k_pages);
+  a.k_scales = static_cast<const char *>(k_scales);
+  a.v_pages = static_cast<const char *>(v_pages);
+  a.v_scales = static_cast<const char *>(v_scales);
+  a.page_table = page_table;
+  a.first = first;
+  a.count = count;
+  a.N = N;
+  a.k = static_cast<char *>(k);
+  a.v = static_cast<char *>(v);
+  a.row_status = row_status;
+  a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
+  const void *fn = f4 ? (const void *)&k_cache_read<uint16_t, true>
+                      : dtype == SV_BF16 ? (const void *)&k_cache_read<uint16_t, false> : (const void *)&k_cache_read<float, false>;
+  return launch(fn, a, (long long)B * a.chunks, NT, stream);
+}
+
+}  // extern "C"
