@@ -39,7 +39,8 @@ EXPORTED = ("spec_verify", "spec_verify_timed", "sv_workspace_bytes", "sv_worksp
             "sv_attention_launch_plan", "spec_cache_append", "spec_cache_commit", "spec_cache_resize",
             "sv_resize_workspace_bytes", "spec_cache_fork", "spec_paged_attention_after", "spec_cache_append_after",
             "spec_cache_commit_after", "spec_cache_append_rotary", "spec_cache_read", "spec_paged_attention4",
-            "sv_attention4_workspace_bytes", "sv_attention4_launch_plan", "spec_cache_commit4", "spec_cache_resize4")
+            "sv_attention4_workspace_bytes", "sv_attention4_launch_plan", "spec_cache_commit4", "spec_cache_resize4",
+            "spec_sample_filtered", "spec_filter_logits", "sv_filter_workspace_bytes", "sv_filter_launch_plan")
 
 
 class SpecVerifyError(RuntimeError):
@@ -133,11 +134,17 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
                      (lib.spec_cache_read, [V, V, V, V, I32, V, V, V, *[I32] * 7, V, V, V, V]),
                      (lib.spec_paged_attention4, [V, SI, SI, *[V] * 9, *[I32] * 8, F32, I32, I32, V, V, V, SZ, V, V, I32, V]),
                      (lib.spec_cache_commit4, [*[V] * 9, *[I32] * 8, V, V, V]),
+                     (lib.spec_sample_filtered, [V, I32, V, I32, I32, V, V, V, V, SZ, V, V, I32, V]),
+                     (lib.spec_filter_logits, [V, I32, I32, I32, V, V, V, V, SZ, V, V, I32, V]),
                      (lib.spec_cache_resize4, [*[V] * 10, *[I32] * 7, V, V, SZ, V])):
         fn.argtypes = args
         fn.restype = I32
     lib.sv_attention_workspace_bytes.argtypes = [I32] * 8
     lib.sv_attention_workspace_bytes.restype = SZ
+    lib.sv_filter_workspace_bytes.argtypes = [I32] * 3
+    lib.sv_filter_workspace_bytes.restype = SZ
+    lib.sv_filter_launch_plan.argtypes = [I32]
+    lib.sv_filter_launch_plan.restype = ctypes.c_char_p
     lib.sv_attention4_workspace_bytes.argtypes = [I32] * 7
     lib.sv_attention4_workspace_bytes.restype = SZ
     lib.sv_attention4_launch_plan.argtypes = [I32] * 4
@@ -336,13 +343,27 @@ def spec_verify(target_logits, draft_logits, draft_tokens, u_accept, u_sample, t
     return res + ((nl,) if events is not None else ())
 
 
-def spec_sample(logits, u, temperature: float, top_k: int = 0, *, workspace: Workspace | None = None,
+def _each(x) -> bool:
+    """Whether a setting is a tensor with an entry for each row."""
+    import torch
+    return isinstance(x, torch.Tensor) and x.dim() > 0
+
+
+def spec_sample(logits, u, temperature: float, top_k: int = 0, *, top_p=1.0, min_p=0.0, workspace: Workspace | None = None,
                 stream=None, out=None, events=None):
     """Batched sampling on the GPU (see include/spec_verify.h): one token per row of
     logits [B, V] (bfloat16 or float32) drawn by inverse CDF with u [B] float32 (None at
     temperature 0).  Returns (tokens [B], row_status [B]) int32 tensors; ``out`` may supply
-    them.  ``events`` as for spec_verify."""
+    them.  ``events`` as for spec_verify.
+
+    With top_p below 1, min_p above 0, or settings of each row's own (temperature, top_p and
+    min_p [B] float32, top_k [B] int32 tensors) the policy and its kernels are those of
+    include/spec_filter.h; ``workspace`` is then a uint8 tensor or None (taken from torch's
+    allocator)."""
     import torch
+    if _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p) or top_p != 1.0 or min_p != 0.0:
+        from . import filter as _filter
+        return _filter.sample(logits, u, temperature, top_k, top_p, min_p, workspace, stream, out, events)
     lib = load_library()
     dev = logits.device
     if dev.type != "cuda":
@@ -586,6 +607,7 @@ _CACHE_NAMES = ("PagePool", "empty_pages", "spec_paged_attention", "spec_cache_a
                 "sv_attention_launch_plan", "ROW_BAD_PAGE", "ROW_BAD_LENGTH", "ROW_NO_PAGES", "ROW_BAD_FORK",
                 "CACHE_MAX_NEW", "CACHE_MAX_SEQS", "Pages4", "empty_pages4", "Rotary", "spec_cache_append_rotary", "spec_cache_read",
                 "sv_attention4_workspace_bytes", "sv_attention4_launch_plan")
+_FILTER_NAMES = ("spec_filter_logits", "sv_filter_workspace_bytes", "sv_filter_launch_plan", "ROW_BAD_POLICY")
 
 
 def __getattr__(name: str):
@@ -593,5 +615,9 @@ def __getattr__(name: str):
     if name in _CACHE_NAMES:
         from . import cache
         value = globals()[name] = getattr(cache, name)
+        return value
+    if name in _FILTER_NAMES:
+        from . import filter as _filter
+        value = globals()[name] = getattr(_filter, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

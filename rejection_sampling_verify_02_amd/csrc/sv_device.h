@@ -25,7 +25,6 @@ constexpr double LOG2E = 1.44269504088896340736;
 
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- element formats
 

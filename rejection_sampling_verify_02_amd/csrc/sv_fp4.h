@@ -6,6 +6,8 @@
 
 namespace sv {
 
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int F4_BLOCK = 32;     // elements that share a scale
 constexpr int F4_NAN = 255;      // the scale byte of a block that is not finite
 constexpr int F4_MIN = -120, F4_MAX = 125;  // exponents of a scale
