@@ -442,6 +442,11 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
   }
   if ((bits & 15) || (((uintptr_t)k_scales | (uintptr_t)v_scales) & 7) || (R && ((uintptr_t)rotary->inv_freq & 3))) return SV_ERR_ALIGN;
   if (overlap(prior, row_status, B)) return SV_ERR_PARAM;
+  if (q) {  // a pair's elements are read and written by different threads
+    const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)q_out, row = (uintptr_t)Hq * D * esz;
+    const uintptr_t q1 = q0 + (uintptr_t)(B - 1) * (uintptr_t)a.q_sb + (uintptr_t)(N - 1) * (uintptr_t)a.q_sn + row, o1 = o0 + (uintptr_t)B * N * row;
+    if (q0 < o1 && o0 < q1) return SV_ERR_PARAM;
+  }
   a.k_pages = static_cast<char *>(k_pages);
   a.k_scales = static_cast<char *>(k_scales);
   a.v_pages = static_cast<char *>(v_pages);
