@@ -4,20 +4,22 @@
 // Each of the three cuts keeps the logits at or above some value, so a row's policy comes down to
 // one threshold, found by weighted selection: the largest value t with W(z >= t) >= a target,
 // where W counts tokens (top-k) or adds their weights (top-p).  Weights are 2^x for
-// x = z log2(e) / T.  They are fixed-point numbers of 64 bits relative to a power of two near the
-// row's largest, so that sums do not depend on their order, and they are computed to about 1e-13
-// in 64 bits: a vocabulary of 10^5 tokens of probability 10^-6 leaves cumulative weights no room
-// for float32's rounding.
+// x = z log2(e) / T.  They are fixed-point numbers relative to a power of two near the row's
+// largest, so that sums do not depend on their order, and they are taken in 64 bits to
+// 4 * 10^-11: a vocabulary of 10^5 tokens of probability 10^-6 leaves cumulative weights no room for
+// float32's rounding.
 //
 //   k_filter_scan    a chunk of a row a workgroup, one read of the logits: the chunk's largest, and
-//                    counts and weights by octave of the weight (ceil(x), the same for every chunk)
-//   k_filter_pick    a row a workgroup: adds the chunks' octaves, finds the octaves in which the
-//                    thresholds lie, and selects inside them.  Where all tokens from the lowest of
-//                    these octaves up fit a list, they are gathered into LDS in one pass over the
-//                    row (which comes from the L2 now) and everything else happens there; otherwise
-//                    each step is a pass over the row.  Then the draw: the chunk whose cumulative
-//                    kept weight passes u times the total, and the token in it.
+//                    counts and weights by quarter octave of the weight (the same ones for every
+//                    chunk)
+//   k_filter_pick    a row a workgroup: adds the chunks' bins, finds the bins in which the
+//                    thresholds lie, gathers what a bin holds into a list in LDS, in one pass over
+//                    the row (which comes from the L2 now), and selects there.  Then the draw: the
+//                    chunk whose cumulative kept weight passes u times the total, and the token in
+//                    it.
 //   k_filter_write   the row again, with -inf below the threshold
+
+#include <type_traits>
 
 #include "sv_common.h"
 
@@ -28,25 +30,27 @@ namespace sv {
 typedef unsigned long long w64;
 
 constexpr int FC = 8192;        // logits of a chunk, counted from the 16-byte block that the row begins in
-constexpr int OCT = 32;         // octaves of weight kept apart; the last takes all that is smaller
-constexpr int PICK_NT = 1024;   // threads of k_filter_pick
-constexpr int LIST = 8192;      // tokens of its list
+constexpr int BINS = 128;       // quarter octaves of weight kept apart; the last takes all that is smaller
+constexpr int LIST = 8192;      // tokens of the list of k_filter_pick
 constexpr int FPT = FC / NT;    // logits of a thread of k_filter_scan
 
 enum { F_ODD = 1, F_FINITE = 2, F_FAR = 4 };  // a chunk's flags: NaN or +inf, some finite logit, weights out of range
 
+// A chunk's bin j holds its tokens in quarter octave q - j: their number from bit 50 up, and below
+// it the sum of their weights relative to the octave that the bin lies in, in units of 2^-35 (8192
+// tokens of at most 2.02: 14 and 50 bits).
+constexpr int W_BITS = 35, W_COUNT = 50;
 struct ChunkSum {
-  double x;        // a whole number, at least every z log2(e) / T of the chunk's finite logits
+  int q;           // the quarter octave of the largest
   unsigned top;    // the largest finite logit's key
-  unsigned flags;
-  w64 mass[OCT];   // relative to 2^x: octave j holds weights in (2^(x - j - 1), 2^(x - j)]
-  unsigned count[OCT];
+  unsigned flags, pad;
+  w64 bin[BINS];
 };
 
 struct FilterArgs {
   const void *logits;
   const float *u;
-  int rows, V, chunks, F;  // F: bits of the fixed point behind the binary point
+  int rows, V, chunks, F;  // F: bits behind the point of a row's weights
   sv_policy policy;
   ChunkSum *sums;          // [rows][chunks]
   uint2 *cut;              // [rows] filter: the threshold's key and the one token kept (-1: all above; -2: a code)
@@ -55,7 +59,7 @@ struct FilterArgs {
 };
 
 struct Policy {
-  double c2;   // log2(e) / T
+  double c64;  // 64 log2(e) / T
   float t, p, m;
   int k;
   bool ok;
@@ -68,12 +72,11 @@ SVD Policy policy_of(const FilterArgs &a, int row) {
   r.p = s.top_ps ? s.top_ps[row] : s.top_p;
   r.m = s.min_ps ? s.min_ps[row] : s.min_p;
   r.ok = r.t >= 0.0f && r.t < INFINITY && r.p > 0.0f && r.p <= 1.0f && r.m >= 0.0f && r.m <= 1.0f;
-  r.c2 = r.ok && r.t > 0.0f ? 1.4426950408889634074 / (double)r.t : 0.0;
+  r.c64 = r.ok && r.t > 0.0f ? 64.0 * 1.4426950408889634074 / (double)r.t : 0.0;
   return r;
 }
 
-// 2^d for d at most about 0, d > -1000: the Taylor series of 2^f on [-1/2, 1/2], whose next term
-// is under 10^-14.
+// 2^d for d > -1000: the Taylor series of 2^f on [-1/2, 1/2], whose next term is under 10^-14.
 SVD double pow2(double d) {
   const double k = rint(d), f = (d - k) * 0.69314718055994530942;
   double p = 1.0 / 39916800.0;
@@ -90,12 +93,44 @@ SVD double pow2(double d) {
   p = fma(p, f, 1.0);
   return ldexp(p, (int)k);
 }
-// 2^d with F bits behind the binary point (F at most 50): adding 2^52 leaves the rounded whole number in the
-// mantissa.
-SVD w64 mass_of(double d, int F) {
-  if (d < -64.0) return 0;
-  return (w64)__double_as_longlong(ldexp(pow2(d), F) + 4503599627370496.0) & 0xfffffffffffffull;
+
+// Weights of a row.  64 x = z * c64 = k + r with k whole, |r| <= 1/2 (adding 1.5 * 2^52 leaves k in
+// the sum's low word; |64 x| is below 2^30): 2^x = 2^(k / 64) * 2^(r / 64), the first from 64 powers
+// in LDS and k's upper bits, the second from three terms of its series (the fourth is under
+// 4 * 10^-11, and always positive).  A token's quarter octave is k >> 4, its octave k >> 6.
+struct Weight {
+  int q;    // quarter octave
+  w64 m;    // 2^x relative to the octave, or to `rest` where that is higher, in units of 2^-35
+};
+SVD void powers(double *tab) {  // [64], before a barrier
+  if (threadIdx.x < 64) tab[threadIdx.x] = pow2(W_BITS + (double)threadIdx.x / 64.0);
 }
+SVD int k64(double z, double c64, double &y) {
+  y = fma(z, c64, 6755399441055744.0);
+  return (int)(unsigned)__double_as_longlong(y);
+}
+SVD int quarter_of(double z, double c64) {
+  double y;
+  return k64(z, c64, y) >> 4;
+}
+SVD Weight weight_of(double z, double c64, const double *tab, int rest) {
+  constexpr double L = 0.69314718055994530942 / 64.0;
+  double y;
+  const int k = k64(z, c64, y);
+  const double r = fma(z, c64, 6755399441055744.0 - y), t = tab[k & 63];
+  const double e = fma(fma(L * L * L / 6.0, r, L * L / 2.0), r, L), v = fma(t * r, e, t);
+  Weight w;
+  w.q = k >> 4;
+  const int down = max(min((k >> 6) - rest, 0), -100);
+  const double x = __hiloint2double(__double2hiint(v) + (down << 20), __double2loint(v)) + 4503599627370496.0;  // its ulp is one unit
+  w.m = (w64)__double_as_longlong(x) & 0xfffffffffffffull;
+  return w;
+}
+// Logits below this are taken as this, so that |64 x| stays below 2^30 (as a float32, not below
+// -10^9 / c64).
+SVD float lowest_of(double c64) { return fmaxf((float)(-0.999e9 / c64), -__FLT_MAX__); }
+SVD int octave_of(int q) { return q >> 2; }
+SVD w64 shifted(w64 m, int left) { return left >= 0 ? m << left : left > -64 ? m >> -left : 0ull; }
 
 // Logits in an order of whole numbers, and back: bf16 in 16 bits.  -0 is taken as 0 (they are equal).
 template <typename T>
@@ -131,45 +166,41 @@ struct RowBlocks {
 
 // ---------------------------------------------------------------- scan
 
-constexpr int COPIES = 16;  // of a workgroup's octaves, so that a wave's lanes seldom add to one place
+constexpr int COPIES = 16;  // of a workgroup's bins, so that a wave's lanes seldom add to one place
 
 template <typename T>
 __global__ __launch_bounds__(NT) void k_filter_scan(const FilterArgs a) {
   constexpr int E = Fmt<T>::VEC, NV = FPT / E;
-  __shared__ w64 s_mass[OCT * COPIES];
-  __shared__ unsigned s_count[OCT * COPIES];
+  __shared__ w64 s_bin[BINS * COPIES];
+  __shared__ double s_tab[64];
   __shared__ unsigned s_top[NW], s_flags[NW];
   const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
   const int row = (int)(blockIdx.x / (unsigned)a.chunks), c = (int)(blockIdx.x % (unsigned)a.chunks);
   const RowBlocks<T> r(a.logits, row, a.V);
   const Policy pol = policy_of(a, row);
+  u32x4 w[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) w[k] = r.load(c * (FC / E) + k * NT + tid);
+  for (int i = tid; i < BINS * COPIES; i += NT) s_bin[i] = 0;
+  powers(s_tab);
   float z[NV][E];
+  float top = -INFINITY;
+  int most = (int)0x80000000;  // of the bits as whole numbers: from +inf up they are not finite
+  unsigned least = 0;          // likewise for negative ones: beyond -inf
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = c * (FC / E) + k * NT + tid;
-    r.unpack(r.load(i), i, z[k]);
-    if (i >= r.n)
-#pragma unroll
-      for (int e = 0; e < E; ++e) z[k][e] = -INFINITY;
-  }
-  for (int i = tid; i < OCT * COPIES; i += NT) {
-    s_mass[i] = 0;
-    s_count[i] = 0;
-  }
-  float top = -INFINITY, low = INFINITY;
-  bool odd = false;
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
+    r.unpack(w[k], c * (FC / E) + k * NT + tid, z[k]);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float x = z[k][e];
-      odd |= !(x < INFINITY);
-      top = fmaxf(top, x);
-      low = x > -INFINITY ? fminf(low, x) : low;
+      top = fmaxf(top, z[k][e]);
+      most = max(most, __float_as_int(z[k][e]));
+      least = max(least, __float_as_uint(z[k][e]));
     }
+  }
+  const bool odd = most >= 0x7f800000 || least > 0xff800000u;
   top = wave_max(top);
-  low = -wave_max(-low);
-  const unsigned far = (fabs((double)top * pol.c2) < 1e12 && fabs((double)low * pol.c2) < 1e12) ? 0u : (unsigned)F_FAR;
+  // out of range: 64 x too large, or temperatures at which even the lowest float32 weighs something
+  const unsigned far = fabs((double)top * pol.c64) < 0.99e9 && pol.c64 > 4e-30 ? 0u : (unsigned)F_FAR;
   const unsigned fl = wave_or((odd ? (unsigned)F_ODD : 0u) | (top > -INFINITY ? F_FINITE | far : 0u));
   if (lane == 0) {
     s_top[wid] = f2key(top);
@@ -183,37 +214,31 @@ __global__ __launch_bounds__(NT) void k_filter_scan(const FilterArgs a) {
     flags |= s_flags[k];
   }
   ChunkSum *out = a.sums + (size_t)row * a.chunks + c;
-  double X = 0.0;
-  if (pol.c2 != 0.0 && flags == F_FINITE) {
-    X = ceil((double)key2f(tk) * pol.c2);
+  const bool weigh = pol.c64 != 0.0 && flags == F_FINITE;
+  const int q = weigh ? quarter_of((double)key2f(tk), pol.c64) : 0;
+  if (weigh) {
+    // Logits so low that they weigh nothing are taken higher (-inf among them: they add nothing to the
+    // last bin but their number, which then only makes it look fuller).
+    const int rest = octave_of(q - (BINS - 1));
+    const float low = lowest_of(pol.c64);
+    w64 *mine = s_bin + (lane & (COPIES - 1));
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float v = z[k][e];
-        if (v == -INFINITY) continue;
-        const double x = (double)v * pol.c2;
-        const int j = min((int)(X - ceil(x)), OCT - 1), at = j * COPIES + (lane & (COPIES - 1));
-        atomicAdd(&s_mass[at], mass_of(x - X, a.F));
-        atomicAdd(&s_count[at], 1u);
+        const Weight x = weight_of((double)fmaxf(z[k][e], low), pol.c64, s_tab, rest);
+        atomicAdd(&mine[min(q - x.q, BINS - 1) * COPIES], x.m | (1ull << W_COUNT));
       }
     __syncthreads();
-    if (tid < OCT) {
-      w64 m = 0;
-      unsigned n = 0;
-      for (int k = 0; k < COPIES; ++k) {
-        m += s_mass[tid * COPIES + (k + tid) % COPIES];
-        n += s_count[tid * COPIES + (k + tid) % COPIES];
-      }
-      out->mass[tid] = m;
-      out->count[tid] = n;
-    }
-  } else if (tid < OCT) {
-    out->mass[tid] = 0;
-    out->count[tid] = 0;
+  }
+  if (tid < BINS) {
+    w64 m = 0;
+#pragma unroll
+    for (int k = 0; k < COPIES; ++k) m += s_bin[tid * COPIES + (k + tid) % COPIES];
+    out->bin[tid] = m;
   }
   if (tid == 0) {
-    out->x = X;
+    out->q = q;
     out->top = tk;
     out->flags = flags;
   }
@@ -221,16 +246,16 @@ __global__ __launch_bounds__(NT) void k_filter_scan(const FilterArgs a) {
 
 // ---------------------------------------------------------------- pick
 
-constexpr int PICK_W = PICK_NT / WAVE;
-
 struct PickShared {
-  w64 mass[OCT], hist[256], total;
-  unsigned count[OCT], cnt[256];
-  w64 wave[PICK_W];
+  w64 mass[BINS], hist[256], total;
+  unsigned count[BINS];
+  double tab[64];
+  w64 wave[16];
   unsigned list_key[LIST];
   int list_at[LIST];
   int n_list, found;
   unsigned key[2];
+  w64 above;
 };
 
 // The smallest key in [lo, hi] of which pred holds, pred(hi) taken to; by every wave alike.
@@ -267,48 +292,46 @@ SVD w64 wave_total64(w64 v) {
   return ((w64)hi << 32) | lo;
 }
 
-template <typename T, bool DRAW>
-__global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
+// PNT: threads of the workgroup.  A row is one workgroup's, and its steps follow one another: what
+// bounds it is latency, the passes over the row (256 KB from the L2) before all else.  Each step
+// that has to look at single tokens asks for those of a range of keys; they come into the list, once
+// for all steps where everything from the lowest threshold's bin up fits it.
+template <typename T, bool DRAW, int PNT>
+__global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k_filter_pick(const FilterArgs a) {
   typedef Key<T> K;
-  constexpr int E = Fmt<T>::VEC;
+  constexpr int E = Fmt<T>::VEC, PW = PNT / WAVE;
   __shared__ PickShared s;
   extern __shared__ w64 s_chunk[];  // [chunks] kept weight
-  const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
+  const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int row = blockIdx.x;
   const RowBlocks<T> r(a.logits, row, a.V);
   const Policy pol = policy_of(a, row);
   const ChunkSum *sums = a.sums + (size_t)row * a.chunks;
 
   // ---- the chunks put together
-  double X = -INFINITY;
-  unsigned tk = 0, flags = 0;
-  for (int c = tid; c < a.chunks; c += PICK_NT) {
-    const unsigned f = sums[c].flags;
-    flags |= f;
-    if (f & F_FINITE) {
-      X = fmax(X, sums[c].x);
-      tk = max(tk, sums[c].top);
-    }
-  }
-  if (tid < OCT) {
+  if (tid < BINS) {
     s.mass[tid] = 0;
     s.count[tid] = 0;
   }
   if (tid == 0) {
     s.key[0] = s.key[1] = 0;
-    s.total = 0;
-    s.n_list = 0;
+    s.n_list = (int)0x80000000;
     s.found = 0x7fffffff;
   }
+  powers(s.tab);
   __syncthreads();
-  if (flags) atomicOr(&s.key[0], flags);
-  if (tk) atomicMax(&s.key[1], tk);
-  // whole numbers below 2^41: their order is that of the bits, offset to be positive
-  if (X > -INFINITY) atomicMax(&s.total, (w64)(long long)(X + 4398046511104.0));
+  for (int c = tid; c < a.chunks; c += PNT) {
+    const unsigned f = sums[c].flags;
+    if (f) atomicOr(&s.key[0], f);
+    if (f & F_FINITE) {
+      atomicMax(&s.key[1], sums[c].top);
+      atomicMax(&s.n_list, sums[c].q);
+    }
+  }
   __syncthreads();
-  flags = s.key[0];
+  const unsigned flags = s.key[0];
   const float zmax = key2f(s.key[1]);
-  X = (double)(long long)s.total - 4398046511104.0;
+  int Q = s.n_list;
   int code = 0;
   float u = 0.0f;
   if (!pol.ok) code = SV_ROW_BAD_POLICY;
@@ -326,33 +349,15 @@ __global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
     return;
   }
   const unsigned top_key = K::of(zmax);
-  __syncthreads();
-
-  // ---- the row, block by block, or the list: f(key, logit, index in blocks)
-  auto over_row = [&](auto f) {
-    constexpr int AHEAD = 4;
-    for (int i0 = tid; i0 < r.n; i0 += AHEAD * PICK_NT) {
-      u32x4 w[AHEAD];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) w[k] = r.load(i0 + k * PICK_NT);
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        const int i = i0 + k * PICK_NT;
-        if (i >= r.n) break;
-        float z[E];
-        r.unpack(w[k], i, z);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f(K::of(z[e]), z[e], i * E + e);
-      }
-    }
-  };
 
   if (pol.t == 0.0f) {  // greedy: the first of the largest
-    int best = 0x7fffffff;
-    over_row([&](unsigned key, float, int at) {
-      if (key == top_key) best = min(best, at - r.lead);
-    });
-    if (best != 0x7fffffff) atomicMin(&s.found, best);
+    for (int i = tid; i < r.n; i += PNT) {
+      float z[E];
+      r.unpack(r.load(i), i, z);
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (z[e] == zmax) atomicMin(&s.found, r.index(i, e));
+    }
     __syncthreads();
     if (tid == 0) {
       if (DRAW) a.tokens[row] = s.found;
@@ -361,128 +366,247 @@ __global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
     return;
   }
 
-  // x of a logit, and its weight relative to 2^X.  Rows whose x pass 2^40 are taken relative to
-  // their largest logit, and counted here.
+  // Rows whose 64 x pass 10^9 are taken relative to their largest logit, and their bins are counted
+  // here; differences so large that their weight is nothing are cut off.
   const bool far = flags & F_FAR;
-  const double off = far ? (double)zmax : 0.0;
-  if (far) X = 0.0;
-  auto x_of = [&](float z) { return ((double)z - off) * pol.c2; };
-  auto weight = [&](float z) { return mass_of(x_of(z) - X, a.F); };
-  auto octave = [&](float z) {
-    const double d = X - ceil(x_of(z));
-    return d < OCT - 1 ? (int)d : OCT - 1;
+  const double off = far ? (double)zmax : 0.0, least = far ? -1e9 / pol.c64 : (double)lowest_of(pol.c64);
+  if (far) Q = 0;
+  const int O = octave_of(Q), rest = octave_of(Q - (BINS - 1));
+  auto arg = [&](float z) { return fmax((double)z - off, least); };
+  auto bin_of = [&](float z) { return min(Q - quarter_of(arg(z), pol.c64), BINS - 1); };
+  auto weight = [&](float z, int &bin) {
+    const Weight w = weight_of(arg(z), pol.c64, s.tab, rest);
+    bin = min(Q - w.q, BINS - 1);
+    return shifted(w.m, a.F - W_BITS - (O - max(octave_of(w.q), rest)));
   };
   if (!far) {
-    for (int i = tid; i < a.chunks * OCT; i += PICK_NT) {
-      const ChunkSum &cs = sums[i / OCT];
-      const unsigned n = cs.count[i % OCT];
-      if (!(cs.flags & F_FINITE) || n == 0) continue;
-      const double sh = X - cs.x;
-      const int up = sh < 64.0 ? (int)sh : 64, j = min(i % OCT + up, OCT - 1);
-      atomicAdd(&s.mass[j], up < 64 ? cs.mass[i % OCT] >> up : 0ull);
-      atomicAdd(&s.count[j], n);
+    for (int i = tid; i < a.chunks * BINS; i += PNT) {
+      const ChunkSum &cs = sums[i / BINS];
+      const w64 x = cs.bin[i % BINS];
+      if (x == 0) continue;
+      const int q = cs.q - i % BINS, j = min(Q - q, BINS - 1);  // a chunk's last bin is relative to its own octave
+      const w64 m = shifted(x & ((1ull << W_COUNT) - 1ull), a.F - W_BITS - (O - octave_of(q)));
+      atomicAdd(&s.mass[j], m);
+      atomicAdd(&s.count[j], (unsigned)(x >> W_COUNT));
     }
-  } else {
-    over_row([&](unsigned, float z, int) {
-      if (z == -INFINITY) return;
-      atomicAdd(&s.mass[octave(z)], weight(z));
-      atomicAdd(&s.count[octave(z)], 1u);
-    });
   }
-  __syncthreads();
-  // The keys of octave j: those from first(j) on that are below first(j - 1).
+  // The first key of bin j, tried near where it has to be.
   auto first_of = [&](int j) {
-    if (j >= OCT - 1) return K::lowest();
-    return first_key(K::lowest(), top_key, [&](unsigned k) { return X - ceil(x_of(K::value(k))) <= (double)j; });
+    if (j >= BINS - 1) return K::lowest();
+    auto in = [&](unsigned k) { return Q - quarter_of(arg(K::value(k)), pol.c64) <= j; };
+    const unsigned g = K::of((float)((double)((Q - j) * 16) / pol.c64 + off));
+    const unsigned lo = max(g, K::lowest() + 32u) - 32u, hi = min(lo + 63u, top_key);
+    const unsigned k = min(lo + (unsigned)lane, hi);
+    const unsigned long long b = __ballot(in(k));
+    if (lo < hi && b != 0 && !(b & 1)) return lo + (unsigned)__ffsll(b) - 1u;
+    return first_key(K::lowest(), top_key, in);
   };
+  __syncthreads();
 
-  // ---- the lowest octave that a threshold can lie in
+  // ---- steps: each looks at the tokens with keys from lo to hi
+  enum { ALL, COUNT, REST, MASS, DRAWN, END };
+  // ALL: a far row's bins.  COUNT: selection by number.  REST: the kept weight of tau's bin.
+  // MASS: selection by weight.  DRAWN: the chunks' kept weight of tau's bin.
   unsigned n_all = 0;
-  w64 w_all = 0;
-  for (int j = 0; j < OCT; ++j) {
-    n_all += s.count[j];
-    w_all += s.mass[j];
-  }
-  const bool by_k = pol.k > 0 && (unsigned)pol.k < n_all, by_p = pol.p < 1.0f;
-  unsigned tau = K::lowest();  // kept: keys from tau on
-  int jt = OCT - 1;            // tau's octave
-  if (pol.m > 0.0f) {
-    const double xm = x_of(zmax);
-    tau = first_key(K::lowest(), top_key, [&](unsigned k) {
-      const double d = x_of(K::value(k)) - xm;
-      return d > -200.0 && pow2(d) >= (double)pol.m;
-    });
-    jt = octave(K::value(tau));
-  }
-  const bool by_m = tau > K::lowest();
-  if (by_k) {
-    unsigned n = 0;
-    int j = 0;
-    for (; j < OCT - 1; ++j) {
-      n += s.count[j];
-      if (n >= (unsigned)pol.k) break;
+  w64 kept = 0, above = 0;
+  double target = 0.0;
+  unsigned tau = K::lowest(), lo = K::lowest(), hi = top_key;  // kept: keys from tau on
+  unsigned list_lo = 1, list_hi = 0;  // the keys of which the list has all tokens
+  int jt = BINS - 1, bin = 0;         // tau's bin, the bin looked at
+  bool by_k = false, by_m = false, cuts = false, whole = false;
+  const bool by_p = pol.p < 1.0f;
+  int step = far ? ALL : END;
+  bool begin = true;  // of a step
+  int next = END;
+  // Lane l has bins 2 l and 2 l + 1, and what lies in front of them.
+  w64 m0 = 0, m1 = 0, pm = 0;
+  unsigned c0 = 0, c1 = 0, pc = 0;
+  auto lane64 = [&](w64 v, int l) {
+    return ((w64)(unsigned)__builtin_amdgcn_readlane((int)(unsigned)(v >> 32), l) << 32) | (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, l);
+  };
+  auto count_in_front = [&](int j) { return (unsigned)__builtin_amdgcn_readlane((int)(pc + ((j & 1) ? c0 : 0u)), j >> 1); };
+  auto mass_in_front = [&](int j) { return lane64(pm + ((j & 1) ? m0 : 0ull), j >> 1); };
+  // The first bin up to and with which there are n tokens, or a weight of w; the last if none.
+  auto bin_by_count = [&](unsigned n) {
+    const unsigned long long b0 = __ballot(pc + c0 >= n), b1 = __ballot(pc + c0 + c1 >= n);
+    return b1 == 0 ? BINS - 1 : 2 * (__ffsll(b1) - 1) + ((b0 >> (__ffsll(b1) - 1)) & 1 ? 0 : 1);
+  };
+  auto bin_by_mass = [&](double w) {
+    const unsigned long long b0 = __ballot((double)(pm + m0) >= w), b1 = __ballot((double)(pm + m0 + m1) >= w);
+    return b1 == 0 ? BINS - 1 : 2 * (__ffsll(b1) - 1) + ((b0 >> (__ffsll(b1) - 1)) & 1 ? 0 : 1);
+  };
+  auto plan = [&]() {  // once the bins are known: the cuts, and what to look at first
+    m0 = s.mass[2 * lane];
+    m1 = s.mass[2 * lane + 1];
+    c0 = s.count[2 * lane];
+    c1 = s.count[2 * lane + 1];
+    const w64 im = wave_incl(m0 + m1);
+    const unsigned ic = scan_add_u(c0 + c1);
+    pm = im - m0 - m1;
+    pc = ic - c0 - c1;
+    n_all = (unsigned)__builtin_amdgcn_readlane((int)ic, WAVE - 1);
+    kept = lane64(im, WAVE - 1);
+    by_k = pol.k > 0 && (unsigned)pol.k < n_all;
+    if (pol.m > 0.0f) {
+      const double xm = arg(zmax) * pol.c64;
+      auto in = [&](unsigned k) {
+        const double d = (arg(K::value(k)) * pol.c64 - xm) * (1.0 / 64.0);
+        return d > -200.0 && pow2(d) >= (double)pol.m;
+      };
+      const unsigned g = K::of(fminf((float)((double)zmax + 64.0 * (double)log2f(pol.m) / pol.c64), zmax));
+      const unsigned l0 = max(g, K::lowest() + 32u) - 32u, h0 = min(l0 + 63u, top_key);
+      const unsigned long long b = __ballot(in(min(l0 + (unsigned)lane, h0)));
+      tau = l0 < h0 && b != 0 && !(b & 1) ? l0 + (unsigned)__ffsll(b) - 1u : first_key(K::lowest(), top_key, in);
+      jt = bin_of(K::value(tau));
     }
-    jt = min(jt, j);
-  }
-  if (by_p && !by_k && !by_m) {
-    w64 w = 0;
-    int j = 0;
-    for (; j < OCT - 1; ++j) {
-      w += s.mass[j];
-      if ((double)w >= (double)pol.p * (double)w_all) break;
+    by_m = tau > K::lowest();
+    if (by_k) {
+      const int j = bin_by_count((unsigned)pol.k);
+      if (j > jt) by_k = false;  // min-p cuts off more
+      else jt = j;
+    } else if (by_p && !by_m) {
+      jt = bin_by_mass((double)pol.p * (double)kept);
     }
-    jt = j;
+    cuts = by_k || by_m || by_p;
+    // everything from the lowest bin up that a threshold can lie in
+    whole = count_in_front(jt) + s.count[jt] <= (unsigned)LIST;
+    next = by_k ? COUNT : by_m ? (by_p ? REST : DRAWN) : by_p ? MASS : DRAWN;
+  };
+  if (!far) {
+    plan();
+    step = next;
   }
-  unsigned n_up = 0;
-  for (int j = 0; j <= jt; ++j) n_up += s.count[j];
-  const unsigned low = first_of(jt);  // everything from here on is n_up tokens
-  const bool cuts = by_k || by_p || by_m;
-  const bool listed = cuts && n_up <= (unsigned)LIST;
-  if (listed) {
-    over_row([&](unsigned key, float z, int at) {
-      const bool in = key >= low && z > -INFINITY;
-      const unsigned long long b = __ballot(in);
-      if (b == 0) return;
-      // lanes that have left the loop are not in the ballot: the first that is in it takes the places
-      int base = 0;
-      const int lead = __ffsll(b) - 1;
-      if (lane == lead) base = atomicAdd(&s.n_list, __popcll(b));
-      base = __builtin_amdgcn_readlane(base, lead);
-      if (in) {
-        const int o = base + __popcll(b & ((1ull << lane) - 1ull));
-        if (o < LIST) {
-          s.list_key[o] = key;
-          s.list_at[o] = at;
+  for (;;) {
+    if (begin) {
+      begin = false;
+      if (step == DRAWN && !DRAW) step = END;
+      if (step == DRAWN) {
+        for (int c = tid; c < a.chunks; c += PNT) s_chunk[c] = 0;
+        if (!cuts && !far) step = END;  // the bins are enough
+      }
+      if (step == END) break;
+      if (step == COUNT) {
+        bin = bin_by_count((unsigned)pol.k);
+        above = count_in_front(bin);
+        target = (double)pol.k;
+        lo = first_of(bin);
+      } else if (step == REST) {
+        bin = jt = bin_of(K::value(tau));
+        lo = tau;
+      } else if (step == MASS) {
+        target = (double)pol.p * (double)kept;
+        bin = min(bin_by_mass(target), by_k || by_m ? jt : BINS - 1);
+        above = mass_in_front(bin);
+        lo = max(tau, first_of(bin));
+      } else if (step == DRAWN) {
+        bin = jt;
+        lo = tau;
+      }
+      hi = bin == 0 || step == ALL || (step == DRAWN && far) ? top_key : first_of(bin - 1) - 1u;
+    }
+    const unsigned span = hi - lo;
+    const int bits = 32 - __clz((int)(span | 1u)), sh = bits > 8 ? bits - 8 : 0;
+    for (int i = tid; i < 256; i += PNT) s.hist[i] = 0;
+    if (tid == 0) s.total = 0;
+
+    auto look = [&](int n) {  // at the first n of the list
+      w64 part = 0;
+      for (int i = tid; i < n; i += PNT) {
+        const unsigned k = s.list_key[i];
+        if (k < lo || k > hi) continue;
+        if (step == COUNT) {
+          atomicAdd(&s.hist[(k - lo) >> sh], 1ull);
+        } else {
+          int j;
+          const w64 w = weight(K::value(k), j);
+          if (step == MASS) {
+            atomicAdd(&s.hist[(k - lo) >> sh], w);
+          } else if (step == REST) {
+            part += w;
+          } else if (step == DRAWN) {
+            atomicAdd(&s_chunk[s.list_at[i] / FC], w);
+          } else {
+            atomicAdd(&s.mass[j], w);
+            atomicAdd(&s.count[j], 1u);
+          }
         }
       }
-    });
-    __syncthreads();
-  }
-  const int n_list = listed ? min(s.n_list, LIST) : 0;
-  // f(key, logit, place) for tokens with keys from lo to hi
-  auto visit = [&](unsigned lo, unsigned hi, auto f) {
-    if (listed) {
-      for (int i = tid; i < n_list; i += PICK_NT) {
-        const unsigned k = s.list_key[i];
-        if (k >= lo && k <= hi) f(k, K::value(k), s.list_at[i]);
+      if (part) atomicAdd(&s.total, part);
+    };
+    if (lo < list_lo || hi > list_hi) {  // gather
+      // all that is to come, if it fits; else this step's range, in pieces where that does not fit
+      const unsigned g_lo = whole && step != ALL ? first_of(jt) : lo, g_hi = whole && step != ALL ? top_key : hi;
+      const bool fits = step != ALL && (whole || (!far && s.count[bin] <= (unsigned)LIST));
+      const float z_lo = K::value(g_lo), z_hi = K::value(g_hi);
+      if (tid == 0) s.n_list = 0;
+      __syncthreads();
+      auto add = [&](const u32x4 &w, int i) {
+        float z[E];
+        r.unpack(w, i, z);
+        unsigned long long b[E];
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          b[e] = __ballot(z[e] >= z_lo && z[e] <= z_hi);
+          n += __popcll(b[e]);
+        }
+        if (n == 0) return;
+        int o = 0;
+        if (lane == 0) o = atomicAdd(&s.n_list, n);
+        o = __builtin_amdgcn_readfirstlane(o);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int at = o + __builtin_amdgcn_mbcnt_hi((unsigned)(b[e] >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)b[e], 0u));
+          if (((b[e] >> lane) & 1) && at < LIST) {
+            s.list_key[at] = K::of(z[e]);
+            s.list_at[at] = i * E + e;
+          }
+          o += __popcll(b[e]);
+        }
+      };
+      if (fits) {
+        constexpr int AHEAD = 8;
+        for (int i0 = tid; i0 - tid < r.n; i0 += AHEAD * PNT) {
+          u32x4 w[AHEAD];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) w[k] = r.load(i0 + k * PNT);
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) add(w[k], i0 + k * PNT);
+        }
+        list_lo = g_lo;
+        list_hi = g_hi;
+      } else {
+        list_lo = 1;
+        list_hi = 0;
+        for (int i0 = tid; i0 - tid < r.n; i0 += PNT) {
+          add(r.load(i0), i0);
+          __syncthreads();
+          look(s.n_list);
+          __syncthreads();
+          if (tid == 0) s.n_list = 0;
+          __syncthreads();
+        }
       }
-    } else {
-      over_row([&](unsigned k, float z, int at) {
-        if (k >= lo && k <= hi && z > -INFINITY) f(k, z, at);
-      });
     }
-  };
-  // The largest key t in [lo, hi] with above + W(lo.. >= t) >= target, by eight bits of the key at
-  // a time; W counts or adds weights.  Returns W of what lies above t's octave and at or above t too.
-  auto select = [&](unsigned lo, unsigned hi, w64 above, double target, bool counts, w64 &at_least) {
-    for (;;) {
-      const unsigned span = hi - lo;
-      const int bits = 32 - __clz((int)(span | 1u)), sh = bits > 8 ? bits - 8 : 0;
-      for (int i = tid; i < 256; i += PICK_NT) s.hist[i] = 0;
+    __syncthreads();
+    if (list_lo <= list_hi) look(min(s.n_list, LIST));
+    __syncthreads();
+
+    if (step == ALL) {
+      plan();
+      step = next;
+      begin = true;
+    } else if (step == REST) {
+      kept = s.total + mass_in_front(jt);
       __syncthreads();
-      visit(lo, hi, [&](unsigned k, float z, int) { atomicAdd(&s.hist[(k - lo) >> sh], counts ? 1ull : weight(z)); });
-      __syncthreads();
-      if (wid == 0) {  // lane l owns bins 255 - 4 l down to 252 - 4 l
+      step = by_p ? MASS : DRAWN;
+      begin = true;
+    } else if (step == DRAWN) {
+      break;
+    } else {
+      // The largest key t of the range with above + W(keys in [t, hi]) >= target, by eight bits of the
+      // key at a time: lane l owns bins 255 - 4 l down to 252 - 4 l.
+      if (wid == 0) {
         w64 h[4], t = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -490,144 +614,78 @@ __global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
           t += h[q];
         }
         w64 run = above + wave_incl(t) - t;
-        int bin = -1, some = -1;
-        w64 over = 0, upto = 0;
+        int pick = -1, some = -1;
+        w64 over = 0, upto = 0, below_some = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (h[q] != 0) some = 255 - 4 * lane - q;
-          if (bin < 0 && h[q] != 0 && (double)(run + h[q]) >= target) {
-            bin = 255 - 4 * lane - q;
+          if (h[q] != 0) {
+            some = 255 - 4 * lane - q;
+            below_some = run;
+          }
+          if (pick < 0 && h[q] != 0 && (double)(run + h[q]) >= target) {
+            pick = 255 - 4 * lane - q;
             over = run;
             upto = run + h[q];
           }
           run += h[q];
         }
-        const unsigned long long b = __ballot(bin >= 0), any = __ballot(some >= 0);
-        if (b != 0) {
-          if (lane == __ffsll(b) - 1) {
-            s.key[0] = (unsigned)bin;
-            s.hist[0] = over;
-            s.total = upto;
-          }
-        } else {  // the target is all there is, up to its rounding: the lowest
-          const int l = any ? 63 - __clzll((long long)any) : 63;
-          if (lane == l) {
-            s.key[0] = (unsigned)max(some, 0);
-            s.hist[0] = run - (some >= 0 ? s.hist[some] : 0ull);
-            s.total = run;
-          }
+        const unsigned long long b = __ballot(pick >= 0), any = __ballot(some >= 0);
+        const int l = b != 0 ? __ffsll(b) - 1 : any != 0 ? 63 - __clzll((long long)any) : 63;
+        if (lane == l) {  // where the target is all there is, up to its rounding: the lowest
+          s.key[0] = (unsigned)(b != 0 ? pick : max(some, 0));
+          s.above = b != 0 ? over : below_some;
+          s.total = b != 0 ? upto : run;
         }
       }
       __syncthreads();
-      const unsigned bin = s.key[0];
-      above = s.hist[0];
-      at_least = s.total;
+      const unsigned pick = s.key[0];
+      above = s.above;
+      const w64 upto = s.total;
       __syncthreads();
-      lo += bin << sh;
+      lo += pick << sh;
       if (hi - lo >= 1u << sh) hi = lo + ((1u << sh) - 1u);
-      if (sh == 0) return lo;
+      if (sh == 0) {
+        begin = true;
+        if (step == COUNT) {
+          tau = max(tau, lo);
+          jt = bin_of(K::value(tau));
+          step = by_p ? REST : DRAWN;
+        } else {
+          tau = lo;
+          jt = bin;
+          kept = upto;
+          step = DRAWN;
+        }
+      }
     }
-  };
-  auto upper_of = [&](int j) { return j == 0 ? top_key : first_of(j - 1) - 1u; };
-
-  // ---- the thresholds
-  if (by_k) {
-    w64 above = 0;
-    int j = 0;
-    for (; j < OCT - 1; ++j) {
-      if (above + s.count[j] >= (w64)pol.k) break;
-      above += s.count[j];
-    }
-    w64 n;
-    const unsigned t = select(first_of(j), upper_of(j), above, (double)pol.k, true, n);
-    tau = max(tau, t);
-  }
-  // the weight of what is kept so far
-  w64 kept = w_all;
-  if (by_k || by_m) {
-    jt = octave(K::value(tau));
-    kept = 0;
-    for (int j = 0; j < jt; ++j) kept += s.mass[j];
-    if (tid == 0) s.total = 0;
-    __syncthreads();
-    w64 part = 0;
-    visit(tau, upper_of(jt), [&](unsigned, float z, int) { part += weight(z); });
-    part = wave_total64(part);
-    if (lane == 0 && part) atomicAdd(&s.total, part);
-    __syncthreads();
-    kept += s.total;
-    __syncthreads();
-  }
-  if (by_p) {
-    const double target = (double)pol.p * (double)kept;
-    w64 above = 0;
-    int j = 0;
-    const int last = (by_k || by_m) ? jt : OCT - 1;
-    for (; j < last; ++j) {
-      if ((double)(above + s.mass[j]) >= target) break;
-      above += s.mass[j];
-    }
-    tau = select(max(tau, first_of(j)), upper_of(j), above, target, false, kept);
-    jt = j;
   }
   if (!DRAW) {
     if (tid == 0) a.cut[row] = make_uint2(tau, (unsigned)-1);
     return;
   }
 
-  // ---- the chunks' kept weights: octaves above tau's from the scan, tau's own token by token
-  for (int c = tid; c < a.chunks; c += PICK_NT) s_chunk[c] = 0;
+  // ---- the chunks' kept weights: bins above tau's from the scan, besides
   __syncthreads();
-  if (!far) {
-    for (int i = tid; i < a.chunks * OCT; i += PICK_NT) {
-      const ChunkSum &cs = sums[i / OCT];
-      if (!(cs.flags & F_FINITE)) continue;
-      const double sh = X - cs.x;
-      const int up = sh < 64.0 ? (int)sh : 64;
-      const int j = min(i % OCT + up, OCT - 1);
-      if (up < 64 && (cuts ? j < jt : true)) {
-        const w64 w = cs.mass[i % OCT] >> up;
-        if (w) atomicAdd(&s_chunk[i / OCT], w);
-      }
+  if (!far)
+    for (int i = tid; i < a.chunks * BINS; i += PNT) {
+      const ChunkSum &cs = sums[i / BINS];
+      const w64 x = cs.bin[i % BINS];
+      if (x == 0) continue;
+      const int q = cs.q - i % BINS, j = min(Q - q, BINS - 1);
+      if (cuts && j >= jt) continue;
+      const w64 m = shifted(x & ((1ull << W_COUNT) - 1ull), a.F - W_BITS - (O - octave_of(q)));
+      if (m) atomicAdd(&s_chunk[i / BINS], m);
     }
-  }
-  if (far || cuts) {
-    const unsigned hi = far ? top_key : upper_of(jt);
-    // a wave's blocks lie in one chunk: their sum is added once
-    if (listed && !far) {
-      visit(tau, hi, [&](unsigned, float z, int at) { atomicAdd(&s_chunk[at / FC], weight(z)); });
-    } else {
-      constexpr int STEP = FC / E;  // blocks of a chunk: a whole number of the workgroup's strides, or the reverse
-      for (int i0 = 0; i0 < r.n; i0 += PICK_NT) {
-        const int i = i0 + tid;
-        w64 part = 0;
-        if (i < r.n) {
-          float z[E];
-          r.unpack(r.load(i), i, z);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const unsigned k = K::of(z[e]);
-            if (k >= tau && k <= hi && z[e] > -INFINITY) part += weight(z[e]);
-          }
-        }
-        if (__any(part != 0)) {
-          part = wave_total64(part);
-          if (lane == 0) atomicAdd(&s_chunk[(i0 + wid * WAVE) / STEP], part);
-        }
-      }
-    }
-  }
   __syncthreads();
   if (wid == 0) {  // the first chunk whose cumulative weight passes the target
     w64 total = 0;
     for (int c0 = 0; c0 < a.chunks; c0 += WAVE) total += wave_total64(c0 + lane < a.chunks ? s_chunk[c0 + lane] : 0ull);
-    const double target = (double)u * (double)total;
-    w64 run = 0, before = 0;
+    const double t = (double)u * (double)total;
+    w64 run = 0, before = 0, fb = 0;
     int pick = -1, fallback = 0;
-    w64 fb = 0;
     for (int c0 = 0; c0 < a.chunks && pick < 0; c0 += WAVE) {
       const w64 w = c0 + lane < a.chunks ? s_chunk[c0 + lane] : 0ull, inc = wave_incl(w);
-      const unsigned long long b = __ballot(w != 0 && (double)(run + inc) > target), some = __ballot(w != 0);
+      const unsigned long long b = __ballot(w != 0 && (double)(run + inc) > t), some = __ballot(w != 0);
       auto at = [&](w64 v, int l) {
         return ((w64)(unsigned)__builtin_amdgcn_readlane((int)(unsigned)(v >> 32), l) << 32) | (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, l);
       };
@@ -644,26 +702,26 @@ __global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
     }
     if (lane == 0) {
       s.n_list = pick >= 0 ? pick : fallback;
-      s.hist[0] = pick >= 0 ? before : fb;
+      s.above = pick >= 0 ? before : fb;
       s.total = total;
+      s.found = -1;
     }
   }
   __syncthreads();
   const int c = s.n_list;
-  const double target = (double)u * (double)s.total;
-  w64 base = s.hist[0];
-  if (tid == 0) s.found = -1;
+  const double goal = (double)u * (double)s.total;
+  w64 base = s.above;
   // ---- the token: the chunk's kept weights in index order
   constexpr int STEP = FC / E;
-  for (int k = 0; k < STEP; k += PICK_NT) {
+  for (int k = 0; k < STEP; k += PNT) {
     const int i = c * STEP + k + tid;
     w64 w[E], sum = 0;
-    const bool in = k + tid < STEP && i < r.n;
     float z[E];
-    if (in) r.unpack(r.load(i), i, z);
+    r.unpack(r.load(i), i, z);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      w[e] = in && z[e] > -INFINITY && K::of(z[e]) >= tau ? weight(z[e]) : 0ull;
+      int j;
+      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= tau ? weight(z[e], j) : 0ull;
       sum += w[e];
     }
     const w64 inc = wave_incl(sum);
@@ -671,7 +729,7 @@ __global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
     if (tid == 0) s.key[0] = 0x7fffffffu;
     __syncthreads();
     w64 run = base, all = 0;
-    for (int v = 0; v < PICK_W; ++v) {
+    for (int v = 0; v < PW; ++v) {
       if (v < wid) run += s.wave[v];
       all += s.wave[v];
     }
@@ -682,7 +740,7 @@ __global__ __launch_bounds__(PICK_NT) void k_filter_pick(const FilterArgs a) {
       run += w[e];
       if (w[e] != 0) {
         last = r.index(i, e);
-        if (pick < 0 && (double)run > target) pick = last;
+        if (pick < 0 && (double)run > goal) pick = last;
       }
     }
     if (pick >= 0) atomicMin(&s.key[0], (unsigned)pick);
@@ -760,7 +818,7 @@ bool filter_plan(int32_t rows, int32_t V, int esz, FilterPlan &p) {
   if (rows < 1 || V < 1 || V > SV_FILTER_MAX_V) return false;
   const int E = 16 / esz;
   p.chunks = (int)(((long long)V + E - 1 + FC - 1) / FC);  // a row may begin anywhere in a block
-  if ((long long)rows * p.chunks > 0xffffffffLL / NT || rows > 0xffffffffLL / PICK_NT) return false;
+  if ((long long)rows * p.chunks > 0xffffffffLL / NT || rows > 0xffffffffLL / 1024) return false;
   size_t o = 0;
   p.sums = o; o = align256(o + (size_t)rows * p.chunks * sizeof(ChunkSum));
   p.cut = o; o = align256(o + (size_t)rows * 8);
@@ -793,10 +851,10 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   a.rows = rows;
   a.V = V;
   a.chunks = p.chunks;
-  // a row's weights are at most 1 each: their sum fits 62 bits
+  // a row's weights are at most 2.02 each: their sum fits 62 bits
   int bits = 0;
   while ((1LL << bits) < V) ++bits;
-  a.F = 62 - bits < 50 ? 62 - bits : 50;
+  a.F = 60 - bits < 48 ? 60 - bits : 48;
   a.policy = *pol;
   a.sums = (ChunkSum *)(base + p.sums);
   a.cut = (uint2 *)(base + p.cut);
@@ -807,10 +865,18 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   Launcher L{(hipStream_t)stream, ev, nev};
   const unsigned grid = (unsigned)((long long)rows * p.chunks);
   L.go(esz == 2 ? (const void *)&k_filter_scan<uint16_t> : (const void *)&k_filter_scan<float>, grid, args);
-  L.block = PICK_NT;
+  // Up to a row for each CU a workgroup of 1024 threads, beyond that two of 512 on a CU.
+  const bool wide = rows <= 256;
+  L.block = wide ? 1024 : 512;
   L.lds = draw ? (unsigned)p.chunks * 8 : 0;
-  if (draw) L.go(esz == 2 ? (const void *)&k_filter_pick<uint16_t, true> : (const void *)&k_filter_pick<float, true>, (unsigned)rows, args);
-  else L.go(esz == 2 ? (const void *)&k_filter_pick<uint16_t, false> : (const void *)&k_filter_pick<float, false>, (unsigned)rows, args);
+  auto pick = [&](auto t, auto d) -> const void * {
+    typedef decltype(t) T;
+    constexpr bool D = decltype(d)::value;
+    return wide ? (const void *)&k_filter_pick<T, D, 1024> : (const void *)&k_filter_pick<T, D, 512>;
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  L.go(esz == 2 ? (draw ? pick(uint16_t{}, yes) : pick(uint16_t{}, no)) : (draw ? pick(0.0f, yes) : pick(0.0f, no)), (unsigned)rows, args);
   if (!draw) {
     L.block = NT;
     L.lds = 0;
