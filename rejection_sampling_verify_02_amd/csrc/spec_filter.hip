@@ -12,14 +12,13 @@
 //   k_filter_scan    a chunk of a row a workgroup, one read of the logits: the chunk's largest, and
 //                    counts and weights by quarter octave of the weight (the same ones for every
 //                    chunk)
-//   k_filter_pick    a row a workgroup: adds the chunks' bins, finds the bins in which the
-//                    thresholds lie, gathers what a bin holds into a list in LDS, in one pass over
-//                    the row (which comes from the L2 now), and selects there.  Then the draw: the
-//                    chunk whose cumulative kept weight passes u times the total, and the token in
-//                    it.
+//   k_filter_plan    a row a workgroup: adds up the row's bins and finds the bin in which the first
+//                    threshold lies
+//   k_filter_gather  a chunk a workgroup again: puts what its chunk has in that bin on the row's list
+//   k_filter_pick    a row a workgroup: selects on the list, looks for more where a further
+//                    threshold needs it, and draws: the chunk whose cumulative kept weight passes u
+//                    times the total, and the token in it
 //   k_filter_write   the row again, with -inf below the threshold
-
-#include <type_traits>
 
 #include "sv_common.h"
 
@@ -47,12 +46,29 @@ struct ChunkSum {
   w64 bin[BINS];
 };
 
+// What k_filter_plan found out about a row.
+struct RowPlan {
+  w64 mass[BINS];        // the row's bins: weights relative to the octave of q, and numbers
+  unsigned count[BINS];
+  w64 above;             // of the first step: what lies above its range
+  double target;         // and what it looks for
+  int q, step, bin, jt;  // the largest's quarter octave; the step, its bin, the lowest threshold's bin
+  unsigned flags, tau, lo, hi, list_lo, list_hi;  // thresholds so far, the step's range, the list's
+  float zmax;
+  int by_k, by_m, cuts, whole;
+};
+
 struct FilterArgs {
   const void *logits;
   const float *u;
   int rows, V, chunks, F;  // F: bits behind the point of a row's weights
   sv_policy policy;
   ChunkSum *sums;          // [rows][chunks]
+  RowPlan *plans;          // [rows]
+  w64 *over;               // [rows][chunks] draw: a chunk's weight in the bins above the lowest threshold's
+  unsigned *n_list;        // [rows]
+  uint2 *list;             // [rows][cap] keys and places (in blocks) of tokens
+  int cap;
   uint2 *cut;              // [rows] filter: the threshold's key and the one token kept (-1: all above; -2: a code)
   int32_t *tokens, *row_status;
   void *out;
@@ -241,21 +257,22 @@ __global__ __launch_bounds__(NT) void k_filter_scan(const FilterArgs a) {
     out->q = q;
     out->top = tk;
     out->flags = flags;
+    if (c == 0) a.n_list[row] = 0;
   }
 }
 
-// ---------------------------------------------------------------- pick
+// ---------------------------------------------------------------- rows
 
-struct PickShared {
-  w64 mass[BINS], hist[256], total;
+enum { ALL, COUNT, REST, MASS, DRAWN, END };
+// Steps of a row.  ALL: a far row's bins.  COUNT: selection by number.  REST: the kept weight of
+// tau's bin.  MASS: selection by weight.  DRAWN: the chunks' kept weight of tau's bin.
+
+struct RowShared {
+  w64 mass[BINS];
   unsigned count[BINS];
   double tab[64];
-  w64 wave[16];
-  unsigned list_key[LIST];
-  int list_at[LIST];
-  int n_list, found;
-  unsigned key[2];
-  w64 above;
+  unsigned flags, top;
+  int q;
 };
 
 // The smallest key in [lo, hi] of which pred holds, pred(hi) taken to; by every wave alike.
@@ -292,150 +309,80 @@ SVD w64 wave_total64(w64 v) {
   return ((w64)hi << 32) | lo;
 }
 
-// PNT: threads of the workgroup.  A row is one workgroup's, and its steps follow one another: what
-// bounds it is latency, the passes over the row (256 KB from the L2) before all else.  Each step
-// that has to look at single tokens asks for those of a range of keys; they come into the list, once
-// for all steps where everything from the lowest threshold's bin up fits it.
-template <typename T, bool DRAW, int PNT>
-__global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k_filter_pick(const FilterArgs a) {
+// A row as both kernels see it once its chunks have been added up.
+template <typename T>
+struct Row {
   typedef Key<T> K;
-  constexpr int E = Fmt<T>::VEC, PW = PNT / WAVE;
-  __shared__ PickShared s;
-  extern __shared__ w64 s_chunk[];  // [chunks] kept weight
-  const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
-  const int row = blockIdx.x;
-  const RowBlocks<T> r(a.logits, row, a.V);
-  const Policy pol = policy_of(a, row);
-  const ChunkSum *sums = a.sums + (size_t)row * a.chunks;
+  RowShared &s;
+  Policy pol;
+  int F, Q, O, rest;
+  unsigned flags, top_key;
+  float zmax;
+  bool far;
+  double off, least;
+  // Lane l has bins 2 l and 2 l + 1, and what lies in front of them.
+  w64 m0, m1, pm, kept;
+  unsigned c0, c1, pc, n_all;
+  // the cuts: kept are keys from tau on; the lowest bin that a threshold can lie in; whether everything
+  // from it up fits a list
+  bool by_k, by_m, by_p, cuts, whole;
+  unsigned tau;
+  int jt;
 
-  // ---- the chunks put together
-  if (tid < BINS) {
-    s.mass[tid] = 0;
-    s.count[tid] = 0;
+  SVD Row(RowShared &sh, const FilterArgs &a, int row) : s(sh), pol(policy_of(a, row)), F(a.F) {}
+  // Rows out of range (F_FAR) are taken relative to their largest logit, and their bins are counted one
+  // token at a time; differences so large that their weight is nothing are cut off.
+  SVD void set(unsigned fl, float z, int q) {
+    flags = fl;
+    zmax = z;
+    top_key = K::of(z);
+    far = fl & F_FAR;
+    Q = far ? 0 : q;
+    O = octave_of(Q);
+    rest = octave_of(Q - (BINS - 1));
+    off = far ? (double)z : 0.0;
+    least = far ? -1e9 / pol.c64 : (double)lowest_of(pol.c64);
+    by_p = pol.p < 1.0f;
   }
-  if (tid == 0) {
-    s.key[0] = s.key[1] = 0;
-    s.n_list = (int)0x80000000;
-    s.found = 0x7fffffff;
-  }
-  powers(s.tab);
-  __syncthreads();
-  for (int c = tid; c < a.chunks; c += PNT) {
-    const unsigned f = sums[c].flags;
-    if (f) atomicOr(&s.key[0], f);
-    if (f & F_FINITE) {
-      atomicMax(&s.key[1], sums[c].top);
-      atomicMax(&s.n_list, sums[c].q);
-    }
-  }
-  __syncthreads();
-  const unsigned flags = s.key[0];
-  const float zmax = key2f(s.key[1]);
-  int Q = s.n_list;
-  int code = 0;
-  float u = 0.0f;
-  if (!pol.ok) code = SV_ROW_BAD_POLICY;
-  else if ((flags & F_ODD) || !(flags & F_FINITE)) code = SV_ROW_BAD_LOGITS;
-  else if (DRAW && pol.t > 0.0f) {
-    u = a.u ? a.u[row] : NAN;
-    if (!(u >= 0.0f && u < 1.0f)) code = SV_ROW_BAD_UNIFORM;
-  }
-  if (tid == 0) a.row_status[row] = code;
-  if (code != 0) {
-    if (tid == 0) {
-      if (DRAW) a.tokens[row] = -1;
-      else a.cut[row] = make_uint2(0u, (unsigned)-2);
-    }
-    return;
-  }
-  const unsigned top_key = K::of(zmax);
-
-  if (pol.t == 0.0f) {  // greedy: the first of the largest
-    for (int i = tid; i < r.n; i += PNT) {
-      float z[E];
-      r.unpack(r.load(i), i, z);
-#pragma unroll
-      for (int e = E - 1; e >= 0; --e)
-        if (z[e] == zmax) atomicMin(&s.found, r.index(i, e));
-    }
-    __syncthreads();
-    if (tid == 0) {
-      if (DRAW) a.tokens[row] = s.found;
-      else a.cut[row] = make_uint2(top_key, (unsigned)s.found);
-    }
-    return;
-  }
-
-  // Rows whose 64 x pass 10^9 are taken relative to their largest logit, and their bins are counted
-  // here; differences so large that their weight is nothing are cut off.
-  const bool far = flags & F_FAR;
-  const double off = far ? (double)zmax : 0.0, least = far ? -1e9 / pol.c64 : (double)lowest_of(pol.c64);
-  if (far) Q = 0;
-  const int O = octave_of(Q), rest = octave_of(Q - (BINS - 1));
-  auto arg = [&](float z) { return fmax((double)z - off, least); };
-  auto bin_of = [&](float z) { return min(Q - quarter_of(arg(z), pol.c64), BINS - 1); };
-  auto weight = [&](float z, int &bin) {
+  SVD double arg(float z) const { return fmax((double)z - off, least); }
+  SVD int bin_of(float z) const { return min(Q - quarter_of(arg(z), pol.c64), BINS - 1); }
+  SVD w64 weight(float z, int &bin) const {
     const Weight w = weight_of(arg(z), pol.c64, s.tab, rest);
     bin = min(Q - w.q, BINS - 1);
-    return shifted(w.m, a.F - W_BITS - (O - max(octave_of(w.q), rest)));
-  };
-  if (!far) {
-    for (int i = tid; i < a.chunks * BINS; i += PNT) {
-      const ChunkSum &cs = sums[i / BINS];
-      const w64 x = cs.bin[i % BINS];
-      if (x == 0) continue;
-      const int q = cs.q - i % BINS, j = min(Q - q, BINS - 1);  // a chunk's last bin is relative to its own octave
-      const w64 m = shifted(x & ((1ull << W_COUNT) - 1ull), a.F - W_BITS - (O - octave_of(q)));
-      atomicAdd(&s.mass[j], m);
-      atomicAdd(&s.count[j], (unsigned)(x >> W_COUNT));
-    }
+    return shifted(w.m, F - W_BITS - (O - max(octave_of(w.q), rest)));
   }
+  // The weight of a chunk's bin, of quarter octave q, as the row's weights are.
+  SVD w64 mass_of_chunk(int q, w64 x) const { return shifted(x & ((1ull << W_COUNT) - 1ull), F - W_BITS - (O - octave_of(q))); }
   // The first key of bin j, tried near where it has to be.
-  auto first_of = [&](int j) {
+  SVD unsigned first_of(int j) const {
     if (j >= BINS - 1) return K::lowest();
     auto in = [&](unsigned k) { return Q - quarter_of(arg(K::value(k)), pol.c64) <= j; };
-    const unsigned g = K::of((float)((double)((Q - j) * 16) / pol.c64 + off));
+    return near_key(K::of((float)((double)((Q - j) * 16) / pol.c64 + off)), in);
+  }
+  template <typename P>
+  SVD unsigned near_key(unsigned g, P in) const {
     const unsigned lo = max(g, K::lowest() + 32u) - 32u, hi = min(lo + 63u, top_key);
-    const unsigned k = min(lo + (unsigned)lane, hi);
-    const unsigned long long b = __ballot(in(k));
+    const unsigned long long b = __ballot(in(min(lo + (unsigned)lane_id(), hi)));
     if (lo < hi && b != 0 && !(b & 1)) return lo + (unsigned)__ffsll(b) - 1u;
     return first_key(K::lowest(), top_key, in);
-  };
-  __syncthreads();
-
-  // ---- steps: each looks at the tokens with keys from lo to hi
-  enum { ALL, COUNT, REST, MASS, DRAWN, END };
-  // ALL: a far row's bins.  COUNT: selection by number.  REST: the kept weight of tau's bin.
-  // MASS: selection by weight.  DRAWN: the chunks' kept weight of tau's bin.
-  unsigned n_all = 0;
-  w64 kept = 0, above = 0;
-  double target = 0.0;
-  unsigned tau = K::lowest(), lo = K::lowest(), hi = top_key;  // kept: keys from tau on
-  unsigned list_lo = 1, list_hi = 0;  // the keys of which the list has all tokens
-  int jt = BINS - 1, bin = 0;         // tau's bin, the bin looked at
-  bool by_k = false, by_m = false, cuts = false, whole = false;
-  const bool by_p = pol.p < 1.0f;
-  int step = far ? ALL : END;
-  bool begin = true;  // of a step
-  int next = END;
-  // Lane l has bins 2 l and 2 l + 1, and what lies in front of them.
-  w64 m0 = 0, m1 = 0, pm = 0;
-  unsigned c0 = 0, c1 = 0, pc = 0;
-  auto lane64 = [&](w64 v, int l) {
+  }
+  SVD unsigned upper_of(int j) const { return j == 0 ? top_key : first_of(j - 1) - 1u; }
+  SVD static w64 lane64(w64 v, int l) {
     return ((w64)(unsigned)__builtin_amdgcn_readlane((int)(unsigned)(v >> 32), l) << 32) | (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, l);
-  };
-  auto count_in_front = [&](int j) { return (unsigned)__builtin_amdgcn_readlane((int)(pc + ((j & 1) ? c0 : 0u)), j >> 1); };
-  auto mass_in_front = [&](int j) { return lane64(pm + ((j & 1) ? m0 : 0ull), j >> 1); };
+  }
+  SVD unsigned count_in_front(int j) const { return (unsigned)__builtin_amdgcn_readlane((int)(pc + ((j & 1) ? c0 : 0u)), j >> 1); }
+  SVD w64 mass_in_front(int j) const { return lane64(pm + ((j & 1) ? m0 : 0ull), j >> 1); }
   // The first bin up to and with which there are n tokens, or a weight of w; the last if none.
-  auto bin_by_count = [&](unsigned n) {
+  SVD int bin_by_count(unsigned n) const {
     const unsigned long long b0 = __ballot(pc + c0 >= n), b1 = __ballot(pc + c0 + c1 >= n);
     return b1 == 0 ? BINS - 1 : 2 * (__ffsll(b1) - 1) + ((b0 >> (__ffsll(b1) - 1)) & 1 ? 0 : 1);
-  };
-  auto bin_by_mass = [&](double w) {
+  }
+  SVD int bin_by_mass(double w) const {
     const unsigned long long b0 = __ballot((double)(pm + m0) >= w), b1 = __ballot((double)(pm + m0 + m1) >= w);
     return b1 == 0 ? BINS - 1 : 2 * (__ffsll(b1) - 1) + ((b0 >> (__ffsll(b1) - 1)) & 1 ? 0 : 1);
-  };
-  auto plan = [&]() {  // once the bins are known: the cuts, and what to look at first
+  }
+  SVD void prefixes() {
+    const int lane = lane_id();
     m0 = s.mass[2 * lane];
     m1 = s.mass[2 * lane + 1];
     c0 = s.count[2 * lane];
@@ -446,17 +393,19 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
     pc = ic - c0 - c1;
     n_all = (unsigned)__builtin_amdgcn_readlane((int)ic, WAVE - 1);
     kept = lane64(im, WAVE - 1);
+  }
+  // Once the bins are known: the cuts.  Returns the first step.
+  SVD int plan() {
+    prefixes();
+    tau = K::lowest();
+    jt = BINS - 1;
     by_k = pol.k > 0 && (unsigned)pol.k < n_all;
     if (pol.m > 0.0f) {
       const double xm = arg(zmax) * pol.c64;
-      auto in = [&](unsigned k) {
+      tau = near_key(K::of(fminf((float)((double)zmax + 64.0 * (double)log2f(pol.m) / pol.c64), zmax)), [&](unsigned k) {
         const double d = (arg(K::value(k)) * pol.c64 - xm) * (1.0 / 64.0);
         return d > -200.0 && pow2(d) >= (double)pol.m;
-      };
-      const unsigned g = K::of(fminf((float)((double)zmax + 64.0 * (double)log2f(pol.m) / pol.c64), zmax));
-      const unsigned l0 = max(g, K::lowest() + 32u) - 32u, h0 = min(l0 + 63u, top_key);
-      const unsigned long long b = __ballot(in(min(l0 + (unsigned)lane, h0)));
-      tau = l0 < h0 && b != 0 && !(b & 1) ? l0 + (unsigned)__ffsll(b) - 1u : first_key(K::lowest(), top_key, in);
+      });
       jt = bin_of(K::value(tau));
     }
     by_m = tau > K::lowest();
@@ -468,57 +417,327 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
       jt = bin_by_mass((double)pol.p * (double)kept);
     }
     cuts = by_k || by_m || by_p;
-    // everything from the lowest bin up that a threshold can lie in
     whole = count_in_front(jt) + s.count[jt] <= (unsigned)LIST;
-    next = by_k ? COUNT : by_m ? (by_p ? REST : DRAWN) : by_p ? MASS : DRAWN;
-  };
-  if (!far) {
-    plan();
-    step = next;
+    return by_k ? COUNT : by_m ? (by_p ? REST : DRAWN) : by_p ? MASS : DRAWN;
   }
+  // Where a step looks.
+  SVD void begin(int step, int &bin, w64 &above, double &target, unsigned &lo, unsigned &hi) {
+    if (step == COUNT) {
+      bin = bin_by_count((unsigned)pol.k);
+      above = count_in_front(bin);
+      target = (double)pol.k;
+      lo = first_of(bin);
+    } else if (step == MASS) {
+      target = (double)pol.p * (double)kept;
+      bin = min(bin_by_mass(target), by_k || by_m ? jt : BINS - 1);
+      above = mass_in_front(bin);
+      lo = max(tau, first_of(bin));
+    } else if (step == REST || step == DRAWN) {
+      bin = jt;
+      lo = tau;
+    }
+    hi = step == ALL || (step == DRAWN && far) ? top_key : upper_of(bin);
+  }
+};
+
+// ---------------------------------------------------------------- plan
+
+constexpr int PLAN_NT = 512;
+
+template <typename T, bool DRAW>
+__global__ __launch_bounds__(PLAN_NT) void k_filter_plan(const FilterArgs a) {
+  typedef Key<T> K;
+  constexpr int E = Fmt<T>::VEC, STEP = PLAN_NT / BINS, AHEAD = 8;
+  __shared__ RowShared s;
+  __shared__ int s_first;
+  const int tid = threadIdx.x;
+  const int row = blockIdx.x;
+  const ChunkSum *sums = a.sums + (size_t)row * a.chunks;
+  // thread: one bin of every fourth chunk, eight of them on their way together
+  const int b = tid % BINS;
+  w64 x[AHEAD];
+  int q[AHEAD];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = min(c0 + k * STEP, a.chunks - 1);
+      x[k] = sums[i].bin[b];
+      q[k] = sums[i].q - b;
+    }
+  };
+  load(tid / BINS);
+  Row<T> R(s, a, row);
+  RowPlan &p = a.plans[row];
+  const float u = DRAW && a.u ? a.u[row] : NAN;
+
+  if (tid < BINS) {
+    s.mass[tid] = 0;
+    s.count[tid] = 0;
+  }
+  if (tid == 0) {
+    s.flags = s.top = 0;
+    s.q = (int)0x80000000;
+    s_first = 0x7fffffff;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.chunks; i += PLAN_NT) {
+    const unsigned f = sums[i].flags, top = sums[i].top;
+    const int qi = sums[i].q;
+    if (f) atomicOr(&s.flags, f);
+    if (f & F_FINITE) {
+      atomicMax(&s.top, top);
+      atomicMax(&s.q, qi);
+    }
+  }
+  __syncthreads();
+  R.set(s.flags, key2f(s.top), s.q);
+  int code = 0;
+  if (!R.pol.ok) code = SV_ROW_BAD_POLICY;
+  else if ((R.flags & F_ODD) || !(R.flags & F_FINITE)) code = SV_ROW_BAD_LOGITS;
+  else if (DRAW && R.pol.t > 0.0f && !(u >= 0.0f && u < 1.0f)) code = SV_ROW_BAD_UNIFORM;
+  if (tid == 0) {
+    a.row_status[row] = code;
+    p.list_lo = 1;
+    p.list_hi = 0;
+    p.step = END;  // unless there is more to do
+    if (code != 0) {
+      if (DRAW) a.tokens[row] = -1;
+      else a.cut[row] = make_uint2(0u, (unsigned)-2);
+    }
+  }
+  if (code != 0) return;
+  if (R.pol.t == 0.0f) {  // greedy: the first of the largest, in the first chunk that has it
+    const RowBlocks<T> r(a.logits, row, a.V);
+    for (int i = tid; i < a.chunks; i += PLAN_NT)
+      if ((sums[i].flags & F_FINITE) && key2f(sums[i].top) == R.zmax) atomicMin(&s_first, i);
+    __syncthreads();
+    const int c = s_first;
+    __syncthreads();
+    if (tid == 0) s_first = 0x7fffffff;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < FC / E; k += PLAN_NT) {
+      const int i = c * (FC / E) + k + tid;
+      float z[E];
+      r.unpack(r.load(i), i, z);
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (z[e] == R.zmax) atomicMin(&s_first, r.index(i, e));
+    }
+    __syncthreads();
+    if (tid == 0) {
+      if (DRAW) a.tokens[row] = s_first;
+      else a.cut[row] = make_uint2(R.top_key, (unsigned)s_first);
+    }
+    return;
+  }
+  int step = ALL, bin = 0;
+  w64 above = 0;
+  double target = 0.0;
+  unsigned lo = K::lowest(), hi = R.top_key, list_lo = 1, list_hi = 0;
+  if (!R.far) {
+    for (int c0 = tid / BINS;;) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (c0 + k * STEP < a.chunks && x[k] != 0) {
+          const int j = min(R.Q - q[k], BINS - 1);
+          atomicAdd(&s.mass[j], R.mass_of_chunk(q[k], x[k]));
+          atomicAdd(&s.count[j], (unsigned)(x[k] >> W_COUNT));
+        }
+      c0 += AHEAD * STEP;
+      if (c0 >= a.chunks) break;
+      load(c0);
+    }
+    __syncthreads();
+    step = R.plan();
+    if (step != DRAWN || (DRAW && R.cuts)) {
+      R.begin(step, bin, above, target, lo, hi);
+      // all that is to come, if it fits; else this step's range, if that does
+      if (R.whole) {
+        list_lo = R.first_of(R.jt);
+        list_hi = R.top_key;
+      } else if (s.count[bin] <= (unsigned)LIST) {
+        list_lo = lo;
+        list_hi = hi;
+      }
+    }
+  }
+  for (int i = tid; i < BINS; i += PLAN_NT) {
+    p.mass[i] = s.mass[i];
+    p.count[i] = s.count[i];
+  }
+  if (tid == 0) {
+    p.above = above;
+    p.target = target;
+    p.q = R.Q;
+    p.step = step;
+    p.bin = bin;
+    p.jt = R.far ? 0 : R.jt;
+    p.flags = R.flags;
+    p.tau = R.far ? K::lowest() : R.tau;
+    p.lo = lo;
+    p.hi = hi;
+    p.list_lo = list_lo;
+    p.list_hi = list_hi;
+    p.zmax = R.zmax;
+    p.by_k = !R.far && R.by_k;
+    p.by_m = !R.far && R.by_m;
+    p.cuts = !R.far && R.cuts;
+    p.whole = !R.far && R.whole;
+  }
+}
+
+// ---------------------------------------------------------------- gather
+
+// As many workgroups as the scan had look through the row's chunks at once (one a row, in
+// k_filter_pick, 64 rows: 11 of its 35 us).
+template <typename T, bool DRAW>
+__global__ __launch_bounds__(NT) void k_filter_gather(const FilterArgs a) {
+  typedef Key<T> K;
+  constexpr int E = Fmt<T>::VEC, NV = FPT / E;
+  __shared__ w64 s_over[NW];
+  const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
+  const int row = (int)(blockIdx.x / (unsigned)a.chunks), c = (int)(blockIdx.x % (unsigned)a.chunks);
+  const RowPlan &p = a.plans[row];
+  const unsigned list_lo = p.list_lo, list_hi = p.list_hi;
+  const bool some = list_lo <= list_hi;
+  const RowBlocks<T> r(a.logits, row, a.V);
+  u32x4 w[NV];
+  if (some) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) w[k] = r.load(c * (FC / E) + k * NT + tid);
+  }
+  const int step = p.step;
+  if (step == END) return;
+  if (DRAW && step != ALL) {  // the chunk's weight in the bins above the lowest threshold's
+    const ChunkSum &cs = a.sums[(size_t)row * a.chunks + c];
+    w64 over = 0;
+    if (tid < BINS) {
+      const w64 x = cs.bin[tid];
+      const int q = cs.q - tid, Q = p.q;
+      if (!p.cuts || Q - q < p.jt) over = shifted(x & ((1ull << W_COUNT) - 1ull), a.F - W_BITS - (octave_of(Q) - octave_of(q)));
+    }
+    over = wave_total64(over);
+    if (lane == 0) s_over[wid] = over;
+    __syncthreads();
+    if (tid == 0) a.over[(size_t)row * a.chunks + c] = s_over[0] + s_over[1];
+  }
+  if (!some) return;
+  const float z_lo = K::value(list_lo), z_hi = K::value(list_hi);
+  float z[NV][E];
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    r.unpack(w[k], c * (FC / E) + k * NT + tid, z[k]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) n += __popcll(__ballot(z[k][e] >= z_lo && z[k][e] <= z_hi));
+  }
+  if (n == 0) return;
+  int o = 0;
+  if (lane == 0) o = (int)atomicAdd(&a.n_list[row], (unsigned)n);
+  o = __builtin_amdgcn_readfirstlane(o);
+  uint2 *list = a.list + (size_t)row * a.cap;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool in = z[k][e] >= z_lo && z[k][e] <= z_hi;
+      const unsigned long long b = __ballot(in);
+      const int at = o + __builtin_amdgcn_mbcnt_hi((unsigned)(b >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)b, 0u));
+      if (in && at < a.cap) list[at] = make_uint2(K::of(z[k][e]), (unsigned)((c * (FC / E) + k * NT + tid) * E + e));
+      o += __popcll(b);
+    }
+}
+
+// ---------------------------------------------------------------- pick
+
+constexpr int PICK_NT = 512;  // threads; two workgroups and their lists fit a CU
+
+struct PickShared {
+  RowShared row;
+  w64 hist[256], total, above;
+  w64 wave[PICK_NT / WAVE];
+  unsigned list_key[LIST];
+  int list_at[LIST];
+  int n_list, found;
+  unsigned key;
+};
+
+// A row is one workgroup's, and its steps follow one another: what bounds it is latency.  Each step
+// looks at the tokens with keys of a range: those that k_filter_gather put on the list, or, where a
+// later threshold lies elsewhere or a bin holds more than a list, those that a pass over the row
+// finds.
+template <typename T, bool DRAW>
+__global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) void k_filter_pick(const FilterArgs a) {
+  typedef Key<T> K;
+  constexpr int E = Fmt<T>::VEC, PW = PICK_NT / WAVE;
+  __shared__ PickShared s;
+  extern __shared__ w64 s_chunk[];  // [chunks] kept weight
+  const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
+  const int row = blockIdx.x;
+  const RowPlan &p = a.plans[row];
+  int step = p.step;
+  if (step == END) return;
+  const RowBlocks<T> r(a.logits, row, a.V);
+  const ChunkSum *sums = a.sums + (size_t)row * a.chunks;
+  Row<T> R(s.row, a, row);
+  R.set(p.flags, p.zmax, p.q);
+  int bin = p.bin;
+  w64 above = p.above;
+  double target = p.target;
+  unsigned lo = p.lo, hi = p.hi, list_lo = p.list_lo, list_hi = p.list_hi;  // the list has all tokens of its keys
+  R.tau = p.tau;
+  R.jt = p.jt;
+  R.by_k = p.by_k;
+  R.by_m = p.by_m;
+  R.cuts = p.cuts;
+  R.whole = p.whole;
+  const int over_jt = R.jt;  // the bin that a.over goes by
+  if (tid < BINS) {
+    s.row.mass[tid] = p.mass[tid];
+    s.row.count[tid] = p.count[tid];
+  }
+  if (list_lo <= list_hi) {
+    const int n = min((int)a.n_list[row], a.cap);
+    const uint2 *list = a.list + (size_t)row * a.cap;
+    for (int i = tid; i < n; i += PICK_NT) {
+      const uint2 x = list[i];
+      s.list_key[i] = x.x;
+      s.list_at[i] = (int)x.y;
+    }
+    if (tid == 0) s.n_list = n;
+  }
+  powers(s.row.tab);
+  __syncthreads();
+  R.prefixes();
+  bool begin = R.far || step == DRAWN;  // of a step: the gather has begun the others
   for (;;) {
     if (begin) {
       begin = false;
       if (step == DRAWN && !DRAW) step = END;
       if (step == DRAWN) {
-        for (int c = tid; c < a.chunks; c += PNT) s_chunk[c] = 0;
-        if (!cuts && !far) step = END;  // the bins are enough
+        const bool ready = !R.far && R.jt == over_jt;
+        for (int c = tid; c < a.chunks; c += PICK_NT) s_chunk[c] = ready ? a.over[(size_t)row * a.chunks + c] : 0ull;
+        if (!R.cuts && !R.far) step = END;  // the bins are enough
       }
       if (step == END) break;
-      if (step == COUNT) {
-        bin = bin_by_count((unsigned)pol.k);
-        above = count_in_front(bin);
-        target = (double)pol.k;
-        lo = first_of(bin);
-      } else if (step == REST) {
-        bin = jt = bin_of(K::value(tau));
-        lo = tau;
-      } else if (step == MASS) {
-        target = (double)pol.p * (double)kept;
-        bin = min(bin_by_mass(target), by_k || by_m ? jt : BINS - 1);
-        above = mass_in_front(bin);
-        lo = max(tau, first_of(bin));
-      } else if (step == DRAWN) {
-        bin = jt;
-        lo = tau;
-      }
-      hi = bin == 0 || step == ALL || (step == DRAWN && far) ? top_key : first_of(bin - 1) - 1u;
+      R.begin(step, bin, above, target, lo, hi);
     }
     const unsigned span = hi - lo;
     const int bits = 32 - __clz((int)(span | 1u)), sh = bits > 8 ? bits - 8 : 0;
-    for (int i = tid; i < 256; i += PNT) s.hist[i] = 0;
+    for (int i = tid; i < 256; i += PICK_NT) s.hist[i] = 0;
     if (tid == 0) s.total = 0;
 
     auto look = [&](int n) {  // at the first n of the list
       w64 part = 0;
-      for (int i = tid; i < n; i += PNT) {
+      for (int i = tid; i < n; i += PICK_NT) {
         const unsigned k = s.list_key[i];
         if (k < lo || k > hi) continue;
         if (step == COUNT) {
           atomicAdd(&s.hist[(k - lo) >> sh], 1ull);
         } else {
           int j;
-          const w64 w = weight(K::value(k), j);
+          const w64 w = R.weight(K::value(k), j);
           if (step == MASS) {
             atomicAdd(&s.hist[(k - lo) >> sh], w);
           } else if (step == REST) {
@@ -526,8 +745,8 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
           } else if (step == DRAWN) {
             atomicAdd(&s_chunk[s.list_at[i] / FC], w);
           } else {
-            atomicAdd(&s.mass[j], w);
-            atomicAdd(&s.count[j], 1u);
+            atomicAdd(&s.row.mass[j], w);
+            atomicAdd(&s.row.count[j], 1u);
           }
         }
       }
@@ -535,9 +754,10 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
     };
     if (lo < list_lo || hi > list_hi) {  // gather
       // all that is to come, if it fits; else this step's range, in pieces where that does not fit
-      const unsigned g_lo = whole && step != ALL ? first_of(jt) : lo, g_hi = whole && step != ALL ? top_key : hi;
-      const bool fits = step != ALL && (whole || (!far && s.count[bin] <= (unsigned)LIST));
+      const unsigned g_lo = R.whole && step != ALL ? R.first_of(R.jt) : lo, g_hi = R.whole && step != ALL ? R.top_key : hi;
+      const bool fits = step != ALL && (R.whole || (!R.far && s.row.count[bin] <= (unsigned)LIST));
       const float z_lo = K::value(g_lo), z_hi = K::value(g_hi);
+      __syncthreads();
       if (tid == 0) s.n_list = 0;
       __syncthreads();
       auto add = [&](const u32x4 &w, int i) {
@@ -566,19 +786,19 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
       };
       if (fits) {
         constexpr int AHEAD = 8;
-        for (int i0 = tid; i0 - tid < r.n; i0 += AHEAD * PNT) {
+        for (int i0 = tid; i0 - tid < r.n; i0 += AHEAD * PICK_NT) {
           u32x4 w[AHEAD];
 #pragma unroll
-          for (int k = 0; k < AHEAD; ++k) w[k] = r.load(i0 + k * PNT);
+          for (int k = 0; k < AHEAD; ++k) w[k] = r.load(i0 + k * PICK_NT);
 #pragma unroll
-          for (int k = 0; k < AHEAD; ++k) add(w[k], i0 + k * PNT);
+          for (int k = 0; k < AHEAD; ++k) add(w[k], i0 + k * PICK_NT);
         }
         list_lo = g_lo;
         list_hi = g_hi;
       } else {
         list_lo = 1;
         list_hi = 0;
-        for (int i0 = tid; i0 - tid < r.n; i0 += PNT) {
+        for (int i0 = tid; i0 - tid < r.n; i0 += PICK_NT) {
           add(r.load(i0), i0);
           __syncthreads();
           look(s.n_list);
@@ -593,13 +813,12 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
     __syncthreads();
 
     if (step == ALL) {
-      plan();
-      step = next;
+      step = R.plan();
       begin = true;
     } else if (step == REST) {
-      kept = s.total + mass_in_front(jt);
+      R.kept = s.total + R.mass_in_front(R.jt);
       __syncthreads();
-      step = by_p ? MASS : DRAWN;
+      step = R.by_p ? MASS : DRAWN;
       begin = true;
     } else if (step == DRAWN) {
       break;
@@ -632,13 +851,13 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
         const unsigned long long b = __ballot(pick >= 0), any = __ballot(some >= 0);
         const int l = b != 0 ? __ffsll(b) - 1 : any != 0 ? 63 - __clzll((long long)any) : 63;
         if (lane == l) {  // where the target is all there is, up to its rounding: the lowest
-          s.key[0] = (unsigned)(b != 0 ? pick : max(some, 0));
+          s.key = (unsigned)(b != 0 ? pick : max(some, 0));
           s.above = b != 0 ? over : below_some;
           s.total = b != 0 ? upto : run;
         }
       }
       __syncthreads();
-      const unsigned pick = s.key[0];
+      const unsigned pick = s.key;
       above = s.above;
       const w64 upto = s.total;
       __syncthreads();
@@ -647,36 +866,36 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
       if (sh == 0) {
         begin = true;
         if (step == COUNT) {
-          tau = max(tau, lo);
-          jt = bin_of(K::value(tau));
-          step = by_p ? REST : DRAWN;
+          R.tau = max(R.tau, lo);
+          R.jt = R.bin_of(K::value(R.tau));
+          step = R.by_p ? REST : DRAWN;
         } else {
-          tau = lo;
-          jt = bin;
-          kept = upto;
+          R.tau = lo;
+          R.jt = bin;
+          R.kept = upto;
           step = DRAWN;
         }
       }
     }
   }
   if (!DRAW) {
-    if (tid == 0) a.cut[row] = make_uint2(tau, (unsigned)-1);
+    if (tid == 0) a.cut[row] = make_uint2(R.tau, (unsigned)-1);
     return;
   }
 
-  // ---- the chunks' kept weights: bins above tau's from the scan, besides
+  // ---- the chunks' kept weights: bins above tau's from the scan, where the gather went by another
   __syncthreads();
-  if (!far)
-    for (int i = tid; i < a.chunks * BINS; i += PNT) {
+  if (!R.far && R.jt != over_jt)
+    for (int i = tid; i < a.chunks * BINS; i += PICK_NT) {
       const ChunkSum &cs = sums[i / BINS];
       const w64 x = cs.bin[i % BINS];
-      if (x == 0) continue;
-      const int q = cs.q - i % BINS, j = min(Q - q, BINS - 1);
-      if (cuts && j >= jt) continue;
-      const w64 m = shifted(x & ((1ull << W_COUNT) - 1ull), a.F - W_BITS - (O - octave_of(q)));
+      const int q = cs.q - i % BINS;
+      if (x == 0 || (R.cuts && min(R.Q - q, BINS - 1) >= R.jt)) continue;
+      const w64 m = R.mass_of_chunk(q, x);
       if (m) atomicAdd(&s_chunk[i / BINS], m);
     }
   __syncthreads();
+  const float u = a.u[row];
   if (wid == 0) {  // the first chunk whose cumulative weight passes the target
     w64 total = 0;
     for (int c0 = 0; c0 < a.chunks; c0 += WAVE) total += wave_total64(c0 + lane < a.chunks ? s_chunk[c0 + lane] : 0ull);
@@ -686,19 +905,16 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
     for (int c0 = 0; c0 < a.chunks && pick < 0; c0 += WAVE) {
       const w64 w = c0 + lane < a.chunks ? s_chunk[c0 + lane] : 0ull, inc = wave_incl(w);
       const unsigned long long b = __ballot(w != 0 && (double)(run + inc) > t), some = __ballot(w != 0);
-      auto at = [&](w64 v, int l) {
-        return ((w64)(unsigned)__builtin_amdgcn_readlane((int)(unsigned)(v >> 32), l) << 32) | (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, l);
-      };
       if (b != 0) {
         const int l = __ffsll(b) - 1;
         pick = c0 + l;
-        before = run + at(inc - w, l);
+        before = run + R.lane64(inc - w, l);
       } else if (some != 0) {
         const int l = 63 - __clzll((long long)some);
         fallback = c0 + l;
-        fb = run + at(inc - w, l);
+        fb = run + R.lane64(inc - w, l);
       }
-      run += at(inc, WAVE - 1);
+      run += R.lane64(inc, WAVE - 1);
     }
     if (lane == 0) {
       s.n_list = pick >= 0 ? pick : fallback;
@@ -713,7 +929,7 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
   w64 base = s.above;
   // ---- the token: the chunk's kept weights in index order
   constexpr int STEP = FC / E;
-  for (int k = 0; k < STEP; k += PNT) {
+  for (int k = 0; k < STEP; k += PICK_NT) {
     const int i = c * STEP + k + tid;
     w64 w[E], sum = 0;
     float z[E];
@@ -721,12 +937,12 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       int j;
-      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= tau ? weight(z[e], j) : 0ull;
+      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= R.tau ? R.weight(z[e], j) : 0ull;
       sum += w[e];
     }
     const w64 inc = wave_incl(sum);
     if (lane == WAVE - 1) s.wave[wid] = inc;
-    if (tid == 0) s.key[0] = 0x7fffffffu;
+    if (tid == 0) s.key = 0x7fffffffu;
     __syncthreads();
     w64 run = base, all = 0;
     for (int v = 0; v < PW; ++v) {
@@ -743,14 +959,14 @@ __global__ __launch_bounds__(PNT) __attribute__((amdgpu_waves_per_eu(4))) void k
         if (pick < 0 && (double)run > goal) pick = last;
       }
     }
-    if (pick >= 0) atomicMin(&s.key[0], (unsigned)pick);
+    if (pick >= 0) atomicMin(&s.key, (unsigned)pick);
     if (last >= 0) atomicMax(&s.found, last);  // in case rounding leaves none
     base += all;
     __syncthreads();
-    if (s.key[0] != 0x7fffffffu) break;
+    if (s.key != 0x7fffffffu) break;
     __syncthreads();
   }
-  if (tid == 0) a.tokens[row] = s.key[0] != 0x7fffffffu ? (int)s.key[0] : s.found;
+  if (tid == 0) a.tokens[row] = s.key != 0x7fffffffu ? (int)s.key : s.found;
 }
 
 // ---------------------------------------------------------------- write
@@ -811,16 +1027,21 @@ using sv_host::align256;
 using sv_host::Launcher;
 
 struct FilterPlan {
-  int chunks;
-  size_t sums, cut, total;
+  int chunks, cap;
+  size_t sums, plans, over, n_list, list, cut, total;
 };
 bool filter_plan(int32_t rows, int32_t V, int esz, FilterPlan &p) {
   if (rows < 1 || V < 1 || V > SV_FILTER_MAX_V) return false;
   const int E = 16 / esz;
   p.chunks = (int)(((long long)V + E - 1 + FC - 1) / FC);  // a row may begin anywhere in a block
-  if ((long long)rows * p.chunks > 0xffffffffLL / NT || rows > 0xffffffffLL / 1024) return false;
+  if ((long long)rows * p.chunks > 0xffffffffLL / NT || rows > 0xffffffffLL / PICK_NT) return false;
   size_t o = 0;
   p.sums = o; o = align256(o + (size_t)rows * p.chunks * sizeof(ChunkSum));
+  p.plans = o; o = align256(o + (size_t)rows * sizeof(RowPlan));
+  p.over = o; o = align256(o + (size_t)rows * p.chunks * 8);
+  p.n_list = o; o = align256(o + (size_t)rows * 4);
+  p.cap = V < LIST ? V : LIST;
+  p.list = o; o = align256(o + (size_t)rows * p.cap * 8);
   p.cut = o; o = align256(o + (size_t)rows * 8);
   p.total = o;
   return true;
@@ -857,6 +1078,11 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   a.F = 60 - bits < 48 ? 60 - bits : 48;
   a.policy = *pol;
   a.sums = (ChunkSum *)(base + p.sums);
+  a.plans = (RowPlan *)(base + p.plans);
+  a.over = (w64 *)(base + p.over);
+  a.n_list = (unsigned *)(base + p.n_list);
+  a.list = (uint2 *)(base + p.list);
+  a.cap = p.cap;
   a.cut = (uint2 *)(base + p.cut);
   a.tokens = tokens;
   a.row_status = status;
@@ -865,22 +1091,21 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   Launcher L{(hipStream_t)stream, ev, nev};
   const unsigned grid = (unsigned)((long long)rows * p.chunks);
   L.go(esz == 2 ? (const void *)&k_filter_scan<uint16_t> : (const void *)&k_filter_scan<float>, grid, args);
-  // Up to a row for each CU a workgroup of 1024 threads, beyond that two of 512 on a CU.
-  const bool wide = rows <= 256;
-  L.block = wide ? 1024 : 512;
+  auto go = [&](const void *h, const void *f, unsigned n) { L.go(esz == 2 ? h : f, n, args); };
+  L.block = PLAN_NT;
+  if (draw) go((const void *)&k_filter_plan<uint16_t, true>, (const void *)&k_filter_plan<float, true>, (unsigned)rows);
+  else go((const void *)&k_filter_plan<uint16_t, false>, (const void *)&k_filter_plan<float, false>, (unsigned)rows);
+  L.block = NT;
+  if (draw) go((const void *)&k_filter_gather<uint16_t, true>, (const void *)&k_filter_gather<float, true>, grid);
+  else go((const void *)&k_filter_gather<uint16_t, false>, (const void *)&k_filter_gather<float, false>, grid);
+  L.block = PICK_NT;
   L.lds = draw ? (unsigned)p.chunks * 8 : 0;
-  auto pick = [&](auto t, auto d) -> const void * {
-    typedef decltype(t) T;
-    constexpr bool D = decltype(d)::value;
-    return wide ? (const void *)&k_filter_pick<T, D, 1024> : (const void *)&k_filter_pick<T, D, 512>;
-  };
-  const std::true_type yes;
-  const std::false_type no;
-  L.go(esz == 2 ? (draw ? pick(uint16_t{}, yes) : pick(uint16_t{}, no)) : (draw ? pick(0.0f, yes) : pick(0.0f, no)), (unsigned)rows, args);
+  if (draw) go((const void *)&k_filter_pick<uint16_t, true>, (const void *)&k_filter_pick<float, true>, (unsigned)rows);
+  else go((const void *)&k_filter_pick<uint16_t, false>, (const void *)&k_filter_pick<float, false>, (unsigned)rows);
   if (!draw) {
     L.block = NT;
     L.lds = 0;
-    L.go(esz == 2 ? (const void *)&k_filter_write<uint16_t> : (const void *)&k_filter_write<float>, grid, args);
+    go((const void *)&k_filter_write<uint16_t>, (const void *)&k_filter_write<float>, grid);
   }
   if (nl) *nl = L.n;
   return L.e == hipSuccess ? SV_OK : SV_ERR_LAUNCH;
@@ -910,6 +1135,6 @@ sv_status spec_filter_logits(const void *logits, sv_dtype dtype, int32_t rows, i
                     n_events, n_launched);
 }
 
-const char *sv_filter_launch_plan(int32_t draw) { return draw ? "k_filter_scan;k_filter_pick" : "k_filter_scan;k_filter_pick;k_filter_write"; }
+const char *sv_filter_launch_plan(int32_t draw) { return draw ? "k_filter_scan;k_filter_plan;k_filter_gather;k_filter_pick" : "k_filter_scan;k_filter_plan;k_filter_gather;k_filter_pick;k_filter_write"; }
 
 }  // extern "C"

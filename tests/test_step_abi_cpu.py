@@ -168,8 +168,8 @@ def test_sizes_and_plans(lib):
     assert sv.sv_attention4_launch_plan(32, 32, 8, 100) == []
     small, large = sv.sv_filter_workspace_bytes(1, 1, sv.SV_F32), sv.sv_filter_workspace_bytes(64, 128256, sv.SV_BF16)
     assert 256 < small < large and sv.sv_filter_workspace_bytes(0, 5, sv.SV_F32) == 256 and sv.sv_filter_workspace_bytes(1, 5, 9) == 256
-    assert sv.sv_filter_launch_plan(True) == ["k_filter_scan", "k_filter_pick"]
-    assert sv.sv_filter_launch_plan(False) == ["k_filter_scan", "k_filter_pick", "k_filter_write"]
+    assert sv.sv_filter_launch_plan(True) == ["k_filter_scan", "k_filter_plan", "k_filter_gather", "k_filter_pick"]
+    assert sv.sv_filter_launch_plan(False) == ["k_filter_scan", "k_filter_plan", "k_filter_gather", "k_filter_pick", "k_filter_write"]
 
 
 def test_binding_refuses_what_is_not_on_the_device():
