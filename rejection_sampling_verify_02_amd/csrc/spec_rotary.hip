@@ -27,6 +27,7 @@ struct RotaryArgs {
 // Tokens of a workgroup: whole units of values (8 slots of bf16, 4 of f32), so that a unit has
 // one writer.
 constexpr int ROT_TOKENS = 8;
+constexpr int F4_LDS = 8192;  // floats of turned keys on their way to 4 bits
 
 // cos t and sin t of t = n * f, in 64 bits: the product of a whole number and a float, rounded
 // once; a quarter turn's multiple taken off in two parts (the first exactly, in the fused
@@ -81,6 +82,27 @@ struct Unit {  // 16 bytes of elements
   }
 };
 
+// E units of E elements turned: element j of unit i becomes element i of unit j.
+template <typename T>
+SVD void transpose(u32x4 (&w)[Unit<T>::E]) {
+  constexpr int E = Unit<T>::E;
+  u32x4 r[E];
+  if constexpr (E == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = u32x4{w[0][i], w[1][i], w[2][i], w[3][i]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // words i: elements 2 i and 2 i + 1
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[2 * i][j] = __builtin_amdgcn_perm(w[2 * j + 1][i], w[2 * j][i], 0x05040100u);
+        r[2 * i + 1][j] = __builtin_amdgcn_perm(w[2 * j + 1][i], w[2 * j][i], 0x07060302u);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) w[i] = r[i];
+}
+
 // x and y of a pair turned.
 SVD void turned(float &x, float &y, const double2 cs) {
   const double a = x, b = y;
@@ -88,9 +110,14 @@ SVD void turned(float &x, float &y, const double2 cs) {
   y = (float)fma(b, cs.x, a * cs.y);
 }
 
+// Where pair j's cosine and sine lie among a token's in LDS: a gap behind every four, so that lanes
+// that read neighbouring units' pairs meet in no bank.
+SV_HD int cs_at(int j) { return j + (j >> 2); }
+SV_HD int cs_row(int pairs) { return cs_at(pairs) + 1; }
+
 // Element d of a head at p, turned: for heads whose pairs do not lie unit against unit.
 template <typename T>
-SVD float turned_one(const char *p, int d, int R, const double2 *cs) {
+SVD float turned_one(const char *p, int d, int R, const double2 *cs) {  // cs: of the token
   const T *x = reinterpret_cast<const T *>(p);
   float a = Fmt<T>::at(x, d);
   if (d >= R) return a;
@@ -98,9 +125,9 @@ SVD float turned_one(const char *p, int d, int R, const double2 *cs) {
   const bool second = d >= h;
   float b = Fmt<T>::at(x, second ? d - h : d + h);
   if (second) {
-    turned(b, a, cs[d - h]);
+    turned(b, a, cs[cs_at(d - h)]);
   } else {
-    turned(a, b, cs[d]);
+    turned(a, b, cs[cs_at(d)]);
   }
   return a;
 }
@@ -130,34 +157,82 @@ SVD int rotary_code(const RotaryArgs &a, int b, int len, int m, uint16_t *s_par)
 // T: the inputs' type; F4: the cache is in 4 bits; PAIRS: pairs lie unit against unit (neighbours
 // interleaved, or halves of whole units), so that a thread turns 16 bytes and their partners.
 template <typename T, bool F4, bool PAIRS>
-__global__ __launch_bounds__(NT) void k_append_rotary(const RotaryArgs a) {
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_append_rotary(const RotaryArgs a) {
   constexpr int E = Unit<T>::E, ESZ = (int)sizeof(T);
-  extern __shared__ double2 s_cs[];  // [tokens][R / 2], then the parents
-  uint16_t *s_par = reinterpret_cast<uint16_t *>(s_cs + ROT_TOKENS * (a.R / 2));
+  extern __shared__ double2 s_cs[];  // [tokens][cs_row], then the parents
   const int tid = threadIdx.x;
   const int part = (int)(blockIdx.x % (unsigned)a.parts);
   const unsigned bc = blockIdx.x / (unsigned)a.parts;
   const int chunk = (int)(bc % (unsigned)a.chunks), b = (int)(bc / (unsigned)a.chunks);
   const int m = a.n_new ? a.n_new[b] : a.N;
   int len = a.cache_len[b];
-  const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D, Hkv = (int)a.pool.Hkv, H2 = a.R / 2;
+  const int sh = a.pool.page_shift, page = 1 << sh, D = (int)a.pool.D, Hkv = (int)a.pool.Hkv, H2 = a.R / 2, CS = cs_row(H2), U = D / E;
+  uint16_t *s_par = reinterpret_cast<uint16_t *>(s_cs + ROT_TOKENS * CS);
   const int32_t *table = a.page_table + (size_t)b * a.pool.W;
-  const int code = rotary_code(a, b, len, m, s_par);
-  if (chunk == 0 && part == 0 && tid == 0) a.row_status[b] = code;
-  if (code != 0) len = 0;
-
-  const int c0 = (len / ROT_TOKENS + chunk) * ROT_TOKENS;
-  const int i0 = max(0, c0 - len), i1 = min(a.N, c0 + ROT_TOKENS - len);  // the workgroup's tokens
-  if (i0 >= i1) return;
-  const int live = code != 0 ? i0 : min(max(m, i0), i1);  // tokens from here on are not new
+  // The workgroup's tokens: those whose slots are in the chunk'th eight from the sequence's first on.
+  auto first_token = [&](int l) { return max(0, chunk * ROT_TOKENS - (l & (ROT_TOKENS - 1))); };
+  auto last_token = [&](int l) { return min(a.N, (chunk + 1) * ROT_TOKENS - (l & (ROT_TOKENS - 1))); };
+  int i0 = first_token(len), i1 = last_token(len);
   // The part's heads of the queries, and of the keys and values.
   const int q0 = (int)((long long)a.Hq * part / a.parts), q1 = (int)((long long)a.Hq * (part + 1) / a.parts);
   const int h0 = (int)((long long)Hkv * part / a.parts), h1 = (int)((long long)Hkv * (part + 1) / a.parts);
-  const int U = D / E;
 
+  // Queries, and the keys of a cache of the inputs' type, in jobs: 16 bytes and, where the head's
+  // halves are turned against each other, their partners, of up to NB tokens.  A job's loads are on
+  // their way while the one before it is turned, the first one's while the sequence is checked.
+  constexpr int NB = 2;
+  const int HU = PAIRS && !a.interleaved ? H2 / E : 0;  // units of a half
+  const int items = U - HU, n_q = q1 - q0, n_heads = n_q + (F4 ? 0 : h1 - h0);
+  struct Job {
+    const char *p;
+    long long stride;
+    int h, y, t0;
+  };
+  auto job_at = [&](int j) {
+    Job o;
+    const int batch = j / (n_heads * items), x = j - batch * (n_heads * items);
+    o.t0 = batch * NB;
+    o.h = x / items;
+    o.y = x - o.h * items;
+    const bool q = o.h < n_q;
+    o.stride = q ? a.q_sn : a.k_sn;
+    o.p = (q ? a.q + (long long)b * a.q_sb + (size_t)(q0 + o.h) * D * ESZ : a.k + (long long)b * a.k_sb + (size_t)(h0 + o.h - n_q) * D * ESZ) +
+          (long long)(i0 + o.t0) * o.stride;
+    return o;
+  };
+  auto load = [&](const Job &o, int n, u32x4 (&lw)[NB], u32x4 (&lv)[NB]) {
+#pragma unroll
+    for (int t = 0; t < NB; ++t)
+      if (t == 0 || o.t0 + t < n) {
+        lw[t] = *reinterpret_cast<const u32x4 *>(o.p + t * o.stride + (o.y < HU ? o.y : o.y + HU) * 16);
+        if (o.y < HU) lv[t] = *reinterpret_cast<const u32x4 *>(o.p + t * o.stride + (o.y + HU) * 16);
+      }
+  };
+  u32x4 lw[NB], lv[NB];
+  Job job = {};
+  int jobs = 0;
+  auto prefetch = [&]() {
+    jobs = i0 < i1 ? n_heads * items * ((i1 - i0 + NB - 1) / NB) : 0;
+    if constexpr (PAIRS)
+      if (tid < jobs) {
+        job = job_at(tid);
+        load(job, i1 - i0, lw, lv);
+      }
+  };
+  prefetch();  // (rows of tokens are there whatever the sequence's length says)
+
+  const int code = rotary_code(a, b, len, m, s_par);
+  if (chunk == 0 && part == 0 && tid == 0) a.row_status[b] = code;
+  if (code != 0) {
+    len = 0;
+    i0 = first_token(0);
+    i1 = last_token(0);
+  }
+  if (i0 >= i1) return;
+  const int live = code != 0 ? i0 : min(max(m, i0), i1);  // tokens from here on are not new
   if (live < i1) {  // queries of no token: zero, or NaN for a sequence with a code
     const unsigned fill = code == 0 ? 0u : ESZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
-    const int n = (q1 - q0) * U;
+    const int n = n_q * U;
     for (int x = tid; x < (i1 - live) * n; x += NT)
       *reinterpret_cast<u32x4 *>(a.q_out + (((size_t)b * a.N + live + x / n) * a.Hq + q0) * D * ESZ + (size_t)(x % n) * 16) =
           u32x4{fill, fill, fill, fill};
@@ -176,144 +251,204 @@ __global__ __launch_bounds__(NT) void k_append_rotary(const RotaryArgs a) {
     }
     double2 cs;
     turn_of(pos, a.inv_freq[j], a.factor, cs.x, cs.y);
-    s_cs[x] = cs;
+    s_cs[t * CS + cs_at(j)] = cs;
   }
   __syncthreads();
 
-  // Queries, and the keys of a cache of the inputs' type: 16 bytes and, where the head's halves
-  // are turned against each other, their partners.  put(head, unit, bytes)
-  auto heads = [&](const char *src, int n_heads, const double2 *cs, auto put) {
-    const int HU = a.interleaved || H2 == 0 ? 0 : H2 / E;  // units of a half
-    const int items = PAIRS ? U - HU : U;
-    for (int x = tid; x < n_heads * items; x += NT) {
-      const int h = x / items, y = x - h * items;
-      const char *p = src + (size_t)h * D * ESZ;
-      if constexpr (!PAIRS) {
-        Unit<T> w;
+  // The workgroup's slots lie in one page (8 slots from a multiple of 8 on).
+  const size_t ph0 = (size_t)table[(len + i0) >> sh] * Hkv;
+  const int at0 = (len + i0) & (page - 1);  // the first slot in it
+
+  char *qo = a.q_out + (((size_t)b * a.N + i0) * a.Hq + q0) * D * ESZ;
+  const size_t hb = head_bytes<T>(a.pool);  // of a cache of the inputs' type
+  char *ko = a.k_pages + (ph0 + h0) * hb + (size_t)at0 * 16;
+  auto put = [&](int t, int h, int u, u32x4 w) {
+    char *o = h < n_q ? qo + ((size_t)t * a.Hq + h) * D * ESZ + u * 16 : ko + (size_t)(h - n_q) * hb + ((size_t)u * page + t) * 16;
+    *reinterpret_cast<u32x4 *>(o) = w;
+  };
+  if constexpr (PAIRS) {
+    for (int j = tid; j < jobs; j += NT) {
+      u32x4 nw[NB], nv[NB];
+      Job after = job;
+      if (j + NT < jobs) {
+        after = job_at(j + NT);
+        load(after, nt, nw, nv);
+      }
 #pragma unroll
-        for (int e = 0; e < E; ++e) w.x[e] = turned_one<T>(p, y * E + e, a.R, cs);
-        put(h, y, w.pack());
-      } else if (y < HU) {
-        Unit<T> w, v;
-        w.load(p + y * 16);
-        v.load(p + (y + HU) * 16);
+      for (int t = 0; t < NB; ++t)
+        if (job.t0 + t < nt) {
+          const double2 *cs = s_cs + (job.t0 + t) * CS;
+          Unit<T> w, v;
+          Fmt<T>::unpack(lw[t], w.x);
+          if (job.y < HU) {
+            Fmt<T>::unpack(lv[t], v.x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) turned(w.x[e], v.x[e], cs[y * E + e]);
-        put(h, y, w.pack());
-        put(h, y + HU, v.pack());
-      } else {
-        const int u = y + HU;
-        Unit<T> w;
-        w.load(p + u * 16);
-        if (a.interleaved)
+            for (int e = 0; e < E; ++e) turned(w.x[e], v.x[e], cs[cs_at(job.y * E + e)]);
+            put(job.t0 + t, job.h, job.y + HU, v.pack());
+          } else if (a.interleaved) {
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e)
-            if (u * E + 2 * e < a.R) turned(w.x[2 * e], w.x[2 * e + 1], cs[u * E / 2 + e]);
-        put(h, u, w.pack());
+            for (int e = 0; e < E / 2; ++e)
+              if (job.y * E + 2 * e < a.R) turned(w.x[2 * e], w.x[2 * e + 1], cs[cs_at(job.y * (E / 2) + e)]);
+          }
+          put(job.t0 + t, job.h, job.y < HU ? job.y : job.y + HU, w.pack());
+        }
+      job = after;
+#pragma unroll
+      for (int t = 0; t < NB; ++t) {
+        lw[t] = nw[t];
+        lv[t] = nv[t];
       }
     }
-  };
-  for (int t = 0; t < nt; ++t) {
-    const int i = i0 + t, s = len + i;
-    const double2 *cs = s_cs + t * H2;
-    char *qo = a.q_out + (((size_t)b * a.N + i) * a.Hq + q0) * D * ESZ;
-    heads(a.q + (long long)b * a.q_sb + (long long)i * a.q_sn + (size_t)q0 * D * ESZ, q1 - q0, cs, [&](int h, int u, u32x4 w) {
-      *reinterpret_cast<u32x4 *>(qo + (size_t)h * D * ESZ + u * 16) = w;
-    });
-    if constexpr (!F4) {
-      const size_t hb = head_bytes<T>(a.pool);
-      char *kp = a.k_pages + ((size_t)table[s >> sh] * Hkv + h0) * hb + (size_t)(s & (page - 1)) * 16;
-      heads(a.k + (long long)b * a.k_sb + (long long)i * a.k_sn + (size_t)h0 * D * ESZ, h1 - h0, cs, [&](int h, int u, u32x4 w) {
-        *reinterpret_cast<u32x4 *>(kp + (size_t)h * hb + (size_t)u * page * 16) = w;
-      });
+  } else {
+    for (int x = tid; x < n_heads * U * nt; x += NT) {
+      const int t = x / (n_heads * U), hy = x - t * (n_heads * U), h = hy / U, y = hy - h * U;
+      const char *p = h < n_q ? a.q + (long long)b * a.q_sb + (long long)(i0 + t) * a.q_sn + (size_t)(q0 + h) * D * ESZ
+                              : a.k + (long long)b * a.k_sb + (long long)(i0 + t) * a.k_sn + (size_t)(h0 + h - n_q) * D * ESZ;
+      Unit<T> w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) w.x[e] = turned_one<T>(p, y * E + e, a.R, s_cs + t * CS);
+      put(t, h, y, w.pack());
     }
   }
   if constexpr (!F4) {
-    // values: a thread gathers the E slots of one d (as k_cache_append does)
-    const int s0 = len + i0, s1 = len + live, u0 = s0 / E, u1 = (s1 - 1) / E;
-    const size_t hb = head_bytes<T>(a.pool);
-    for (int h = h0; h < h1; ++h)
-      for (int x = tid; x < (u1 - u0 + 1) * D; x += NT) {
-        const int u = u0 + x / D, d = x % D, f = u * E;
-        T e[E];
+    // values: a whole unit of slots, E tokens, is turned in registers; of others single elements
+    const int s0 = len + i0, s1 = len + live;
+    for (int x = tid; x < (h1 - h0) * U; x += NT) {
+      const int h = x / U, u = x - h * U;
+      for (int f = s0 / E * E; f < s1; f += E) {
+        const char *vs = a.v + (long long)b * a.v_sb + (long long)(f - len) * a.v_sn + ((size_t)(h0 + h) * D + u * E) * ESZ;
+        char *out = a.v_pages + (ph0 + h0 + h) * hb + ((size_t)((f & (page - 1)) / E) * D + u * E) * 16;
+        u32x4 w[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int s = min(max(f + j, s0), s1 - 1);
-          e[j] = *reinterpret_cast<const T *>(a.v + (long long)b * a.v_sb + (long long)(s - len) * a.v_sn + ((size_t)h * D + d) * sizeof(T));
-        }
-        T *out = reinterpret_cast<T *>(a.v_pages + ((size_t)table[f >> sh] * Hkv + h) * hb + ((size_t)((f & (page - 1)) / E) * D + d) * 16);
+        for (int j = 0; j < E; ++j) w[j] = *reinterpret_cast<const u32x4 *>(vs + (long long)(min(max(f + j, s0), s1 - 1) - f) * a.v_sn);
         if (f >= s0 && f + E <= s1) {
-          u32x4 w;
-          __builtin_memcpy(&w, e, 16);
-          *reinterpret_cast<u32x4 *>(out) = w;
+          transpose<T>(w);
+#pragma unroll
+          for (int j = 0; j < E; ++j) *reinterpret_cast<u32x4 *>(out + j * 16) = w[j];
         } else {
 #pragma unroll
           for (int j = 0; j < E; ++j)
-            if (f + j >= s0 && f + j < s1) out[j] = e[j];
-        }
-      }
-  } else {
-    // blocks of 32 elements, a thread each: keys, then values
-    const int G = D / F4_BLOCK, n = nt * (h1 - h0) * G, B = D / 32;
-    for (int x = tid; x < 2 * n; x += NT) {
-      const bool val = x >= n;
-      const int y = val ? x - n : x, u = y % G, th = y / G, t = th / (h1 - h0), h = h0 + th % (h1 - h0);
-      const int i = i0 + t, s = len + i, at = s & (page - 1);
-      const double2 *cs = s_cs + t * H2;
-      const char *p = val ? a.v + (long long)b * a.v_sb + (long long)i * a.v_sn + (size_t)h * D * ESZ
-                          : a.k + (long long)b * a.k_sb + (long long)i * a.k_sn + (size_t)h * D * ESZ;
-      float f[F4_BLOCK];
-      if (val || PAIRS || u * F4_BLOCK >= a.R) {
+            if (f + j >= s0 && f + j < s1) {
+              T e[E];
+              __builtin_memcpy(e, &w[j], 16);
 #pragma unroll
-        for (int j = 0; j < F4_BLOCK / E; ++j) {
-          Unit<T> w;
-          w.load(p + (u * (F4_BLOCK / E) + j) * 16);
-#pragma unroll
-          for (int e = 0; e < E; ++e) f[j * E + e] = w.x[e];
-        }
-      }
-      if (!val && u * F4_BLOCK < a.R) {
-        if constexpr (PAIRS) {
-          if (a.interleaved) {
-#pragma unroll
-            for (int e = 0; e < F4_BLOCK / 2; ++e)
-              if (u * F4_BLOCK + 2 * e < a.R) turned(f[2 * e], f[2 * e + 1], cs[u * (F4_BLOCK / 2) + e]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < F4_BLOCK / E; ++j) {  // a unit lies in one half
-              const int d = u * F4_BLOCK + j * E;
-              if (d >= a.R) continue;
-              const bool second = d >= H2;
-              Unit<T> w;
-              w.load(p + (second ? d - H2 : d + H2) * ESZ);
-#pragma unroll
-              for (int e = 0; e < E; ++e) {
-                float o = w.x[e];
-                if (second) turned(o, f[j * E + e], cs[d - H2 + e]);
-                else turned(f[j * E + e], o, cs[d + e]);
-              }
+              for (int d = 0; d < E; ++d) reinterpret_cast<T *>(out + d * 16)[j] = e[d];
             }
+        }
+      }
+    }
+  } else {
+    // 4 bits: a thread codes 8 elements of a token, a word; the four threads of a block share its
+    // largest.  Word w of unit u (8 elements) of the token in slot at.
+    auto code8 = [&](const float (&f)[8], unsigned &byte) {
+      unsigned w;
+      byte = f4_encode8(f, w);
+      return w;
+    };
+    // keys: turned into LDS, some heads at a time, since a block's elements come from different threads
+    const int group = F4_LDS / (ROT_TOKENS * D);
+    float *s_k = reinterpret_cast<float *>(s_cs + ROT_TOKENS * CS + (a.parent ? (a.N * 2 + 15) / 16 : 0));
+    for (int g0 = h0; g0 < h1; g0 += group) {
+      const int gn = min(group, h1 - g0);
+      if (g0 > h0) __syncthreads();
+      const char *ks = a.k + (long long)b * a.k_sb + (long long)i0 * a.k_sn + (size_t)g0 * D * ESZ;
+      for (int x = tid; x < nt * gn * items; x += NT) {
+        const int t = x / (gn * items), hy = x - t * (gn * items), h = hy / items, y = hy - h * items;
+        const char *p = ks + (long long)t * a.k_sn + (size_t)h * D * ESZ;
+        const double2 *cs = s_cs + t * CS;
+        float *o = s_k + (size_t)(t * gn + h) * D;
+        auto keep = [&](int u, const Unit<T> &w) {
+          *reinterpret_cast<float4 *>(o + u * 8) = make_float4(w.x[0], w.x[1], w.x[2], w.x[3]);
+          *reinterpret_cast<float4 *>(o + u * 8 + 4) = make_float4(w.x[4], w.x[5], w.x[6], w.x[7]);
+        };
+        Unit<T> w, v;
+        if constexpr (!PAIRS) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) w.x[e] = turned_one<T>(p, y * E + e, a.R, cs);
+          keep(y, w);
+        } else {
+          const int u = y < HU ? y : y + HU;
+          w.load(p + u * 16);
+          if (y < HU) {
+            v.load(p + (y + HU) * 16);
+#pragma unroll
+            for (int e = 0; e < E; ++e) turned(w.x[e], v.x[e], cs[cs_at(y * E + e)]);
+            keep(y + HU, v);
+          } else if (a.interleaved) {
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+              if (u * E + 2 * e < a.R) turned(w.x[2 * e], w.x[2 * e + 1], cs[cs_at(u * (E / 2) + e)]);
           }
+          keep(u, w);
+        }
+      }
+      __syncthreads();
+      for (int x = tid; x < nt * gn * U; x += NT) {
+        const int t = x / (gn * U), hu = x - t * (gn * U), h = hu / U, u = hu - h * U;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = s_k[(size_t)(t * gn + h) * D + u * 8 + e];
+        unsigned byte;
+        const unsigned w = code8(f, byte);
+        const size_t ph = ph0 + g0 + h;
+        *reinterpret_cast<unsigned *>(a.k_pages + ph * f4_codes(a.pool) + f4_key(a.pool, u / 4, at0 + t) + (u & 3) * 4) = w;
+        if ((u & 3) == 0) a.k_scales[ph * f4_scales(a.pool) + f4_scale(a.pool, u / 4, at0 + t)] = (char)byte;
+      }
+    }
+    // values: a thread's words of all tokens, in 16 bytes where eight slots are written
+    const bool full = nt == ROT_TOKENS && at0 % ROT_TOKENS == 0;
+    for (int x = tid; x < (h1 - h0) * U; x += NT) {
+      const int h = x / U, u = x - h * U;
+      const char *vs = a.v + (long long)b * a.v_sb + (long long)i0 * a.v_sn + ((size_t)(h0 + h) * D + u * 8) * ESZ;
+      const size_t ph = ph0 + h0 + h;
+      char *o = a.v_pages + ph * f4_codes(a.pool);
+      char *sc = a.v_scales + ph * f4_scales(a.pool) + f4_scale(a.pool, u / 4, at0);
+      u32x4 in[ROT_TOKENS];
+#pragma unroll
+      for (int t = 0; t < ROT_TOKENS; ++t)
+        if (t < nt) in[t] = *reinterpret_cast<const u32x4 *>(vs + (long long)t * a.v_sn);
+      unsigned w[ROT_TOKENS], bytes[2] = {0, 0};
+#pragma unroll
+      for (int t = 0; t < ROT_TOKENS; ++t)
+        if (t < nt) {
+          float f[8];
+          Fmt<T>::unpack(in[t], f);
+          unsigned byte;
+          w[t] = code8(f, byte);
+          bytes[t / 4] |= byte << (8 * (t & 3));
+        }
+      if (full) {
+        if ((u & 3) == 0) *reinterpret_cast<uint2 *>(sc) = make_uint2(bytes[0], bytes[1]);
+        if (D == 128) {
+          *reinterpret_cast<u32x4 *>(o + f4_value(a.pool, at0, u)) = u32x4{w[0], w[1], w[2], w[3]};
+          *reinterpret_cast<u32x4 *>(o + f4_value(a.pool, at0 + 4, u)) = u32x4{w[4], w[5], w[6], w[7]};
+        } else if (D == 64) {
+          u32x4 lo, hi;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            lo[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
+            hi[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
+          }
+          *reinterpret_cast<u32x4 *>(o + f4_value(a.pool, at0, 2 * u)) = lo;
+          *reinterpret_cast<u32x4 *>(o + f4_value(a.pool, at0, 2 * u + 1)) = hi;
         } else {
 #pragma unroll
-          for (int e = 0; e < F4_BLOCK; ++e) f[e] = turned_one<T>(p, u * F4_BLOCK + e, a.R, cs);
+          for (int t = 0; t < ROT_TOKENS; ++t) *reinterpret_cast<unsigned *>(o + f4_value(a.pool, at0 + t, u / 2) + (u & 1) * 4) = w[t];
         }
-      }
-      unsigned w[4];
-      const unsigned byte = f4_encode(f, w);
-      const size_t ph = (size_t)table[s >> sh] * Hkv + h;
-      (val ? a.v_scales : a.k_scales)[ph * f4_scales(a.pool) + f4_scale(a.pool, u, at)] = (char)byte;
-      if (!val) {
-        *reinterpret_cast<u32x4 *>(a.k_pages + ph * f4_codes(a.pool) + f4_key(a.pool, u, at)) = u32x4{w[0], w[1], w[2], w[3]};
       } else {
-        char *o = a.v_pages + ph * f4_codes(a.pool);
-        const int pieces = 16 / B;  // of a block: its elements in D / 16 at a time
-        for (int r = 0; r < pieces; ++r) {
-          char *to = o + f4_value(a.pool, at, u * pieces + r);
-          if (B == 2) *reinterpret_cast<uint16_t *>(to) = (uint16_t)(w[r / 2] >> (16 * (r & 1)));
-          else if (B == 4) *reinterpret_cast<unsigned *>(to) = w[r];
-          else *reinterpret_cast<uint2 *>(to) = make_uint2(w[2 * r], w[2 * r + 1]);
-        }
+#pragma unroll
+        for (int t = 0; t < ROT_TOKENS; ++t)
+          if (t < nt) {
+            if ((u & 3) == 0) sc[t] = (char)(bytes[t / 4] >> (8 * (t & 3)));
+            if (D == 64) {
+              *reinterpret_cast<uint16_t *>(o + f4_value(a.pool, at0 + t, 2 * u)) = (uint16_t)w[t];
+              *reinterpret_cast<uint16_t *>(o + f4_value(a.pool, at0 + t, 2 * u + 1)) = (uint16_t)(w[t] >> 16);
+            } else if (D == 128) {
+              *reinterpret_cast<unsigned *>(o + f4_value(a.pool, at0 + t, u)) = w[t];
+            } else {
+              *reinterpret_cast<unsigned *>(o + f4_value(a.pool, at0 + t, u / 2) + (u & 1) * 4) = w[t];
+            }
+          }
       }
     }
   }
@@ -469,7 +604,8 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
   a.row_status = row_status;
   a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
   const bool pairs = a.interleaved || (R / 2) % E == 0;
-  const unsigned lds = ROT_TOKENS * (R / 2) * 16 + (parent ? (unsigned)N * 2 : 0u);
+  unsigned lds = ROT_TOKENS * cs_row(R / 2) * 16 + (parent ? ((unsigned)N * 2 + 15) / 16 * 16 : 0u);
+  if (f4) lds += (Hkv / a.parts + 1 < F4_LDS / (ROT_TOKENS * D) ? (unsigned)(Hkv / a.parts + 1) * ROT_TOKENS * D : F4_LDS) * 4;
   const void *fn = f4 ? (pairs ? (const void *)&k_append_rotary<uint16_t, true, true> : (const void *)&k_append_rotary<uint16_t, true, false>)
                  : esz == 2 ? (pairs ? (const void *)&k_append_rotary<uint16_t, false, true> : (const void *)&k_append_rotary<uint16_t, false, false>)
                             : (pairs ? (const void *)&k_append_rotary<float, false, true> : (const void *)&k_append_rotary<float, false, false>);

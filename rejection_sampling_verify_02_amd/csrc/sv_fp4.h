@@ -28,33 +28,33 @@ SVD unsigned f4_value(const Pool &p, int t, int m) {
 // What a scale byte stands for; NaN for 255, so that what is multiplied with it is NaN.
 SVD float f4_factor(unsigned byte) { return __uint_as_float(byte == F4_NAN ? 0x7fc00000u : byte << 23); }
 
-// A block's codes, eight to a word, and its scale byte.  The conversion rounds x / scale to the
-// nearest code, ties to the even one.
-SVD unsigned f4_encode(const float (&x)[F4_BLOCK], unsigned (&w)[4]) {
+// Eight elements of a block, the other three threads of the quad having the rest: their codes in a
+// word, and the block's scale byte.  The conversion rounds x / scale to the nearest code, ties to
+// the even one.
+SVD unsigned f4_encode8(const float (&x)[8], unsigned &w) {
   float top = 0.0f;
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < F4_BLOCK; ++i) {
-    const float y = fabsf(x[i]);
-    odd |= !(y < INFINITY);
-    top = fmaxf(top, y);
+  for (int i = 0; i < 8; ++i) {
+    odd |= !(fabsf(x[i]) < INFINITY);
+    top = fmaxf(top, fabsf(x[i]));
   }
+  unsigned u = odd ? 0x7f800000u : __float_as_uint(top);
+  u = max(u, (unsigned)__builtin_amdgcn_update_dpp(0, (int)u, 0xb1, 0xf, 0xf, false));  // quad_perm 1 0 3 2
+  u = max(u, (unsigned)__builtin_amdgcn_update_dpp(0, (int)u, 0x4e, 0xf, 0xf, false));  // quad_perm 2 3 0 1
   // top = m 2^E with m in [1/2, 1): 6 = 3/4 * 2^3
-  const unsigned u = __float_as_uint(top);
   int e = (int)(u >> 23) - 126 - ((u & 0x7fffffu) <= 0x400000u ? 3 : 2);
   e = min(max(e, F4_MIN), F4_MAX);
   const float scale = __uint_as_float((unsigned)(e + 127) << 23), most = 6.0f * scale;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    unsigned c = 0;
-    auto y = [&](int i) { return fminf(fmaxf(x[8 * j + i], -most), most); };
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(0), y(1), scale, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(2), y(3), scale, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(4), y(5), scale, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(6), y(7), scale, 3);
-    w[j] = odd ? 0u : c;
-  }
-  return odd ? F4_NAN : (unsigned)(e + 127);
+  auto y = [&](int i) { return fminf(fmaxf(x[i], -most), most); };
+  unsigned c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(0), y(1), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(2), y(3), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(4), y(5), scale, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y(6), y(7), scale, 3);
+  const bool none = u >= 0x7f800000u;
+  w = none ? 0u : c;
+  return none ? F4_NAN : (unsigned)(e + 127);
 }
 
 // Codes 2 I and 2 I + 1 of a word as two bf16 numbers, times a power of two.
