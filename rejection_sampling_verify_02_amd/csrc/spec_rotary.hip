@@ -19,7 +19,7 @@ struct RotaryArgs {
   const int32_t *page_table, *cache_len, *n_new, *parent, *positions, *prior;
   int N, Hq, R, interleaved;
   double factor;
-  int chunks, parts;  // workgroups of a sequence: chunks of tokens times parts of the heads
+  int chunks, parts, q_parts, q_part, kv_part;  // workgroups of a sequence: chunks of tokens times parts of the heads
   int32_t *row_status;
   Pool pool;
 };
@@ -27,7 +27,7 @@ struct RotaryArgs {
 // Tokens of a workgroup: whole units of values (8 slots of bf16, 4 of f32), so that a unit has
 // one writer.
 constexpr int ROT_TOKENS = 8;
-constexpr int F4_LDS = 8192;  // floats of turned keys on their way to 4 bits
+constexpr int F4_LDS = 4096;  // floats of turned keys on their way to 4 bits
 
 // cos t and sin t of t = n * f, in 64 bits: the product of a whole number and a float, rounded
 // once; a quarter turn's multiple taken off in two parts (the first exactly, in the fused
@@ -79,6 +79,29 @@ struct Unit {  // 16 bytes of elements
       for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(x[j]);
     }
     return w;
+  }
+};
+
+// A thread's place in a space of t, h < H, y < I, and on to NT places further without dividing.
+struct Walk {
+  int t, h, y, H, I, dh, dy;
+  SVD Walk(int x, int H_, int I_) : H(H_), I(I_), dh(NT / I_), dy(NT % I_) {
+    h = x / I;
+    y = x - h * I;
+    t = h / H;
+    h -= t * H;
+  }
+  SVD void on() {
+    y += dy;
+    h += dh;
+    if (y >= I) {
+      y -= I;
+      ++h;
+    }
+    while (h >= H) {
+      h -= H;
+      ++t;
+    }
   }
 };
 
@@ -174,8 +197,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
   auto last_token = [&](int l) { return min(a.N, (chunk + 1) * ROT_TOKENS - (l & (ROT_TOKENS - 1))); };
   int i0 = first_token(len), i1 = last_token(len);
   // The part's heads of the queries, and of the keys and values.
-  const int q0 = (int)((long long)a.Hq * part / a.parts), q1 = (int)((long long)a.Hq * (part + 1) / a.parts);
-  const int h0 = (int)((long long)Hkv * part / a.parts), h1 = (int)((long long)Hkv * (part + 1) / a.parts);
+  const int q0 = part < a.q_parts ? min(a.Hq, part * a.q_part) : a.Hq, q1 = min(a.Hq, q0 + a.q_part);
+  const int h0 = part < a.q_parts ? Hkv : min(Hkv, (part - a.q_parts) * a.kv_part), h1 = min(Hkv, h0 + a.kv_part);
 
   // Queries, and the keys of a cache of the inputs' type, in jobs: 16 bytes and, where the head's
   // halves are turned against each other, their partners, of up to NB tokens.  A job's loads are on
@@ -188,12 +211,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
     long long stride;
     int h, y, t0;
   };
-  auto job_at = [&](int j) {
+  auto job_at = [&](const Walk &w) {
     Job o;
-    const int batch = j / (n_heads * items), x = j - batch * (n_heads * items);
-    o.t0 = batch * NB;
-    o.h = x / items;
-    o.y = x - o.h * items;
+    o.t0 = w.t * NB;
+    o.h = w.h;
+    o.y = w.y;
     const bool q = o.h < n_q;
     o.stride = q ? a.q_sn : a.k_sn;
     o.p = (q ? a.q + (long long)b * a.q_sb + (size_t)(q0 + o.h) * D * ESZ : a.k + (long long)b * a.k_sb + (size_t)(h0 + o.h - n_q) * D * ESZ) +
@@ -210,16 +232,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
   };
   u32x4 lw[NB], lv[NB];
   Job job = {};
-  int jobs = 0;
-  auto prefetch = [&]() {
-    jobs = i0 < i1 ? n_heads * items * ((i1 - i0 + NB - 1) / NB) : 0;
-    if constexpr (PAIRS)
-      if (tid < jobs) {
-        job = job_at(tid);
-        load(job, i1 - i0, lw, lv);
-      }
-  };
-  prefetch();  // (rows of tokens are there whatever the sequence's length says)
+  Walk walk(tid, max(n_heads, 1), items);
+  const int jobs = i0 < i1 ? n_heads * items * ((i1 - i0 + NB - 1) / NB) : 0;
+  if constexpr (PAIRS)
+    if (tid < jobs) {  // (rows of tokens are there whatever the sequence's length says)
+      job = job_at(walk);
+      load(job, i1 - i0, lw, lv);
+    }
 
   const int code = rotary_code(a, b, len, m, s_par);
   if (chunk == 0 && part == 0 && tid == 0) a.row_status[b] = code;
@@ -232,10 +251,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
   const int live = code != 0 ? i0 : min(max(m, i0), i1);  // tokens from here on are not new
   if (live < i1) {  // queries of no token: zero, or NaN for a sequence with a code
     const unsigned fill = code == 0 ? 0u : ESZ == 2 ? 0x7fc07fc0u : 0x7fc00000u;
-    const int n = n_q * U;
-    for (int x = tid; x < (i1 - live) * n; x += NT)
-      *reinterpret_cast<u32x4 *>(a.q_out + (((size_t)b * a.N + live + x / n) * a.Hq + q0) * D * ESZ + (size_t)(x % n) * 16) =
-          u32x4{fill, fill, fill, fill};
+    for (int i = live; i < i1; ++i)
+      for (int x = tid; x < n_q * U; x += NT)
+        *reinterpret_cast<u32x4 *>(a.q_out + (((size_t)b * a.N + i) * a.Hq + q0) * D * ESZ + (size_t)x * 16) = u32x4{fill, fill, fill, fill};
   }
   if (live <= i0) return;
   const int nt = live - i0;
@@ -271,7 +289,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
       u32x4 nw[NB], nv[NB];
       Job after = job;
       if (j + NT < jobs) {
-        after = job_at(j + NT);
+        walk.on();
+        after = job_at(walk);
         load(after, nt, nw, nv);
       }
 #pragma unroll
@@ -352,8 +371,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
       const int gn = min(group, h1 - g0);
       if (g0 > h0) __syncthreads();
       const char *ks = a.k + (long long)b * a.k_sb + (long long)i0 * a.k_sn + (size_t)g0 * D * ESZ;
-      for (int x = tid; x < nt * gn * items; x += NT) {
-        const int t = x / (gn * items), hy = x - t * (gn * items), h = hy / items, y = hy - h * items;
+      Walk from(tid, gn, items);
+      for (int x = tid; x < nt * gn * items; x += NT, from.on()) {
+        const int t = from.t, h = from.h, y = from.y;
         const char *p = ks + (long long)t * a.k_sn + (size_t)h * D * ESZ;
         const double2 *cs = s_cs + t * CS;
         float *o = s_k + (size_t)(t * gn + h) * D;
@@ -383,8 +403,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
         }
       }
       __syncthreads();
-      for (int x = tid; x < nt * gn * U; x += NT) {
-        const int t = x / (gn * U), hu = x - t * (gn * U), h = hu / U, u = hu - h * U;
+      Walk at(tid, gn, U);
+      for (int x = tid; x < nt * gn * U; x += NT, at.on()) {
+        const int t = at.t, h = at.h, u = at.y;
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = s_k[(size_t)(t * gn + h) * D + u * 8 + e];
@@ -555,13 +576,17 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
   if (rotary && !(fabsf(rotary->factor) <= __FLT_MAX__)) return SV_ERR_PARAM;
   RotaryArgs a = {};
   a.chunks = (N + ROT_TOKENS - 2) / ROT_TOKENS + 1;  // the first may begin anywhere in a chunk
-  // Parts of the heads: so that small calls use more of the card (each part computes the tokens'
-  // angles anew).
+  // Parts of the heads, queries apart from keys and values, so that small calls use more of the card
+  // and the steps of a workgroup are few (each part computes the tokens' angles anew).
   const long long wgs = (long long)B * a.chunks;
-  a.parts = (int)(wgs >= 1024 ? 1 : (1024 + wgs - 1) / wgs);
-  if (a.parts > 8) a.parts = 8;
-  if (a.parts > Hkv) a.parts = Hkv;
+  const int want = (int)(wgs >= 512 ? 1 : (512 + wgs - 1) / wgs);
+  auto parts = [&](int heads) { return heads < want ? heads : want; };
+  a.q_parts = parts(Hq < 8 ? Hq : 8);
+  const int kv_parts = parts(Hkv < 8 ? Hkv : 8);
+  a.parts = a.q_parts + kv_parts;
   if (wgs > MAX_WGS / a.parts) return SV_ERR_SHAPE;
+  a.q_part = a.q_parts ? (Hq + a.q_parts - 1) / a.q_parts : 0;
+  a.kv_part = (Hkv + kv_parts - 1) / kv_parts;
   if (!k || !v || !k_pages || !v_pages || (f4 && (!k_scales || !v_scales)) || !page_table || !cache_len || !row_status ||
       (q && !q_out) || (R && !rotary->inv_freq))
     return SV_ERR_NULL;
@@ -605,7 +630,7 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
   a.pool = pool_of(Hkv, D, page_size, num_pages, table_width);
   const bool pairs = a.interleaved || (R / 2) % E == 0;
   unsigned lds = ROT_TOKENS * cs_row(R / 2) * 16 + (parent ? ((unsigned)N * 2 + 15) / 16 * 16 : 0u);
-  if (f4) lds += (Hkv / a.parts + 1 < F4_LDS / (ROT_TOKENS * D) ? (unsigned)(Hkv / a.parts + 1) * ROT_TOKENS * D : F4_LDS) * 4;
+  if (f4) lds += (a.kv_part < F4_LDS / (ROT_TOKENS * D) ? (unsigned)a.kv_part * ROT_TOKENS * D : F4_LDS) * 4;
   const void *fn = f4 ? (pairs ? (const void *)&k_append_rotary<uint16_t, true, true> : (const void *)&k_append_rotary<uint16_t, true, false>)
                  : esz == 2 ? (pairs ? (const void *)&k_append_rotary<uint16_t, false, true> : (const void *)&k_append_rotary<uint16_t, false, false>)
                             : (pairs ? (const void *)&k_append_rotary<float, false, true> : (const void *)&k_append_rotary<float, false, false>);
