@@ -10,11 +10,18 @@
 //                 are D / 16 neighbours d of eight slots, all of one block: a conversion gives two
 //                 neighbours of one slot, and a byte permutation makes pairs of slots of them, the
 //                 second product's operand.  Row tile j of the output then holds d = D / 16 m + j,
-//                 m the row of the matrix instruction.
+//                 m the row of the matrix instruction.  Each wave has its tiles sent to LDS, where
+//                 they wait without registers.  Bound by the cache's bytes: 64 sequences of 257 to
+//                 16001 slots, 8 key heads of 128: 104 us, 5.4 TB/s; its loads alone take 98.  (With
+//                 the codes in registers, one tile ahead, and shares of equal length: 135.)  The
+//                 keys could go into the scaled matrix instruction as they are, the queries as two
+//                 8-bit parts; but that one's sums are only good to 2^-12 of their terms.
 //   k_attn4_wide  more rows.  The waves share each tile through LDS as bf16, converted once by one
 //                 of them.
 
 #include "sv_attention.h"
+
+#include <type_traits>
 
 #include "sv_fp4.h"
 
@@ -30,6 +37,79 @@ template <int D>
 struct UnitsWithin {
   static constexpr int KH = D / 32 < 4 ? D / 32 : 4;
   SVD static int at(int k, int g) { return k / KH * (4 * KH) + KH * g + k % KH; }
+};
+
+// Waits until at most N of the wave's memory operations are on their way.
+template <int N>
+SVD void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0xf70);
+  asm volatile("" ::: "memory");
+}
+
+// A tile's codes and scales on their way from memory to LDS, with no registers in between: a wave's
+// loads put 16 bytes (scales: 4) of lane after lane one behind the other.  Written as assembly
+// because the compiler, where it sees them, has every read of LDS wait for all of them; their
+// order and wait_loads see to that here.  They return nothing in registers.
+// In LDS: keys, a load being what 64 lanes multiply in a step; values, in the pool's order; then
+// scales [block][slot], of keys and of values.
+template <int D>
+struct Fetch {
+  static constexpr int KL = D / 64, SL = D <= 128 ? 1 : 2, LOADS = 2 * KL + SL;  // of keys (of values as many), of scales
+  static constexpr int VALUES = KL * 1024, SCALES = 2 * KL * 1024, VSCALES = SCALES + D, BYTES = SCALES + SL * 256;
+  const char *kh, *vh;   // the head in page 0
+  const char *sh[SL];    // of the lane's scales: its pool, block and slot of a half tile
+
+  // 16 bytes a lane, from a place that all lanes know and one of its own
+  SVD static void line(const char *at, unsigned own, unsigned lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(own), "s"(at), "{m0}"(lds) : "memory");
+  }
+  SVD static void line(const char *own, unsigned lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(own), "{m0}"(lds) : "memory");
+  }
+  SVD static void word(const char *own, unsigned lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(own), "{m0}"(lds) : "memory");
+  }
+
+  SVD void head(const Attn4Args &a, int h, int lane) {
+    const unsigned page = 1u << a.page_shift, codes = page * D / 2, scales = page * D / F4_BLOCK;
+    kh = a.k_pages + (size_t)h * codes;
+    vh = a.v_pages + (size_t)h * codes;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+      const int x = (SL == 2 ? j * 64 + lane : lane) % (D / 2);  // D / 4 words of keys' scales, as many of values'; at D = 64 all of it twice
+      const char *pool = x < D / 4 ? a.k_scales : a.v_scales;
+      sh[j] = pool + (size_t)h * scales + (x % (D / 4) / 8 * page + x % 4 * 4);
+    }
+  }
+  // The tile at slot t0, its halves in pages pa and pb, to `lds`.
+  SVD void send(const Attn4Args &a, int t0, int pa, int pb, unsigned lds, int lane) const {
+    const unsigned page = 1u << a.page_shift;
+    const unsigned long long page_codes = (unsigned long long)a.Hkv * (page * D / 2), page_scales = (unsigned long long)a.Hkv * (page * D / F4_BLOCK);
+    const unsigned ta = (unsigned)t0 & (page - 1), tb = (unsigned)(t0 + 16) & (page - 1);
+    const unsigned long long ca = (unsigned)pa * page_codes, cb = (unsigned)pb * page_codes;
+    if constexpr (D == 64) {
+      const bool kb = lane & 16, vb = lane & 32;
+      line(kh + (kb ? cb : ca) + ((unsigned)(lane / 32) * page + (kb ? tb : ta) + (unsigned)(lane & 15)) * 16u, lds);
+      line(vh + (vb ? cb : ca) + ((vb ? tb : ta) / 8 * 16 + (unsigned)(lane & 31)) * 16u, lds + VALUES);
+    } else {
+      const unsigned own = (unsigned)(lane / 16 * page + lane % 16) * 16u;
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const int t2 = i / (KL / 2), b = i % (KL / 2);
+        line(kh + (t2 ? cb : ca) + (4 * b * page + (t2 ? tb : ta)) * 16u, own, lds + i * 1024);
+      }
+      constexpr int S = 512 / D, PER = 4 * S;  // slots of a unit, and of a load
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const bool hb = i * PER >= 16;
+        line(vh + (hb ? cb : ca) + ((hb ? tb : ta) + i * PER % 16) / S * 256u, (unsigned)lane * 16u, lds + VALUES + i * 1024);
+      }
+    }
+    const unsigned long long sa = (unsigned)pa * page_scales + ta, sb = (unsigned)pb * page_scales + tb;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) word(sh[j] + (lane & 4 ? sb : sa), lds + SCALES + j * 256);
+  }
 };
 
 // A lane's codes of a 32-slot tile, and their scales: of keys slots 16 t2 + m, of values slots
@@ -73,11 +153,37 @@ struct Codes {
     for (int u = 0; u < VU; ++u) v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(c + u * 256));
     vs = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(vsh + p * page_scales + (unsigned)(m * DPL / F4_BLOCK * page) + t));
   }
+  // The same, of a tile that Fetch put into LDS.
+  SVD void read_k(const char *t, int m, int g) {
+    typedef Fetch<D> F;
+#pragma unroll
+    for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const int u = D == 64 ? g / 2 : g + 4 * b;
+        ks[t2][b] = *reinterpret_cast<const unsigned char *>(t + F::SCALES + u * 32 + 16 * t2 + m);
+        if constexpr (D == 64) {
+          const u32x2 w = *reinterpret_cast<const u32x2 *>(t + (u * 32 + 16 * t2 + m) * 16 + (g & 1) * 8);
+          k[t2][0] = w.x;
+          k[t2][1] = w.y;
+        } else {
+          const u32x4 w = *reinterpret_cast<const u32x4 *>(t + ((t2 * KB + b) * 64 + 16 * g + m) * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) k[t2][4 * b + j] = w[j];
+        }
+      }
+  }
+  SVD void read_v(const char *t, int m, int g) {
+    typedef Fetch<D> F;
+#pragma unroll
+    for (int u = 0; u < VU; ++u) v[u] = *reinterpret_cast<const u32x4 *>(t + F::VALUES + ((g * VU + u) * 16 + m) * 16);
+    vs = *reinterpret_cast<const u32x2 *>(t + F::VSCALES + m * DPL / F4_BLOCK * 32 + 8 * g);
+  }
   // Step k4's operand of score tile t2.
   SVD u32x4 key(int t2, int k4) const { return f4_unit(k[t2][k4], f4_factor(ks[t2][D == 64 ? 0 : k4 / 4])); }
   SVD void factors(float (&f)[8]) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = f4_factor((vs[e / 4] >> (8 * (e % 4))) & 255u);
+    for (int e = 0; e < 8; ++e) f[e] = f4_factor(vs[e / 4], e % 4);
   }
   // Elements 2 i and 2 i + 1 of the lane's D / 16, of its eight slots: the operands of output
   // tiles 2 i and 2 i + 1.
@@ -122,8 +228,17 @@ constexpr unsigned least_part4() {
   return n > 1 ? n : 1;
 }
 
+// Workgroups of a CU, and tiles of LDS that a wave has: 70 KB of a CU on their way at D = 64 and
+// 128, where more is slower (D = 128, the 64 sequences below: 105 us so, 108 with three tiles, 111
+// with three workgroups as well).
 template <int D, int R>
-constexpr int attn4_occ() { return R * D <= 128 ? 3 : 2; }
+constexpr int attn4_occ() { return D > 64 ? 2 : R == 1 ? 4 : 3; }
+template <int D>
+constexpr int attn4_stages() { return D == 64 ? 3 : 2; }
+// What the start of a unit costs a workgroup, in rounds: it waits for the unit's page ids, then its
+// first tiles, and joins at the end.  Without it the workgroup with ten short sequences was the
+// last one by 25 of 130 us.
+constexpr unsigned ATTN4_LEAD = 5;
 
 template <int D, int R>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D, R>()))) void k_attn4(const Attn4Args a) {
@@ -131,45 +246,54 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D,
   typedef Mma<T> M;
   constexpr int RT = 16 * R, KS = D / 32, DT = D / 16, Q = D / 64;
   constexpr int PADD = D + 4;  // rows of the LDS join tile, padded against bank conflicts
+  constexpr int ST = attn4_stages<D>();
+  typedef Fetch<D> F;
   extern __shared__ unsigned s_books[];
   const SharedBooks s = books_at(s_books, RT, a.N, a.group);
-  __shared__ float s_o[NW * RT * PADD];
+  constexpr int RING = NW * ST * F::BYTES, JOIN = NW * RT * PADD * 4;
+  __shared__ __attribute__((aligned(16))) char s_buf[RING > JOIN ? RING : JOIN];  // tiles on their way, and the join behind them
+  float *const s_o = reinterpret_cast<float *>(s_buf);
   __shared__ float s_m[NW * RT], s_l[NW * RT];
 
   const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int m = lane & 15, g = lane >> 4;
-  const int page = 1 << a.page_shift;
-  const unsigned head_codes = (unsigned)page * D / 2, head_scales = (unsigned)page * D / F4_BLOCK;
-  const unsigned long long page_codes = (unsigned long long)a.Hkv * head_codes, page_scales = (unsigned long long)a.Hkv * head_scales;
+  const char *const ring = s_buf + wid * (ST * F::BYTES);
+  const unsigned ring_at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char *)ring;
 
   Rows<T, D, R, UnitsWithin<D>> rows;
-  Codes<D> c;
-  auto load_k = [&](const Segment &sg, int t0, int pa, int pb) {
-    c.load_k(a.k_pages + (size_t)sg.h * head_codes, a.k_scales + (size_t)sg.h * head_scales, page_codes, page_scales, page, t0, pa, pb, m, g);
-  };
-  auto load_v = [&](const Segment &sg, int t0, int pa, int pb) {
-    c.load_v(a.v_pages + (size_t)sg.h * head_codes, a.v_scales + (size_t)sg.h * head_scales, page_codes, page_scales, page, t0, pa, pb, m, g);
-  };
-  auto begin = [&](const Segment &sg) {
-    const int t0 = sg.tile(min(sg.l0 + wid, sg.l1 - 1));
+  F fetch;
+  auto send = [&](const Segment &sg, int l, int slot) {
+    const int t0 = sg.tile(l);
     int pa, pb;
     sg.pages(a, t0, pa, pb);
-    load_k(sg, t0, pa, pb);
-    load_v(sg, t0, pa, pb);
+    pa = __builtin_amdgcn_readfirstlane(pa);
+    pb = __builtin_amdgcn_readfirstlane(pb);
+    fetch.send(a, t0, pa, pb, ring_at + slot * F::BYTES, lane);
+  };
+  auto begin = [&](const Segment &sg) {
     rows.load(a, sg, sg.rt * RT, m, g);
+    fetch.head(a, __builtin_amdgcn_readfirstlane(sg.h), lane);
+#pragma unroll
+    for (int k = 0; k < ST; ++k)
+      if (sg.l0 + wid + k * NW < sg.l1) send(sg, sg.l0 + wid + k * NW, k);
   };
 
-  attn_share<T, D, RT, NW, false, least_part4<RT, NW>()>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+  attn_share<T, D, RT, NW, false, least_part4<RT, NW>(), ATTN4_LEAD>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
     rows.clear();
     int l = sg.l0 + wid;
     if (sg.sp.i0 <= sg.sp.i1 && code == 0 && l < sg.l1) {
       rows.depths(sg, s);
       bool odd_any = false;
-      for (;;) {
-        const bool last = l + NW >= sg.l1;
-        const int t0 = sg.tile(l), tn = sg.tile(last ? l : l + NW);
-        int pa, pb;
-        sg.pages(a, tn, pa, pb);
+      int slot = 0;
+      auto work = [&](auto plain) {  // whether every row sees the whole tile: the rest of the code is kept apart from theirs
+        const int t0 = sg.tile(l);
+        const char *tile = ring + slot * F::BYTES;
+        // what may still be on its way: the tiles behind this one
+        if (l + (ST - 1) * NW < sg.l1) wait_loads<(ST - 1) * F::LOADS>();
+        else if (ST > 2 && l + NW < sg.l1) wait_loads<F::LOADS>();
+        else wait_loads<0>();
+        Codes<D> c;
+        c.read_k(tile, m, g);
         f32x4 sc[R][2];
         {
           typename M::Dot dot[R][2] = {};
@@ -186,11 +310,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D,
 #pragma unroll
             for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = M::score(dot[r][t2]);
         }
-        load_k(sg, tn, pa, pb);
-        const bool plain = sg.plain(a, t0);
+        c.read_v(tile, m, g);
         const int n = sg.end() - t0 - 8 * g;  // slots behind the sequence hold anything
         bool odd = false;
-        if (!plain) {
+        if constexpr (!plain) {
           rows.mask(a, sg, s, t0, g, sc);
           odd = __any(c.odd(n));
           odd_any |= odd;
@@ -205,7 +328,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D,
           c.values(i, f, v[0], v[1]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            if (!plain) {
+            if constexpr (!plain) {
               v[j] = M::cut(v[j], n);
               if (odd) v[j] = M::finite(v[j]);
             }
@@ -214,19 +337,28 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D,
             for (int r = 0; r < R; ++r) rows.o[r][2 * i + j] = M::pv(one, pw[r], rows.o[r][2 * i + j]);
           }
         }
-        if (last) break;
+        if (l + ST * NW < sg.l1) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the tile has been read
+          send(sg, l + ST * NW, slot);
+        }
+        slot = slot + 1 == ST ? 0 : slot + 1;
         l += NW;
-        load_v(sg, tn, pa, pb);
+      };
+      while (l < sg.l1) {
+        while (l < sg.l1 && sg.plain(a, sg.tile(l))) work(std::true_type{});
+        while (l < sg.l1 && !sg.plain(a, sg.tile(l))) work(std::false_type{});
       }
       if (odd_any)
         for (l = sg.l0 + wid; l < sg.l1; l += NW) {
           const int t0 = sg.tile(l);
           if (sg.plain(a, t0)) continue;
-          int pa, pb;
-          sg.pages(a, t0, pa, pb);
-          load_v(sg, t0, pa, pb);
+          send(sg, l, 0);
+          wait_loads<0>();
+          Codes<D> c;
+          c.read_v(ring, m, g);
           float f[8];
           c.factors(f);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const unsigned vis = rows.view(a, sg, s, t0, r, g);
@@ -243,6 +375,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D,
           }
         }
     }
+
+    wait_loads<0>();  // of a sequence that is refused, too
+    __syncthreads();
 
     // the four waves joined: rows' maxima and sums, then the output tiles
 #pragma unroll

@@ -86,12 +86,12 @@ SVD Span span_of(const AttnArgs &a, const Seq &s, int rt) {
 template <int ROUND>
 SVD unsigned rounds_of(const Span &p) { return (unsigned)(p.tiles + ROUND - 1) / ROUND; }
 // The parts that a unit of r rounds is cut into, at most `most` rounds each, and a head's row
-// tiles together (most = 1: its rounds).
+// tiles together (most = 1: its rounds).  `lead`: parts that a unit is charged for its start.
 SVD unsigned parts_of(unsigned r, unsigned most) { return (r + most - 1) / most; }
 template <int RT, int ROUND>
-SVD unsigned head_parts(const AttnArgs &a, const Seq &s, unsigned most) {
+SVD unsigned head_parts(const AttnArgs &a, const Seq &s, unsigned most, unsigned lead = 0) {
   unsigned t = 0;
-  for (int rt = 0; rt < a.n_rt; ++rt) t += parts_of(rounds_of<ROUND>(span_of<RT>(a, s, rt)), most);
+  for (int rt = 0; rt < a.n_rt; ++rt) t += parts_of(rounds_of<ROUND>(span_of<RT>(a, s, rt)), most) + lead;
   return t;
 }
 
@@ -443,7 +443,7 @@ constexpr unsigned least_part() {
 // sink(row, reference, sum of weights).  begin is called for every segment, also one whose rows
 // are no new tokens (its tile 0 is then some page's, and not used): what it leaves in registers
 // would have to be kept from segment to segment otherwise.
-template <typename T, int D, int RT, int ROUND, bool WIDE, unsigned LEAST = least_part<T, RT, ROUND>(), typename Begin, typename Run>
+template <typename T, int D, int RT, int ROUND, bool WIDE, unsigned LEAST = least_part<T, RT, ROUND>(), unsigned LEAD = 0, typename Begin, typename Run>
 SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run run) {
   constexpr int ESZ = (int)sizeof(T);
   const int tid = threadIdx.x;
@@ -454,11 +454,11 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   // single rounds and shares of them as equal as can be (units of 257 to 16001 slots, one a
   // workgroup: 392 us, so 343).
   const bool aligned = (unsigned)a.B * (unsigned)(a.Hkv * a.n_rt) <= a.grid && ((long long)a.W << a.page_shift) < (1 << 27);
-  unsigned v = 0, ex = 0, total = 0;
+  unsigned v = 0, ex = 0, total = 0, lead = 0;
   auto scan = [&](unsigned most) {  // of every sequence's parts; for the first NT (all of them, mostly) v and ex stay
     total = 0;
     for (int b0 = (a.B - 1) / NT * NT; b0 >= 0; b0 -= NT) {
-      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most) * (unsigned)a.Hkv : 0u;
+      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most, lead) * (unsigned)a.Hkv : 0u;
       unsigned tot;
       ex = block_excl_scan(v, s.w, tot);
       total += tot;
@@ -496,6 +496,12 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     most = LEAST;
     scan(most);
   }
+  // Shares that run on: a unit that begins in one costs it the time of LEAD rounds besides its own.
+  if (LEAD > 0 && most == 1u && share > 1u) {
+    lead = LEAD;
+    scan(1u);
+    share = (total + a.grid - 1) / a.grid;
+  }
   // Consecutive shares on one XCD (block p runs on XCD p % LANES), as many on each: the row
   // tiles of a key head read the same keys and values through that XCD's L2.
   const unsigned shares = (total + share - 1) / share, per_xcd = (shares + LANES - 1) / LANES;
@@ -511,7 +517,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   } else {
     unsigned seen = 0;
     for (int b0 = 0; seen <= pos; b0 += NT) {
-      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most) * (unsigned)a.Hkv : 0u;
+      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most, lead) * (unsigned)a.Hkv : 0u;
       unsigned tot;
       ex = seen + block_excl_scan(v, s.w, tot);
       if (pos >= ex && pos < ex + v) {
@@ -529,7 +535,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   int code = 0, code_b = -1;           // the code of sequence code_b
   int books_b = -1, books_rt = -1;     // the row tile whose books are in LDS
   while (pos < pos_end) {
-    const unsigned per_head = head_parts<RT, ROUND>(a, g.sq, most);
+    const unsigned per_head = head_parts<RT, ROUND>(a, g.sq, most, lead);
     if (off >= per_head * (unsigned)a.Hkv) {
       off -= per_head * (unsigned)a.Hkv;
       g.sq = seq_of(a, ++g.b);
@@ -539,21 +545,24 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     unsigned r0 = off - (unsigned)g.h * per_head;
     g.rt = 0;
     g.sp = span_of<RT>(a, g.sq, 0);
-    unsigned rounds = rounds_of<ROUND>(g.sp), parts = parts_of(rounds, most);
+    unsigned rounds = rounds_of<ROUND>(g.sp), parts = parts_of(rounds, most) + lead;
     while (r0 >= parts) {
       r0 -= parts;
       g.sp = span_of<RT>(a, g.sq, ++g.rt);
       rounds = rounds_of<ROUND>(g.sp);
-      parts = parts_of(rounds, most);
+      parts = parts_of(rounds, most) + lead;
     }
     const unsigned r1 = min(parts, r0 + (pos_end - pos));
     // parts of a unit differ by a round at most (parts <= grid and rounds < 2^22 where they are not the same)
-    g.l0 = (int)((parts == rounds ? r0 : r0 * rounds / parts) * ROUND);
-    g.l1 = min(g.sp.tiles, (int)((parts == rounds ? r1 : r1 * rounds / parts) * ROUND));
+    // (with a lead: the rounds behind it, none perhaps)
+    auto round_at = [&](unsigned r) { return lead > 0 ? max(r, lead) - lead : parts == rounds ? r : r * rounds / parts; };
+    g.l0 = (int)(round_at(r0) * ROUND);
+    g.l1 = min(g.sp.tiles, (int)(round_at(r1) * ROUND));
+    const bool first = r0 == 0;
     g.table = (TablePtr)(a.page_table + (size_t)g.b * a.W);
     g.par = a.parent ? a.parent + (size_t)g.b * a.N : nullptr;
     g.words = (g.sq.m + 31) >> 5;
-    g.masks = a.window > 0 || g.tile(g.l1 - 1) + TILE > g.sq.len;
+    g.masks = a.window > 0 || (g.l1 > g.l0 && g.tile(g.l1 - 1) + TILE > g.sq.len);
     const bool whole = r0 == 0 && r1 == parts;
 
     __syncthreads();  // the previous segment is done with the LDS
@@ -562,8 +571,8 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
       code = seq_code(a, g.sq, g.b, s);
       code_b = g.b;
     }
-    if (tid == 0 && g.h == 0 && g.rt == 0 && g.l0 == 0) a.row_status[g.b] = code;
-    if (tid == 0 && g.l0 == 0) {
+    if (tid == 0 && g.h == 0 && g.rt == 0 && first) a.row_status[g.b] = code;
+    if (tid == 0 && first) {
       const unsigned last = (pos + parts - 1) / share;
       a.desc[(g.b * a.Hkv + g.h) * a.n_rt + g.rt] =
           make_uint4(w, last - w + 1, (code ? 0x80000000u : 0u) | (unsigned)(g.sq.ok ? g.sq.m : 0), 0u);
@@ -574,7 +583,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
       books_rt = g.rt;
     }
 
-    const unsigned slot = 2 * w + (g.l0 == 0 ? 1u : 0u);
+    const unsigned slot = 2 * w + (first ? 1u : 0u);
     auto sink = [&](int row, float mt, float ls) {
       RowSink<T, D> to;
       const int rg = g.rt * RT + row, i = rg / a.group, hh = rg - i * a.group;

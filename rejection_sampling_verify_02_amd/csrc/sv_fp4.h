@@ -25,8 +25,10 @@ SVD unsigned f4_value(const Pool &p, int t, int m) {
   return (unsigned)((t / S * 16 + m) * 16 + (t % S) * B);
 }
 
-// What a scale byte stands for; NaN for 255, so that what is multiplied with it is NaN.
-SVD float f4_factor(unsigned byte) { return __uint_as_float(byte == F4_NAN ? 0x7fc00000u : byte << 23); }
+// What a scale byte stands for, as the conversions want it: they read the exponent alone, and with
+// that of byte 255 they give NaN whatever the code.  So a byte of a word need not be cut out.
+SVD float f4_factor(unsigned byte) { return __uint_as_float(byte << 23); }
+SVD float f4_factor(unsigned word, int i) { return __uint_as_float(i == 3 ? word >> 1 : word << (23 - 8 * i)); }
 
 // Eight elements of a block, the other three threads of the quad having the rest: their codes in a
 // word, and the block's scale byte.  The conversion rounds x / scale to the nearest code, ties to
