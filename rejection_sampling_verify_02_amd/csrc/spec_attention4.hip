@@ -17,7 +17,11 @@
 //                 keys could go into the scaled matrix instruction as they are, the queries as two
 //                 8-bit parts; but that one's sums are only good to 2^-12 of their terms.
 //   k_attn4_wide  more rows.  The waves share each tile through LDS as bf16, converted once by one
-//                 of them.
+//                 of them.  16 trees of 32 nodes, 4 heads a key head: 92 us; the products alone
+//                 would be 37.  The rest is what a wave does between them, weights and conversions,
+//                 with one other wave on its SIMD to fill in: all its registers are taken.  (Two
+//                 tiles at a time, one's weights beside the other's products, spills in the loop:
+//                 166 to 193 us a call for 100.)
 
 #include "sv_attention.h"
 
@@ -419,6 +423,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(attn4_occ<D,
 // Tiles of a stage and workgroups of a CU: as for bf16 pages, whose tiles the stages hold.
 template <int D>
 constexpr int wide4_stage() { return D <= 128 ? 2 : 1; }
+// What the start of a unit costs, in rounds of a stage (64 sequences of 100 to 4000 slots, 32 nodes
+// each: 195 us without, 158 so).
+constexpr unsigned WIDE4_LEAD = 3;
 template <int D, int R>
 constexpr int wide4_occ() { return R * D <= 256 ? 2 : 1; }
 
@@ -436,7 +443,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
   constexpr int ST = wide4_stage<D>();
   extern __shared__ unsigned s_books[];
   const SharedBooks s = books_at(s_books, RT, a.N, a.group);
-  __shared__ u32x4 s_a[ST][2 * UNITS], s_b[ST][2 * UNITS];
+  __shared__ u32x4 s_t[2][ST][2 * UNITS];
   __shared__ int s_odd;
 
   const int tid = threadIdx.x, lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -489,12 +496,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
     send(sg, sg.l0);
   };
 
-  attn_share<T, D, RT, ST, true, least_part4<RT, ST>()>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
+  attn_share<T, D, RT, ST, true, least_part4<RT, ST>(), WIDE4_LEAD>(a, s, begin, [&](const Segment &sg, int code, auto sink) {
     rows.clear();
     if (sg.sp.i0 <= sg.sp.i1 && code == 0) {
       rows.depths(sg, s);
       rows.arrived();
-      convert(sg, sg.l0, s_a);
+      convert(sg, sg.l0, s_t[0]);
       send(sg, sg.l0 + ST);
       // Slots behind the sequence hold anything, and values that are not finite are left out of
       // the products where not every row sees them.
@@ -509,10 +516,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
         if (odd) s_odd = 1;
         __syncthreads();
       };
-      auto work = [&](int l, u32x4 *buf) {
-        const int t0 = sg.tile(l);
-        const bool plain = sg.plain(a, t0);
-        if (!plain) clean(t0, buf + UNITS);
+      auto scores = [&](const u32x4 *buf, f32x4 (&sc)[R][2]) {
         typename M::Dot dot[R][2] = {};
 #pragma unroll
         for (int k4 = 0; k4 < KS; ++k4)
@@ -522,14 +526,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
 #pragma unroll
             for (int r = 0; r < R; ++r) M::qk(k, rows.q[r][k4], dot[r][t2]);
           }
-        f32x4 sc[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int t2 = 0; t2 < 2; ++t2) sc[r][t2] = M::score(dot[r][t2]);
-        if (!plain) rows.mask(a, sg, s, t0, g, sc);
-        typename M::P pw[R];
-        rows.soften(a, sc, pw);
+      };
+      auto add = [&](const u32x4 *buf, const typename M::P (&pw)[R]) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const u32x4 v[1] = {buf[UNITS + g * D + 16 * d + m]};
@@ -537,18 +539,24 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
           for (int r = 0; r < R; ++r) rows.o[r][d] = M::pv(v, pw[r], rows.o[r][d]);
         }
       };
-      auto stage = [&](int l, u32x4 (&now)[ST][2 * UNITS], u32x4 (&next)[ST][2 * UNITS]) {
+      auto work = [&](int l, u32x4 *buf) {
+        const int t0 = sg.tile(l);
+        const bool plain = sg.plain(a, t0);
+        if (!plain) clean(t0, buf + UNITS);
+        f32x4 sc[R][2];
+        scores(buf, sc);
+        if (!plain) rows.mask(a, sg, s, t0, g, sc);
+        typename M::P pw[R];
+        rows.soften(a, sc, pw);
+        add(buf, pw);
+      };
+      for (int l = sg.l0, at = 0; l < sg.l1; l += ST, at ^= 1) {
         __syncthreads();  // this stage is whole, and nobody reads the other buffer any more
-        convert(sg, l + ST, next);
+        convert(sg, l + ST, s_t[at ^ 1]);
         send(sg, l + 2 * ST);
 #pragma unroll 1
         for (int k = 0; k < ST; ++k)
-          if (l + k < sg.l1) work(l + k, now[k]);
-      };
-
-      for (int l = sg.l0; l < sg.l1; l += 2 * ST) {
-        stage(l, s_a, s_b);
-        if (l + ST < sg.l1) stage(l + ST, s_b, s_a);
+          if (l + k < sg.l1) work(l + k, s_t[at][k]);
       }
       __syncthreads();
       if (s_odd)
@@ -557,7 +565,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
           if (sg.plain(a, t0)) continue;
           if (my_tile == 0) {
             send(sg, l);
-            convert(sg, l, s_a);
+            convert(sg, l, s_t[0]);
           }
           __syncthreads();
 #pragma unroll
@@ -565,7 +573,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(wide4_occ<D,
             const unsigned vis = rows.view(a, sg, s, t0, r, g);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-              const u32x4 v[1] = {M::cut(s_a[0][UNITS + g * D + 16 * d + m], sg.end() - t0 - 8 * g)};
+              const u32x4 v[1] = {M::cut(s_t[0][0][UNITS + g * D + 16 * d + m], sg.end() - t0 - 8 * g)};
               rows.odd_values(r, d, v, vis);
             }
           }

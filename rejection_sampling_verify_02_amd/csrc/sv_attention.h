@@ -454,8 +454,8 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   // single rounds and shares of them as equal as can be (units of 257 to 16001 slots, one a
   // workgroup: 392 us, so 343).
   const bool aligned = (unsigned)a.B * (unsigned)(a.Hkv * a.n_rt) <= a.grid && ((long long)a.W << a.page_shift) < (1 << 27);
-  unsigned v = 0, ex = 0, total = 0, lead = 0;
-  auto scan = [&](unsigned most) {  // of every sequence's parts; for the first NT (all of them, mostly) v and ex stay
+  unsigned v = 0, ex = 0, total = 0;
+  auto scan = [&](unsigned most, unsigned lead = 0) {  // of every sequence's parts; for the first NT (all of them, mostly) v and ex stay
     total = 0;
     for (int b0 = (a.B - 1) / NT * NT; b0 >= 0; b0 -= NT) {
       v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most, lead) * (unsigned)a.Hkv : 0u;
@@ -498,10 +498,10 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   }
   // Shares that run on: a unit that begins in one costs it the time of LEAD rounds besides its own.
   if (LEAD > 0 && most == 1u && share > 1u) {
-    lead = LEAD;
-    scan(1u);
+    scan(1u, LEAD);
     share = (total + a.grid - 1) / a.grid;
   }
+  auto lead = [&] { return LEAD > 0 && most == 1u && share > 1u ? LEAD : 0u; };
   // Consecutive shares on one XCD (block p runs on XCD p % LANES), as many on each: the row
   // tiles of a key head read the same keys and values through that XCD's L2.
   const unsigned shares = (total + share - 1) / share, per_xcd = (shares + LANES - 1) / LANES;
@@ -517,7 +517,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   } else {
     unsigned seen = 0;
     for (int b0 = 0; seen <= pos; b0 += NT) {
-      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most, lead) * (unsigned)a.Hkv : 0u;
+      v = (b0 + tid < a.B) ? head_parts<RT, ROUND>(a, seq_of(a, b0 + tid), most, lead()) * (unsigned)a.Hkv : 0u;
       unsigned tot;
       ex = seen + block_excl_scan(v, s.w, tot);
       if (pos >= ex && pos < ex + v) {
@@ -535,7 +535,7 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
   int code = 0, code_b = -1;           // the code of sequence code_b
   int books_b = -1, books_rt = -1;     // the row tile whose books are in LDS
   while (pos < pos_end) {
-    const unsigned per_head = head_parts<RT, ROUND>(a, g.sq, most, lead);
+    const unsigned per_head = head_parts<RT, ROUND>(a, g.sq, most, lead());
     if (off >= per_head * (unsigned)a.Hkv) {
       off -= per_head * (unsigned)a.Hkv;
       g.sq = seq_of(a, ++g.b);
@@ -545,17 +545,21 @@ SVD void attn_share(const AttnArgs &a, const SharedBooks &s, Begin begin, Run ru
     unsigned r0 = off - (unsigned)g.h * per_head;
     g.rt = 0;
     g.sp = span_of<RT>(a, g.sq, 0);
-    unsigned rounds = rounds_of<ROUND>(g.sp), parts = parts_of(rounds, most) + lead;
+    unsigned rounds = rounds_of<ROUND>(g.sp), parts = parts_of(rounds, most) + lead();
     while (r0 >= parts) {
       r0 -= parts;
       g.sp = span_of<RT>(a, g.sq, ++g.rt);
       rounds = rounds_of<ROUND>(g.sp);
-      parts = parts_of(rounds, most) + lead;
+      parts = parts_of(rounds, most) + lead();
     }
     const unsigned r1 = min(parts, r0 + (pos_end - pos));
     // parts of a unit differ by a round at most (parts <= grid and rounds < 2^22 where they are not the same)
     // (with a lead: the rounds behind it, none perhaps)
-    auto round_at = [&](unsigned r) { return lead > 0 ? max(r, lead) - lead : parts == rounds ? r : r * rounds / parts; };
+    auto round_at = [&](unsigned r) {
+      if constexpr (LEAD > 0)
+        if (lead() > 0) return (unsigned)__builtin_amdgcn_readfirstlane((int)(max(r, LEAD) - LEAD));
+      return parts == rounds ? r : r * rounds / parts;
+    };
     g.l0 = (int)(round_at(r0) * ROUND);
     g.l1 = min(g.sp.tiles, (int)(round_at(r1) * ROUND));
     const bool first = r0 == 0;
@@ -682,13 +686,19 @@ struct Rows {
   // in it, which for scores around 10^9 is more than 2^7, and the weights were infinite or none.
   SVD void soften(const AttnArgs &a, f32x4 (&sc)[R][2], typename M::P (&p)[R]) {
     float top[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) top[r] = top_of(sc[r]);
+    follow(a, top);
+    weigh(a, sc, p);
+  }
+  SVD static float top_of(const f32x4 (&sc)[2]) {
+    const f32x4 x = sc[0], y = sc[1];
+    return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+  }
+  SVD void follow(const AttnArgs &a, const float (&top)[R]) {
     bool past = false;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const f32x4 x = sc[r][0], y = sc[r][1];
-      top[r] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
-      past |= top[r] > lim[r];
-    }
+    for (int r = 0; r < R; ++r) past |= top[r] > lim[r];
     if (__any(past)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -702,6 +712,8 @@ struct Rows {
         lim[r] = mx + a.slack;
       }
     }
+  }
+  SVD void weigh(const AttnArgs &a, f32x4 (&sc)[R][2], typename M::P (&p)[R]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
 #pragma unroll
