@@ -19,6 +19,10 @@
 //                    threshold needs it, and draws: the chunk whose cumulative kept weight passes u
 //                    times the total, and the token in it
 //   k_filter_write   the row again, with -inf below the threshold
+//
+// Bound by the weights: 26 vector instructions and a place in LDS for a logit.  320 rows of 128256
+// in bf16, top-p 0.9: scan 42 us (its bytes 12), plan 10, gather 27, pick 13, write 28 (the
+// row read and written; a copy takes 34).  64 rows drawn from: 13, 9, 10, 13.
 
 #include "sv_common.h"
 

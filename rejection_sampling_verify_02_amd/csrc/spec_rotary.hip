@@ -6,6 +6,12 @@
 // t = position * inv_freq[j].  What a call has to move is its inputs once and its outputs once;
 // the angles are one for each token and pair, whatever the heads, so a workgroup takes a few
 // tokens, computes their cosines and sines once into LDS and streams the heads past them.
+//
+// Bound by bytes where there are many tokens: 8 prompts of up to 999, 32 query and 8 key heads of
+// 128 in bf16, 36 us for 140 MB read and written (3.9 TB/s; a copy reaches 4.8), into 4 bits 39 us.
+// 64 chains of 5 take 6 and 13 us: latency.  Queries have workgroups apart from keys and values,
+// each with the next piece's loads on their way while it turns this one's (together and one piece
+// at a time: 54 us into 4 bits).
 
 #include "sv_fp4.h"
 
