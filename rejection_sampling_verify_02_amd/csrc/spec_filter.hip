@@ -697,6 +697,8 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
   R.cuts = p.cuts;
   R.whole = p.whole;
   const int over_jt = R.jt;  // the bin that a.over goes by
+  unsigned here = ~0u;       // the tokens of this step's range, at most
+  unsigned least = 0;        // no token below this key is kept, and what is kept fits the list
   if (tid < BINS) {
     s.row.mass[tid] = p.mass[tid];
     s.row.count[tid] = p.count[tid];
@@ -726,40 +728,39 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
       }
       if (step == END) break;
       R.begin(step, bin, above, target, lo, hi);
+      here = ~0u;
     }
+    if (here == ~0u && !R.far) here = s.row.count[bin];
     const unsigned span = hi - lo;
     const int bits = 32 - __clz((int)(span | 1u)), sh = bits > 8 ? bits - 8 : 0;
     for (int i = tid; i < 256; i += PICK_NT) s.hist[i] = 0;
     if (tid == 0) s.total = 0;
 
-    auto look = [&](int n) {  // at the first n of the list
-      w64 part = 0;
-      for (int i = tid; i < n; i += PICK_NT) {
-        const unsigned k = s.list_key[i];
-        if (k < lo || k > hi) continue;
-        if (step == COUNT) {
-          atomicAdd(&s.hist[(k - lo) >> sh], 1ull);
+    w64 part = 0;
+    auto take = [&](unsigned k, int at) {  // a token's key, and its place in the row
+      if (k < lo || k > hi) return;
+      if (step == COUNT) {
+        atomicAdd(&s.hist[(k - lo) >> sh], 1ull);
+      } else {
+        int j;
+        const w64 w = R.weight(K::value(k), j);
+        if (step == MASS) {
+          atomicAdd(&s.hist[(k - lo) >> sh], w);
+        } else if (step == REST) {
+          part += w;
+        } else if (step == DRAWN) {
+          atomicAdd(&s_chunk[at / FC], w);
         } else {
-          int j;
-          const w64 w = R.weight(K::value(k), j);
-          if (step == MASS) {
-            atomicAdd(&s.hist[(k - lo) >> sh], w);
-          } else if (step == REST) {
-            part += w;
-          } else if (step == DRAWN) {
-            atomicAdd(&s_chunk[s.list_at[i] / FC], w);
-          } else {
-            atomicAdd(&s.row.mass[j], w);
-            atomicAdd(&s.row.count[j], 1u);
-          }
+          atomicAdd(&s.row.mass[j], w);
+          atomicAdd(&s.row.count[j], 1u);
         }
       }
-      if (part) atomicAdd(&s.total, part);
     };
+    bool direct = false;
     if (lo < list_lo || hi > list_hi) {  // gather
-      // all that is to come, if it fits; else this step's range, in pieces where that does not fit
-      const unsigned g_lo = R.whole && step != ALL ? R.first_of(R.jt) : lo, g_hi = R.whole && step != ALL ? R.top_key : hi;
-      const bool fits = step != ALL && (R.whole || (!R.far && s.row.count[bin] <= (unsigned)LIST));
+      // all that is to come, if it fits; else this step's range, without a list where that does not fit
+      const unsigned g_lo = R.whole && step != ALL ? max(R.first_of(R.jt), least) : lo, g_hi = R.whole && step != ALL ? R.top_key : hi;
+      direct = step == ALL || (!R.whole && here > (unsigned)LIST);
       const float z_lo = K::value(g_lo), z_hi = K::value(g_hi);
       __syncthreads();
       if (tid == 0) s.n_list = 0;
@@ -788,32 +789,35 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
           o += __popcll(b[e]);
         }
       };
-      if (fits) {
-        constexpr int AHEAD = 8;
-        for (int i0 = tid; i0 - tid < r.n; i0 += AHEAD * PICK_NT) {
-          u32x4 w[AHEAD];
+      constexpr int AHEAD = 8;
+      for (int i0 = tid; i0 - tid < r.n; i0 += AHEAD * PICK_NT) {
+        u32x4 w[AHEAD];
 #pragma unroll
-          for (int k = 0; k < AHEAD; ++k) w[k] = r.load(i0 + k * PICK_NT);
+        for (int k = 0; k < AHEAD; ++k) w[k] = r.load(i0 + k * PICK_NT);
+        if (!direct) {
 #pragma unroll
           for (int k = 0; k < AHEAD; ++k) add(w[k], i0 + k * PICK_NT);
+          continue;
         }
-        list_lo = g_lo;
-        list_hi = g_hi;
-      } else {
-        list_lo = 1;
-        list_hi = 0;
-        for (int i0 = tid; i0 - tid < r.n; i0 += PICK_NT) {
-          add(r.load(i0), i0);
-          __syncthreads();
-          look(s.n_list);
-          __syncthreads();
-          if (tid == 0) s.n_list = 0;
-          __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < AHEAD; ++k) {  // one stretch of code for all of them, w[0] being the next
+          const int i = i0 + k * PICK_NT;
+          float z[E];
+          r.unpack(w[0], i, z);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (z[e] >= z_lo && z[e] <= z_hi) take(K::of(z[e]), i * E + e);
+#pragma unroll
+          for (int j = 0; j + 1 < AHEAD; ++j) w[j] = w[j + 1];
         }
       }
+      list_lo = direct ? 1u : g_lo;
+      list_hi = direct ? 0u : g_hi;
     }
     __syncthreads();
-    if (list_lo <= list_hi) look(min(s.n_list, LIST));
+    if (!direct)
+      for (int i = tid, n = min(s.n_list, LIST); i < n; i += PICK_NT) take(s.list_key[i], s.list_at[i]);
+    if (part) atomicAdd(&s.total, part);
     __syncthreads();
 
     if (step == ALL) {
@@ -864,6 +868,7 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
       const unsigned pick = s.key;
       above = s.above;
       const w64 upto = s.total;
+      if (step == COUNT) here = (unsigned)s.hist[pick];
       __syncthreads();
       lo += pick << sh;
       if (hi - lo >= 1u << sh) hi = lo + ((1u << sh) - 1u);
@@ -872,6 +877,10 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
         if (step == COUNT) {
           R.tau = max(R.tau, lo);
           R.jt = R.bin_of(K::value(R.tau));
+          if (!R.whole && upto <= (unsigned)LIST) {  // of the tokens from tau up
+            R.whole = true;
+            least = R.tau;
+          }
           step = R.by_p ? REST : DRAWN;
         } else {
           R.tau = lo;
