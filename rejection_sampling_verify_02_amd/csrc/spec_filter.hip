@@ -1078,6 +1078,16 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   const uintptr_t in = (uintptr_t)logits, to = (uintptr_t)out, size = (uintptr_t)rows * (uintptr_t)V * esz;
   if (!draw && in != to && in < to + size && to < in + size) return SV_ERR_PARAM;
   if (ws_bytes < p.total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
+  // several kernels read what is set for each row
+  const void *const read[] = {u, pol->temperatures, pol->top_ks, pol->top_ps, pol->min_ps}, *const written[] = {status, tokens};
+  auto meet = [&](const void *x, const void *y) {
+    const uintptr_t p = (uintptr_t)x, q = (uintptr_t)y, n = (uintptr_t)rows * 4;
+    return p && q && p < q + n && q < p + n;
+  };
+  for (const void *w : written)
+    for (const void *r : read)
+      if (meet(w, r)) return SV_ERR_PARAM;
+  if (meet(status, tokens)) return SV_ERR_PARAM;
   char *base = static_cast<char *>(ws);
   FilterArgs a = {};
   a.logits = logits;

@@ -160,6 +160,19 @@ def test_filter_refuses(lib, kw, status):
     assert filtered(lib, **kw) == status
 
 
+def test_outputs_apart_from_settings(lib):
+    """An output on u, on a row's settings or on the other output would be read by later kernels: refused."""
+    far = [FAKE + i * 4096 for i in range(8)]
+    for i in range(4):
+        pol = [None] * 4
+        pol[i] = far[i]
+        for at in (far[i], far[i] + 12, far[i] - 12):
+            assert sample(lib, pol=(1.0, 0, 0.9, 0.0, *pol), u=far[4], tok=far[5], st=at) == 8
+            assert sample(lib, pol=(1.0, 0, 0.9, 0.0, *pol), u=far[4], tok=at, st=far[5]) == 8
+            assert filtered(lib, pol=(1.0, 0, 0.9, 0.0, *pol), st=at) == 8
+    assert sample(lib, u=far[4], tok=far[5], st=far[4]) == 8 and sample(lib, u=far[4], tok=far[5], st=far[5] + 8) == 8
+
+
 def test_sizes_and_plans(lib):
     small, large = (sv.sv_attention4_workspace_bytes(*x) for x in ((1, 1, 8, 8, 64, 16, 1), (64, 32, 32, 8, 128, 64, 1000)))
     assert 256 < small < large and small % 256 == 0 and large % 256 == 0 and sv.sv_attention4_workspace_bytes(1, 1, 8, 8, 80, 16, 1) == 256
