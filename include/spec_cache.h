@@ -283,8 +283,9 @@ sv_status spec_cache_fork(int32_t *page_table, int32_t *seq_pages, int32_t *ref_
  *   positions    [B, N] int32 or NULL
  *   q_out        [B, N, Hq, D] dtype out, not overlapping q: rows of nodes behind n_new are zero,
  *                those of a sequence with a code NaN
- *   row_status   [B] int32 out: 0, prior's code, SV_ROW_BAD_LENGTH, SV_ROW_BAD_TREE or
- *                SV_ROW_BAD_PAGE; nothing of the sequence is then written to the cache
+ *   row_status   [B] int32 out, on none of the int32 inputs: 0, prior's code, SV_ROW_BAD_LENGTH,
+ *                SV_ROW_BAD_TREE or SV_ROW_BAD_PAGE; nothing of the sequence is then written to the
+ *                cache
  * q, k, v, their strides, the pages and q_out are multiples of 16 bytes.  The slots' pages must be
  * the sequence's own, as for the append. */
 typedef struct {
@@ -323,7 +324,7 @@ sv_status spec_cache_read(const void *k_pages, const void *k_scales, const void 
 /* ---- attention over a cache in 4 bits ----
  *
  * spec_paged_attention_after with such a cache: q and out are bf16, keys and values what their
- * codes stand for. */
+ * codes stand for, and row_status lies on none of the int32 inputs of a sequence. */
 size_t sv_attention4_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
                                      int32_t page_size, int32_t table_width);
 sv_status spec_paged_attention4(const void *q, int64_t q_stride_b, int64_t q_stride_n,

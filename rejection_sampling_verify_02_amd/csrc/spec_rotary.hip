@@ -613,6 +613,7 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
     const uintptr_t q1 = q0 + (uintptr_t)(B - 1) * (uintptr_t)a.q_sb + (uintptr_t)(N - 1) * (uintptr_t)a.q_sn + row, o1 = o0 + (uintptr_t)B * N * row;
     if (q0 < o1 && o0 < q1) return SV_ERR_PARAM;
   }
+  if (codes_on_inputs(row_status, B, N, cache_len, n_new, parent, positions)) return SV_ERR_PARAM;
   a.k_pages = static_cast<char *>(k_pages);
   a.k_scales = static_cast<char *>(k_scales);
   a.v_pages = static_cast<char *>(v_pages);

@@ -160,6 +160,17 @@ def test_filter_refuses(lib, kw, status):
     assert filtered(lib, **kw) == status
 
 
+def test_codes_apart_from_inputs(lib):
+    """Row codes on what other workgroups may still have to read of a sequence: refused."""
+    far = [FAKE + i * 4096 for i in range(1, 6)]
+    for name, last in (("lens", 12), ("news", 12), ("parent", 76), ("pos", 76)):
+        own = dict(zip(("lens", "news", "parent", "pos"), far))
+        for at in (own[name], own[name] - 12, own[name] + last):
+            assert rotary(lib, **{**own, "st": at}) == 8
+            if name != "pos":
+                assert attention(lib, **{k: v for k, v in own.items() if k != "pos"}, st=at) == 8
+
+
 def test_outputs_apart_from_settings(lib):
     """An output on u, on a row's settings or on the other output would be read by later kernels: refused."""
     far = [FAKE + i * 4096 for i in range(8)]
