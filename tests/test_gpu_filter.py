@@ -100,6 +100,29 @@ def test_large_vocabularies(dev, dtype, kind):
                 assert near < NEAR or np.array_equal(out[b].double().cpu().numpy(), np.where(z[b] >= low, z[b], -np.inf))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [0.02, 0.15, 0.6])
+def test_top_k_among_tokens_of_hardly_any_weight(dev, dtype, T):
+    """The k-th token lies among tens of thousands whose weights are below 2^-32 of the largest, which
+    are counted together; what is kept is few again."""
+    import torch
+    import rejection_sampling_verify_02_amd as sv
+    rows, V = 3, 40009
+    rng = np.random.default_rng(17)
+    t, z = logits(rng, rows, V, dtype, "peaked")
+    t = t.to(dev)
+    u = np.array([0.2, 0.9, 1 - 2.0 ** -24], np.float32)
+    for k, p, m in ((2, 0.9, 0.0), (72, 0.9, 0.0), (500, 1.0, 0.0), (9000, 0.999, 0.0), (9000, 1.0, 1e-30), (20000, 0.5, 1e-12)):
+        tok, st = sv.spec_sample(t, torch.from_numpy(u).to(dev), T, k, top_p=p, min_p=m)
+        want = [step_ref.draw(z[b], u[b], T, k, p, m) for b in range(rows)]
+        sure = np.array([x for _, x in want]) > NEAR
+        assert not st.any() and np.array_equal(tok.cpu().numpy()[sure], np.array([x for x, _ in want])[sure])
+        out, _ = sv.spec_filter_logits(t, T, k, top_p=p, min_p=m)
+        for b in range(rows):
+            low, near = step_ref.kept(z[b], T, k, p, m)
+            assert near < NEAR or np.array_equal(out[b].double().cpu().numpy(), np.where(z[b] >= low, z[b], -np.inf))
+
+
 def test_rows_with_settings_of_their_own(dev):
     import torch
     import rejection_sampling_verify_02_amd as sv
