@@ -17,7 +17,7 @@
 //                 keys could go into the scaled matrix instruction as they are, the queries as two
 //                 8-bit parts; but that one's sums are only good to 2^-12 of their terms.
 //   k_attn4_wide  more rows.  The waves share each tile through LDS as bf16, converted once by one
-//                 of them.  16 trees of 32 nodes, 4 heads a key head: 92 us; the products alone
+//                 of them.  16 trees of 32 nodes, 4 heads a key head: 94 us; the products alone
 //                 would be 37.  The rest is what a wave does between them, weights and conversions,
 //                 with one other wave on its SIMD to fill in: all its registers are taken.  (Two
 //                 tiles at a time, one's weights beside the other's products, spills in the loop:

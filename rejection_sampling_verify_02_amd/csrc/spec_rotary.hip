@@ -9,7 +9,7 @@
 //
 // Bound by bytes where there are many tokens: 8 prompts of up to 999, 32 query and 8 key heads of
 // 128 in bf16, 36 us for 140 MB read and written (3.9 TB/s; a copy reaches 4.8), into 4 bits 39 us.
-// 64 chains of 5 take 6 and 13 us: latency.  Queries have workgroups apart from keys and values,
+// 64 chains of 5 take 7 and 11 us: latency.  Queries have workgroups apart from keys and values,
 // each with the next piece's loads on their way while it turns this one's (together and one piece
 // at a time: 54 us into 4 bits).
 
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
   auto last_token = [&](int l) { return min(a.N, (chunk + 1) * ROT_TOKENS - (l & (ROT_TOKENS - 1))); };
   int i0 = first_token(len), i1 = last_token(len);
   // The part's heads of the queries, and of the keys and values.
-  const int q0 = part < a.q_parts ? min(a.Hq, part * a.q_part) : a.Hq, q1 = min(a.Hq, q0 + a.q_part);
+  const int q0 = part < a.q_parts ? min(a.Hq, part * a.q_part) : a.Hq, q1 = q0 + min(a.Hq - q0, a.q_part);
   const int h0 = part < a.q_parts ? Hkv : min(Hkv, (part - a.q_parts) * a.kv_part), h1 = min(Hkv, h0 + a.kv_part);
 
   // Queries, and the keys of a cache of the inputs' type, in jobs: 16 bytes and, where the head's
@@ -591,8 +591,8 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
   const int kv_parts = parts(Hkv < 8 ? Hkv : 8);
   a.parts = a.q_parts + kv_parts;
   if (wgs > MAX_WGS / a.parts) return SV_ERR_SHAPE;
-  a.q_part = a.q_parts ? (Hq + a.q_parts - 1) / a.q_parts : 0;
-  a.kv_part = (Hkv + kv_parts - 1) / kv_parts;
+  a.q_part = a.q_parts ? (Hq - 1) / a.q_parts + 1 : 0;
+  a.kv_part = (Hkv - 1) / kv_parts + 1;
   if (!k || !v || !k_pages || !v_pages || (f4 && (!k_scales || !v_scales)) || !page_table || !cache_len || !row_status ||
       (q && !q_out) || (R && !rotary->inv_freq))
     return SV_ERR_NULL;
