@@ -9,9 +9,9 @@
 //
 // Bound by bytes where there are many tokens: 8 prompts of up to 999, 32 query and 8 key heads of
 // 128 in bf16, 36 us for 140 MB read and written (3.9 TB/s; a copy reaches 4.8), into 4 bits 39 us.
-// 64 chains of 5 take 7 and 11 us: latency.  Queries have workgroups apart from keys and values,
-// each with the next piece's loads on their way while it turns this one's (together and one piece
-// at a time: 54 us into 4 bits).
+// A token each of 64 sequences takes 7 us, short chains into 4 bits 11: latency.  Queries have
+// workgroups apart from keys and values, each with the next piece's loads on their way while it
+// turns this one's (together and one piece at a time: 54 us into 4 bits).
 
 #include "sv_fp4.h"
 
