@@ -21,8 +21,8 @@
 //   k_filter_write   the row again, with -inf below the threshold
 //
 // Bound by the weights: 26 vector instructions and a place in LDS for a logit.  320 rows of 128256
-// in bf16, top-p 0.9: scan 42 us (its bytes 12), plan 10, gather 27, pick 13, write 28 (the
-// row read and written; a copy takes 34).  64 rows drawn from: 13, 9, 10, 13.
+// in bf16, top-p 0.9: scan 42 us (its bytes 12), plan 10, gather 21, pick 14, write 28 (the
+// row read and written; a copy takes 34).  64 rows drawn from: 13, 8, 8, 13.
 
 #include "sv_common.h"
 
@@ -594,12 +594,14 @@ __global__ __launch_bounds__(PLAN_NT) void k_filter_plan(const FilterArgs a) {
 // ---------------------------------------------------------------- gather
 
 // As many workgroups as the scan had look through the row's chunks at once (one a row, in
-// k_filter_pick, 64 rows: 11 of its 35 us).
+// k_filter_pick, 64 rows: 11 of its 35 us).  Their places on the row's list are given out a workgroup
+// at a time (a wave at a time, 320 rows: 28 us for 21).
 template <typename T, bool DRAW>
 __global__ __launch_bounds__(NT) void k_filter_gather(const FilterArgs a) {
   typedef Key<T> K;
   constexpr int E = Fmt<T>::VEC, NV = FPT / E;
   __shared__ w64 s_over[NW];
+  __shared__ int s_n[NW], s_at;
   const int tid = threadIdx.x, lane = lane_id(), wid = tid / WAVE;
   const int row = (int)(blockIdx.x / (unsigned)a.chunks), c = (int)(blockIdx.x % (unsigned)a.chunks);
   const RowPlan &p = a.plans[row];
@@ -636,9 +638,19 @@ __global__ __launch_bounds__(NT) void k_filter_gather(const FilterArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) n += __popcll(__ballot(z[k][e] >= z_lo && z[k][e] <= z_hi));
   }
+  if (lane == 0) s_n[wid] = n;
+  __syncthreads();
+  if (tid == 0) {  // one addition a workgroup
+    int all = 0;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) all += s_n[v];
+    s_at = all ? (int)atomicAdd(&a.n_list[row], (unsigned)all) : 0;
+  }
+  __syncthreads();
   if (n == 0) return;
-  int o = 0;
-  if (lane == 0) o = (int)atomicAdd(&a.n_list[row], (unsigned)n);
+  int o = s_at;
+#pragma unroll
+  for (int v = 0; v < NW; ++v) o += v < wid ? s_n[v] : 0;
   o = __builtin_amdgcn_readfirstlane(o);
   uint2 *list = a.list + (size_t)row * a.cap;
 #pragma unroll
