@@ -295,16 +295,10 @@ SVD unsigned first_key(unsigned lo, unsigned hi, F pred) {
   return hi;
 }
 
-SVD w64 shfl_up64(w64 v, int d) {
-  const unsigned lo = __shfl_up((unsigned)v, d), hi = __shfl_up((unsigned)(v >> 32), d);
-  return ((w64)hi << 32) | lo;
-}
 SVD w64 wave_incl(w64 v) {
-#pragma unroll
-  for (int d = 1; d < WAVE; d <<= 1) {
-    const w64 y = shfl_up64(v, d);
-    if (lane_id() >= d) v += y;
-  }
+#define STEP(C, R) v += ((w64)dpp_u<C, R>((unsigned)(v >> 32), 0u) << 32) | dpp_u<C, R>((unsigned)v, 0u);
+  SV_SCAN_STEPS(STEP)
+#undef STEP
   return v;
 }
 SVD w64 wave_total64(w64 v) {
