@@ -317,7 +317,7 @@ struct Row {
   unsigned flags, top_key;
   float zmax;
   bool far;
-  double off, least;
+  double off, least, inv64;
   // Lane l has bins 2 l and 2 l + 1, and what lies in front of them.
   w64 m0, m1, pm, kept;
   unsigned c0, c1, pc, n_all;
@@ -339,6 +339,7 @@ struct Row {
     O = octave_of(Q);
     rest = octave_of(Q - (BINS - 1));
     off = far ? (double)z : 0.0;
+    inv64 = 1.0 / pol.c64;  // for guesses
     least = far ? -1e9 / pol.c64 : (double)lowest_of(pol.c64);
     by_p = pol.p < 1.0f;
   }
@@ -355,7 +356,7 @@ struct Row {
   SVD unsigned first_of(int j) const {
     if (j >= BINS - 1) return K::lowest();
     auto in = [&](unsigned k) { return Q - quarter_of(arg(K::value(k)), pol.c64) <= j; };
-    return near_key(K::of((float)((double)((Q - j) * 16) / pol.c64 + off)), in);
+    return near_key(K::of((float)((double)((Q - j) * 16) * inv64 + off)), in);
   }
   template <typename P>
   SVD unsigned near_key(unsigned g, P in) const {
@@ -947,12 +948,16 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
   const double goal = (double)u * (double)s.total;
   w64 base = s.above;
   // ---- the token: the chunk's kept weights in index order
-  constexpr int STEP = FC / E;
-  for (int k = 0; k < STEP; k += PICK_NT) {
-    const int i = c * STEP + k + tid;
+  constexpr int TURNS = FC / E / PICK_NT;
+  u32x4 raw[TURNS];
+#pragma unroll
+  for (int k = 0; k < TURNS; ++k) raw[k] = r.load((c * TURNS + k) * PICK_NT + tid);
+#pragma unroll
+  for (int k = 0; k < TURNS; ++k) {
+    const int i = (c * TURNS + k) * PICK_NT + tid;
     w64 w[E], sum = 0;
     float z[E];
-    r.unpack(r.load(i), i, z);
+    r.unpack(raw[k], i, z);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       int j;
