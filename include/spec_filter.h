@@ -11,8 +11,8 @@
  * Tokens with equal logits are kept or dropped together, so that the kept set is all logits at or
  * above one of them, whatever their order.  T == 0 keeps the lowest-index largest logit alone.
  * Weights are taken in 64 bits and summed as whole numbers: the same call gives the same bits, and
- * a draw is that of the definition but where a cumulative weight lies within about 10^-10 of its
- * threshold.
+ * draws and thresholds are those of the definition but where a cumulative weight lies within 10^-10
+ * of the total of its threshold, for any V.
  *
  * spec_filter_logits writes the logits that are kept, and -inf elsewhere: spec_verify,
  * spec_tree_verify, spec_overlap and spec_typical_verify take such rows with top_k = 0 and the same

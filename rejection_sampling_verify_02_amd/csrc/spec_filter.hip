@@ -6,8 +6,12 @@
 // where W counts tokens (top-k) or adds their weights (top-p).  Weights are 2^x for
 // x = z log2(e) / T.  They are fixed-point numbers relative to a power of two near the row's
 // largest, so that sums do not depend on their order, and they are taken in 64 bits to
-// 4 * 10^-11: a vocabulary of 10^5 tokens of probability 10^-6 leaves cumulative weights no room for
-// float32's rounding.
+// 5 * 10^-11: a vocabulary of 10^5 tokens of probability 10^-6 leaves cumulative weights no room for
+// float32's rounding.  Bins add up weights as they are, each token's to a unit of 2^-35 of its own
+// octave; where weights of different octaves meet, the unit goes by the row's total, which is put
+// between 2^59 and 2^61 units: cutting off what is smaller costs a sum over 2^24 tokens, the largest of
+// them or all, 2^-35 of itself at most (a unit that went by the vocabulary's size and the row's largest:
+// 10^-8 at 2^18 tokens, 2 * 10^-5 at 2^24, and thresholds with hundreds of tokens too many).
 //
 //   k_filter_scan    a chunk of a row a workgroup, one read of the logits: the chunk's largest, and
 //                    counts and weights by quarter octave of the weight (the same ones for every
@@ -52,11 +56,11 @@ struct ChunkSum {
 
 // What k_filter_plan found out about a row.
 struct RowPlan {
-  w64 mass[BINS];        // the row's bins: weights relative to the octave of q, and numbers
+  w64 mass[BINS];        // the row's bins: weights in units of 2^-35 of each bin's octave, and numbers
   unsigned count[BINS];
   w64 above;             // of the first step: what lies above its range
   double target;         // and what it looks for
-  int q, step, bin, jt;  // the largest's quarter octave; the step, its bin, the lowest threshold's bin
+  int q, F, step, bin, jt;  // the largest's quarter octave; its octave's units; the step, its bin, the lowest threshold's bin
   unsigned flags, tau, lo, hi, list_lo, list_hi;  // thresholds so far, the step's range, the list's
   float zmax;
   int by_k, by_m, cuts, whole;
@@ -65,7 +69,7 @@ struct RowPlan {
 struct FilterArgs {
   const void *logits;
   const float *u;
-  int rows, V, chunks, F;  // F: bits behind the point of a row's weights
+  int rows, V, chunks, F0;  // F0: 2^F0 units of the largest's octave, V times, fit 62 bits
   sv_policy policy;
   ChunkSum *sums;          // [rows][chunks]
   RowPlan *plans;          // [rows]
@@ -313,12 +317,12 @@ struct Row {
   typedef Key<T> K;
   RowShared &s;
   Policy pol;
-  int F, Q, O, rest;
+  int F, F0, Q, O, rest;
   unsigned flags, top_key;
   float zmax;
   bool far;
   double off, least, inv64;
-  // Lane l has bins 2 l and 2 l + 1, and what lies in front of them.
+  // Lane l has bins 2 l and 2 l + 1, and what lies in front of them, in units of 2^-F of the octave O.
   w64 m0, m1, pm, kept;
   unsigned c0, c1, pc, n_all;
   // the cuts: kept are keys from tau on; the lowest bin that a threshold can lie in; whether everything
@@ -327,7 +331,7 @@ struct Row {
   unsigned tau;
   int jt;
 
-  SVD Row(RowShared &sh, const FilterArgs &a, int row) : s(sh), pol(policy_of(a, row)), F(a.F) {}
+  SVD Row(RowShared &sh, const FilterArgs &a, int row) : s(sh), pol(policy_of(a, row)), F(a.F0), F0(a.F0) {}
   // Rows out of range (F_FAR) are taken relative to their largest logit, and their bins are counted one
   // token at a time; differences so large that their weight is nothing are cut off.
   SVD void set(unsigned fl, float z, int q) {
@@ -345,13 +349,14 @@ struct Row {
   }
   SVD double arg(float z) const { return fmax((double)z - off, least); }
   SVD int bin_of(float z) const { return min(Q - quarter_of(arg(z), pol.c64), BINS - 1); }
-  SVD w64 weight(float z, int &bin) const {
-    const Weight w = weight_of(arg(z), pol.c64, s.tab, rest);
-    bin = min(Q - w.q, BINS - 1);
+  SVD Weight plain_weight(float z) const { return weight_of(arg(z), pol.c64, s.tab, rest); }
+  SVD w64 weight(float z) const {
+    const Weight w = plain_weight(z);
     return shifted(w.m, F - W_BITS - (O - max(octave_of(w.q), rest)));
   }
-  // The weight of a chunk's bin, of quarter octave q, as the row's weights are.
+  // The weight of a chunk's bin, of quarter octave q: as the row's weights are, and as its bin j adds them up.
   SVD w64 mass_of_chunk(int q, w64 x) const { return shifted(x & ((1ull << W_COUNT) - 1ull), F - W_BITS - (O - octave_of(q))); }
+  SVD w64 mass_for_bin(int q, int j, w64 x) const { return shifted(x & ((1ull << W_COUNT) - 1ull), octave_of(q) - octave_of(Q - j)); }
   // The first key of bin j, tried near where it has to be.
   SVD unsigned first_of(int j) const {
     if (j >= BINS - 1) return K::lowest();
@@ -380,10 +385,16 @@ struct Row {
     const unsigned long long b0 = __ballot((double)(pm + m0) >= w), b1 = __ballot((double)(pm + m0 + m1) >= w);
     return b1 == 0 ? BINS - 1 : 2 * (__ffsll(b1) - 1) + ((b0 >> (__ffsll(b1) - 1)) & 1 ? 0 : 1);
   }
-  SVD void prefixes() {
+  SVD void prefixes(bool units) {
     const int lane = lane_id();
-    m0 = s.mass[2 * lane];
-    m1 = s.mass[2 * lane + 1];
+    const w64 a0 = s.mass[2 * lane], a1 = s.mass[2 * lane + 1];
+    const int d0 = W_BITS + O - octave_of(Q - 2 * lane), d1 = W_BITS + O - octave_of(Q - 2 * lane - 1);
+    if (units) {  // the total in units of 2^(30 - F0), more than it is by 64 at most; F puts it below 2^61 units
+      const unsigned part = (unsigned)((shifted(a0, F0 - d0) + shifted(a1, F0 - d1)) >> 30);
+      F = F0 - 1 + __clz(__builtin_amdgcn_readlane((int)scan_add_u(part), WAVE - 1) + WAVE);
+    }
+    m0 = shifted(a0, F - d0);
+    m1 = shifted(a1, F - d1);
     c0 = s.count[2 * lane];
     c1 = s.count[2 * lane + 1];
     const w64 im = wave_incl(m0 + m1);
@@ -395,7 +406,7 @@ struct Row {
   }
   // Once the bins are known: the cuts.  Returns the first step.
   SVD int plan() {
-    prefixes();
+    prefixes(true);
     tau = K::lowest();
     jt = BINS - 1;
     by_k = pol.k > 0 && (unsigned)pol.k < n_all;
@@ -540,7 +551,7 @@ __global__ __launch_bounds__(PLAN_NT) void k_filter_plan(const FilterArgs a) {
       for (int k = 0; k < AHEAD; ++k)
         if (c0 + k * STEP < a.chunks && x[k] != 0) {
           const int j = min(R.Q - q[k], BINS - 1);
-          atomicAdd(&s.mass[j], R.mass_of_chunk(q[k], x[k]));
+          atomicAdd(&s.mass[j], R.mass_for_bin(q[k], j, x[k]));
           atomicAdd(&s.count[j], (unsigned)(x[k] >> W_COUNT));
         }
       c0 += AHEAD * STEP;
@@ -569,6 +580,7 @@ __global__ __launch_bounds__(PLAN_NT) void k_filter_plan(const FilterArgs a) {
     p.above = above;
     p.target = target;
     p.q = R.Q;
+    p.F = R.F;
     p.step = step;
     p.bin = bin;
     p.jt = R.far ? 0 : R.jt;
@@ -616,7 +628,7 @@ __global__ __launch_bounds__(NT) void k_filter_gather(const FilterArgs a) {
     if (tid < BINS) {
       const w64 x = cs.bin[tid];
       const int q = cs.q - tid, Q = p.q;
-      if (!p.cuts || Q - q < p.jt) over = shifted(x & ((1ull << W_COUNT) - 1ull), a.F - W_BITS - (octave_of(Q) - octave_of(q)));
+      if (!p.cuts || Q - q < p.jt) over = shifted(x & ((1ull << W_COUNT) - 1ull), p.F - W_BITS - (octave_of(Q) - octave_of(q)));
     }
     over = wave_total64(over);
     if (lane == 0) s_over[wid] = over;
@@ -722,7 +734,8 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
   }
   powers(s.row.tab);
   __syncthreads();
-  R.prefixes();
+  R.F = p.F;
+  R.prefixes(false);
   bool begin = R.far || step == DRAWN;  // of a step: the gather has begun the others
   for (;;) {
     if (begin) {
@@ -749,17 +762,20 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
       if (step == COUNT) {
         atomicAdd(&s.hist[(k - lo) >> sh], 1ull);
       } else {
-        int j;
-        const w64 w = R.weight(K::value(k), j);
+        if (step == ALL) {
+          const Weight w = R.plain_weight(K::value(k));
+          const int j = min(R.Q - w.q, BINS - 1);
+          atomicAdd(&s.row.mass[j], w.m);
+          atomicAdd(&s.row.count[j], 1u);
+          return;
+        }
+        const w64 w = R.weight(K::value(k));
         if (step == MASS) {
           atomicAdd(&s.hist[(k - lo) >> sh], w);
         } else if (step == REST) {
           part += w;
-        } else if (step == DRAWN) {
-          atomicAdd(&s_chunk[at / FC], w);
         } else {
-          atomicAdd(&s.row.mass[j], w);
-          atomicAdd(&s.row.count[j], 1u);
+          atomicAdd(&s_chunk[at / FC], w);
         }
       }
     };
@@ -960,8 +976,7 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
     r.unpack(raw[k], i, z);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      int j;
-      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= R.tau ? R.weight(z[e], j) : 0ull;
+      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= R.tau ? R.weight(z[e]) : 0ull;
       sum += w[e];
     }
     const w64 inc = wave_incl(sum);
@@ -1106,10 +1121,10 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   a.rows = rows;
   a.V = V;
   a.chunks = p.chunks;
-  // a row's weights are at most 2.02 each: their sum fits 62 bits
+  // a row's weights are at most 2.02 each
   int bits = 0;
   while ((1LL << bits) < V) ++bits;
-  a.F = 60 - bits < 48 ? 60 - bits : 48;
+  a.F0 = 60 - bits;
   a.policy = *pol;
   a.sums = (ChunkSum *)(base + p.sums);
   a.plans = (RowPlan *)(base + p.plans);
