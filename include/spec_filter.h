@@ -36,7 +36,8 @@ extern "C" {
 /* A setting is the scalar, or where the pointer is not NULL the row's entry of a device array.
  *   temperature  finite, >= 0;  top_k  any (<= 0: off);  top_p  in (0, 1];  min_p  in [0, 1]
  * Scalars outside are refused: SV_ERR_TEMPERATURE, SV_ERR_PARAM.  So is an output that shares memory
- * with the other, with u or with an array of settings: SV_ERR_PARAM. */
+ * with the other, with the logits (but for rows filtered in place), with u or with an array of
+ * settings: SV_ERR_PARAM. */
 typedef struct {
   float temperature;
   int32_t top_k;

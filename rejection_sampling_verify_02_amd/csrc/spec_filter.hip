@@ -1104,16 +1104,23 @@ sv_status filter_run(bool draw, const void *logits, sv_dtype dt, const float *u,
   const uintptr_t in = (uintptr_t)logits, to = (uintptr_t)out, size = (uintptr_t)rows * (uintptr_t)V * esz;
   if (!draw && in != to && in < to + size && to < in + size) return SV_ERR_PARAM;
   if (ws_bytes < p.total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
-  // several kernels read what is set for each row
-  const void *const read[] = {u, pol->temperatures, pol->top_ks, pol->top_ps, pol->min_ps}, *const written[] = {status, tokens};
-  auto meet = [&](const void *x, const void *y) {
-    const uintptr_t p = (uintptr_t)x, q = (uintptr_t)y, n = (uintptr_t)rows * 4;
-    return p && q && p < q + n && q < p + n;
+  // Several kernels read the logits and what is set for each row, and write for each row while others
+  // still read: what is written lies apart from all that is read, and from what else is written (rows
+  // over logits have been looked at above).
+  struct Range {
+    const void *p;
+    uintptr_t n;
   };
-  for (const void *w : written)
-    for (const void *r : read)
-      if (meet(w, r)) return SV_ERR_PARAM;
-  if (meet(status, tokens)) return SV_ERR_PARAM;
+  const uintptr_t ints = (uintptr_t)rows * 4;
+  const Range read[] = {{logits, size}, {u, ints}, {pol->temperatures, ints}, {pol->top_ks, ints}, {pol->top_ps, ints}, {pol->min_ps, ints}};
+  const Range written[] = {{status, ints}, {tokens, ints}, {out, size}};
+  auto meet = [](const Range &x, const Range &y) {
+    return x.p && y.p && (uintptr_t)x.p < (uintptr_t)y.p + y.n && (uintptr_t)y.p < (uintptr_t)x.p + x.n;
+  };
+  for (const Range &w : written)
+    for (const Range &r : read)
+      if (meet(w, r) && !(&w == &written[2] && &r == &read[0])) return SV_ERR_PARAM;
+  if (meet(written[0], written[1]) || meet(written[0], written[2])) return SV_ERR_PARAM;
   char *base = static_cast<char *>(ws);
   FilterArgs a = {};
   a.logits = logits;
