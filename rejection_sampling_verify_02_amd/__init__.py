@@ -349,6 +349,15 @@ def _each(x) -> bool:
     return isinstance(x, torch.Tensor) and x.dim() > 0
 
 
+def _number(x, dtype, logits, u, workspace):
+    """A tensor of one element as the number that it holds, unless it is the setting of the one row that
+    there is: of that shape, type and device, in a call that the policy's kernels take."""
+    if _each(x) and x.numel() == 1 and (x.shape != logits.shape[:1] or x.dtype is not dtype or x.device != logits.device or u is None
+                                        or isinstance(workspace, Workspace)):
+        return x.item()
+    return x
+
+
 def spec_sample(logits, u, temperature: float, top_k: int = 0, *, top_p=1.0, min_p=0.0, workspace: Workspace | None = None,
                 stream=None, out=None, events=None):
     """Batched sampling on the GPU (see include/spec_verify.h): one token per row of
@@ -359,8 +368,11 @@ def spec_sample(logits, u, temperature: float, top_k: int = 0, *, top_p=1.0, min
     With top_p below 1, min_p above 0, or settings of each row's own (temperature, top_p and
     min_p [B] float32, top_k [B] int32 tensors) the policy and its kernels are those of
     include/spec_filter.h; ``workspace`` is then a uint8 tensor or None (taken from torch's
-    allocator)."""
+    allocator).  Other tensors of one element are taken as numbers."""
     import torch
+    if _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p):
+        temperature, top_p, min_p = (_number(x, torch.float32, logits, u, workspace) for x in (temperature, top_p, min_p))
+        top_k = _number(top_k, torch.int32, logits, u, workspace)
     if _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p) or top_p != 1.0 or min_p != 0.0:
         from . import filter as _filter
         return _filter.sample(logits, u, temperature, top_k, top_p, min_p, workspace, stream, out, events)
