@@ -223,8 +223,9 @@ __global__ __launch_bounds__(NT) void k_filter_scan(const FilterArgs a) {
   }
   const bool odd = most >= 0x7f800000 || least > 0xff800000u;
   top = wave_max(top);
-  // out of range: 64 x too large, or temperatures at which even the lowest float32 weighs something
-  const unsigned far = fabs((double)top * pol.c64) < 0.99e9 && pol.c64 > 4e-30 ? 0u : (unsigned)F_FAR;
+  // out of range: 64 x too large, or temperatures at which even the lowest float32 weighs something (a
+  // chunk all far below zero says nothing of its row: k_filter_plan looks at the row's largest)
+  const unsigned far = (double)top * pol.c64 < 0.99e9 && pol.c64 > 4e-30 ? 0u : (unsigned)F_FAR;
   const unsigned fl = wave_or((odd ? (unsigned)F_ODD : 0u) | (top > -INFINITY ? F_FINITE | far : 0u));
   if (lane == 0) {
     s_top[wid] = f2key(top);
@@ -239,12 +240,12 @@ __global__ __launch_bounds__(NT) void k_filter_scan(const FilterArgs a) {
   }
   ChunkSum *out = a.sums + (size_t)row * a.chunks + c;
   const bool weigh = pol.c64 != 0.0 && flags == F_FINITE;
-  const int q = weigh ? quarter_of((double)key2f(tk), pol.c64) : 0;
+  // Logits so low that they weigh nothing are taken higher (-inf among them: they add nothing to the
+  // last bin but their number, which then only makes it look fuller).
+  const float low = lowest_of(pol.c64);
+  const int q = weigh ? quarter_of((double)fmaxf(key2f(tk), low), pol.c64) : 0;
   if (weigh) {
-    // Logits so low that they weigh nothing are taken higher (-inf among them: they add nothing to the
-    // last bin but their number, which then only makes it look fuller).
     const int rest = octave_of(q - (BINS - 1));
-    const float low = lowest_of(pol.c64);
     w64 *mine = s_bin + (lane & (COPIES - 1));
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -500,7 +501,10 @@ __global__ __launch_bounds__(PLAN_NT) void k_filter_plan(const FilterArgs a) {
     }
   }
   __syncthreads();
-  R.set(s.flags, key2f(s.top), s.q);
+  // A row with a larger logit than this has none that weighs something among those that the scan took
+  // higher, 3 * 10^5 octaves below.
+  const float zmax = key2f(s.top);
+  R.set(s.flags | ((double)zmax * R.pol.c64 < -0.98e9 ? (unsigned)F_FAR : 0u), zmax, s.q);
   int code = 0;
   if (!R.pol.ok) code = SV_ROW_BAD_POLICY;
   else if ((R.flags & F_ODD) || !(R.flags & F_FINITE)) code = SV_ROW_BAD_LOGITS;

@@ -137,3 +137,19 @@ def test_rows_without_cuts_among_others(dev, dtype):
     # no cut by numbers alone: the rows as they are
     out, st = sv.spec_filter_logits(t.to(dev), 0.9)
     assert not st.any() and torch.equal(out.cpu(), t)
+
+
+@pytest.mark.parametrize("T", [1.0, 0.01])
+def test_rows_around_the_ends_of_the_range(dev, T):
+    """Row maxima where |z| / T passes 1.06 * 10^7 and 1.08 * 10^7 (64 z log2(e) / T near 10^9), some
+    chunks of the row a little lower, some far below."""
+    V, rng = 30011, np.random.default_rng(26)
+    edge = np.array([1.0613, 1.06143, 1.0616, 1.0722, 1.0724, 1.08196, 1.0821, 1.085]) * 1e7
+    for sign in (-1, 1):
+        z = sign * T * edge[:, None] - 0.5 * T * rng.integers(0, 40, (len(edge), V))
+        z[:, 8192:16384] -= 12 * T
+        z[:, 16384:24576] = sign * T * 1.09e7 - T * 2e6
+        z = z.astype(np.float32)
+        u = np.linspace(0.05, 0.95, len(edge)).astype(np.float32)
+        for k, p, m in ((0, 0.9, 0.0), (9000, 1.0, 0.0), (0, 1.0, 0.0), (0, 1.0, 0.01)):
+            check(dev, z, "f32", u, float(np.float32(T)), k, p, m, 4)
