@@ -281,7 +281,7 @@ sv_status spec_cache_fork(int32_t *page_table, int32_t *seq_pages, int32_t *ref_
  *                256; keys are rounded to float32 after the rotation and then coded)
  *   parent       [B, N] int32 or NULL (a chain), for the depths
  *   positions    [B, N] int32 or NULL
- *   q_out        [B, N, Hq, D] dtype out, not overlapping q: rows of nodes behind n_new are zero,
+ *   q_out        [B, N, Hq, D] dtype out, not overlapping q, k or v: rows of nodes behind n_new are zero,
  *                those of a sequence with a code NaN
  *   row_status   [B] int32 out, on none of the int32 inputs: 0, prior's code, SV_ROW_BAD_LENGTH,
  *                SV_ROW_BAD_TREE or SV_ROW_BAD_PAGE; nothing of the sequence is then written to the
@@ -313,7 +313,7 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
  *   first        [B] int32;  count [B] int32, 0 .. N, or NULL (N)
  *   k, v         [B, N, Hkv, D] dtype out; rows behind count are zero, those of a sequence with a
  *                code NaN
- *   row_status   [B] int32 out: 0, SV_ROW_BAD_LENGTH or SV_ROW_BAD_PAGE */
+ *   row_status   [B] int32 out, on none of the int32 inputs: 0, SV_ROW_BAD_LENGTH or SV_ROW_BAD_PAGE */
 sv_status spec_cache_read(const void *k_pages, const void *k_scales, const void *v_pages,
                           const void *v_scales, sv_dtype dtype, const int32_t *page_table,
                           const int32_t *first, const int32_t *count, int32_t B, int32_t N,

@@ -447,7 +447,7 @@ def spec_cache_append_rotary(q, k, v, k_pages, v_pages, page_table, cache_len, r
     position is cache_len + its depth in the chain or in the tree parent [B, N], or positions [B, N];
     q may be None, and rotary too (nothing is turned).  Strides as for spec_cache_append.  Returns
     (the turned queries [B, N, Hq, D] or None, row_status [B]), which ``out`` may supply; the queries
-    do not overlap q."""
+    do not overlap q, k or v."""
     dev = _device(k, "k")
     elsewhere = _elsewhere(dev, stream)
     if elsewhere is not None:

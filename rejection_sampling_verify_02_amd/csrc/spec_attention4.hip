@@ -665,7 +665,7 @@ sv_status spec_paged_attention4(const void *q, int64_t q_stride_b, int64_t q_str
     return SV_ERR_ALIGN;
   if (workspace_bytes < p.total || ((uintptr_t)workspace & 255)) return SV_ERR_WORKSPACE;
   // several workgroups read prior, and one writes the status
-  if (overlap(prior, row_status, B) || codes_on_inputs(row_status, B, N, cache_len, n_new, parent, nullptr)) return SV_ERR_PARAM;
+  if (overlap(prior, row_status, B) || codes_on_inputs(row_status, B, N, table_width, page_table, cache_len, n_new, parent, nullptr)) return SV_ERR_PARAM;
   Attn4Args a = {};
   a.k_pages = static_cast<const char *>(k_codes);
   a.k_scales = static_cast<const char *>(k_scales);

@@ -608,12 +608,15 @@ sv_status spec_cache_append_rotary(const void *q, int64_t q_stride_b, int64_t q_
   }
   if ((bits & 15) || (((uintptr_t)k_scales | (uintptr_t)v_scales) & 7) || (R && ((uintptr_t)rotary->inv_freq & 3))) return SV_ERR_ALIGN;
   if (overlap(prior, row_status, B)) return SV_ERR_PARAM;
-  if (q) {  // a pair's elements are read and written by different threads
-    const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)q_out, row = (uintptr_t)Hq * D * esz;
-    const uintptr_t q1 = q0 + (uintptr_t)(B - 1) * (uintptr_t)a.q_sb + (uintptr_t)(N - 1) * (uintptr_t)a.q_sn + row, o1 = o0 + (uintptr_t)B * N * row;
-    if (q0 < o1 && o0 < q1) return SV_ERR_PARAM;
+  if (q) {  // a pair's elements are read and written by different threads, keys and values by other workgroups
+    const uintptr_t head = (uintptr_t)D * esz, o0 = (uintptr_t)q_out, o1 = o0 + (uintptr_t)B * N * Hq * head;
+    auto meets = [&](const void *x, int heads, long long sb, long long sn) {
+      const uintptr_t x0 = (uintptr_t)x, x1 = x0 + (uintptr_t)(B - 1) * (uintptr_t)sb + (uintptr_t)(N - 1) * (uintptr_t)sn + (uintptr_t)heads * head;
+      return x0 < o1 && o0 < x1;
+    };
+    if (meets(q, Hq, a.q_sb, a.q_sn) || meets(k, Hkv, a.k_sb, a.k_sn) || meets(v, Hkv, a.v_sb, a.v_sn)) return SV_ERR_PARAM;
   }
-  if (codes_on_inputs(row_status, B, N, cache_len, n_new, parent, positions)) return SV_ERR_PARAM;
+  if (codes_on_inputs(row_status, B, N, table_width, page_table, cache_len, n_new, parent, positions)) return SV_ERR_PARAM;
   a.k_pages = static_cast<char *>(k_pages);
   a.k_scales = static_cast<char *>(k_scales);
   a.v_pages = static_cast<char *>(v_pages);
@@ -660,7 +663,7 @@ sv_status spec_cache_read(const void *k_pages, const void *k_scales, const void 
   if (!k_pages || !v_pages || (f4 && (!k_scales || !v_scales)) || !page_table || !first || !k || !v || !row_status) return SV_ERR_NULL;
   if ((((uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)k | (uintptr_t)v) & 15) || (((uintptr_t)k_scales | (uintptr_t)v_scales) & 7))
     return SV_ERR_ALIGN;
-  if (overlap(first, row_status, B) || overlap(count, row_status, B)) return SV_ERR_PARAM;
+  if (codes_on_inputs(row_status, B, 1, table_width, page_table, first, count, nullptr, nullptr)) return SV_ERR_PARAM;
   a.k_pages = static_cast<const char *>(k_pages);
   a.k_scales = static_cast<const char *>(k_scales);
   a.v_pages = static_cast<const char *>(v_pages);

@@ -41,12 +41,12 @@ inline Pool pool_of(int32_t Hkv, int32_t D, int32_t page, int32_t P, int32_t W) 
 inline bool overlap(const int32_t *x, const int32_t *y, int32_t n) {
   return x && y && (uintptr_t)x < (uintptr_t)(y + n) && (uintptr_t)y < (uintptr_t)(x + n);
 }
-// Whether row codes [B] lie on what several workgroups read of a sequence: lengths, counts, nodes' entries.
-inline bool codes_on_inputs(const int32_t *codes, int32_t B, int32_t N, const int32_t *cache_len, const int32_t *n_new,
-                            const int32_t *parent, const int32_t *positions) {
+// Whether row codes [B] lie on what several workgroups read of a sequence: its pages, lengths, counts, nodes' entries.
+inline bool codes_on_inputs(const int32_t *codes, int32_t B, int32_t N, int32_t W, const int32_t *table, const int32_t *cache_len,
+                            const int32_t *n_new, const int32_t *parent, const int32_t *positions) {
   const uintptr_t c0 = (uintptr_t)codes, c1 = c0 + (uintptr_t)B * 4;
-  auto on = [&](const int32_t *p) { return p && c0 < (uintptr_t)p + (uintptr_t)B * N * 4 && (uintptr_t)p < c1; };
-  return overlap(codes, cache_len, B) || overlap(codes, n_new, B) || on(parent) || on(positions);
+  auto on = [&](const int32_t *p, int32_t n) { return p && c0 < (uintptr_t)p + (uintptr_t)B * (uintptr_t)n * 4 && (uintptr_t)p < c1; };
+  return on(table, W) || overlap(codes, cache_len, B) || overlap(codes, n_new, B) || on(parent, N) || on(positions, N);
 }
 
 template <typename A>

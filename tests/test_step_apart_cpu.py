@@ -3,7 +3,7 @@ reads, or on each other, are refused before any HIP call: all of it without a GP
 import pytest
 
 import rejection_sampling_verify_02_amd as sv
-from test_step_abi_cpu import FAKE, filtered, lib, sample  # noqa: F401 (lib: the fixture)
+from test_step_abi_cpu import FAKE, attention, filtered, lib, read, rotary, sample  # noqa: F401 (lib: the fixture)
 
 PARAM = 8
 FAR = [FAKE + i * (1 << 16) for i in range(12)]  # places that nothing of one call reaches from another's
@@ -30,3 +30,21 @@ def test_tokens_and_codes_apart_from_logits(lib, dt, size):
     for at in (FAR[0], FAR[0] + size - 4, FAR[0] - 12):
         assert sample(lib, z=FAR[0], dt=dt, u=FAR[1], tok=at, st=FAR[2]) == PARAM
         assert sample(lib, z=FAR[0], dt=dt, u=FAR[1], tok=FAR[2], st=at) == PARAM
+
+
+def test_turned_queries_apart_from_what_other_workgroups_read(lib):
+    """4 sequences of 5 nodes: queries of 8 heads, keys and values of 2 heads of 128, in bf16."""
+    own = dict(q=FAR[0], k=FAR[1], v=FAR[2], out=FAR[3], kp=FAR[4], vp=FAR[5], table=FAR[6], lens=FAR[7], st=FAR[8])
+    last = (3 * 1280 + 4 * 256 + 256) * 2 - 16  # the last 16 bytes of keys or values
+    for name in ("k", "v"):
+        for at in (own["out"], own["out"] + 4 * 5 * 1024 * 2 - 16, own["out"] - last):
+            assert rotary(lib, **{**own, name: at}) == PARAM
+            assert rotary(lib, **{**own, name: at}, ks=FAR[9], vs=FAR[10]) == PARAM
+
+
+def test_codes_apart_from_page_tables(lib):
+    own = dict(table=FAR[1], lens=FAR[2])
+    for at in (FAR[1], FAR[1] - 12, FAR[1] + (4 * 7 - 1) * 4):
+        assert rotary(lib, q=FAR[3], k=FAR[4], v=FAR[5], out=FAR[6], **own, st=at) == PARAM
+        assert attention(lib, **own, st=at) == PARAM
+        assert read(lib, table=FAR[1], first=FAR[2], st=at) == PARAM
