@@ -132,11 +132,21 @@ SVD void transpose(u32x4 (&w)[Unit<T>::E]) {
   for (int i = 0; i < E; ++i) w[i] = r[i];
 }
 
-// x and y of a pair turned.
+// A double as a float32, or where it goes on to be a bf16 number as one that is rounded as the double
+// would be (to float32 and on to bf16 one in 10^5 went the other way): the double's upper word, with its
+// last bit set for what is cut off, is exact in float32 and far from a bf16 number's last bit.
+template <typename T>
+SVD float narrowed(double x) {
+  if constexpr (sizeof(T) == 4) return (float)x;
+  else return (float)__hiloint2double(__double2hiint(x) | (int)min((unsigned)__double2loint(x), 1u), 0);
+}
+
+// x and y of a pair turned, to become Ts.
+template <typename T>
 SVD void turned(float &x, float &y, const double2 cs) {
   const double a = x, b = y;
-  x = (float)fma(a, cs.x, -(b * cs.y));
-  y = (float)fma(b, cs.x, a * cs.y);
+  x = narrowed<T>(fma(a, cs.x, -(b * cs.y)));
+  y = narrowed<T>(fma(b, cs.x, a * cs.y));
 }
 
 // Where pair j's cosine and sine lie among a token's in LDS: a gap behind every four, so that lanes
@@ -144,8 +154,8 @@ SVD void turned(float &x, float &y, const double2 cs) {
 SV_HD int cs_at(int j) { return j + (j >> 2); }
 SV_HD int cs_row(int pairs) { return cs_at(pairs) + 1; }
 
-// Element d of a head at p, turned: for heads whose pairs do not lie unit against unit.
-template <typename T>
+// Element d of a head at p, turned, to become a To: for heads whose pairs do not lie unit against unit.
+template <typename T, typename To>
 SVD float turned_one(const char *p, int d, int R, const double2 *cs) {  // cs: of the token
   const T *x = reinterpret_cast<const T *>(p);
   float a = Fmt<T>::at(x, d);
@@ -154,9 +164,9 @@ SVD float turned_one(const char *p, int d, int R, const double2 *cs) {  // cs: o
   const bool second = d >= h;
   float b = Fmt<T>::at(x, second ? d - h : d + h);
   if (second) {
-    turned(b, a, cs[cs_at(d - h)]);
+    turned<To>(b, a, cs[cs_at(d - h)]);
   } else {
-    turned(a, b, cs[cs_at(d)]);
+    turned<To>(a, b, cs[cs_at(d)]);
   }
   return a;
 }
@@ -308,12 +318,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
           if (job.y < HU) {
             Fmt<T>::unpack(lv[t], v.x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) turned(w.x[e], v.x[e], cs[cs_at(job.y * E + e)]);
+            for (int e = 0; e < E; ++e) turned<T>(w.x[e], v.x[e], cs[cs_at(job.y * E + e)]);
             put(job.t0 + t, job.h, job.y + HU, v.pack());
           } else if (a.interleaved) {
 #pragma unroll
             for (int e = 0; e < E / 2; ++e)
-              if (job.y * E + 2 * e < a.R) turned(w.x[2 * e], w.x[2 * e + 1], cs[cs_at(job.y * (E / 2) + e)]);
+              if (job.y * E + 2 * e < a.R) turned<T>(w.x[2 * e], w.x[2 * e + 1], cs[cs_at(job.y * (E / 2) + e)]);
           }
           put(job.t0 + t, job.h, job.y < HU ? job.y : job.y + HU, w.pack());
         }
@@ -331,7 +341,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
                               : a.k + (long long)b * a.k_sb + (long long)(i0 + t) * a.k_sn + (size_t)(h0 + h - n_q) * D * ESZ;
       Unit<T> w;
 #pragma unroll
-      for (int e = 0; e < E; ++e) w.x[e] = turned_one<T>(p, y * E + e, a.R, s_cs + t * CS);
+      for (int e = 0; e < E; ++e) w.x[e] = turned_one<T, T>(p, y * E + e, a.R, s_cs + t * CS);
       put(t, h, y, w.pack());
     }
   }
@@ -390,7 +400,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
         Unit<T> w, v;
         if constexpr (!PAIRS) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) w.x[e] = turned_one<T>(p, y * E + e, a.R, cs);
+          for (int e = 0; e < E; ++e) w.x[e] = turned_one<T, float>(p, y * E + e, a.R, cs);
           keep(y, w);
         } else {
           const int u = y < HU ? y : y + HU;
@@ -398,12 +408,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void k_
           if (y < HU) {
             v.load(p + (y + HU) * 16);
 #pragma unroll
-            for (int e = 0; e < E; ++e) turned(w.x[e], v.x[e], cs[cs_at(y * E + e)]);
+            for (int e = 0; e < E; ++e) turned<float>(w.x[e], v.x[e], cs[cs_at(y * E + e)]);
             keep(y + HU, v);
           } else if (a.interleaved) {
 #pragma unroll
             for (int e = 0; e < E / 2; ++e)
-              if (u * E + 2 * e < a.R) turned(w.x[2 * e], w.x[2 * e + 1], cs[cs_at(u * (E / 2) + e)]);
+              if (u * E + 2 * e < a.R) turned<float>(w.x[2 * e], w.x[2 * e + 1], cs[cs_at(u * (E / 2) + e)]);
           }
           keep(u, w);
         }
