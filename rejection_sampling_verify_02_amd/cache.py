@@ -117,7 +117,7 @@ class Rotary(NamedTuple):
         it, the context the model was trained on, pairs that turn at least `fast` times over that
         context keep their frequency, those that turn at most `slow` times have it divided, those
         between in proportion, and the turned elements are multiplied by 1 + ln(stretch) / 10
-        (interpolation by parts; "YaRN", Peng et al. 2023)."""
+        (interpolation by parts; "YaRN", Peng et al. 2023; `_replace(factor=1.0)` leaves that out)."""
         if rot_dim < 2 or rot_dim % 2 or not base > 0 or not stretch >= 1 or (trained is not None and (trained < 1 or not slow < fast)):
             raise ValueError(f"rot_dim must be even and positive, base positive, stretch at least 1, trained positive and slow below fast, "
                              f"got {rot_dim}, {base}, {stretch}, {trained}, {slow}, {fast}")
