@@ -56,7 +56,7 @@ struct ChunkSum {
 
 // What k_filter_plan found out about a row.
 struct RowPlan {
-  w64 mass[BINS];        // the row's bins: weights in units of 2^-35 of each bin's octave, and numbers
+  w64 mass[BINS];        // the row's bins: weights in units of 2^-F of the octave of q, and numbers
   unsigned count[BINS];
   w64 above;             // of the first step: what lies above its range
   double target;         // and what it looks for
@@ -351,10 +351,7 @@ struct Row {
   SVD double arg(float z) const { return fmax((double)z - off, least); }
   SVD int bin_of(float z) const { return min(Q - quarter_of(arg(z), pol.c64), BINS - 1); }
   SVD Weight plain_weight(float z) const { return weight_of(arg(z), pol.c64, s.tab, rest); }
-  SVD w64 weight(float z) const {
-    const Weight w = plain_weight(z);
-    return shifted(w.m, F - W_BITS - (O - max(octave_of(w.q), rest)));
-  }
+  SVD w64 in_units(const Weight &w) const { return shifted(w.m, F - W_BITS - (O - max(octave_of(w.q), rest))); }
   // The weight of a chunk's bin, of quarter octave q: as the row's weights are, and as its bin j adds them up.
   SVD w64 mass_of_chunk(int q, w64 x) const { return shifted(x & ((1ull << W_COUNT) - 1ull), F - W_BITS - (O - octave_of(q))); }
   SVD w64 mass_for_bin(int q, int j, w64 x) const { return shifted(x & ((1ull << W_COUNT) - 1ull), octave_of(q) - octave_of(Q - j)); }
@@ -386,18 +383,22 @@ struct Row {
     const unsigned long long b0 = __ballot((double)(pm + m0) >= w), b1 = __ballot((double)(pm + m0 + m1) >= w);
     return b1 == 0 ? BINS - 1 : 2 * (__ffsll(b1) - 1) + ((b0 >> (__ffsll(b1) - 1)) & 1 ? 0 : 1);
   }
-  SVD void prefixes(bool units) {
+  SVD int bits_down(int j) const { return W_BITS + O - octave_of(Q - j); }  // of bin j's own units below the octave O
+  // `own`: the bins are in units of their own, and F is yet to be chosen.
+  SVD void prefixes(bool own) {
     const int lane = lane_id();
-    const w64 a0 = s.mass[2 * lane], a1 = s.mass[2 * lane + 1];
-    const int d0 = W_BITS + O - octave_of(Q - 2 * lane), d1 = W_BITS + O - octave_of(Q - 2 * lane - 1);
-    if (units) {  // the total in units of 2^(30 - F0), more than it is by 64 at most; F puts it below 2^61 units
-      const unsigned part = (unsigned)((shifted(a0, F0 - d0) + shifted(a1, F0 - d1)) >> 30);
-      F = F0 - 1 + __clz(__builtin_amdgcn_readlane((int)scan_add_u(part), WAVE - 1) + WAVE);
-    }
-    m0 = shifted(a0, F - d0);
-    m1 = shifted(a1, F - d1);
+    m0 = s.mass[2 * lane];
+    m1 = s.mass[2 * lane + 1];
     c0 = s.count[2 * lane];
     c1 = s.count[2 * lane + 1];
+    if (own) {
+      // the total in units of 2^(30 - F0), more than it is by 64 at most; F puts it below 2^61 units
+      const int d0 = bits_down(2 * lane), d1 = bits_down(2 * lane + 1);
+      const unsigned part = (unsigned)((shifted(m0, F0 - d0) + shifted(m1, F0 - d1)) >> 30);
+      F = F0 - 1 + __clz(__builtin_amdgcn_readlane((int)scan_add_u(part), WAVE - 1) + WAVE);
+      m0 = shifted(m0, F - d0);
+      m1 = shifted(m1, F - d1);
+    }
     const w64 im = wave_incl(m0 + m1);
     const unsigned ic = scan_add_u(c0 + c1);
     pm = im - m0 - m1;
@@ -577,7 +578,7 @@ __global__ __launch_bounds__(PLAN_NT) void k_filter_plan(const FilterArgs a) {
     }
   }
   for (int i = tid; i < BINS; i += PLAN_NT) {
-    p.mass[i] = s.mass[i];
+    p.mass[i] = shifted(s.mass[i], R.F - R.bits_down(i));
     p.count[i] = s.count[i];
   }
   if (tid == 0) {
@@ -738,7 +739,7 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
   }
   powers(s.row.tab);
   __syncthreads();
-  R.F = p.F;
+  R.F = __builtin_amdgcn_readfirstlane(p.F);
   R.prefixes(false);
   bool begin = R.far || step == DRAWN;  // of a step: the gather has begun the others
   for (;;) {
@@ -766,20 +767,18 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
       if (step == COUNT) {
         atomicAdd(&s.hist[(k - lo) >> sh], 1ull);
       } else {
-        if (step == ALL) {
-          const Weight w = R.plain_weight(K::value(k));
-          const int j = min(R.Q - w.q, BINS - 1);
-          atomicAdd(&s.row.mass[j], w.m);
-          atomicAdd(&s.row.count[j], 1u);
-          return;
-        }
-        const w64 w = R.weight(K::value(k));
+        const Weight x = R.plain_weight(K::value(k));
+        const w64 w = R.in_units(x);
         if (step == MASS) {
           atomicAdd(&s.hist[(k - lo) >> sh], w);
         } else if (step == REST) {
           part += w;
-        } else {
+        } else if (step == DRAWN) {
           atomicAdd(&s_chunk[at / FC], w);
+        } else {
+          const int j = min(R.Q - x.q, BINS - 1);
+          atomicAdd(&s.row.mass[j], x.m);
+          atomicAdd(&s.row.count[j], 1u);
         }
       }
     };
@@ -980,7 +979,7 @@ __global__ __launch_bounds__(PICK_NT) __attribute__((amdgpu_waves_per_eu(4))) vo
     r.unpack(raw[k], i, z);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= R.tau ? R.weight(z[e]) : 0ull;
+      w[e] = i < r.n && z[e] > -INFINITY && K::of(z[e]) >= R.tau ? R.in_units(R.plain_weight(z[e])) : 0ull;
       sum += w[e];
     }
     const w64 inc = wave_incl(sum);
