@@ -15,7 +15,9 @@
 //                 16001 slots, 8 key heads of 128: 104 us, 5.4 TB/s; its loads alone take 98.  (With
 //                 the codes in registers, one tile ahead, and shares of equal length: 135.)  The
 //                 keys could go into the scaled matrix instruction as they are, the queries as two
-//                 8-bit parts; but that one's sums are only good to 2^-12 of their terms.
+//                 8-bit parts; but that one's sums are only good to 2^-12 of their terms.  With 17
+//                 to 32 rows, 64 chains of 5 over the same slots, 158 us, twice its bytes' time:
+//                 256 registers, and 13 more in scratch memory.
 //   k_attn4_wide  more rows.  The waves share each tile through LDS as bf16, converted once by one
 //                 of them.  16 trees of 32 nodes, 4 heads a key head: 94 us; the products alone
 //                 would be 37.  The rest is what a wave does between them, weights and conversions,

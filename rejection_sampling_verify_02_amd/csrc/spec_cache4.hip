@@ -19,8 +19,8 @@ struct Commit4Args {
 // its threads hold in registers: everything a batch moves is read before any of it is written, and
 // later batches read nothing that earlier ones wrote, since sources lie behind their targets.  An
 // entry is D / 32 blocks of a key, 16 pieces of a value and 2 D / 32 scale bytes, an item each
-// (16 trees of 32 nodes, 32 layers, D = 128: in bytes a quarter of the bf16 cache's commit; bound
-// by the partial lines that it touches).
+// (16 trees of 32 nodes, 32 layers, 8 heads of 128: 18 us for 5.6 MB, the bf16 cache's commit 23;
+// bound by the partial lines that it touches).
 constexpr int COMMIT4_R = 2;  // items a thread holds
 
 __global__ __launch_bounds__(NT) void k_cache_commit4(const Commit4Args a) {
@@ -139,7 +139,8 @@ struct Copy4Args {
 constexpr int COPY4_WGS = 1024;  // 4 a CU, whatever there is to copy: the host does not know
 
 // The kept slots of a page into another: a workgroup moves one head of one layer at a time, in
-// units of 16 bytes, the ends of rows in smaller ones.
+// units of 16 bytes, the ends of rows in smaller ones.  Bound by bytes: 128 pages in 32 layers of 8
+// heads of 128, 267 MB read and written in 54 us, a copy's rate.
 __global__ __launch_bounds__(NT) void k_cache_copy4(const Copy4Args a) {
   const unsigned per = a.L * a.pool.Hkv;
   const unsigned long long items = (unsigned long long)*a.n_copy * per;

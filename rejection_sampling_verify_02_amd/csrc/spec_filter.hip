@@ -25,8 +25,8 @@
 //   k_filter_write   the row again, with -inf below the threshold
 //
 // Bound by the weights: 26 vector instructions and a place in LDS for a logit.  320 rows of 128256
-// in bf16, top-p 0.9: scan 42 us (its bytes 12), plan 10, gather 21, pick 13, write 28 (the
-// row read and written; a copy takes 34).  64 rows drawn from: 13, 8, 8, 12.
+// in bf16, top-p 0.9: scan 43 us (its bytes 12), plan 10, gather 21, pick 14, write 28 (the
+// row read and written; a copy takes 34).  64 rows drawn from: 13, 8, 8, 13.
 
 #include "sv_common.h"
 
