@@ -11,7 +11,7 @@
 // octave; where weights of different octaves meet, the unit goes by the row's total, which is put
 // between 2^59 and 2^61 units: cutting off what is smaller costs a sum over 2^24 tokens, the largest of
 // them or all, 2^-35 of itself at most (a unit that went by the vocabulary's size and the row's largest:
-// 10^-8 at 2^18 tokens, 2 * 10^-5 at 2^24, and thresholds with hundreds of tokens too many).
+// 2 * 10^-9 at 2^18 tokens, 2 * 10^-5 at 2^24, and thresholds with hundreds of tokens too many).
 //
 //   k_filter_scan    a chunk of a row a workgroup, one read of the logits: the chunk's largest, and
 //                    counts and weights by quarter octave of the weight (the same ones for every
