@@ -345,6 +345,8 @@ def spec_verify(target_logits, draft_logits, draft_tokens, u_accept, u_sample, t
 
 def _each(x) -> bool:
     """Whether a setting is a tensor with an entry for each row."""
+    if x.__class__ is float or x.__class__ is int:
+        return False
     import torch
     return isinstance(x, torch.Tensor) and x.dim() > 0
 
@@ -370,10 +372,12 @@ def spec_sample(logits, u, temperature: float, top_k: int = 0, *, top_p=1.0, min
     include/spec_filter.h; ``workspace`` is then a uint8 tensor or None (taken from torch's
     allocator).  Other tensors of one element are taken as numbers."""
     import torch
-    if _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p):
+    each = _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p)
+    if each:
         temperature, top_p, min_p = (_number(x, torch.float32, logits, u, workspace) for x in (temperature, top_p, min_p))
         top_k = _number(top_k, torch.int32, logits, u, workspace)
-    if _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p) or top_p != 1.0 or min_p != 0.0:
+        each = _each(temperature) or _each(top_k) or _each(top_p) or _each(min_p)
+    if each or top_p != 1.0 or min_p != 0.0:
         from . import filter as _filter
         return _filter.sample(logits, u, temperature, top_k, top_p, min_p, workspace, stream, out, events)
     lib = load_library()
